@@ -207,6 +207,51 @@ int dualkv_fold(const void* g_rep, void* g_packed, int P, int N, const int32_t* 
                 void* stream);
 
 /*
+ * Per-head norm and position rotation of q and k: the step between the
+ * projections and dualkv_fwd, and (backward) between dualkv_bwd and the
+ * projections' gradients, on packed rows.  Positions follow from the layout: t in
+ * the prompt, P + r for response token r of any segment.  For a head's row x:
+ *   n = x * (mean(x^2) + eps)^-1/2 * (weight + weight_offset)     (n = x without weights)
+ *   y = n with each pair j < rope_dim/2 turned by the angle position * inv_freq[j]:
+ *       (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin), where (a, b) is
+ *       (j, j + rope_dim/2), or (2j, 2j + 1) if interleaved; values from rope_dim on are kept.
+ * Computed in fp32 (angles in fp64) and rounded to bf16 once, at the end.
+ *
+ *   q, k            device bf16: head h of row t at [t * stride + h * D].  q_stride >= Hq * D
+ *                   and k_stride >= Hkv * D in elements, multiples of 8, so q and k may be
+ *                   columns of one fused projection's rows
+ *   q_weight, k_weight  device [D] of weight_dtype (DUALKV_BF16 or DUALKV_F32), or both NULL:
+ *                   no norm.  weight_offset is added to them (1 where a model stores w - 1)
+ *   inv_freq        device fp32 [rope_dim / 2]; rope_dim a multiple of 16, 0 .. D (0: no rotation)
+ *   D               64, 128 or 512; N <= 4095 (DUALKV_ERR_UNSUPPORTED beyond)
+ *   q_out, k_out    device bf16 [T, Hq, D] and [T, Hkv, D], contiguous, written
+ * Backward:
+ *   dq_out, dk_out  device bf16, contiguous: the gradients of q_out and k_out
+ *   dq, dk          device bf16, written: the gradients of q and k, rows dq_stride / dk_stride
+ *                   elements apart (same rules as q_stride, k_stride)
+ *   dq_weight, dk_weight  device fp32 [D], written; sums over rows and heads in a fixed order
+ *                   (not written without weights)
+ *   workspace       device, 256-byte aligned, >= dualkv_qk_norm_rope_bwd_workspace_bytes()
+ *                   (0 for invalid input); not needed without weights
+ * No output may share memory with an input or with another output (columns of one fused
+ * buffer with equal strides may interleave): DUALKV_ERR_INVALID.
+ * These calls keep nothing between calls and may be captured into a CUDA graph.
+ */
+#define DUALKV_BF16 0
+#define DUALKV_F32 1
+int dualkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                        const void* k_weight, int weight_dtype, float weight_offset, float eps, const float* inv_freq,
+                        int rope_dim, int interleaved, int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D,
+                        void* q_out, void* k_out, void* stream);
+size_t dualkv_qk_norm_rope_bwd_workspace_bytes(int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D);
+int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+                            const void* dk_out, const void* q_weight, const void* k_weight, int weight_dtype,
+                            float weight_offset, float eps, const float* inv_freq, int rope_dim, int interleaved, int P,
+                            int N, const int32_t* R_offsets, int Hq, int Hkv, int D, void* dq, int64_t dq_stride,
+                            void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Token-reduction factor rho = sum_n (P + R_n) / (P + sum_n R_n) (paper
  * abstract: rho = N(P+R)/(P+NR) for equal lengths).  Host only; -1 on invalid input.
  */
@@ -243,7 +288,8 @@ const char* dualkv_error_string(int code);
 #define DUALKV_KERNEL_REDUCE 3
 #define DUALKV_KERNEL_DQ 4
 #define DUALKV_KERNEL_PACK 5 /* dualkv_pack, dualkv_unpack and dualkv_fold */
-#define DUALKV_KERNEL_KINDS 6
+#define DUALKV_KERNEL_ROPE 6 /* dualkv_qk_norm_rope and its backward */
+#define DUALKV_KERNEL_KINDS 7
 int dualkv_profile_enable(int on);
 int dualkv_profile_read(double* ms, int64_t* launches);
 

@@ -16,6 +16,7 @@
 #include "kernels.h"
 #include "plan.h"
 #include "plan_cache.h"
+#include "segs.cuh"
 
 using namespace dkv;
 
@@ -466,6 +467,94 @@ int pack_call(int kind, const void* src, void* dst, int P, int N, const int32_t*
   return mark_use(&o->last_use, st);
 }
 
+// ---------------------------------------------------------------- per-token operators
+// `rows` rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void* p;
+  uint64_t stride, width, rows;
+};
+
+Rows flat(const void* p, uint64_t bytes) { return Rows{p, bytes, bytes, 1}; }
+
+// Whether two row sets share a byte.  Interleaved ones (column ranges of one buffer)
+// are told apart when their strides agree; otherwise any overlap of the spans counts.
+bool rows_overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || !a.rows || !b.rows || !a.width || !b.width) return false;
+  const uint64_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t a1 = a0 + (a.rows - 1) * a.stride + a.width, b1 = b0 + (b.rows - 1) * b.stride + b.width;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.stride != b.stride || a.rows == 1 || b.rows == 1) return true;
+  const uint64_t d = b0 >= a0 ? (b0 - a0) % a.stride : (a.stride - (a0 - b0) % a.stride) % a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
+
+// Whether an output shares a byte with an input or with another output.
+bool outputs_overlap(const std::vector<Rows>& outs, const std::vector<Rows>& ins) {
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (const Rows& r : ins)
+      if (rows_overlap(outs[i], r)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (rows_overlap(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+constexpr int64_t kMaxRowStride = int64_t(1) << 31;  // elements: rows x stride x 4 bytes stays far inside 64 bits
+
+int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+              const void* dk_out, const void* q_weight, const void* k_weight, int weight_dtype, float weight_offset,
+              float eps, const float* inv_freq, int rope_dim, int interleaved, int P, int N, const int32_t* R_offsets,
+              int Hq, int Hkv, int D, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+              float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  if (validate_layout(P, N, R_offsets, Hq, Hkv, D)) return DUALKV_ERR_INVALID;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if (wq > INT32_MAX) return DUALKV_ERR_INVALID;
+  if (!q || !k || !q_out || !k_out || (backward && (!dq_out || !dk_out))) return DUALKV_ERR_INVALID;
+  for (int64_t s : {q_stride, q_out_stride})
+    if (s < wq || s > kMaxRowStride || s % 8) return DUALKV_ERR_INVALID;
+  for (int64_t s : {k_stride, k_out_stride})
+    if (s < wk || s > kMaxRowStride || s % 8) return DUALKV_ERR_INVALID;
+  const bool norm = q_weight != nullptr;
+  if (norm != (k_weight != nullptr)) return DUALKV_ERR_INVALID;
+  if (norm && backward && (!dq_weight || !dk_weight)) return DUALKV_ERR_INVALID;
+  if (weight_dtype != DUALKV_BF16 && weight_dtype != DUALKV_F32) return DUALKV_ERR_INVALID;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset)) return DUALKV_ERR_INVALID;
+  if (rope_dim < 0 || rope_dim > D || rope_dim % 16 || (rope_dim && !inv_freq)) return DUALKV_ERR_INVALID;
+  for (const void* p : {q, k, dq_out, dk_out, q_weight, k_weight, (const void*)inv_freq, (const void*)q_out,
+                        (const void*)k_out, (const void*)dq_weight, (const void*)dk_weight})
+    if (!aligned16(p)) return DUALKV_ERR_ALIGN;
+  if (N > kMaxSegs) return DUALKV_ERR_UNSUPPORTED;
+  const int64_t T = (int64_t)P + R_offsets[N];
+  const size_t need = norm && backward ? rope_workspace_bytes(T, D) : 0;
+  if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
+    return DUALKV_ERR_WORKSPACE;
+  const uint64_t uT = (uint64_t)T, wbytes = (uint64_t)D * (weight_dtype == DUALKV_F32 ? 4 : 2);
+  std::vector<Rows> ins = {Rows{q, (uint64_t)q_stride * 2, (uint64_t)wq * 2, uT},
+                           Rows{k, (uint64_t)k_stride * 2, (uint64_t)wk * 2, uT},
+                           flat(q_weight, wbytes), flat(k_weight, wbytes), flat(inv_freq, (uint64_t)rope_dim * 2),
+                           flat(dq_out, uT * wq * 2), flat(dk_out, uT * wk * 2)};
+  std::vector<Rows> outs = {Rows{q_out, (uint64_t)q_out_stride * 2, (uint64_t)wq * 2, uT},
+                            Rows{k_out, (uint64_t)k_out_stride * 2, (uint64_t)wk * 2, uT}};
+  if (need) {
+    outs.push_back(flat(dq_weight, (uint64_t)D * 4));
+    outs.push_back(flat(dk_weight, (uint64_t)D * 4));
+    outs.push_back(flat(workspace, need));
+  }
+  if (outputs_overlap(outs, ins)) return DUALKV_ERR_INVALID;
+  typedef __nv_bfloat16 bf;
+  RopeArgs a{static_cast<const bf*>(q), static_cast<const bf*>(k), q_stride, k_stride, static_cast<const bf*>(dq_out),
+             static_cast<const bf*>(dk_out), static_cast<bf*>(q_out), static_cast<bf*>(k_out), q_out_stride,
+             k_out_stride, q_weight, k_weight, inv_freq, static_cast<float*>(workspace), T, Hq, Hkv, rope_dim / 2,
+             weight_offset, eps, weight_dtype == DUALKV_F32, interleaved != 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (timed(DUALKV_KERNEL_ROPE, st, [&] {
+        return launch_rope(backward, D, a, P, N, R_offsets, dq_weight, dk_weight, st);
+      }) != cudaSuccess)
+    return DUALKV_ERR_CUDA;
+  return DUALKV_OK;
+}
+
 bool supported_d(int D) { return D == 64 || D == 128 || D == 512; }  // backward
 bool supported_fwd_d(int D) { return D == 64 || D == 128 || D == 512; }
 
@@ -748,6 +837,31 @@ int dualkv_unpack(const void* x_packed, void* x_rep, int P, int N, const int32_t
 int dualkv_fold(const void* g_rep, void* g_packed, int P, int N, const int32_t* R_offsets, int row_elems,
                 void* stream) {
   return pack_call(2, g_rep, g_packed, P, N, R_offsets, row_elems, stream);
+}
+
+int dualkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                        const void* k_weight, int weight_dtype, float weight_offset, float eps, const float* inv_freq,
+                        int rope_dim, int interleaved, int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D,
+                        void* q_out, void* k_out, void* stream) {
+  return rope_impl(false, q, q_stride, k, k_stride, nullptr, nullptr, q_weight, k_weight, weight_dtype, weight_offset,
+                   eps, inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, q_out, (int64_t)Hq * D, k_out,
+                   (int64_t)Hkv * D, nullptr, nullptr, nullptr, 0, stream);
+}
+
+size_t dualkv_qk_norm_rope_bwd_workspace_bytes(int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D) {
+  if (validate_layout(P, N, R_offsets, Hq, Hkv, D) || N > kMaxSegs) return 0;
+  return rope_workspace_bytes((int64_t)P + R_offsets[N], D);
+}
+
+int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+                            const void* dk_out, const void* q_weight, const void* k_weight, int weight_dtype,
+                            float weight_offset, float eps, const float* inv_freq, int rope_dim, int interleaved, int P,
+                            int N, const int32_t* R_offsets, int Hq, int Hkv, int D, void* dq, int64_t dq_stride,
+                            void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return rope_impl(true, q, q_stride, k, k_stride, dq_out, dk_out, q_weight, k_weight, weight_dtype, weight_offset, eps,
+                   inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dq_stride, dk, dk_stride,
+                   dq_weight, dk_weight, workspace, workspace_bytes, stream);
 }
 
 int dualkv_check_status(void* stream) {

@@ -159,4 +159,26 @@ int pack_group_lanes(int row_elems);
 cudaError_t launch_pack(int kind, const void* src, void* dst, const int32_t* d_off, int P, int N, int64_t T,
                         int row_elems, int num_sms, cudaStream_t st);
 
+// ---- per-head norm and rotation of q and k (rope.cu)
+constexpr int kRopeMaxBlocks = 152 * 6;  // resident blocks of 8 warps
+
+struct RopeArgs {
+  const __nv_bfloat16 *q, *k;            // projections' rows, head h of row t at t * stride + h * D
+  int64_t q_stride, k_stride;            // elements
+  const __nv_bfloat16 *dq_out, *dk_out;  // backward: gradients of the rotated q and k, contiguous
+  __nv_bfloat16 *q_out, *k_out;          // written: rotated q and k, or (backward) the gradients of q and k
+  int64_t q_out_stride, k_out_stride;
+  const void *q_weight, *k_weight;       // D values each; both null: no norm
+  const float* inv_freq;                 // half values
+  float* partial;                        // backward: [block][2][D] weight gradients
+  int64_t T;
+  int Hq, Hkv, half;                     // half = rope_dim / 2
+  float w0, eps;
+  bool weight_f32, inter;
+};
+// One launch over all rows; the backward adds a second one that sums the weight gradients.
+cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, const int32_t* off, float* dqw,
+                        float* dkw, cudaStream_t st);
+size_t rope_workspace_bytes(int64_t T, int D);
+
 }  // namespace dkv

@@ -8,6 +8,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -33,9 +34,12 @@ EXPORTS = ("dualkv_fwd", "dualkv_bwd_workspace_bytes", "dualkv_bwd", "dualkv_bui
            "dualkv_profile_read", "dualkv_selftest_timeout", "dualkv_bwd_noalloc", "dualkv_release",
            "dualkv_pack", "dualkv_unpack", "dualkv_fold", "dualkv_fwd_heads", "dualkv_bwd_heads",
            "dualkv_fwd_layers", "dualkv_bwd_layers", "dualkv_bwd_layers_workspace_bytes",
-           "dualkv_selftest_kernel", "dualkv_plan_cache_info")
+           "dualkv_selftest_kernel", "dualkv_plan_cache_info", "dualkv_qk_norm_rope",
+           "dualkv_qk_norm_rope_bwd", "dualkv_qk_norm_rope_bwd_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 32 << 20
-KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack")
+KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope")
+DUALKV_BF16 = 0
+DUALKV_F32 = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +107,15 @@ def load(path: Optional[str] = None):
         lib.dualkv_bwd_layers.argtypes = [ci, vp, vp, vp, vp, vp, vp, i32p, ci, ci, i32p, ci, ci, ci, cf, vp, vp, vp,
                                           vp, ctypes.c_size_t, vp]
         lib.dualkv_bwd_layers.restype = ci
+        i64 = ctypes.c_int64
+        rope = [vp, vp, ci, cf, cf, vp, ci, ci, ci, ci, i32p, ci, ci, ci]
+        lib.dualkv_qk_norm_rope.argtypes = [vp, i64, vp, i64] + rope + [vp, vp, vp]
+        lib.dualkv_qk_norm_rope.restype = ci
+        lib.dualkv_qk_norm_rope_bwd_workspace_bytes.argtypes = [ci, ci, i32p, ci, ci, ci]
+        lib.dualkv_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.dualkv_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp] + rope + [vp, i64, vp, i64, vp, vp, vp,
+                                                                                     ctypes.c_size_t, vp]
+        lib.dualkv_qk_norm_rope_bwd.restype = ci
         lib.dualkv_release.argtypes = []
         lib.dualkv_release.restype = None
         _lib = lib
@@ -114,6 +127,10 @@ def error_string(code: int) -> str:
 
 
 def _offsets(R_offsets: Sequence[int]):
+    """R_offsets as a ctypes int32 array; one that already is such an array is passed on as it is,
+    so a program with one layout for many calls can convert it once (``offsets``)."""
+    if isinstance(R_offsets, ctypes.Array) and R_offsets._type_ is ctypes.c_int32:
+        return R_offsets
     arr = (ctypes.c_int32 * len(R_offsets))(*[int(x) for x in R_offsets])
     return arr
 
@@ -348,6 +365,122 @@ def dualkv_fold(g_rep, g_packed, P, N, R_offsets, stream=None) -> None:
     _pack_call(load().dualkv_fold, "dualkv_fold", g_rep, g_packed, P, N, R_offsets, stream)
 
 
+def offsets(R_offsets: Sequence[int]):
+    """R_offsets as a ctypes int32 array, which every call here takes in place of the sequence."""
+    return _offsets(R_offsets)
+
+
+# ------------------------------------------------------------------ per-token operators
+_WEIGHT_DTYPES = {torch.bfloat16: DUALKV_BF16, torch.float32: DUALKV_F32}
+
+
+def _check_tensor(where, name, t, shape, dtypes, device, rows=False):
+    """A CUDA tensor on the calling thread's current device with this shape and one of these dtypes: contiguous, or
+    (rows) only contiguous within a row of its first dimension."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{where}: {name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)} for this call, got {tuple(t.shape)}")
+    if not t.is_contiguous() and not (rows and (t.shape[0] == 0 or t[0].is_contiguous())):
+        raise ValueError(f"{where}: {name} must be contiguous" + (" within its rows" if rows else ""))
+
+
+def _row_stride(t):
+    """Elements between the rows of t's first dimension (a single row has the stride that its width gives)."""
+    width = t.numel() // max(t.shape[0], 1)
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _layout_rows(where, P, N, R_offsets):
+    N = int(N)
+    if N < 1 or len(R_offsets) != N + 1:
+        raise ValueError(f"{where}: R_offsets must hold N + 1 = {N + 1} entries, got {len(R_offsets)}")
+    return int(P) + int(R_offsets[N])
+
+
+def _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D):
+    """Checks shared by the forward and the backward; returns (T, device, the C call's weight dtype)."""
+    T = _layout_rows(where, P, N, R_offsets)
+    dev = torch.cuda.current_device()
+    bf = (torch.bfloat16,)
+    _check_tensor(where, "q", q, (T, Hq, D), bf, dev, rows=True)
+    _check_tensor(where, "k", k, (T, Hkv, D), bf, dev, rows=True)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError(f"{where}: q_weight and k_weight go together")
+    wd = DUALKV_F32
+    if q_weight is not None:
+        _check_tensor(where, "q_weight", q_weight, (D,), tuple(_WEIGHT_DTYPES), dev)
+        _check_tensor(where, "k_weight", k_weight, (D,), (q_weight.dtype,), dev)
+        wd = _WEIGHT_DTYPES[q_weight.dtype]
+    if int(rope_dim):
+        _check_tensor(where, "inv_freq", inv_freq, (int(rope_dim) // 2,), (torch.float32,), dev)
+    return T, dev, wd
+
+
+def dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P, N, R_offsets,
+                        Hq, Hkv, D, q_out, k_out, stream=None) -> None:
+    """Per-head RMS norm and position rotation of packed q [T, Hq, D] and k [T, Hkv, D] (rows may be strided, as
+    columns of a fused projection are) into the contiguous q_out, k_out that dualkv_fwd reads."""
+    where = "dualkv_qk_norm_rope"
+    T, dev, wd = _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D)
+    _check_tensor(where, "q_out", q_out, (T, Hq, D), (torch.bfloat16,), dev)
+    _check_tensor(where, "k_out", k_out, (T, Hkv, D), (torch.bfloat16,), dev)
+    rc = load().dualkv_qk_norm_rope(_ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(q_weight), _ptr(k_weight), wd,
+                                    float(weight_offset), float(eps), _ptr(inv_freq), int(rope_dim),
+                                    1 if interleaved else 0, int(P), int(N), _offsets(R_offsets), int(Hq), int(Hkv),
+                                    int(D), _ptr(q_out), _ptr(k_out), _stream(stream))
+    _raise(rc, where)
+
+
+def dualkv_qk_norm_rope_bwd_workspace_bytes(P, N, R_offsets, Hq, Hkv, D) -> int:
+    return int(load().dualkv_qk_norm_rope_bwd_workspace_bytes(int(P), int(N), _offsets(R_offsets), int(Hq), int(Hkv),
+                                                              int(D)))
+
+
+def dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved,
+                            P, N, R_offsets, Hq, Hkv, D, dq, dk, dq_weight, dk_weight, workspace, workspace_bytes=None,
+                            stream=None) -> None:
+    """Gradients of dualkv_qk_norm_rope: dq, dk (rows may be strided) and, with weights, dq_weight, dk_weight."""
+    where = "dualkv_qk_norm_rope_bwd"
+    T, dev, wd = _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D)
+    bf = (torch.bfloat16,)
+    _check_tensor(where, "dq_out", dq_out, (T, Hq, D), bf, dev)
+    _check_tensor(where, "dk_out", dk_out, (T, Hkv, D), bf, dev)
+    _check_tensor(where, "dq", dq, (T, Hq, D), bf, dev, rows=True)
+    _check_tensor(where, "dk", dk, (T, Hkv, D), bf, dev, rows=True)
+    if q_weight is not None:
+        _check_tensor(where, "dq_weight", dq_weight, (D,), (torch.float32,), dev)
+        _check_tensor(where, "dk_weight", dk_weight, (D,), (torch.float32,), dev)
+    workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
+    rc = load().dualkv_qk_norm_rope_bwd(_ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(dq_out), _ptr(dk_out),
+                                        _ptr(q_weight), _ptr(k_weight), wd, float(weight_offset), float(eps),
+                                        _ptr(inv_freq), int(rope_dim), 1 if interleaved else 0, int(P), int(N),
+                                        _offsets(R_offsets), int(Hq), int(Hkv), int(D), _ptr(dq), _row_stride(dq),
+                                        _ptr(dk), _row_stride(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+                                        workspace_bytes, _stream(stream))
+    _raise(rc, where)
+
+
+def _workspace_bytes(where, workspace, workspace_bytes, device):
+    """Bytes of a workspace tensor (0 for None); no more than it holds may be claimed."""
+    if workspace is None:
+        return 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != device:
+        raise ValueError(f"{where}: workspace is on cuda:{workspace.get_device()}, the current device is cuda:{device}")
+    held = workspace.numel() * workspace.element_size()
+    if workspace_bytes is None:
+        return held
+    if int(workspace_bytes) > held:
+        raise ValueError(f"{where}: workspace holds {held} bytes, not {workspace_bytes}")
+    return int(workspace_bytes)
+
+
 def dualkv_build_index(P, N, R_offsets):
     """Host index builder: returns (seg_id, pos_id, cu_seqlens_rep, rep2pack) as int32 CPU tensors."""
     T = int(P) + int(R_offsets[N])
@@ -448,3 +581,44 @@ def backward(q, k, v, out, lse, dout, P, R_offsets, window=0, scale=None, worksp
     dualkv_bwd(q, k, v, out, lse, dout, P, N, R_offsets, Hq, Hkv, D, scale, window, dq, dk, dv, workspace,
                None, stream)
     return dq, dk, dv
+
+
+def _allocating_on(stream):
+    """Context in which tensors are allocated for use on `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def qk_norm_rope(q, k, P, R_offsets, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0,
+                 interleaved=False, stream=None):
+    """Allocate q_out, k_out and run dualkv_qk_norm_rope; rope_dim is twice the length of inv_freq (None: no rotation)."""
+    (T, Hq, D), Hkv = q.shape, k.shape[1]
+    rope_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    with _allocating_on(stream):
+        q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(T, Hkv, D, dtype=k.dtype, device=k.device)
+        dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P,
+                            len(R_offsets) - 1, R_offsets, Hq, Hkv, D, q_out, k_out)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, P, R_offsets, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                          weight_offset=0.0, interleaved=False, stream=None):
+    """Allocate the gradients (and the workspace) and run dualkv_qk_norm_rope_bwd.
+    Returns (dq, dk, dq_weight, dk_weight), the last two None without weights."""
+    (T, Hq, D), Hkv, N = q.shape, k.shape[1], len(R_offsets) - 1
+    rope_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    dqw = dkw = ws = None
+    with _allocating_on(stream):
+        dq = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+        dk = torch.empty(T, Hkv, D, dtype=k.dtype, device=k.device)
+        if q_weight is not None:
+            dqw, dkw = (torch.empty(D, dtype=torch.float32, device=q.device) for _ in range(2))
+            nbytes = dualkv_qk_norm_rope_bwd_workspace_bytes(P, N, R_offsets, Hq, Hkv, D)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim,
+                                interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dk, dqw, dkw, ws)
+    return dq, dk, dqw, dkw
