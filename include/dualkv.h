@@ -252,6 +252,96 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
                             size_t workspace_bytes, void* stream);
 
 /*
+ * Log-probabilities (and entropies) of the response tokens from the logits, and the
+ * gradient of the logits.  `logits` holds the packed rows that can predict a response
+ * token: rows P - 1 .. T - 1 (M = 1 + R_offsets[N] rows, the first being the prompt's
+ * last one), or without a prompt (P = 0) all rows 0 .. T - 1.  Response token i is
+ * predicted by the row before it in its own sequence: the prompt's last row if i opens
+ * its segment, else the row of token i - 1.  Without a prompt a token that opens its
+ * segment is not predicted by any row.  With z = scale * logits:
+ *   lse = log sum_v exp(z_v);  logp[i] = z[tokens[i]] - lse;  entropy[i] = lse - sum_v p_v z_v
+ *   dlogits_v = scale * sum over the row's tokens i of
+ *               dlogp[i] (1[v = tokens[i]] - p_v) - dentropy[i] p_v (z_v - lse + entropy[i])
+ * (the prompt's last row sums over the segments).  Statistics are fp32.
+ *
+ *   logits      device, bf16 or fp32 (dtype DUALKV_BF16 / DUALKV_F32), [M, V], rows row_stride >= V
+ *               elements apart; only element alignment is needed.  -inf marks masked entries;
+ *               a NaN or +inf makes its row's results NaN; a row that is -inf throughout has
+ *               lse = logp = -inf, entropy 0 and gradient 0
+ *   scale       > 0, an inverse temperature
+ *   tokens      device int64 [R_offsets[N]], 0 .. V - 1; negative: ignored.  One past the
+ *               vocabulary is ignored and reported by dualkv_check_status()
+ *   logp, entropy  device fp32 [R_offsets[N]], written; 0 for a token that is ignored or not
+ *               predicted.  entropy may be NULL
+ *   lse         device fp32 [M], written, may be NULL in the forward; 0 for a row that predicts
+ *               no token (such rows are not read)
+ * Backward: lse (and entropy, with dentropy) as the forward wrote them;
+ *   dlogp, dentropy  device fp32 [R_offsets[N]]; dentropy may be NULL
+ *   dlogits     device, dtype, [M, V], rows dlogits_stride >= V apart, written whole (values
+ *               between the rows are left as they are): zeros in rows into which nothing
+ *               flows.  May be `logits` itself, with the same stride; otherwise no
+ *               output may share memory with an input (DUALKV_ERR_INVALID)
+ * N <= 4095 (DUALKV_ERR_UNSUPPORTED beyond).  These calls keep nothing between calls and
+ * may be captured into a CUDA graph.
+ */
+int dualkv_token_logprobs(const void* logits, int64_t row_stride, int dtype, int V, float scale, const int64_t* tokens,
+                          int P, int N, const int32_t* R_offsets, float* logp, float* entropy, float* lse, void* stream);
+int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype, int V, float scale,
+                              const int64_t* tokens, int P, int N, const int32_t* R_offsets, const float* lse,
+                              const float* entropy, const float* dlogp, const float* dentropy, void* dlogits,
+                              int64_t dlogits_stride, void* stream);
+
+/*
+ * Clipped policy loss over the packed response tokens, with a KL term and an entropy
+ * bonus.  Per live token, with ratio = exp(logp - old_logp), x = ref_logp - logp and
+ * advantage A:
+ *   policy = -A min(ratio, 1 + clip_high) if A > 0, -A max(ratio, 1 - clip_low) if A < 0, there
+ *            at most -A dual_clip unless dual_clip is 0, and 0 if A = 0
+ *   kl     = exp(x) - x - 1
+ *   loss   = sum_n w_n sum over live tokens of segment n of (policy + kl_coef kl - entropy_coef entropy)
+ * and w_n, 0 for a segment without a live token, is
+ *   DUALKV_LOSS_TOKEN_MEAN  1 / (live tokens of the batch)
+ *   DUALKV_LOSS_SEQ_MEAN    1 / (N * live tokens of segment n)
+ *   DUALKV_LOSS_SEQ_SUM     1 / N
+ * Gradients: a token beyond a bound passes none through its ratio; one exactly on it does.
+ * The comparisons with the bounds are exact in fp64.
+ *
+ *   logp, old_logp  device fp32 [R_offsets[N]] in packed order
+ *   ref_logp    same, or NULL if kl_coef is 0;  entropy  same, or NULL if entropy_coef is 0
+ *   advantages  device fp32, [N], or [R_offsets[N]] if per_token
+ *   mask        device bytes [R_offsets[N]], 0: not live, nothing of the token's other
+ *               inputs is used; NULL: all are live
+ *   clip_low    in [0, 1); clip_high >= 0; dual_clip 0 or > 1
+ *   loss        device fp32 [1], written
+ *   stats       device fp32 [4], written: the weighted sums of policy, kl (0 without
+ *               ref_logp) and entropy (0 without entropy), and the share of live tokens
+ *               beyond a bound
+ *   weights     device fp32 [N], written: w_n, read by the backward
+ *   workspace   device, 256-byte aligned, >= dualkv_policy_loss_workspace_bytes() (0 for invalid input)
+ * Backward:
+ *   dloss       device fp32 [1], the gradient of the loss
+ *   dlogp       device fp32 [R_offsets[N]], written, 0 for tokens that are not live
+ *   dentropy    same, or NULL
+ * fp32 pointers need 4-byte alignment only.  No output may share memory with an input or another
+ * output (DUALKV_ERR_INVALID).  N <= 4095 (DUALKV_ERR_UNSUPPORTED beyond).  Sums run in a fixed
+ * order.  These calls keep nothing between calls and may be captured into a CUDA graph; calls
+ * that may overlap need a workspace each.
+ */
+#define DUALKV_LOSS_TOKEN_MEAN 0
+#define DUALKV_LOSS_SEQ_MEAN 1
+#define DUALKV_LOSS_SEQ_SUM 2
+size_t dualkv_policy_loss_workspace_bytes(int N, const int32_t* R_offsets);
+int dualkv_policy_loss(const float* logp, const float* old_logp, const float* ref_logp, const float* entropy,
+                       const float* advantages, int per_token, const uint8_t* mask, int N, const int32_t* R_offsets,
+                       double clip_low, double clip_high, double dual_clip, double kl_coef, double entropy_coef,
+                       int reduction, float* loss, float* stats, float* weights, void* workspace,
+                       size_t workspace_bytes, void* stream);
+int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float* ref_logp, const float* advantages,
+                           int per_token, const uint8_t* mask, int N, const int32_t* R_offsets, double clip_low,
+                           double clip_high, double dual_clip, double kl_coef, double entropy_coef, const float* dloss,
+                           const float* weights, float* dlogp, float* dentropy, void* stream);
+
+/*
  * Token-reduction factor rho = sum_n (P + R_n) / (P + sum_n R_n) (paper
  * abstract: rho = N(P+R)/(P+NR) for equal lengths).  Host only; -1 on invalid input.
  */
@@ -289,7 +379,9 @@ const char* dualkv_error_string(int code);
 #define DUALKV_KERNEL_DQ 4
 #define DUALKV_KERNEL_PACK 5 /* dualkv_pack, dualkv_unpack and dualkv_fold */
 #define DUALKV_KERNEL_ROPE 6 /* dualkv_qk_norm_rope and its backward */
-#define DUALKV_KERNEL_KINDS 7
+#define DUALKV_KERNEL_LOGPROBS 7 /* dualkv_token_logprobs and its backward */
+#define DUALKV_KERNEL_POLICY 8   /* dualkv_policy_loss and its backward */
+#define DUALKV_KERNEL_KINDS 9
 int dualkv_profile_enable(int on);
 int dualkv_profile_read(double* ms, int64_t* launches);
 

@@ -261,9 +261,18 @@ int status_word(int device, uint32_t** out) {
     *out = it->second;
     return DUALKV_OK;
   }
+  // Set up on a stream of its own and, for this thread, outside the rules of a running
+  // stream capture: the first call on a device may be one that is being captured.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return DUALKV_ERR_CUDA;
   uint32_t* p = nullptr;
-  if (cudaMalloc(&p, 256) != cudaSuccess) return DUALKV_ERR_CUDA;
-  if (cudaMemset(p, 0, 256) != cudaSuccess) return DUALKV_ERR_CUDA;
+  cudaStream_t own = nullptr;
+  bool ok = cudaMalloc(&p, 256) == cudaSuccess && cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+            cudaMemsetAsync(p, 0, 256, own) == cudaSuccess && cudaStreamSynchronize(own) == cudaSuccess;
+  if (own) cudaStreamDestroy(own);
+  if (!ok && p) cudaFree(p);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (!ok) return DUALKV_ERR_CUDA;
   g_status[device] = p;
   *out = p;
   return DUALKV_OK;
@@ -551,6 +560,133 @@ int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int
   if (timed(DUALKV_KERNEL_ROPE, st, [&] {
         return launch_rope(backward, D, a, P, N, R_offsets, dq_weight, dk_weight, st);
       }) != cudaSuccess)
+    return DUALKV_ERR_CUDA;
+  return DUALKV_OK;
+}
+
+// P, N and R_offsets of a call whose head counts do not matter.
+int check_segments(int P, int N, const int32_t* off) {
+  if (validate_layout(P, N, off, 1, 1, 64)) return DUALKV_ERR_INVALID;
+  return N > kMaxSegs ? DUALKV_ERR_UNSUPPORTED : DUALKV_OK;
+}
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int logp_impl(bool backward, const void* logits, int64_t row_stride, int dtype, int V, float scale,
+              const int64_t* tokens, int P, int N, const int32_t* R_offsets, float* logp, float* entropy, float* lse,
+              const float* dlogp, const float* dentropy, void* dlogits, int64_t dlogits_stride, void* stream) {
+  const int rc_layout = check_segments(P, N, R_offsets);
+  if (rc_layout) return rc_layout;
+  const int64_t n = R_offsets[N], M = n + (P > 0 ? 1 : 0);
+  if (dtype != DUALKV_BF16 && dtype != DUALKV_F32) return DUALKV_ERR_INVALID;
+  if (V < 1 || row_stride < V || row_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return DUALKV_ERR_INVALID;
+  if (!logits || (n > 0 && !tokens)) return DUALKV_ERR_INVALID;
+  const uint64_t esz = dtype == DUALKV_F32 ? 4 : 2, un = (uint64_t)n, uM = (uint64_t)M;
+  if (!aligned_to(logits, esz) || !aligned_to(tokens, 8)) return DUALKV_ERR_ALIGN;
+  for (const void* p : {(const void*)logp, (const void*)entropy, (const void*)lse, (const void*)dlogp,
+                        (const void*)dentropy})
+    if (!aligned_to(p, 4)) return DUALKV_ERR_ALIGN;
+  const Rows in{logits, (uint64_t)row_stride * esz, (uint64_t)V * esz, uM};
+  if (!backward) {
+    if (n > 0 && !logp) return DUALKV_ERR_INVALID;
+    if (outputs_overlap({flat(logp, un * 4), flat(entropy, un * 4), flat(lse, uM * 4)}, {in, flat(tokens, un * 8)}))
+      return DUALKV_ERR_INVALID;
+  } else {
+    if (!lse || !dlogits || (n > 0 && (!dlogp || (dentropy && !entropy)))) return DUALKV_ERR_INVALID;
+    if (dlogits_stride < V || dlogits_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
+    if (!aligned_to(dlogits, esz)) return DUALKV_ERR_ALIGN;
+    const Rows out{dlogits, (uint64_t)dlogits_stride * esz, (uint64_t)V * esz, uM};
+    std::vector<Rows> ins = {flat(tokens, un * 8), flat(lse, uM * 4), flat(dlogp, un * 4)};
+    if (dentropy) {
+      ins.push_back(flat(entropy, un * 4));
+      ins.push_back(flat(dentropy, un * 4));
+    }
+    if (dlogits != logits || dlogits_stride != row_stride) ins.push_back(in);  // in place, or apart
+    if (outputs_overlap({out}, ins)) return DUALKV_ERR_INVALID;
+  }
+  LogpArgs a{logits, row_stride, V, scale, tokens, logp, entropy, lse, dlogp, dentropy, dlogits, dlogits_stride, nullptr};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DUALKV_ERR_CUDA;
+  const int rc = status_word(dev, &a.status);
+  if (rc) return rc;
+  if (timed(DUALKV_KERNEL_LOGPROBS, st, [&] {
+        return launch_logprobs(backward, dtype == DUALKV_F32, a, P, N, R_offsets, st);
+      }) != cudaSuccess)
+    return DUALKV_ERR_CUDA;
+  return DUALKV_OK;
+}
+
+Bound bound_of(double v) {
+  const float hi = (float)v;
+  return Bound{hi, (float)(v - (double)hi)};
+}
+
+int policy_impl(bool backward, const float* logp, const float* old_logp, const float* ref_logp, const float* entropy,
+                const float* advantages, int per_token, const uint8_t* mask, int N, const int32_t* R_offsets,
+                double clip_low, double clip_high, double dual_clip, double kl_coef, double entropy_coef, int reduction,
+                float* loss, float* stats, float* weights, void* workspace, size_t workspace_bytes, const float* dloss,
+                float* dlogp, float* dentropy, void* stream) {
+  const int rc_layout = check_segments(1, N, R_offsets);  // a batch without tokens is one with loss 0
+  if (rc_layout) return rc_layout;
+  if (!(clip_low >= 0.0 && clip_low < 1.0) || !(clip_high >= 0.0) || !std::isfinite(clip_high)) return DUALKV_ERR_INVALID;
+  if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !std::isfinite(dual_clip))) return DUALKV_ERR_INVALID;
+  if (!std::isfinite(kl_coef) || !std::isfinite(entropy_coef)) return DUALKV_ERR_INVALID;
+  if (reduction < 0 || reduction > DUALKV_LOSS_SEQ_SUM) return DUALKV_ERR_INVALID;
+  const uint64_t n = (uint64_t)R_offsets[N];
+  if (n > 0 && (!logp || !old_logp || !advantages || (kl_coef != 0.0 && !ref_logp))) return DUALKV_ERR_INVALID;
+  if (!weights) return DUALKV_ERR_INVALID;
+  for (const void* p : {(const void*)logp, (const void*)old_logp, (const void*)ref_logp, (const void*)entropy,
+                        (const void*)advantages, (const void*)loss, (const void*)stats, (const void*)weights,
+                        (const void*)dloss, (const void*)dlogp, (const void*)dentropy})
+    if (!aligned_to(p, 4)) return DUALKV_ERR_ALIGN;
+  std::vector<Rows> ins = {flat(logp, n * 4), flat(old_logp, n * 4), flat(ref_logp, n * 4),
+                           flat(advantages, (per_token ? n : (uint64_t)N) * 4), flat(mask, n)};
+  std::vector<Rows> outs;
+  if (!backward) {
+    if (!loss || !stats || (n > 0 && entropy_coef != 0.0 && !entropy)) return DUALKV_ERR_INVALID;
+    const size_t need = policy_workspace_bytes(N, R_offsets);
+    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < need) return DUALKV_ERR_WORKSPACE;
+    ins.push_back(flat(entropy, n * 4));
+    outs = {flat(loss, 4), flat(stats, 16), flat(weights, (uint64_t)N * 4), flat(workspace, need)};
+  } else {
+    if (!dloss || (n > 0 && !dlogp)) return DUALKV_ERR_INVALID;
+    ins.push_back(flat(dloss, 4));
+    ins.push_back(flat(weights, (uint64_t)N * 4));
+    outs = {flat(dlogp, n * 4), flat(dentropy, n * 4)};
+  }
+  if (outputs_overlap(outs, ins)) return DUALKV_ERR_INVALID;
+  if (backward && n == 0) return DUALKV_OK;
+  PolicyArgs a{};
+  a.logp = logp;
+  a.old_logp = old_logp;
+  a.ref_logp = backward && kl_coef == 0.0 ? nullptr : ref_logp;
+  a.entropy = entropy;
+  a.adv = advantages;
+  a.mask = mask;
+  a.per_token = per_token != 0;
+  a.reduction = reduction;
+  a.has_dual = dual_clip != 0.0;
+  a.up = bound_of(std::log1p(clip_high));
+  a.down = bound_of(std::log1p(-clip_low));
+  if (a.has_dual) a.dual = bound_of(std::log(dual_clip));
+  a.ratio_up = (float)(1.0 + clip_high);
+  a.ratio_down = (float)(1.0 - clip_low);
+  a.ratio_dual = (float)dual_clip;
+  a.kl_coef = kl_coef;
+  a.entropy_coef = entropy_coef;
+  a.loss = loss;
+  a.stats = stats;
+  a.weights = weights;
+  a.records = workspace;
+  a.dloss = dloss;
+  a.dlogp = dlogp;
+  a.dentropy = dentropy;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (timed(DUALKV_KERNEL_POLICY, st, [&] { return launch_policy(backward, a, N, R_offsets, st); }) != cudaSuccess)
     return DUALKV_ERR_CUDA;
   return DUALKV_OK;
 }
@@ -862,6 +998,44 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
   return rope_impl(true, q, q_stride, k, k_stride, dq_out, dk_out, q_weight, k_weight, weight_dtype, weight_offset, eps,
                    inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dq_stride, dk, dk_stride,
                    dq_weight, dk_weight, workspace, workspace_bytes, stream);
+}
+
+int dualkv_token_logprobs(const void* logits, int64_t row_stride, int dtype, int V, float scale, const int64_t* tokens,
+                          int P, int N, const int32_t* R_offsets, float* logp, float* entropy, float* lse, void* stream) {
+  return logp_impl(false, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, logp, entropy, lse, nullptr,
+                   nullptr, nullptr, 0, stream);
+}
+
+int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype, int V, float scale,
+                              const int64_t* tokens, int P, int N, const int32_t* R_offsets, const float* lse,
+                              const float* entropy, const float* dlogp, const float* dentropy, void* dlogits,
+                              int64_t dlogits_stride, void* stream) {
+  return logp_impl(true, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, nullptr,
+                   const_cast<float*>(entropy), const_cast<float*>(lse), dlogp, dentropy, dlogits, dlogits_stride,
+                   stream);
+}
+
+size_t dualkv_policy_loss_workspace_bytes(int N, const int32_t* R_offsets) {
+  return check_segments(1, N, R_offsets) ? 0 : policy_workspace_bytes(N, R_offsets);
+}
+
+int dualkv_policy_loss(const float* logp, const float* old_logp, const float* ref_logp, const float* entropy,
+                       const float* advantages, int per_token, const uint8_t* mask, int N, const int32_t* R_offsets,
+                       double clip_low, double clip_high, double dual_clip, double kl_coef, double entropy_coef,
+                       int reduction, float* loss, float* stats, float* weights, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return policy_impl(false, logp, old_logp, ref_logp, entropy, advantages, per_token, mask, N, R_offsets, clip_low,
+                     clip_high, dual_clip, kl_coef, entropy_coef, reduction, loss, stats, weights, workspace,
+                     workspace_bytes, nullptr, nullptr, nullptr, stream);
+}
+
+int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float* ref_logp, const float* advantages,
+                           int per_token, const uint8_t* mask, int N, const int32_t* R_offsets, double clip_low,
+                           double clip_high, double dual_clip, double kl_coef, double entropy_coef, const float* dloss,
+                           const float* weights, float* dlogp, float* dentropy, void* stream) {
+  return policy_impl(true, logp, old_logp, ref_logp, nullptr, advantages, per_token, mask, N, R_offsets, clip_low,
+                     clip_high, dual_clip, kl_coef, entropy_coef, DUALKV_LOSS_TOKEN_MEAN, nullptr, nullptr,
+                     const_cast<float*>(weights), nullptr, 0, dloss, dlogp, dentropy, stream);
 }
 
 int dualkv_check_status(void* stream) {

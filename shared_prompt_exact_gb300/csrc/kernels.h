@@ -181,4 +181,43 @@ cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, c
                         float* dkw, cudaStream_t st);
 size_t rope_workspace_bytes(int64_t T, int D);
 
+// ---- token log-probabilities (logprobs.cu)
+struct LogpArgs {
+  const void* logits;       // bf16 or fp32 rows of V values, `stride` elements apart
+  int64_t stride;
+  int V;
+  float scale;
+  const int64_t* tokens;    // response tokens in packed order; < 0: ignored
+  float *logp, *entropy, *lse;  // forward: written (entropy, lse may be null); backward: entropy, lse read
+  const float *dlogp, *dentropy;
+  void* dlogits;
+  int64_t dstride;
+  uint32_t* status;
+};
+cudaError_t launch_logprobs(bool backward, bool f32, const LogpArgs& a, int P, int N, const int32_t* off,
+                            cudaStream_t st);
+
+// ---- clipped policy loss (policy.cu)
+constexpr int kPolicyChunk = 2048;  // response tokens of one block
+
+// A bound on a difference of log-probabilities, as the sum of two fp32 values.
+struct Bound {
+  float hi, lo;
+};
+struct PolicyArgs {
+  const float *logp, *old_logp, *ref_logp, *entropy, *adv;  // ref_logp, entropy may be null
+  const uint8_t* mask;                                      // null: every token is live
+  int per_token, reduction, has_dual;
+  Bound up, down, dual;
+  float ratio_up, ratio_down, ratio_dual;
+  double kl_coef, entropy_coef;
+  float *loss, *stats, *weights;  // forward: written; backward: weights read
+  void* records;
+  const float* dloss;
+  float *dlogp, *dentropy;
+};
+// Forward: the sums and a second launch of one block that joins them.  Backward: one launch.
+cudaError_t launch_policy(bool backward, const PolicyArgs& a, int N, const int32_t* off, cudaStream_t st);
+size_t policy_workspace_bytes(int N, const int32_t* off);
+
 }  // namespace dkv

@@ -35,11 +35,14 @@ EXPORTS = ("dualkv_fwd", "dualkv_bwd_workspace_bytes", "dualkv_bwd", "dualkv_bui
            "dualkv_pack", "dualkv_unpack", "dualkv_fold", "dualkv_fwd_heads", "dualkv_bwd_heads",
            "dualkv_fwd_layers", "dualkv_bwd_layers", "dualkv_bwd_layers_workspace_bytes",
            "dualkv_selftest_kernel", "dualkv_plan_cache_info", "dualkv_qk_norm_rope",
-           "dualkv_qk_norm_rope_bwd", "dualkv_qk_norm_rope_bwd_workspace_bytes")
+           "dualkv_qk_norm_rope_bwd", "dualkv_qk_norm_rope_bwd_workspace_bytes", "dualkv_token_logprobs",
+           "dualkv_token_logprobs_bwd", "dualkv_policy_loss", "dualkv_policy_loss_bwd",
+           "dualkv_policy_loss_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 32 << 20
-KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope")
+KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope", "logprobs", "policy")
 DUALKV_BF16 = 0
 DUALKV_F32 = 1
+LOSS_REDUCTIONS = {"token_mean": 0, "seq_mean": 1, "seq_sum": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -116,6 +119,19 @@ def load(path: Optional[str] = None):
         lib.dualkv_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp] + rope + [vp, i64, vp, i64, vp, vp, vp,
                                                                                      ctypes.c_size_t, vp]
         lib.dualkv_qk_norm_rope_bwd.restype = ci
+        logp = [vp, i64, ci, ci, cf, vp, ci, ci, i32p]
+        lib.dualkv_token_logprobs.argtypes = logp + [vp, vp, vp, vp]
+        lib.dualkv_token_logprobs.restype = ci
+        lib.dualkv_token_logprobs_bwd.argtypes = logp + [vp, vp, vp, vp, vp, i64, vp]
+        lib.dualkv_token_logprobs_bwd.restype = ci
+        cd = ctypes.c_double
+        lib.dualkv_policy_loss_workspace_bytes.argtypes = [ci, i32p]
+        lib.dualkv_policy_loss_workspace_bytes.restype = ctypes.c_size_t
+        lib.dualkv_policy_loss.argtypes = [vp, vp, vp, vp, vp, ci, vp, ci, i32p, cd, cd, cd, cd, cd, ci, vp, vp, vp, vp,
+                                           ctypes.c_size_t, vp]
+        lib.dualkv_policy_loss.restype = ci
+        lib.dualkv_policy_loss_bwd.argtypes = [vp, vp, vp, vp, ci, vp, ci, i32p, cd, cd, cd, cd, cd, vp, vp, vp, vp, vp]
+        lib.dualkv_policy_loss_bwd.restype = ci
         lib.dualkv_release.argtypes = []
         lib.dualkv_release.restype = None
         _lib = lib
@@ -465,6 +481,132 @@ def dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_off
     _raise(rc, where)
 
 
+def _check_logits(where, logits, tokens, P, N, R_offsets):
+    """Checks shared by the forward and the backward; returns (rows, tokens, device)."""
+    n = _layout_rows(where, 0, N, R_offsets)
+    M = n + (1 if int(P) > 0 else 0)
+    dev = torch.cuda.current_device()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError(f"{where}: logits must be a tensor of rows")
+    _check_tensor(where, "logits", logits, (M, logits.shape[1]), tuple(_WEIGHT_DTYPES), dev, rows=True)
+    _check_tensor(where, "tokens", tokens, (n,), (torch.int64,), dev)
+    return M, n, dev
+
+
+def _check_floats(where, dev, shape, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            _check_tensor(where, name, t, shape, (torch.float32,), dev)
+
+
+def dualkv_token_logprobs(logits, tokens, scale, P, N, R_offsets, logp, entropy, lse, stream=None) -> None:
+    """Log-probabilities (and, unless None, entropies) of the response tokens from the logits of packed rows
+    P - 1 .. T - 1 (all rows if P = 0); lse, unless None, gets each row's log-sum-exp."""
+    where = "dualkv_token_logprobs"
+    M, n, dev = _check_logits(where, logits, tokens, P, N, R_offsets)
+    if logp is None:
+        raise ValueError(f"{where}: logp is missing")
+    _check_floats(where, dev, (n,), logp=logp, entropy=entropy)
+    _check_floats(where, dev, (M,), lse=lse)
+    rc = load().dualkv_token_logprobs(_ptr(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype], logits.shape[1],
+                                      float(scale), _ptr(tokens), int(P), int(N), _offsets(R_offsets), _ptr(logp),
+                                      _ptr(entropy), _ptr(lse), _stream(stream))
+    _raise(rc, where)
+
+
+def dualkv_token_logprobs_bwd(logits, tokens, scale, P, N, R_offsets, lse, entropy, dlogp, dentropy, dlogits,
+                              stream=None) -> None:
+    """Gradient of the logits from dlogp (and, unless None, dentropy); dlogits may be logits itself."""
+    where = "dualkv_token_logprobs_bwd"
+    M, n, dev = _check_logits(where, logits, tokens, P, N, R_offsets)
+    if lse is None or dlogp is None or (dentropy is not None and entropy is None):
+        raise ValueError(f"{where}: lse and dlogp are needed, and entropy with dentropy")
+    _check_floats(where, dev, (n,), dlogp=dlogp, dentropy=dentropy, entropy=entropy)
+    _check_floats(where, dev, (M,), lse=lse)
+    _check_tensor(where, "dlogits", dlogits, logits.shape, (logits.dtype,), dev, rows=True)
+    rc = load().dualkv_token_logprobs_bwd(_ptr(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype],
+                                          logits.shape[1], float(scale), _ptr(tokens), int(P), int(N),
+                                          _offsets(R_offsets), _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
+                                          _ptr(dlogits), _row_stride(dlogits), _stream(stream))
+    _raise(rc, where)
+
+
+def _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction, per_token):
+    """Checks shared by the forward and the backward; returns (tokens, device, per-token advantages)."""
+    n = _layout_rows(where, 0, N, R_offsets)
+    dev = torch.cuda.current_device()
+    if reduction not in LOSS_REDUCTIONS:
+        raise ValueError(f"{where}: reduction must be one of {tuple(LOSS_REDUCTIONS)}, got {reduction!r}")
+    if logp is None or old_logp is None or advantages is None or (float(kl_coef) != 0.0 and ref_logp is None):
+        raise ValueError(f"{where}: logp, old_logp and advantages are needed, and ref_logp with kl_coef")
+    _check_floats(where, dev, (n,), logp=logp, old_logp=old_logp, ref_logp=ref_logp)
+    per_token = _per_token(where, advantages, N, n, R_offsets, per_token)
+    _check_floats(where, dev, (n if per_token else int(N),), advantages=advantages)
+    if mask is not None:
+        _check_tensor(where, "mask", mask, (n,), (torch.bool, torch.uint8), dev)
+    return n, dev, per_token
+
+
+def _per_token(where, advantages, N, n, R_offsets, per_token):
+    """Whether advantages hold one value per token rather than per segment: as the caller says, else by their length.
+    A length that fits both ways in a layout where it makes a difference has to be told."""
+    if per_token is not None:
+        return 1 if per_token else 0
+    if not isinstance(advantages, torch.Tensor) or advantages.dim() != 1:
+        raise ValueError(f"{where}: advantages must be a tensor of one dimension")
+    if n == int(N) and any(int(R_offsets[i]) != i for i in range(n)):
+        raise ValueError(f"{where}: {n} advantages for {n} segments of {n} tokens in all: pass per_token")
+    return 1 if advantages.shape[0] != int(N) else 0
+
+
+def dualkv_policy_loss_workspace_bytes(N, R_offsets) -> int:
+    return int(load().dualkv_policy_loss_workspace_bytes(int(N), _offsets(R_offsets)))
+
+
+def dualkv_policy_loss(logp, old_logp, ref_logp, entropy, advantages, mask, N, R_offsets, clip_low, clip_high, dual_clip,
+                       kl_coef, entropy_coef, reduction, loss, stats, weights, workspace, workspace_bytes=None,
+                       stream=None, per_token=None) -> None:
+    """Clipped policy loss with a KL term and an entropy bonus over packed response tokens.  advantages: [N], or one
+    per token (per_token, by default told from the length)."""
+    where = "dualkv_policy_loss"
+    n, dev, per_token = _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction,
+                                      per_token)
+    if float(entropy_coef) != 0.0 and entropy is None:
+        raise ValueError(f"{where}: entropy_coef needs entropy")
+    _check_floats(where, dev, (n,), entropy=entropy)
+    _check_tensor(where, "loss", loss, (1,), (torch.float32,), dev)
+    _check_tensor(where, "stats", stats, (4,), (torch.float32,), dev)
+    _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
+    workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
+    rc = load().dualkv_policy_loss(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(entropy), _ptr(advantages), per_token,
+                                   _ptr(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
+                                   float(dual_clip), float(kl_coef), float(entropy_coef), LOSS_REDUCTIONS[reduction],
+                                   _ptr(loss), _ptr(stats), _ptr(weights), _ptr(workspace), workspace_bytes,
+                                   _stream(stream))
+    _raise(rc, where)
+
+
+def dualkv_policy_loss_bwd(logp, old_logp, ref_logp, advantages, mask, N, R_offsets, clip_low, clip_high, dual_clip,
+                           kl_coef, entropy_coef, reduction, dloss, weights, dlogp, dentropy, stream=None,
+                           per_token=None) -> None:
+    """Gradients of dualkv_policy_loss: dlogp and, unless None, dentropy (the reduction is in weights)."""
+    where = "dualkv_policy_loss_bwd"
+    n, dev, per_token = _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction,
+                                      per_token)
+    if dlogp is None:
+        raise ValueError(f"{where}: dlogp is missing")
+    _check_floats(where, dev, (n,), dlogp=dlogp, dentropy=dentropy)
+    if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
+        raise ValueError(f"{where}: dloss must be a tensor of one value")
+    _check_tensor(where, "dloss", dloss, dloss.shape, (torch.float32,), dev)
+    _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
+    rc = load().dualkv_policy_loss_bwd(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), per_token,
+                                       _ptr(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
+                                       float(dual_clip), float(kl_coef), float(entropy_coef), _ptr(dloss), _ptr(weights),
+                                       _ptr(dlogp), _ptr(dentropy), _stream(stream))
+    _raise(rc, where)
+
+
 def _workspace_bytes(where, workspace, workspace_bytes, device):
     """Bytes of a workspace tensor (0 for None); no more than it holds may be claimed."""
     if workspace is None:
@@ -622,3 +764,49 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, P, R_offsets, inv_freq=None, q_w
         dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim,
                                 interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dk, dqw, dkw, ws)
     return dq, dk, dqw, dkw
+
+
+def token_logprobs(logits, tokens, P, R_offsets, scale=1.0, entropy=False, stream=None):
+    """Allocate the outputs and run dualkv_token_logprobs: (logp, entropy or None, lse)."""
+    n, f32 = int(tokens.shape[0]), dict(dtype=torch.float32, device=logits.device)
+    with _allocating_on(stream):
+        logp, lse = torch.empty(n, **f32), torch.empty(logits.shape[0], **f32)
+        ent = torch.empty(n, **f32) if entropy else None
+        dualkv_token_logprobs(logits, tokens, scale, P, len(R_offsets) - 1, R_offsets, logp, ent, lse)
+    return logp, ent, lse
+
+
+def token_logprobs_backward(logits, tokens, lse, dlogp, P, R_offsets, scale=1.0, entropy=None, dentropy=None,
+                            inplace=False, stream=None):
+    """Allocate dlogits (or, inplace, write it over logits) and run dualkv_token_logprobs_bwd."""
+    with _allocating_on(stream):
+        dlogits = logits if inplace else torch.empty_like(logits)
+        dualkv_token_logprobs_bwd(logits, tokens, scale, P, len(R_offsets) - 1, R_offsets, lse, entropy, dlogp, dentropy,
+                                  dlogits)
+    return dlogits
+
+
+def policy_loss(logp, old_logp, advantages, R_offsets, ref_logp=None, entropy=None, mask=None, clip_low=0.2,
+                clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0, reduction="token_mean", stream=None,
+                per_token=None):
+    """Allocate the outputs and the workspace and run dualkv_policy_loss: (loss [1], stats [4], weights [N])."""
+    N, f32 = len(R_offsets) - 1, dict(dtype=torch.float32, device=logp.device)
+    with _allocating_on(stream):
+        loss, stats, weights = torch.empty(1, **f32), torch.empty(4, **f32), torch.empty(N, **f32)
+        ws = torch.empty(dualkv_policy_loss_workspace_bytes(N, R_offsets), dtype=torch.uint8, device=logp.device)
+        dualkv_policy_loss(logp, old_logp, ref_logp, entropy, advantages, mask, N, R_offsets, clip_low, clip_high,
+                           dual_clip, kl_coef, entropy_coef, reduction, loss, stats, weights, ws, per_token=per_token)
+    return loss, stats, weights
+
+
+def policy_loss_backward(logp, old_logp, advantages, R_offsets, dloss, weights, ref_logp=None, mask=None, clip_low=0.2,
+                         clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0, stream=None, per_token=None):
+    """Allocate the gradients and run dualkv_policy_loss_bwd: (dlogp, dentropy or None without entropy_coef)."""
+    N, f32 = len(R_offsets) - 1, dict(dtype=torch.float32, device=logp.device)
+    with _allocating_on(stream):
+        dlogp = torch.empty(logp.shape[0], **f32)
+        dentropy = torch.empty(logp.shape[0], **f32) if entropy_coef else None
+        dualkv_policy_loss_bwd(logp, old_logp, ref_logp, advantages, mask, N, R_offsets, clip_low, clip_high, dual_clip,
+                               kl_coef, entropy_coef, "token_mean", dloss, weights, dlogp, dentropy,
+                               per_token=per_token)
+    return dlogp, dentropy

@@ -73,3 +73,74 @@ def test_rope_backward_refusals(lib):
 def test_offsets_are_converted_once():
     off = dk.offsets(OK_OFF)
     assert dk.offsets(off) is off and list(off) == OK_OFF
+
+
+def _logp(lib, backward=False, **kw):
+    a = dict(x=0x100000, xs=64, dt=dk.DUALKV_BF16, V=64, scale=1.0, tok=0x200000, P=4, N=2, off=OK_OFF, lp=0x300000,
+             ent=0x301000, lse=0x302000, dlp=0x303000, dent=0x304000, dx=0x400000, dxs=64)
+    a.update(kw)
+    off = None if a["off"] is None else (ctypes.c_int32 * len(a["off"]))(*a["off"])
+    head = [_vp(a["x"]), a["xs"], a["dt"], a["V"], a["scale"], _vp(a["tok"]), a["P"], a["N"], off]
+    if not backward:
+        return lib.dualkv_token_logprobs(*head, _vp(a["lp"]), _vp(a["ent"]), _vp(a["lse"]), None)
+    return lib.dualkv_token_logprobs_bwd(*head, _vp(a["lse"]), _vp(a["ent"]), _vp(a["dlp"]), _vp(a["dent"]), _vp(a["dx"]),
+                                         a["dxs"], None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_logprobs_refusals(lib, backward):
+    for kw in (dict(P=-1), dict(N=0), dict(off=None), dict(off=[0, 3, 2]), dict(P=0, off=[0, 0, 0]), dict(dt=2), dict(V=0),
+               dict(xs=63), dict(xs=1 << 40), dict(scale=0.0), dict(scale=float("inf")), dict(x=0), dict(tok=0)):
+        assert _logp(lib, backward, **kw) == dk.DUALKV_ERR_INVALID, kw
+    for kw in (dict(x=0x100001), dict(x=0x100002, dt=dk.DUALKV_F32), dict(tok=0x200004), dict(lse=0x302002)):
+        assert _logp(lib, backward, **kw) == dk.DUALKV_ERR_ALIGN, kw
+    assert _logp(lib, backward, N=4096, off=[0] * 4096 + [1]) == dk.DUALKV_ERR_UNSUPPORTED
+
+
+def test_logprobs_overlaps(lib):
+    bad = dk.DUALKV_ERR_INVALID
+    for kw in (dict(lp=0), dict(lp=0x100000), dict(lse=0x200008), dict(ent=0x300008)):
+        assert _logp(lib, **kw) == bad, kw
+    for kw in (dict(lse=0), dict(dlp=0), dict(ent=0), dict(dx=0), dict(dxs=63), dict(dx=0x100080), dict(dx=0x1fff80),
+               dict(dx=0x303000), dict(dx=0x100000, dxs=65), dict(dx=0x304000)):
+        assert _logp(lib, True, **kw) == bad, kw
+    assert _logp(lib, True, dx=0x400001) == dk.DUALKV_ERR_ALIGN
+
+
+def _policy(lib, backward=False, **kw):
+    a = dict(lp=0x100000, old=0x101000, ref=0x102000, ent=0x103000, adv=0x104000, pt=0, mask=0x105000, N=2, off=OK_OFF, lo=0.2,
+             hi=0.2, dual=0.0, kl=0.1, ec=0.1, red=0, loss=0x106000, stats=0x107000, w=0x108000, ws=0x109000, wsb=1 << 20,
+             dl=0x300000, g=0x301000, gh=0x302000)
+    a.update(kw)
+    off = None if a["off"] is None else (ctypes.c_int32 * len(a["off"]))(*a["off"])
+    mid = [_vp(a["adv"]), a["pt"], _vp(a["mask"]), a["N"], off, a["lo"], a["hi"], a["dual"], a["kl"], a["ec"]]
+    if not backward:
+        return lib.dualkv_policy_loss(_vp(a["lp"]), _vp(a["old"]), _vp(a["ref"]), _vp(a["ent"]), *mid, a["red"],
+                                      _vp(a["loss"]), _vp(a["stats"]), _vp(a["w"]), _vp(a["ws"]), a["wsb"], None)
+    return lib.dualkv_policy_loss_bwd(_vp(a["lp"]), _vp(a["old"]), _vp(a["ref"]), *mid, _vp(a["dl"]), _vp(a["w"]),
+                                      _vp(a["g"]), _vp(a["gh"]), None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_policy_refusals(lib, backward):
+    nan = float("nan")
+    for kw in (dict(N=0), dict(off=None), dict(off=[0, 3, 2]), dict(off=[1, 2, 3]), dict(lp=0), dict(old=0), dict(ref=0),
+               dict(adv=0), dict(w=0), dict(lo=1.0), dict(lo=-0.1), dict(lo=nan), dict(hi=-1.0), dict(hi=nan), dict(dual=1.0),
+               dict(dual=nan), dict(kl=nan), dict(ec=float("inf"))):
+        assert _policy(lib, backward, **kw) == dk.DUALKV_ERR_INVALID, kw
+    for kw in (dict(lp=0x100002), dict(adv=0x104001), dict(w=0x108003)):
+        assert _policy(lib, backward, **kw) == dk.DUALKV_ERR_ALIGN, kw
+    assert _policy(lib, backward, N=4096, off=[0] * 4096 + [1]) == dk.DUALKV_ERR_UNSUPPORTED
+
+
+def test_policy_outputs_and_workspace(lib):
+    bad = dk.DUALKV_ERR_INVALID
+    for kw in (dict(red=3), dict(red=-1), dict(loss=0), dict(stats=0), dict(ent=0), dict(loss=0x100000), dict(stats=0x106000 - 8),
+               dict(w=0x105000), dict(loss=0x109010)):
+        assert _policy(lib, **kw) == bad, kw
+    for kw in (dict(ws=0), dict(ws=0x109010), dict(wsb=8)):
+        assert _policy(lib, **kw) == dk.DUALKV_ERR_WORKSPACE, kw
+    for kw in (dict(dl=0), dict(g=0), dict(g=0x100004), dict(gh=0x301004), dict(g=0x105000), dict(gh=0x300000)):
+        assert _policy(lib, True, **kw) == bad, kw
+    assert lib.dualkv_policy_loss_workspace_bytes(2, dk.offsets(OK_OFF)) > 0
+    assert lib.dualkv_policy_loss_workspace_bytes(2, dk.offsets([0, 3, 1])) == 0
