@@ -160,7 +160,7 @@ cudaError_t launch_pack(int kind, const void* src, void* dst, const int32_t* d_o
                         int row_elems, int num_sms, cudaStream_t st);
 
 // ---- per-head norm and rotation of q and k (rope.cu)
-constexpr int kRopeMaxBlocks = 152 * 6;  // resident blocks of 8 warps
+constexpr int kRopeMaxBlocks = 152 * 4;  // two rounds of the resident blocks
 
 struct RopeArgs {
   const __nv_bfloat16 *q, *k;            // projections' rows, head h of row t at t * stride + h * D

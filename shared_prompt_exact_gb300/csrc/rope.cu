@@ -11,19 +11,26 @@
 //
 // Both passes read each value once and write each once (the backward recomputes
 // r from x instead of loading it) and are bound by HBM bandwidth.  One warp
-// takes one packed row with all its heads: the row's cosines and sines are
-// computed once and stay in registers while the warp walks the heads.  A head
-// is spread over G = D/16 lanes; a lane holds two 16-byte vectors A and B
-// chosen so that both members of every pair lie in the same lane.
+// takes one packed row with all its heads, so the row's cosines and sines are
+// computed once and stay in registers; a head is spread over G = D/16 lanes, a
+// lane holding two 16-byte vectors A and B chosen so that both members of every
+// pair lie in it.  Loads run ahead of their use through shared memory
+// (cp.async); arithmetic is on f32x2 pairs, because with plain fp32 the backward
+// was bound by issue (64 % of the slots) as much as by memory.  Measured: forward
+// 228 us for 71,680 rows of 32 + 8 heads of 128 (6.4 TB/s, 0.95 of the measured
+// copy bandwidth; 331 us with loads straight into registers), backward 420 us for
+// 84,997 such rows (6.2 TB/s) and 190 us for 36,522 rows of 8 + 2 heads of 512
+// (5.9 TB/s).
 //
-// Angles: p f is formed in fp64, reduced to turns there, and only the fraction
-// of a turn goes to fp32; at p = 10^5 a product in fp32 would already be off by
-// 0.004 rad.  Everything else is fp32; the only rounding to bf16 is the final
-// one.  Weight gradients are summed in fp32 per warp, then per block and across
-// blocks in a fixed order.
+// Angles: p f is formed in 64-bit fixed point as a fraction of a turn, and only
+// that fraction goes to fp32; at p = 10^5 a product in fp32 would already be off
+// by 0.004 rad.  Everything else is fp32; the only rounding to bf16 is the final
+// one.  Weight gradients are summed in fp32 per lane, per block and across blocks, in
+// a fixed order.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 #include "segs.cuh"
 
 namespace dkv {
@@ -32,213 +39,290 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
+// Steps in a lane's ring: the one in use and those that its copies run ahead.  Three keep 32 KB
+// (forward) and 64 KB (backward) per SM in flight; with 4 to 6 and grids of 304 to 1216 blocks the
+// times below moved by less than 4 %, two blocks per SM in each case.
+constexpr int kDepth = 3;
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = __bfloat1622float2(h[e]);
-    f[2 * e] = t.x;
-    f[2 * e + 1] = t.y;
-  }
+// Eight consecutive values as four f32x2 pairs: (0, 2), (4, 6), (1, 3), (5, 7).  That order costs
+// nothing to form from bf16 words, and both pairings of the rotation are then element-wise.
+struct Vec8 {
+  float2 v[4];
+};
+__host__ __device__ constexpr int vec8_at(int d) { return (d & ~7) | ((d & 7) >> 1) | ((d & 1) << 2); }
+
+__device__ __forceinline__ Vec8 unpack8(const uint4& w) {
+  auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+  auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
+  Vec8 r;
+  r.v[0] = make_float2(lo(w.x), lo(w.y));
+  r.v[1] = make_float2(lo(w.z), lo(w.w));
+  r.v[2] = make_float2(hi(w.x), hi(w.y));
+  r.v[3] = make_float2(hi(w.z), hi(w.w));
+  return r;
+}
+__device__ __forceinline__ uint4 pack8(const Vec8& r) {
+  uint4 w;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
+  h[0] = __floats2bfloat162_rn(r.v[0].x, r.v[2].x);
+  h[1] = __floats2bfloat162_rn(r.v[0].y, r.v[2].y);
+  h[2] = __floats2bfloat162_rn(r.v[1].x, r.v[3].x);
+  h[3] = __floats2bfloat162_rn(r.v[1].y, r.v[3].y);
+  return w;
+}
+__device__ __forceinline__ Vec8 load8(const float* p, const float* q) {  // 4 floats each
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(q);
+  return Vec8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  uint4 v;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-  return v;
-}
-
-// Where a lane's vectors A and B lie in a head, and whether they are turned.
+// Where a lane's vectors A and B lie in a head, and the angles that turn them: 4 from ja
+// and 4 from jb on (both of no use where the lane's values are not turned).  In both layouts
+// neighbouring lanes read neighbouring vectors.
 struct LaneMap {
-  int a, b;   // element offsets
-  bool turn;
+  int a, b, ja, jb;
+  bool ta, tb;
 };
 
 template <int D>
 __device__ __forceinline__ LaneMap lane_map(int i, int half, bool inter) {
-  if (inter) return LaneMap{16 * i, 16 * i + 8, 8 * i < half};
-  if (8 * i < half) return LaneMap{8 * i, half + 8 * i, true};
-  return LaneMap{16 * i, 16 * i + 8, false};  // 2 half + 16 (i - half / 8)
+  if (inter) return LaneMap{8 * i, D / 2 + 8 * i, 4 * i, D / 4 + 4 * i, 4 * i < half, D / 4 + 4 * i < half};
+  if (8 * i < half) return LaneMap{8 * i, half + 8 * i, 8 * i, 8 * i + 4, true, true};
+  return LaneMap{half + 8 * i, D / 2 + 8 * i, 0, 0, false, false};  // behind the turned 2 half values
 }
 
-// cos and sin of the 8 angles of this lane's pairs (1 and 0 in lanes that are not
-// turned).  The S = 32/G lanes with the same i share the work.
+// Frequencies as fractions of a turn in 64-bit fixed point: a row's angle is then
+// position * frequency in integer arithmetic, whose overflow drops whole turns.  f / 2 pi
+// comes from fp64 once per block; the error of the angle is below 2^-32 turns plus 2^-53 of it.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+  double t = (double)f * 0.15915494309189533577;
+  t -= floor(t);
+  return (uint64_t)__double2ull_rd(t * 18446744073709551616.0);  // t < 1; 2^64 itself saturates
+}
+
+// What a block keeps in shared memory: frequencies, effective weights w + w0 of q and k in
+// Vec8 order, and every warp's cosines and sines.
 template <int D>
-__device__ __forceinline__ void row_angles(int p, const float* __restrict__ inv_freq, int i, int slot, bool turn,
-                                           float* cs, float* sn) {
-  constexpr int G = D / 16, S = 32 / G, PER = 8 / S;
-  float c[PER], s[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
-    if (turn) {
-      double t = (double)p * (double)__ldg(inv_freq + 8 * i + slot * PER + e) * 0.15915494309189533577;
-      t -= rint(t);
-      sincospif((float)(2.0 * t), &s[e], &c[e]);
+struct RopeShared {
+  alignas(16) float w[2][D];
+  alignas(16) float cs[kRopeWarps][D / 2];
+  alignas(16) float sn[kRopeWarps][D / 2];
+  uint64_t freq[D / 2];
+};
+
+template <int D>
+__device__ __forceinline__ void load_shared(const RopeArgs& A, RopeShared<D>& s) {
+  for (int j = threadIdx.x; j < A.half; j += kRopeThreads) s.freq[j] = turn_fraction(A.inv_freq[j]);
+  if (A.q_weight) {
+    for (int d = threadIdx.x; d < 2 * D; d += kRopeThreads) {
+      const void* w = d < D ? A.q_weight : A.k_weight;
+      const int e = d % D;
+      s.w[d / D][vec8_at(e)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
+                                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]));
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = __shfl_sync(0xffffffffu, c[e % PER], (e / PER) * G + i);
-    sn[e] = __shfl_sync(0xffffffffu, s[e % PER], (e / PER) * G + i);
-  }
+  __syncthreads();
 }
 
-// Turns the pairs of (a, b) by the angles (cs, sn).
-__device__ __forceinline__ void rotate(float* a, float* b, const float* cs, const float* sn, bool inter, float sign) {
-  if (inter) {
+// A lane's cosines and sines, in the order of its values; neg = -sn.
+struct Angles {
+  Vec8 cs, sn, neg;
+};
+
+// The warp's cosines and sines of one row in shared memory, then the lane's own 8 of
+// each (1 and 0 where its values are not turned).
+__device__ __forceinline__ Angles row_angles(int p, const uint64_t* freq, int half, float* wc, float* ws, int lane,
+                                             const LaneMap& m, bool inter) {
+  __syncwarp();
+  for (int j = lane; j < half; j += 32) {
+    const int turns = (int)(uint32_t)(((uint64_t)(uint32_t)p * freq[j]) >> 32);
+    const int at = inter ? j : vec8_at(j);
+    sincospif((float)turns * 4.656612873077393e-10f, ws + at, wc + at);  // 2^-31: half turns
+  }
+  __syncwarp();
+  Angles r{load8(wc + m.ja, wc + m.jb), load8(ws + m.ja, ws + m.jb), {}};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float c0 = cs[e], s0 = sign * sn[e], c1 = cs[4 + e], s1 = sign * sn[4 + e];
-      const float x0 = a[2 * e], x1 = a[2 * e + 1], z0 = b[2 * e], z1 = b[2 * e + 1];
-      a[2 * e] = x0 * c0 - x1 * s0;
-      a[2 * e + 1] = x1 * c0 + x0 * s0;
-      b[2 * e] = z0 * c1 - z1 * s1;
-      b[2 * e + 1] = z1 * c1 + z0 * s1;
+  for (int e = 0; e < 4; ++e) {
+    if (!(e < 2 ? m.ta : m.tb)) {
+      r.cs.v[e] = make_float2(1.f, 1.f);
+      r.sn.v[e] = make_float2(0.f, 0.f);
     }
+    r.neg.v[e] = make_float2(-r.sn.v[e].x, -r.sn.v[e].y);
+  }
+  return r;
+}
+
+// (u, v) <- (u c - v s, v c + u s)
+__device__ __forceinline__ void turn2(float2& u, float2& v, float2 c, float2 s, float2 neg) {
+  const float2 x = ffma2(v, neg, fmul2(u, c));
+  v = ffma2(u, s, fmul2(v, c));
+  u = x;
+}
+__device__ __forceinline__ void rotate(Vec8& a, Vec8& b, const Vec8& c, const Vec8& s, const Vec8& neg, bool inter) {
+  if (inter) {
+    turn2(a.v[0], a.v[2], c.v[0], s.v[0], neg.v[0]);
+    turn2(a.v[1], a.v[3], c.v[1], s.v[1], neg.v[1]);
+    turn2(b.v[0], b.v[2], c.v[2], s.v[2], neg.v[2]);
+    turn2(b.v[1], b.v[3], c.v[3], s.v[3], neg.v[3]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = sign * sn[e], x = a[e], z = b[e];
-      a[e] = x * cs[e] - z * s;
-      b[e] = z * cs[e] + x * s;
-    }
+    for (int e = 0; e < 4; ++e) turn2(a.v[e], b.v[e], c.v[e], s.v[e], neg.v[e]);
   }
 }
 
 template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float group_sum(float2 p) {
+  float v = p.x + p.y;
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The lane's 16 effective weights w + w0.
-__device__ __forceinline__ void load_weights(const void* w, int f32, float w0, const LaneMap& m, float* wa, float* wb) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wa[e] = w0 + (f32 ? __ldg(static_cast<const float*>(w) + m.a + e)
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[m.a + e]));
-    wb[e] = w0 + (f32 ? __ldg(static_cast<const float*>(w) + m.b + e)
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[m.b + e]));
-  }
+// cp.async: each lane copies the vectors that it will use itself into its own slots of a ring
+// in shared memory, some steps ahead of their use, so enough bytes are in flight without
+// holding registers and without any barrier.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-__device__ __forceinline__ void fwd_heads(const RopeArgs& A, const __nv_bfloat16* __restrict__ x,
-                                          __nv_bfloat16* __restrict__ y, int H, const LaneMap& m, int slot,
-                                          const void* w, const float* cs, const float* sn) {
-  constexpr int G = D / 16, S = 32 / G;
-  float wa[8], wb[8];
-  if (w) load_weights(w, A.weight_f32, A.w0, m, wa, wb);
-  for (int h0 = 0; h0 < H; h0 += S) {
-    const int h = h0 + slot;
-    float a[8], b[8];
-    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-    if (h < H) {
-      va = __ldg(reinterpret_cast<const uint4*>(x + h * D + m.a));
-      vb = __ldg(reinterpret_cast<const uint4*>(x + h * D + m.b));
-    }
-    unpack8(va, a);
-    unpack8(vb, b);
-    if (w) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-      const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= r * wa[e];
-        b[e] *= r * wb[e];
-      }
-    }
-    rotate(a, b, cs, sn, A.inter, 1.f);
-    if (h < H) {
-      *reinterpret_cast<uint4*>(y + h * D + m.a) = pack8(a);
-      *reinterpret_cast<uint4*>(y + h * D + m.b) = pack8(b);
+// The copies' place in a warp's walk: rows t, t + stride, ..., in each row q's heads in nq steps
+// of S = 32 / G heads, then k's up to `steps`.  x and g are the lane's vector A in the head and in
+// its upstream gradient (backward); vector B lies m.b - m.a behind.
+template <int D, bool BWD>
+struct Ahead {
+  static constexpr int S = 32 / (D / 16);
+  const __nv_bfloat16 *x, *g;
+  int h, H, s;
+  int64_t t;
+
+  __device__ __forceinline__ void row(const RopeArgs& A, int64_t row, int slot, int a) {
+    t = row;
+    s = 0;
+    h = slot;
+    H = A.Hq;
+    x = A.q + t * A.q_stride + slot * D + a;
+    if (BWD) g = A.dq_out + (t * A.Hq + slot) * D + a;
+  }
+  __device__ __forceinline__ void step(const RopeArgs& A, int nq, int steps, int64_t stride, int slot, int a) {
+    h += S;
+    x += S * D;
+    if (BWD) g += S * D;
+    if (++s == nq) {
+      h = slot;
+      H = A.Hkv;
+      x = A.k + t * A.k_stride + slot * D + a;
+      if (BWD) g = A.dk_out + (t * A.Hkv + slot) * D + a;
+    } else if (s == steps) {
+      row(A, t + stride, slot, a);
     }
   }
-}
+};
 
 template <int D, int CAP>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeArgs A,
-                                                                const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int G = D / 16;
-  const int lane = threadIdx.x & 31, slot = lane / G, i = lane % G;
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArgs A,
+                                                                    const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int G = D / 16, S = 32 / G;
+  extern __shared__ uint4 ring[];  // [kDepth][2][threads]
+  __shared__ RopeShared<D> sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
-  for (int64_t t = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < A.T; t += (int64_t)gridDim.x * kRopeWarps) {
-    float cs[8], sn[8];
-    row_angles<D>(position_of(seg, (int)t), A.inv_freq, i, slot, m.turn, cs, sn);
-    fwd_heads<D>(A, A.q + t * A.q_stride, A.q_out + t * A.q_out_stride, A.Hq, m, slot, A.q_weight, cs, sn);
-    fwd_heads<D>(A, A.k + t * A.k_stride, A.k_out + t * A.k_out_stride, A.Hkv, m, slot, A.k_weight, cs, sn);
+  const bool norm = A.q_weight != nullptr;
+  const int nq = (A.Hq + S - 1) / S, nk = (A.Hkv + S - 1) / S, steps = nq + nk, db = m.b - m.a;
+  const int64_t stride = (int64_t)gridDim.x * kRopeWarps, first = (int64_t)blockIdx.x * kRopeWarps + warp;
+  uint4* mine = ring + threadIdx.x;
+  Ahead<D, false> ahead;
+  ahead.row(A, first, slot, m.a);
+  auto fetch = [&](int stage) {
+    if (ahead.t < A.T) {
+      uint4* to = mine + 2 * stage * kRopeThreads;
+      if (ahead.h < ahead.H) {
+        copy16(to, ahead.x);
+        copy16(to + kRopeThreads, ahead.x + db);
+      }
+      ahead.step(A, nq, steps, stride, slot, m.a);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+  load_shared<D>(A, sh);
+  int stage = 0;
+  for (int64_t t = first; t < A.T; t += stride) {
+    const Angles ang =
+        row_angles(position_of(seg, (int)t), sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
+    auto heads = [&](int n, int H, const float* w, __nv_bfloat16* y) {
+      for (int s = 0, h = slot; s < n; ++s, h += S, y += S * D) {
+        fetch(stage == 0 ? kDepth - 1 : stage - 1);
+        copies_wait<kDepth - 1>();
+        Vec8 a = unpack8(mine[2 * stage * kRopeThreads]), b = unpack8(mine[(2 * stage + 1) * kRopeThreads]);
+        stage = stage == kDepth - 1 ? 0 : stage + 1;
+        if (norm) {
+          float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
+          const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
+          const float2 rr = make_float2(r, r);
+          const Vec8 wa = load8(w + m.a, w + m.a + 4), wb = load8(w + m.b, w + m.b + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
+            b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
+          }
+        }
+        rotate(a, b, ang.cs, ang.sn, ang.neg, A.inter);
+        if (h < H) {
+          *reinterpret_cast<uint4*>(y) = pack8(a);
+          *reinterpret_cast<uint4*>(y + db) = pack8(b);
+        }
+      }
+    };
+    heads(nq, A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a);
+    heads(nk, A.Hkv, sh.w[1], A.k_out + t * A.k_out_stride + slot * D + m.a);
   }
 }
 
-// Input gradients of one row's heads; adds the lane's weight gradients to (da, db).
+// One head's input gradient from the gradient turned back (g, f) and the head (a, b), in place; adds
+// the lane's weight gradients to (da, db).
 template <int D>
-__device__ __forceinline__ void bwd_heads(const RopeArgs& A, const __nv_bfloat16* __restrict__ x,
-                                          const __nv_bfloat16* __restrict__ dy, __nv_bfloat16* __restrict__ dx, int H,
-                                          const LaneMap& m, int slot, const void* w, const float* cs, const float* sn,
-                                          float* da, float* db) {
-  constexpr int G = D / 16, S = 32 / G;
-  float wa[8], wb[8];
-  if (w) load_weights(w, A.weight_f32, A.w0, m, wa, wb);
-  for (int h0 = 0; h0 < H; h0 += S) {
-    const int h = h0 + slot;
-    uint4 va = make_uint4(0, 0, 0, 0), vb = va, ga = va, gb = va;
-    if (h < H) {
-      ga = __ldg(reinterpret_cast<const uint4*>(dy + h * D + m.a));
-      gb = __ldg(reinterpret_cast<const uint4*>(dy + h * D + m.b));
-      if (w) {
-        va = __ldg(reinterpret_cast<const uint4*>(x + h * D + m.a));
-        vb = __ldg(reinterpret_cast<const uint4*>(x + h * D + m.b));
-      }
-    }
-    float g[8], f[8];
-    unpack8(ga, g);
-    unpack8(gb, f);
-    rotate(g, f, cs, sn, A.inter, -1.f);
-    if (w) {
-      float a[8], b[8];
-      unpack8(va, a);
-      unpack8(vb, b);
-      float ss = 0.f, ux = 0.f;
+__device__ __forceinline__ void norm_backward(Vec8& g, Vec8& f, const Vec8& a, const Vec8& b, const float* w,
+                                              const LaneMap& m, float eps, Vec8& da, Vec8& db) {
+  constexpr int G = D / 16;
+  const Vec8 wa = load8(w + m.a, w + m.a + 4), wb = load8(w + m.b, w + m.b + 4);
+  float2 ss = make_float2(0.f, 0.f), ux = ss;
+  Vec8 ua, ub;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss += a[e] * a[e] + b[e] * b[e];
-        ux += g[e] * wa[e] * a[e] + f[e] * wb[e] * b[e];
-      }
-      const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
-      const float mean = group_sum<G>(ux) * r * (1.f / D);  // mean(u x r)
+  for (int e = 0; e < 4; ++e) {
+    ua.v[e] = fmul2(g.v[e], wa.v[e]);
+    ub.v[e] = fmul2(f.v[e], wb.v[e]);
+    ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
+    ux = ffma2(ub.v[e], b.v[e], ffma2(ua.v[e], a.v[e], ux));
+  }
+  const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + eps);
+  const float k = -group_sum<G>(ux) * (1.f / D) * r * r * r;  // dx = r u - x r^3 mean(u x)
+  const float2 rr = make_float2(r, r), kk = make_float2(k, k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xa = a[e] * r, xb = b[e] * r;
-        da[e] += g[e] * xa;
-        db[e] += f[e] * xb;
-        g[e] = r * (g[e] * wa[e] - xa * mean);
-        f[e] = r * (f[e] * wb[e] - xb * mean);
-      }
-    }
-    if (h < H) {
-      *reinterpret_cast<uint4*>(dx + h * D + m.a) = pack8(g);
-      *reinterpret_cast<uint4*>(dx + h * D + m.b) = pack8(f);
-    }
+  for (int e = 0; e < 4; ++e) {
+    da.v[e] = ffma2(g.v[e], fmul2(a.v[e], rr), da.v[e]);
+    db.v[e] = ffma2(f.v[e], fmul2(b.v[e], rr), db.v[e]);
+    g.v[e] = ffma2(a.v[e], kk, fmul2(ua.v[e], rr));
+    f.v[e] = ffma2(b.v[e], kk, fmul2(ub.v[e], rr));
   }
 }
 
 // Sum of the block's weight gradients in a fixed order -> out[D].
 template <int D>
-__device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m, int slot, const float* da,
-                                                  const float* db, float* out) {
-  constexpr int G = D / 16, S = 32 / G;
+__device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m, int slot, const Vec8& da,
+                                                  const Vec8& db, float* out) {
+  constexpr int G = D / 16;
   const int warp = threadIdx.x >> 5;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float a = da[e], b = db[e];
+    const int k = vec8_at(e) >> 1;
+    float a = vec8_at(e) & 1 ? da.v[k].y : da.v[k].x, b = vec8_at(e) & 1 ? db.v[k].y : db.v[k].x;
 #pragma unroll
     for (int o = G; o < 32; o <<= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -260,59 +344,112 @@ __device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m,
 }
 
 template <int D, int CAP>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const RopeArgs A,
-                                                                const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int G = D / 16;
-  __shared__ float smem[kRopeWarps * D];
-  const int lane = threadIdx.x & 31, slot = lane / G, i = lane % G;
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs A,
+                                                                    const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int G = D / 16, S = 32 / G;
+  extern __shared__ uint4 ring[];  // [kDepth][4][threads]
+  __shared__ RopeShared<D> sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
-  float qa[8] = {}, qb[8] = {}, ka[8] = {}, kb[8] = {};
-  for (int64_t t = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < A.T; t += (int64_t)gridDim.x * kRopeWarps) {
-    float cs[8], sn[8];
-    row_angles<D>(position_of(seg, (int)t), A.inv_freq, i, slot, m.turn, cs, sn);
-    bwd_heads<D>(A, A.q + t * A.q_stride, A.dq_out + t * A.Hq * D, A.q_out + t * A.q_out_stride, A.Hq, m, slot,
-                 A.q_weight, cs, sn, qa, qb);
-    bwd_heads<D>(A, A.k + t * A.k_stride, A.dk_out + t * A.Hkv * D, A.k_out + t * A.k_out_stride, A.Hkv, m, slot,
-                 A.k_weight, cs, sn, ka, kb);
+  const bool norm = A.q_weight != nullptr;
+  const int nq = (A.Hq + S - 1) / S, nk = (A.Hkv + S - 1) / S, steps = nq + nk, db = m.b - m.a;
+  const int64_t stride = (int64_t)gridDim.x * kRopeWarps, first = (int64_t)blockIdx.x * kRopeWarps + warp;
+  uint4* mine = ring + threadIdx.x;
+  Ahead<D, true> ahead;
+  ahead.row(A, first, slot, m.a);
+  auto fetch = [&](int stage) {
+    if (ahead.t < A.T) {
+      uint4* to = mine + 4 * stage * kRopeThreads;
+      if (ahead.h < ahead.H) {
+        copy16(to, ahead.g);
+        copy16(to + kRopeThreads, ahead.g + db);
+        if (norm) {
+          copy16(to + 2 * kRopeThreads, ahead.x);
+          copy16(to + 3 * kRopeThreads, ahead.x + db);
+        }
+      } else {  // an idle slot adds nothing to the weight gradients
+#pragma unroll
+        for (int v = 0; v < 4; ++v) to[v * kRopeThreads] = make_uint4(0, 0, 0, 0);
+      }
+      ahead.step(A, nq, steps, stride, slot, m.a);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+  load_shared<D>(A, sh);
+  Vec8 qa{}, qb{}, ka{}, kb{};
+  int stage = 0;
+  for (int64_t t = first; t < A.T; t += stride) {
+    const Angles ang =
+        row_angles(position_of(seg, (int)t), sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
+    auto heads = [&](int n, int H, const float* w, __nv_bfloat16* y, Vec8& da, Vec8& db_) {
+      for (int s = 0, h = slot; s < n; ++s, h += S, y += S * D) {
+        fetch(stage == 0 ? kDepth - 1 : stage - 1);
+        copies_wait<kDepth - 1>();
+        const uint4* from = mine + 4 * stage * kRopeThreads;
+        stage = stage == kDepth - 1 ? 0 : stage + 1;
+        Vec8 g = unpack8(from[0]), f = unpack8(from[kRopeThreads]);
+        rotate(g, f, ang.cs, ang.neg, ang.sn, A.inter);  // by minus the angle
+        if (norm)
+          norm_backward<D>(g, f, unpack8(from[2 * kRopeThreads]), unpack8(from[3 * kRopeThreads]), w, m, A.eps, da, db_);
+        if (h < H) {
+          *reinterpret_cast<uint4*>(y) = pack8(g);
+          *reinterpret_cast<uint4*>(y + db) = pack8(f);
+        }
+      }
+    };
+    heads(nq, A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a, qa, qb);
+    heads(nk, A.Hkv, sh.w[1], A.k_out + t * A.k_out_stride + slot * D + m.a, ka, kb);
   }
-  if (A.q_weight) {
+  if (norm) {
+    // every lane has waited for its own copies; the ring becomes the place of the block's sums
+    copies_wait<0>();
+    __syncthreads();
+    float* smem = reinterpret_cast<float*>(ring);
     block_weight_grad<D>(smem, m, slot, qa, qb, A.partial + (int64_t)blockIdx.x * 2 * D);
     block_weight_grad<D>(smem, m, slot, ka, kb, A.partial + (int64_t)blockIdx.x * 2 * D + D);
   }
 }
 
 // Weight gradients: column d of the blocks' partial sums, added in block order.
-// A block of 32 x 8 threads takes 32 columns; the 8 rows of threads take
-// contiguous eighths of the blocks, which are then added in order.
-__global__ void __launch_bounds__(256) rope_weight_kernel(const float* __restrict__ partial, int blocks, int D,
-                                                          float* __restrict__ dqw, float* __restrict__ dkw) {
-  __shared__ double part[8][32];
-  const int col = blockIdx.x * 32 + threadIdx.x, per = (blocks + 7) / 8;
+// A block of 32 x 32 threads takes 32 columns; its rows of threads take contiguous
+// shares of the blocks, which are then added in order.
+__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restrict__ partial, int blocks, int D,
+                                                           float* __restrict__ dqw, float* __restrict__ dkw) {
+  __shared__ float part[32][33];
+  const int col = blockIdx.x * 32 + threadIdx.x, per = (blocks + 31) / 32;
   const int b0 = threadIdx.y * per, b1 = min(blocks, b0 + per);
-  double v = 0.0;
-#pragma unroll 4
-  for (int b = b0; b < b1; ++b) v += (double)partial[(int64_t)b * 2 * D + col];
+  float v = 0.f;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) v += partial[(int64_t)b * 2 * D + col];
   part[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y) return;
-  for (int k = 1; k < 8; ++k) v += part[k][threadIdx.x];
-  if (col < D) dqw[col] = (float)v;
-  else dkw[col - D] = (float)v;
+#pragma unroll
+  for (int k = 1; k < 32; ++k) v += part[k][threadIdx.x];
+  if (col < D) dqw[col] = v;
+  else dkw[col - D] = v;
+}
+
+template <int D, int CAP>
+cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, int grid,
+                          cudaStream_t st) {
+  const SegTable<CAP> s = make_segs<CAP>(P, N, off);
+  const int smem = (backward ? 4 * kDepth : 2 * kDepth) * kRopeThreads * (int)sizeof(uint4);
+  const cudaError_t e = backward ? cudaFuncSetAttribute(rope_bwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+                                 : cudaFuncSetAttribute(rope_fwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  if (backward) rope_bwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
+  else rope_fwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
+  return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_rope_d(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, int grid,
                           cudaStream_t st) {
-  if (N <= kSmallSegs) {
-    const SegTable<kSmallSegs> s = make_segs<kSmallSegs>(P, N, off);
-    if (backward) rope_bwd_kernel<D, kSmallSegs><<<grid, kRopeThreads, 0, st>>>(a, s);
-    else rope_fwd_kernel<D, kSmallSegs><<<grid, kRopeThreads, 0, st>>>(a, s);
-  } else {
-    const SegTable<kMaxSegs> s = make_segs<kMaxSegs>(P, N, off);
-    if (backward) rope_bwd_kernel<D, kMaxSegs><<<grid, kRopeThreads, 0, st>>>(a, s);
-    else rope_fwd_kernel<D, kMaxSegs><<<grid, kRopeThreads, 0, st>>>(a, s);
-  }
-  return cudaGetLastError();
+  return N <= kSmallSegs ? launch_rope_c<D, kSmallSegs>(backward, a, P, N, off, grid, st)
+                         : launch_rope_c<D, kMaxSegs>(backward, a, P, N, off, grid, st);
 }
 
 int rope_grid(int64_t T) {
@@ -340,7 +477,7 @@ cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, c
       return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || !backward || !a.q_weight) return e;
-  rope_weight_kernel<<<2 * D / 32, dim3(32, 8), 0, st>>>(a.partial, grid, D, dqw, dkw);
+  rope_weight_kernel<<<2 * D / 32, dim3(32, 32), 0, st>>>(a.partial, grid, D, dqw, dkw);
   return cudaGetLastError();
 }
 

@@ -51,7 +51,8 @@ def _reference(c, old, ref):
     """Token log-probabilities and gradients of fp64 autograd on the replicated sequences."""
     w = {k: v.double().cpu().requires_grad_() for k, v in c.w.items()}
     x = c.x.double().cpu().requires_grad_()
-    f, tok, mask, adv, old, ref = (t.cpu() for t in (c.f.double(), c.tok, c.mask, adv, old.double(), ref.double()))
+    f, tok, mask, adv, old, ref = (t.cpu() for t in (c.f.double(), c.tok, c.mask, c.adv.double(), old.double(),
+                                                      ref.double()))
     half = c.D // 2
     parts, entropies = [], []
     for s in range(c.N):
