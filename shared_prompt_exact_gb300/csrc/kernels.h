@@ -198,7 +198,7 @@ cudaError_t launch_logprobs(bool backward, bool f32, const LogpArgs& a, int P, i
                             cudaStream_t st);
 
 // ---- clipped policy loss (policy.cu)
-constexpr int kPolicyChunk = 2048;  // response tokens of one block
+constexpr int kPolicyChunk = 1024;  // response tokens of one block
 
 // A bound on a difference of log-probabilities, as the sum of two fp32 values.
 struct Bound {

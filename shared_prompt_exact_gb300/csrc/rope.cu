@@ -436,10 +436,11 @@ template <int D, int CAP>
 cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, int grid,
                           cudaStream_t st) {
   const SegTable<CAP> s = make_segs<CAP>(P, N, off);
-  const int smem = (backward ? 4 * kDepth : 2 * kDepth) * kRopeThreads * (int)sizeof(uint4);
-  const cudaError_t e = backward ? cudaFuncSetAttribute(rope_bwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-                                 : cudaFuncSetAttribute(rope_fwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  const int smem = (backward ? 4 : 2) * kDepth * kRopeThreads * (int)sizeof(uint4);
+  if (backward) {  // the forward stays within the 48 KB that need no asking
+    const cudaError_t e = cudaFuncSetAttribute(rope_bwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   if (backward) rope_bwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
   else rope_fwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
   return cudaGetLastError();

@@ -393,6 +393,9 @@ _WEIGHT_DTYPES = {torch.bfloat16: DUALKV_BF16, torch.float32: DUALKV_F32}
 def _check_tensor(where, name, t, shape, dtypes, device, rows=False):
     """A CUDA tensor on the calling thread's current device with this shape and one of these dtypes: contiguous, or
     (rows) only contiguous within a row of its first dimension."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_cuda
+            and t.get_device() == device and (t.is_contiguous() or (rows and _rows_contiguous(t)))):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{where}: {name} must be a CUDA tensor")
     if t.get_device() != device:
@@ -401,14 +404,34 @@ def _check_tensor(where, name, t, shape, dtypes, device, rows=False):
         raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)} for this call, got {tuple(t.shape)}")
-    if not t.is_contiguous() and not (rows and (t.shape[0] == 0 or t[0].is_contiguous())):
-        raise ValueError(f"{where}: {name} must be contiguous" + (" within its rows" if rows else ""))
+    raise ValueError(f"{where}: {name} must be contiguous" + (" within its rows" if rows else ""))
+
+
+def _rows_contiguous(t):
+    """Whether each slice of t along its first dimension is contiguous."""
+    width = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != width:
+            return False
+        width *= n
+    return True
 
 
 def _row_stride(t):
     """Elements between the rows of t's first dimension (a single row has the stride that its width gives)."""
-    width = t.numel() // max(t.shape[0], 1)
-    return t.stride(0) if t.shape[0] > 1 else width
+    n = t.shape[0]
+    return t.stride(0) if n > 1 else t.numel() // max(n, 1)
+
+
+def _stream_of(stream, device):
+    """The stream's handle: the current one of the (current) device unless given."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _layout_rows(where, P, N, R_offsets):
@@ -445,10 +468,10 @@ def dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, 
     T, dev, wd = _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D)
     _check_tensor(where, "q_out", q_out, (T, Hq, D), (torch.bfloat16,), dev)
     _check_tensor(where, "k_out", k_out, (T, Hkv, D), (torch.bfloat16,), dev)
-    rc = load().dualkv_qk_norm_rope(_ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(q_weight), _ptr(k_weight), wd,
-                                    float(weight_offset), float(eps), _ptr(inv_freq), int(rope_dim),
+    rc = load().dualkv_qk_norm_rope(_at(q), _row_stride(q), _at(k), _row_stride(k), _at(q_weight), _at(k_weight), wd,
+                                    float(weight_offset), float(eps), _at(inv_freq), int(rope_dim),
                                     1 if interleaved else 0, int(P), int(N), _offsets(R_offsets), int(Hq), int(Hkv),
-                                    int(D), _ptr(q_out), _ptr(k_out), _stream(stream))
+                                    int(D), _at(q_out), _at(k_out), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -472,12 +495,12 @@ def dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_off
         _check_tensor(where, "dq_weight", dq_weight, (D,), (torch.float32,), dev)
         _check_tensor(where, "dk_weight", dk_weight, (D,), (torch.float32,), dev)
     workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
-    rc = load().dualkv_qk_norm_rope_bwd(_ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(dq_out), _ptr(dk_out),
-                                        _ptr(q_weight), _ptr(k_weight), wd, float(weight_offset), float(eps),
-                                        _ptr(inv_freq), int(rope_dim), 1 if interleaved else 0, int(P), int(N),
-                                        _offsets(R_offsets), int(Hq), int(Hkv), int(D), _ptr(dq), _row_stride(dq),
-                                        _ptr(dk), _row_stride(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
-                                        workspace_bytes, _stream(stream))
+    rc = load().dualkv_qk_norm_rope_bwd(_at(q), _row_stride(q), _at(k), _row_stride(k), _at(dq_out), _at(dk_out),
+                                        _at(q_weight), _at(k_weight), wd, float(weight_offset), float(eps),
+                                        _at(inv_freq), int(rope_dim), 1 if interleaved else 0, int(P), int(N),
+                                        _offsets(R_offsets), int(Hq), int(Hkv), int(D), _at(dq), _row_stride(dq),
+                                        _at(dk), _row_stride(dk), _at(dq_weight), _at(dk_weight), _at(workspace),
+                                        workspace_bytes, _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -508,9 +531,9 @@ def dualkv_token_logprobs(logits, tokens, scale, P, N, R_offsets, logp, entropy,
         raise ValueError(f"{where}: logp is missing")
     _check_floats(where, dev, (n,), logp=logp, entropy=entropy)
     _check_floats(where, dev, (M,), lse=lse)
-    rc = load().dualkv_token_logprobs(_ptr(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype], logits.shape[1],
-                                      float(scale), _ptr(tokens), int(P), int(N), _offsets(R_offsets), _ptr(logp),
-                                      _ptr(entropy), _ptr(lse), _stream(stream))
+    rc = load().dualkv_token_logprobs(_at(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype], logits.shape[1],
+                                      float(scale), _at(tokens), int(P), int(N), _offsets(R_offsets), _at(logp),
+                                      _at(entropy), _at(lse), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -524,10 +547,10 @@ def dualkv_token_logprobs_bwd(logits, tokens, scale, P, N, R_offsets, lse, entro
     _check_floats(where, dev, (n,), dlogp=dlogp, dentropy=dentropy, entropy=entropy)
     _check_floats(where, dev, (M,), lse=lse)
     _check_tensor(where, "dlogits", dlogits, logits.shape, (logits.dtype,), dev, rows=True)
-    rc = load().dualkv_token_logprobs_bwd(_ptr(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype],
-                                          logits.shape[1], float(scale), _ptr(tokens), int(P), int(N),
-                                          _offsets(R_offsets), _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
-                                          _ptr(dlogits), _row_stride(dlogits), _stream(stream))
+    rc = load().dualkv_token_logprobs_bwd(_at(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype],
+                                          logits.shape[1], float(scale), _at(tokens), int(P), int(N),
+                                          _offsets(R_offsets), _at(lse), _at(entropy), _at(dlogp), _at(dentropy),
+                                          _at(dlogits), _row_stride(dlogits), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -578,11 +601,11 @@ def dualkv_policy_loss(logp, old_logp, ref_logp, entropy, advantages, mask, N, R
     _check_tensor(where, "stats", stats, (4,), (torch.float32,), dev)
     _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
     workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
-    rc = load().dualkv_policy_loss(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(entropy), _ptr(advantages), per_token,
-                                   _ptr(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
+    rc = load().dualkv_policy_loss(_at(logp), _at(old_logp), _at(ref_logp), _at(entropy), _at(advantages), per_token,
+                                   _at(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
                                    float(dual_clip), float(kl_coef), float(entropy_coef), LOSS_REDUCTIONS[reduction],
-                                   _ptr(loss), _ptr(stats), _ptr(weights), _ptr(workspace), workspace_bytes,
-                                   _stream(stream))
+                                   _at(loss), _at(stats), _at(weights), _at(workspace), workspace_bytes,
+                                   _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -600,10 +623,10 @@ def dualkv_policy_loss_bwd(logp, old_logp, ref_logp, advantages, mask, N, R_offs
         raise ValueError(f"{where}: dloss must be a tensor of one value")
     _check_tensor(where, "dloss", dloss, dloss.shape, (torch.float32,), dev)
     _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
-    rc = load().dualkv_policy_loss_bwd(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), per_token,
-                                       _ptr(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
-                                       float(dual_clip), float(kl_coef), float(entropy_coef), _ptr(dloss), _ptr(weights),
-                                       _ptr(dlogp), _ptr(dentropy), _stream(stream))
+    rc = load().dualkv_policy_loss_bwd(_at(logp), _at(old_logp), _at(ref_logp), _at(advantages), per_token,
+                                       _at(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
+                                       float(dual_clip), float(kl_coef), float(entropy_coef), _at(dloss), _at(weights),
+                                       _at(dlogp), _at(dentropy), _stream_of(stream, dev))
     _raise(rc, where)
 
 

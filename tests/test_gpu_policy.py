@@ -80,6 +80,9 @@ LAYOUTS = [
     ("tiny", [0, 32, 64, 96, 128]),
     ("empty-segments", [0, 0, 5, 5, 17, 17]),
     ("chunk-edges", [0, 2048, 4096, 8193, 8193, 10240, 10241]),
+    ("chunks-of-one-block", [0, 1023, 2047, 2048, 3073, 4097]),
+    ("cluster-edge", [0, 1024, 1024, 2048, 3050]),
+    ("past-the-cluster", [0, 1024, 1024, 2048, 4096]),
     ("long", [0, 30011]),
     ("many-segments", [0] + np.cumsum(np.arange(600) % 5).tolist()),
     ("most-segments", [0] + np.cumsum(np.arange(4095) % 3).tolist()),
