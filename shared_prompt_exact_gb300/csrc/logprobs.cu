@@ -14,7 +14,13 @@
 //
 // Forward: one pass over a row with a running maximum, sum and (for H) weighted
 // sum; reads each logit once.  Backward: one pass, reads each logit and writes
-// each gradient once.  Both are bound by HBM bandwidth.  Statistics are fp32.
+// each gradient once.  Statistics are fp32.  Both are bound by HBM bandwidth, given
+// enough loads in flight and few instructions per logit: batches of 8 (forward) and 4
+// vectors per thread, bf16 maxima two at a time, sums on f32x2 pairs.  Measured at
+// 131,072 bf16 logits a row: 17,096 rows with entropies 640 us (7.0 TB/s read, 1.03 of the
+// measured copy bandwidth; one vector at a time 841 us), the gradient of 10,479 rows with
+// entropies 790 us (6.8 TB/s, 1.0; one vector at a time 883 us).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -26,7 +32,11 @@ namespace dkv {
 
 namespace {
 
-constexpr int kLogpThreads = 512;
+namespace cg = cooperative_groups;
+
+constexpr int kLogpThreads = 256;
+constexpr int kFwdBatch = 8, kBwdBatch = 4;  // vectors that a thread has in flight
+constexpr int kMaxParts = 8;                 // blocks of a forward cluster
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,43 +51,81 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float x, float* d) { *d = x; }
 __device__ __forceinline__ void from_f(float x, __nv_bfloat16* d) { *d = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
-  f[0] = __uint_as_float(v.x);
-  f[1] = __uint_as_float(v.y);
-  f[2] = __uint_as_float(v.z);
-  f[3] = __uint_as_float(v.w);
+// A vector's values as f32x2 pairs (bf16: neighbours, fp32: neighbours).
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(w[e] << 16);
-    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
+  for (int e = 0; e < 4; ++e) f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+__device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
   uint4 v;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[e].x, f[e].y);
   return v;
 }
 
-// A row's 16-byte vectors: elements [head, head + nv * E), between two ragged ends.
+// Largest value of K vectors; a NaN does not count.
+template <int K>
+__device__ __forceinline__ float max_of(const uint4 (&v)[K], float) {
+  float m = -CUDART_INF_F;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    m = fmax3(m, __uint_as_float(v[k].x), __uint_as_float(v[k].y));
+    m = fmax3(m, __uint_as_float(v[k].z), __uint_as_float(v[k].w));
+  }
+  return m;
+}
+template <int K>
+__device__ __forceinline__ float max_of(const uint4 (&v)[K], __nv_bfloat16) {
+  __nv_bfloat162 m = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v[k]);
+    m = __hmax2(m, __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// A 16-byte load that does not stay in L1 (every logit is read once).
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// The 16-byte vectors of `n` values: [head, head + nv * E), between two ragged ends.
 template <typename T>
 struct RowVectors {
   static constexpr int E = 16 / sizeof(T);
-  int head, nv, tail;  // tail: first element behind the vectors
-  __device__ __forceinline__ RowVectors(const T* row, int V) {
+  int head, nv, tail, ends;  // tail: first element behind the vectors; ends: elements outside them
+  __device__ __forceinline__ RowVectors(const T* row, int n) {
     head = (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T));
-    head = head < V ? head : V;
-    nv = (V - head) / E;
+    head = head < n ? head : n;
+    nv = (n - head) / E;
     tail = head + nv * E;
+    ends = head + n - tail;
   }
+  __device__ __forceinline__ int end(int k) const { return k < head ? k : tail + k - head; }
 };
+
+// Columns [lo, hi) of part `r` of `parts` of a row: whole vectors, with a ragged end at the row's.
+template <typename T>
+__device__ __forceinline__ void part_of(const T* row, int V, int r, int parts, int* lo, int* hi) {
+  const RowVectors<T> v(row, V);
+  *lo = r == 0 ? 0 : v.head + (int)((int64_t)v.nv * r / parts) * RowVectors<T>::E;
+  *hi = r == parts - 1 ? V : v.head + (int)((int64_t)v.nv * (r + 1) / parts) * RowVectors<T>::E;
+}
 
 // The token that a row other than the prompt's last one predicts: its index, or -1.
 // `open` is the index of a segment-opening token that no row predicts (P = 0) and that
@@ -106,12 +154,18 @@ __device__ __forceinline__ int token_at(const LogpArgs& A, int i) {
 }
 
 // Running maximum m of the raw logits, sum s of e = 2^((z - m) c) and sum t of e (z - m) c,
-// where c = scale log2(e).  While only -inf has been seen m is -inf and s, t are 0 (NaN after a NaN).
+// where c = scale log2(e), each as two partial sums.  While only -inf has been seen m is -inf
+// and s, t are 0 (NaN after a NaN).
 struct Running {
-  float m, s, t;
+  float m;
+  float2 s, t;
 };
 
-// (z - m) c, with 0 in place of a maximum of -inf.
+__device__ __forceinline__ Running nothing_yet() {
+  return Running{-CUDART_INF_F, make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+}
+
+// 0 in place of a maximum of -inf.
 __device__ __forceinline__ float floor_of(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
 // Moves (s, t) from their maximum to a larger one.
@@ -119,8 +173,8 @@ __device__ __forceinline__ void rebase(Running& r, float m, float c) {
   if (r.m != -CUDART_INF_F) {
     const float d = (r.m - floor_of(m)) * c, f = ex2(d);
     // d is -inf only below a maximum of +inf, whose own term makes the sums NaN
-    r.t = (r.t + d * r.s) * f;
-    r.s *= f;
+    r.t = fmul2(ffma2(make_float2(d, d), r.s, r.t), make_float2(f, f));
+    r.s = fmul2(r.s, make_float2(f, f));
   }
   r.m = m;
 }
@@ -129,45 +183,70 @@ __device__ __forceinline__ Running join(Running a, Running b, float c) {
   const float m = fmaxf(a.m, b.m);
   rebase(a, m, c);
   rebase(b, m, c);
-  return Running{m, a.s + b.s, a.t + b.t};
+  return Running{m, fadd2(a.s, b.s), fadd2(a.t, b.t)};
 }
 
+// Adds pairs of values no larger than r.m.
 template <bool ENT, int K>
-__device__ __forceinline__ void absorb(Running& r, const float (&z)[K], float c) {
-  float m = z[0];
-#pragma unroll
-  for (int e = 1; e < K; ++e) m = fmaxf(m, z[e]);
-  if (m > r.m) rebase(r, m, c);
+__device__ __forceinline__ void accumulate(Running& r, const float2 (&z)[K], float c) {
   const float base = floor_of(r.m);
+  const float2 b2 = make_float2(base, base), c2 = make_float2(c, c);
 #pragma unroll
   for (int e = 0; e < K; ++e) {
-    const float y = (z[e] - base) * c, x = ex2(y);
-    r.s += x;
-    if (ENT) r.t = fmaf(x, fmaxf(y, -1e30f), r.t);  // a masked logit adds 0, not 0 * inf
+    // subtracted first: exactly 0 at the maximum, whatever its size
+    float2 y = fmul2(fsub2(z[e], b2), c2);
+    const float2 x = make_float2(ex2(y.x), ex2(y.y));
+    r.s = fadd2(r.s, x);
+    if (ENT) {
+      y = make_float2(fmaxf(y.x, -1e30f), fmaxf(y.y, -1e30f));  // a masked logit adds 0, not 0 * inf
+      r.t = ffma2(x, y, r.t);
+    }
   }
 }
 
-__device__ __forceinline__ Running block_join(Running r, float c) {
-  __shared__ Running part[kLogpThreads / 32];
+template <typename T, bool ENT, int K>
+__device__ __forceinline__ void absorb(Running& r, const uint4 (&v)[K], float c) {
+  const float m = max_of(v, T());
+  if (m > r.m) rebase(r, m, c);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float2 z[RowVectors<T>::E / 2];
+    unpack(v[k], z);
+    accumulate<ENT>(r, z, c);
+  }
+}
+
+__device__ __forceinline__ Running warp_join(Running r, float c) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Running b{__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o),
-                    __shfl_xor_sync(0xffffffffu, r.t, o)};
+    Running b;
+    b.m = __shfl_xor_sync(0xffffffffu, r.m, o);
+    b.s = make_float2(__shfl_xor_sync(0xffffffffu, r.s.x, o), 0.f);
+    b.t = make_float2(__shfl_xor_sync(0xffffffffu, r.t.x, o), 0.f);
     r = join(r, b, c);
   }
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = r;
-  __syncthreads();
-  r = part[0];
-  for (int k = 1; k < kLogpThreads / 32; ++k) r = join(r, part[k], c);
   return r;
 }
 
+// The block's sums, in its first warp (in the x halves).
+__device__ __forceinline__ Running block_join(Running r, float c) {
+  __shared__ Running part[kLogpThreads / 32];
+  r.s = make_float2(r.s.x + r.s.y, 0.f);
+  r.t = make_float2(r.t.x + r.t.y, 0.f);
+  r = warp_join(r, c);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = r;
+  __syncthreads();
+  if (threadIdx.x >= 32) return r;
+  return warp_join(threadIdx.x < kLogpThreads / 32 ? part[threadIdx.x] : nothing_yet(), c);
+}
+
+// One row per cluster of `parts` blocks (a part of the columns each), joined by its first block.
 template <typename T, bool ENT, int CAP>
-__global__ void __launch_bounds__(kLogpThreads) logp_fwd_kernel(const LogpArgs A,
-                                                                const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int E = RowVectors<T>::E;
-  const int64_t row = blockIdx.x;
-  const int n = seg.off[seg.N], tid = threadIdx.x;
+__global__ void __launch_bounds__(kLogpThreads, 4) logp_fwd_kernel(const LogpArgs A, int parts,
+                                                                   const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int U = kFwdBatch;
+  const int64_t row = blockIdx.x / parts;
+  const int rank = blockIdx.x % parts, n = seg.off[seg.N], tid = threadIdx.x;
   const bool shared_row = seg.P > 0 && row == 0;
   int open = -1, mine = -1, live = 0;
   if (shared_row) {
@@ -177,57 +256,77 @@ __global__ void __launch_bounds__(kLogpThreads) logp_fwd_kernel(const LogpArgs A
   } else {
     mine = predicted(seg, row, &open);
     if (mine >= 0) live = token_at(A, mine) >= 0;
-    if (seg.P == 0 && row == 0 && tid == 0 && n > 0) {  // token 0 opens its segment
+    if (seg.P == 0 && row == 0 && rank == 0 && tid == 0 && n > 0) {  // token 0 opens its segment
       A.logp[0] = 0.f;
       if (ENT) A.entropy[0] = 0.f;
     }
   }
-  const float c = A.scale * kLog2e;
-  const T* x = static_cast<const T*>(A.logits) + row * A.stride;
-  if (live) {
-    const RowVectors<T> v(x, A.V);
-    Running r{-CUDART_INF_F, 0.f, 0.f};
-    const uint4* xv = reinterpret_cast<const uint4*>(x + v.head);
-    for (int k = tid; k < v.nv; k += kLogpThreads) {
-      float z[E];
-      unpack(__ldg(xv + k), z);
-      absorb<ENT>(r, z, c);
-    }
-    for (int k = tid; k < v.head + A.V - v.tail; k += kLogpThreads) {
-      const float z[1] = {to_f(x[k < v.head ? k : v.tail + k - v.head])};
-      absorb<ENT>(r, z, c);
-    }
-    r = block_join(r, c);
-    // r.s is 0 only in a row that is -inf throughout: lse and logp are -inf there, H is 0
-    const bool none = r.s == 0.f;
-    const float ln_sum = logf(r.s), ent = none ? 0.f : ln_sum - r.t / r.s * kLn2;
-    auto write = [&](int i) {
-      const int tok = token_at(A, i);
-      // smaller terms than z - lse, so a likelier token keeps more digits
-      const float lp = tok < 0 ? 0.f : none ? -CUDART_INF_F : (to_f(x[tok]) - r.m) * A.scale - ln_sum;
-      A.logp[i] = lp;
-      if (ENT) A.entropy[i] = tok < 0 ? 0.f : ent;
-    };
+  if (!live) {  // the same in all blocks of the row
+    if (rank) return;
     if (shared_row) {
       for (int s = tid; s < seg.N; s += kLogpThreads)
-        if (seg.off[s] < seg.off[s + 1]) write(seg.off[s]);
-    } else if (tid == 0) {
-      write(mine);
+        if (seg.off[s] < seg.off[s + 1]) {
+          A.logp[seg.off[s]] = 0.f;
+          if (ENT) A.entropy[seg.off[s]] = 0.f;
+        }
+    } else if (tid == 0 && (mine >= 0 || open >= 0)) {
+      A.logp[mine >= 0 ? mine : open] = 0.f;
+      if (ENT) A.entropy[mine >= 0 ? mine : open] = 0.f;
     }
-    if (tid == 0 && A.lse) A.lse[row] = none ? -CUDART_INF_F : fmaf(r.m, A.scale, ln_sum);
+    if (tid == 0 && A.lse) A.lse[row] = 0.f;
     return;
   }
-  if (shared_row) {
-    for (int s = tid; s < seg.N; s += kLogpThreads)
-      if (seg.off[s] < seg.off[s + 1]) {
-        A.logp[seg.off[s]] = 0.f;
-        if (ENT) A.entropy[seg.off[s]] = 0.f;
-      }
-  } else if (tid == 0 && (mine >= 0 || open >= 0)) {
-    A.logp[mine >= 0 ? mine : open] = 0.f;
-    if (ENT) A.entropy[mine >= 0 ? mine : open] = 0.f;
+  const float c = A.scale * kLog2e;
+  const T* x = static_cast<const T*>(A.logits) + row * A.stride;
+  int lo, hi;
+  part_of(x, A.V, rank, parts, &lo, &hi);
+  const RowVectors<T> v(x + lo, hi - lo);
+  Running r = nothing_yet();
+  const uint4* xv = reinterpret_cast<const uint4*>(x + lo + v.head);
+  int k = tid;
+  for (; k + (U - 1) * kLogpThreads < v.nv; k += U * kLogpThreads) {
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = load_once(xv + k + u * kLogpThreads);
+    absorb<T, ENT>(r, w, c);
   }
-  if (tid == 0 && A.lse) A.lse[row] = 0.f;
+  for (; k < v.nv; k += kLogpThreads) {
+    const uint4 w[1] = {load_once(xv + k)};
+    absorb<T, ENT>(r, w, c);
+  }
+  for (k = tid; k < v.ends; k += kLogpThreads) {
+    const float2 z[1] = {make_float2(to_f(x[lo + v.end(k)]), -CUDART_INF_F)};
+    if (z[0].x > r.m) rebase(r, z[0].x, c);
+    accumulate<ENT>(r, z, c);
+  }
+  r = block_join(r, c);
+  if (parts > 1) {
+    __shared__ Running joined[kMaxParts];
+    cg::cluster_group cluster = cg::this_cluster();
+    if (tid == 0) *cluster.map_shared_rank(&joined[rank], 0) = r;
+    cluster.sync();
+    if (rank) return;
+    if (tid < 32) r = warp_join(tid < parts ? joined[tid] : nothing_yet(), c);
+  }
+  // the first warp has the row's sums; s is 0 only in a row that is -inf throughout: lse and logp
+  // are -inf there, H is 0
+  if (tid >= 32) return;
+  const bool none = r.s.x == 0.f;
+  const float ln_sum = logf(r.s.x), ent = none ? 0.f : ln_sum - r.t.x / r.s.x * kLn2;
+  auto write = [&](int i) {
+    const int tok = token_at(A, i);
+    // smaller terms than z - lse, so a likelier token keeps more digits
+    const float lp = tok < 0 ? 0.f : none ? -CUDART_INF_F : (to_f(x[tok]) - r.m) * A.scale - ln_sum;
+    A.logp[i] = lp;
+    if (ENT) A.entropy[i] = tok < 0 ? 0.f : ent;
+  };
+  if (shared_row) {
+    for (int s = tid; s < seg.N; s += 32)
+      if (seg.off[s] < seg.off[s + 1]) write(seg.off[s]);
+  } else if (tid == 0) {
+    write(mine);
+  }
+  if (tid == 0 && A.lse) A.lse[row] = none ? -CUDART_INF_F : fmaf(r.m, A.scale, ln_sum);
 }
 
 __device__ __forceinline__ float block_sum(float v) {
@@ -250,31 +349,47 @@ __device__ __forceinline__ float grad_of(float z, float scale, float lse, float 
   return ENT ? p * fmaf(fmaxf(d, -1e30f), k1, k0) : p * k0;
 }
 
+// The same for pairs.
+template <bool ENT>
+__device__ __forceinline__ float2 grad_of(float2 z, float scale, float lse, float k0, float k1) {
+  const float2 d = ffma2(z, make_float2(scale, scale), make_float2(-lse, -lse));
+  const float2 y = fmul2(d, make_float2(kLog2e, kLog2e)), p = make_float2(ex2(y.x), ex2(y.y)), k = make_float2(k0, k0);
+  if (!ENT) return fmul2(p, k);
+  return fmul2(p, ffma2(make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), make_float2(k1, k1), k));
+}
+
+// Block (row, part): one part of one row's columns.
 template <typename T, bool ENT, int CAP>
-__global__ void __launch_bounds__(kLogpThreads) logp_bwd_kernel(const LogpArgs A,
-                                                                const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int E = RowVectors<T>::E;
+__global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArgs A, int parts,
+                                                                   const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int P2 = RowVectors<T>::E / 2, U = kBwdBatch;
   extern __shared__ uint32_t dyn[];
   int* s_tok = reinterpret_cast<int*>(dyn);              // [N] the shared row's targets (-1: none)
   float* s_g = reinterpret_cast<float*>(dyn) + seg.N;    // [N] their upstream gradients
   float* s_v = s_g + seg.N;                              // [N] the targets' logit gradients
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x / parts;
   const int tid = threadIdx.x;
   const bool shared_row = seg.P > 0 && row == 0;
   const T* x = static_cast<const T*>(A.logits) + row * A.stride;
   T* y = static_cast<T*>(A.dlogits) + row * A.dstride;
+  int lo, hi;
+  part_of(y, A.V, (int)(blockIdx.x % parts), parts, &lo, &hi);
   const float lse = A.lse[row];
   float g = 0.f, h = 0.f, ent = 0.f;
   int tok = -1;
+  bool flows;
   if (shared_row) {
     int any = -1;
+    bool targets = false;  // gradients that cancel in g still reach their targets
     for (int s = tid; s < seg.N; s += kLogpThreads) {
       const int i = seg.off[s];
       const int t = i < seg.off[s + 1] ? token_at(A, i) : -1;
+      const float gi = t >= 0 ? A.dlogp[i] : 0.f;
       s_tok[s] = t;
-      s_g[s] = t >= 0 ? A.dlogp[i] : 0.f;
+      s_g[s] = gi;
+      targets |= gi != 0.f;
       if (t >= 0) {
-        g += A.dlogp[i];
+        g += gi;
         if (ENT) h += A.dentropy[i];
         any = i;
       }
@@ -290,6 +405,7 @@ __global__ void __launch_bounds__(kLogpThreads) logp_bwd_kernel(const LogpArgs A
       __syncthreads();
       ent = last >= 0 ? A.entropy[last] : 0.f;
     }
+    flows = __syncthreads_or(targets) || h != 0.f;
   } else {
     int open;
     const int i = predicted(seg, row, &open);
@@ -301,79 +417,112 @@ __global__ void __launch_bounds__(kLogpThreads) logp_bwd_kernel(const LogpArgs A
         ent = A.entropy[i];
       }
     }
+    flows = g != 0.f || h != 0.f;
   }
-  const RowVectors<T> v(y, A.V);
-  const int ends = v.head + A.V - v.tail;
-  uint4* yv = reinterpret_cast<uint4*>(y + v.head);
-  bool targets = false;  // a shared row whose gradients cancel in g may still have targets
-  if (shared_row) {
-    for (int s = tid; s < seg.N; s += kLogpThreads) targets |= s_g[s] != 0.f;
-    targets = __syncthreads_or(targets);
-  }
-  if ((g == 0.f && h == 0.f && !targets) || lse == -CUDART_INF_F) {
+  const RowVectors<T> v(y + lo, hi - lo);
+  uint4* yv = reinterpret_cast<uint4*>(y + lo + v.head);
+  if (!flows || lse == -CUDART_INF_F) {
     // nothing flows into this row (or it is masked throughout): zeros, without reading it
     for (int k = tid; k < v.nv; k += kLogpThreads) yv[k] = make_uint4(0, 0, 0, 0);
-    for (int k = tid; k < ends; k += kLogpThreads) from_f(0.f, y + (k < v.head ? k : v.tail + k - v.head));
+    for (int k = tid; k < v.ends; k += kLogpThreads) from_f(0.f, y + lo + v.end(k));
     return;
   }
   const float scale = A.scale;
   const float k1 = -scale * h, k0 = -scale * fmaf(h, ent, g);
+  auto here = [&](int t) { return t >= lo && t < hi; };  // targets in this block's columns
   // The targets' gradients, from logits that an in-place pass is about to overwrite.  Equal
   // targets of the shared row all get the same sum over them, in segment order.
   float vt = 0.f;
   if (shared_row) {
     for (int s = tid; s < seg.N; s += kLogpThreads) {
       const int t = s_tok[s];
-      if (t < 0) continue;
+      if (!here(t)) continue;
       float sum = 0.f;
       for (int u = 0; u < seg.N; ++u) sum += s_tok[u] == t ? s_g[u] : 0.f;
       s_v[s] = fmaf(scale, sum, grad_of<ENT>(to_f(x[t]), scale, lse, k0, k1));
     }
-  } else if (tid == 0) {
+  } else if (tid == 0 && here(tok)) {
     vt = fmaf(scale, g, grad_of<ENT>(to_f(x[tok]), scale, lse, k0, k1));
   }
   __syncthreads();
   if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) == 0) {
-    const uint4* xv = reinterpret_cast<const uint4*>(x + v.head);
-    for (int k = tid; k < v.nv; k += kLogpThreads) {
-      float z[E];
-      unpack(xv[k], z);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + lo + v.head);
+    auto grads = [&](const uint4& w) {
+      float2 z[P2];
+      unpack(w, z);
 #pragma unroll
-      for (int e = 0; e < E; ++e) z[e] = grad_of<ENT>(z[e], scale, lse, k0, k1);
-      yv[k] = pack(z);
+      for (int e = 0; e < P2; ++e) z[e] = grad_of<ENT>(z[e], scale, lse, k0, k1);
+      return pack(z);
+    };
+    int k = tid;
+    for (; k + (U - 1) * kLogpThreads < v.nv; k += U * kLogpThreads) {
+      uint4 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = load_once(xv + k + u * kLogpThreads);
+#pragma unroll
+      for (int u = 0; u < U; ++u) yv[k + u * kLogpThreads] = grads(w[u]);
     }
-    for (int k = tid; k < ends; k += kLogpThreads) {
-      const int j = k < v.head ? k : v.tail + k - v.head;
+    for (; k < v.nv; k += kLogpThreads) yv[k] = grads(load_once(xv + k));
+    for (k = tid; k < v.ends; k += kLogpThreads) {
+      const int j = lo + v.end(k);
       from_f(grad_of<ENT>(to_f(x[j]), scale, lse, k0, k1), y + j);
     }
-  } else {
-    for (int j = tid; j < A.V; j += kLogpThreads) from_f(grad_of<ENT>(to_f(x[j]), scale, lse, k0, k1), y + j);
+  } else {  // rows that start at different offsets within 16 bytes
+#pragma unroll 4
+    for (int j = lo + tid; j < hi; j += kLogpThreads) from_f(grad_of<ENT>(to_f(x[j]), scale, lse, k0, k1), y + j);
   }
   __syncthreads();
   if (shared_row) {
     for (int s = tid; s < seg.N; s += kLogpThreads)
-      if (s_tok[s] >= 0) from_f(s_v[s], y + s_tok[s]);
-  } else if (tid == 0) {
+      if (here(s_tok[s])) from_f(s_v[s], y + s_tok[s]);
+  } else if (tid == 0 && here(tok)) {
     from_f(vt, y + tok);
   }
+}
+
+// Blocks per row of the forward: one where the rows fill the GPU, else up to a cluster, which costs
+// a join.  At 131,072 bf16 logits: 80 rows 14.5 us in parts, 19.6 whole (cold, launch included);
+// 320 rows 26 us whole, 30 in parts.
+int fwd_parts(int64_t rows, int64_t bytes) {
+  int parts = 1;
+  while (parts < kMaxParts && rows * parts * 2 <= 608 && bytes / (parts * 2) >= 32768) parts *= 2;
+  return parts;
+}
+
+// Blocks per row of the backward, which nothing has to join: parts of 64 KB, which leave a shorter
+// last round of blocks than whole rows (10,479 rows of 256 KB: 782 us, whole 808, parts of 16 KB
+// 900), and of 16 KB where even those are few (20 rows: 11.4 us against 13.4).
+int bwd_parts(int64_t rows, int64_t bytes) {
+  const int64_t parts = (bytes + 65535) / 65536;
+  return (int)(rows * parts < 608 ? (bytes + 16383) / 16384 : parts);
 }
 
 template <typename T, bool ENT, int CAP>
 cudaError_t launch_logp_c(bool backward, const LogpArgs& a, int P, int N, const int32_t* off, cudaStream_t st) {
   const SegTable<CAP> s = make_segs<CAP>(P, N, off);
-  const unsigned grid = (unsigned)(off[N] + (P > 0 ? 1 : 0));
+  const int64_t rows = off[N] + (P > 0 ? 1 : 0);
+  const int64_t bytes = (int64_t)a.V * sizeof(T);
+  const int parts = backward ? bwd_parts(rows, bytes) : fwd_parts(rows, bytes);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * parts));
+  cfg.blockDim = dim3(kLogpThreads);
+  cfg.stream = st;
   if (!backward) {
-    logp_fwd_kernel<T, ENT, CAP><<<grid, kLogpThreads, 0, st>>>(a, s);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = parts;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, logp_fwd_kernel<T, ENT, CAP>, a, parts, s);
   }
-  const size_t smem = (size_t)N * 12;
-  if (smem > 32768) {  // beyond 48 KB with the kernel's static arrays
+  cfg.dynamicSmemBytes = P > 0 ? (size_t)N * 12 : 0;
+  if (cfg.dynamicSmemBytes > 32768) {  // beyond 48 KB with the kernel's static arrays
     const cudaError_t e = cudaFuncSetAttribute(logp_bwd_kernel<T, ENT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kMaxSegs * 12);
     if (e != cudaSuccess) return e;
   }
-  logp_bwd_kernel<T, ENT, CAP><<<grid, kLogpThreads, smem, st>>>(a, s);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, logp_bwd_kernel<T, ENT, CAP>, a, parts, s);
 }
 
 template <typename T, bool ENT>

@@ -350,3 +350,37 @@ def test_binding_refuses_what_does_not_fit():
     two = torch.empty(8, V, dtype=BF, device="cuda")
     with pytest.raises(dk.DualKVError):  # overlapping, but not in place
         dk.dualkv_token_logprobs_bwd(two[:4], tok, 1.0, P, 1, off, lse, None, dlogp, None, two[1:5])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 3, 40, 80, 160, 320])
+def test_rows_split_over_blocks(rows, dtype):
+    # few rows are split over a cluster (forward) or into smaller parts (backward): targets, masked
+    # stretches and the maximum in different parts, an empty part, odd ends
+    V, P, off = 70003, 1, [0, rows]
+    logits, tok, dlogp, dent = _inputs(P, off, V, dtype, 3, rows, ignored=0.0)
+    tok[0], tok[-1] = V - 1, 0
+    logits[:, 20000:45000] = -float("inf")
+    logits[0, 60000] = 30.0
+    got = dk.token_logprobs(logits, tok, P, off, entropy=True)
+    pick = sorted({0, rows // 2, rows - 1})
+    few = logits[pick].contiguous()
+    ftok, flse = tok[pick], got[2][pick]
+    z = _np(few)
+    want = opl.logprobs(np.concatenate([z, z[:1]]), ftok.tolist(), 1.0, 1, [0, len(pick)])
+    for k, i in enumerate(pick):  # row i of the batch predicts token i, as row k of the few does token k
+        top, p = z[k].max(), np.exp(z[k] - want[2][k])
+        y = np.where(p > 0, np.maximum(z[k] - top, -1e30), 0.0)
+        A, A2, K = (p * np.abs(y)).sum(), (p * y * y).sum(), 100 + V / 128
+        base = 2 * A + K + 4 * abs(top)
+        assert abs(float(flse[k]) - want[2][k]) <= U * (base + 4 * abs(want[2][k]))
+        if want[0][k] == -np.inf:  # a masked target
+            assert float(got[0][i]) == -np.inf
+        else:
+            assert abs(float(got[0][i]) - want[0][k]) <= U * (base + 4 * abs(z[k, ftok[k]] - top) + 4 * abs(want[0][k]))
+        assert abs(float(got[1][i]) - want[1][k]) <= U * ((1 + A + A2) * (K + 8) + 4 * abs(want[1][k]))
+    d = dk.token_logprobs_backward(logits, tok, got[2], dlogp, P, off, entropy=got[1], dentropy=dent)
+    sub = torch.cat((few, few[:1]))
+    lse2 = torch.cat((flse, torch.zeros(1, device="cuda")))
+    dsub = torch.cat((d[pick], torch.zeros_like(d[:1])))
+    _check_backward(dsub, sub, ftok, 1.0, 1, [0, len(pick)], lse2, got[1][pick], dlogp[pick], dent[pick])
