@@ -672,9 +672,9 @@ int policy_impl(bool backward, const float* logp, const float* old_logp, const f
   a.up = bound_of(std::log1p(clip_high));
   a.down = bound_of(std::log1p(-clip_low));
   if (a.has_dual) a.dual = bound_of(std::log(dual_clip));
-  a.ratio_up = (float)(1.0 + clip_high);
-  a.ratio_down = (float)(1.0 - clip_low);
-  a.ratio_dual = (float)dual_clip;
+  a.add_up = bound_of(clip_high);
+  a.add_down = bound_of(-clip_low);
+  a.add_dual = bound_of(dual_clip - 1.0);
   a.kl_coef = kl_coef;
   a.entropy_coef = entropy_coef;
   a.loss = loss;

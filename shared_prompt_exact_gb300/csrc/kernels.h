@@ -200,7 +200,7 @@ cudaError_t launch_logprobs(bool backward, bool f32, const LogpArgs& a, int P, i
 // ---- clipped policy loss (policy.cu)
 constexpr int kPolicyChunk = 1024;  // response tokens of one block
 
-// A bound on a difference of log-probabilities, as the sum of two fp32 values.
+// An fp64 value as the sum of two fp32 values.
 struct Bound {
   float hi, lo;
 };
@@ -208,8 +208,8 @@ struct PolicyArgs {
   const float *logp, *old_logp, *ref_logp, *entropy, *adv;  // ref_logp, entropy may be null
   const uint8_t* mask;                                      // null: every token is live
   int per_token, reduction, has_dual;
-  Bound up, down, dual;
-  float ratio_up, ratio_down, ratio_dual;
+  Bound up, down, dual;              // the bounds on the ratio, as differences of log-probabilities
+  Bound add_up, add_down, add_dual;  // and as the ratio less 1
   double kl_coef, entropy_coef;
   float *loss, *stats, *weights;  // forward: written; backward: weights read
   void* records;

@@ -12,20 +12,23 @@
 // and its rounding error, with log(1 + hi) and the others as sums of two fp32 values
 // from fp64.  So no token changes sides by rounding.
 //
+// Policy terms of either sign cancel in the sum, so each is summed as -A and -A (ratio - 1): -A is
+// exact, ratio - 1 comes from the same series as the KL term, and the sums keep their rounding
+// errors beside them.  fp64 would do the same, but its adds run at two lanes per clock and SM
+// here: with fp64 trees a call on 4M tokens took 172 us instead of 39.
+//
 // A block takes up to kPolicyChunk tokens of ONE segment, all of whose loads are issued before
-// the first is used, and makes one record of sums (fp32 trees); a single block then turns the
-// records into weights and the loss, with compensated fp32 sums (two values each) in a fixed
-// order.  fp64 adds run at two lanes per clock and SM here: with them in the trees a call on 4M
-// tokens took 172 us instead of 32.  Blocks are numbered without a list: segment n owns blocks
-// [off[n] / chunk + n, off[n + 1] / chunk + n + 1), at least as many as it has chunks.  Up to
-// kClusterBlocks blocks run as one cluster whose first block joins the records from its shared
+// the first is used, and makes one record of sums; a single block then turns the records into
+// weights and the loss in a fixed order.  Blocks are numbered without a list: segment n owns
+// blocks [off[n] / chunk + n, off[n + 1] / chunk + n + 1), at least as many as it has chunks.  Up
+// to kClusterBlocks blocks run as one cluster whose first block joins the records from its shared
 // memory; more write them to the workspace for a second launch.
 //
-// Up to some 100,000 tokens a call is launch latency (about 6 us in a graph).  At 4.04M tokens
-// (1,024 responses, every input in use) the forward takes 32 us, 2.7 TB/s: 26 for the records,
-// bound by memory latency and issue together (about 160 instructions a token and warp), the rest
-// the join; the gradients take 24 us, 4.2 TB/s.  Chunks of 1,024 and 4 tokens a thread beat 2,048
-// and 8 (40 against 50 us cold): more resident threads outweigh fewer loads in flight each.
+// Up to some 100,000 tokens a call is launch latency (6 to 9 us in a graph).  At 4.04M tokens
+// (1,024 responses, every input in use) the forward takes 39 us, 2.2 TB/s, 7 of them the join, and
+// is bound by issue (about 200 instructions a token and warp) and memory latency together; the
+// gradients take 28 us, 3.6 TB/s.  Four tokens a thread in chunks of 1,024 beat eight in 2,048
+// (40 against 46 us cold): more resident threads outweigh fewer blocks.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -42,10 +45,28 @@ constexpr int kPolicyThreads = 256;
 constexpr int kPerThread = kPolicyChunk / kPolicyThreads;
 constexpr int kClusterBlocks = 8;
 
+// A sum kept as hi + lo, with the rounding errors of the additions in lo (NaN once hi is not finite).
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 add(const Sum2& a, const Sum2& b) {
+  const float s = a.hi + b.hi, bb = s - a.hi;
+  return Sum2{s, (a.hi - (s - bb)) + (b.hi - bb) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Sum2 times(float w, const Sum2& v) {
+  const float p = w * v.hi;
+  return Sum2{p, fmaf(w, v.lo, fmaf(w, v.hi, -p))};
+}
+__device__ __forceinline__ double value(const Sum2& v) {
+  return fabsf(v.hi) <= 3.4e38f ? (double)v.hi + (double)v.lo : (double)v.hi;
+}
+
 // A chunk's sums; counts holds the live tokens and, in the upper half, those beyond a bound.
-struct alignas(16) Record {
-  float policy, kl, ent;
+struct alignas(8) Record {
+  Sum2 policy;
+  float kl, ent;
   uint32_t counts;
+  int seg;
 };
 
 // The segments of every 2^shift-th block, so that a block finds its own among few.
@@ -129,47 +150,53 @@ __device__ __forceinline__ Kl kl_of(float x) {
   return Kl{p, p + x};
 }
 
-// A token's ratio, the ratio that its policy term uses, and whether that is a bound.
+// A token's bounded ratio less 1, as v + rest, and whether it is a bound.  The difference from 1 is
+// kept apart because policy terms of either sign cancel: -A (1 + v + rest) is then summed from -A,
+// which is exact, and two products of small factors.
 struct Term {
-  float ratio, bounded;
+  float v, rest;
   bool clipped;
 };
 __device__ __forceinline__ Term term_of(const PolicyArgs& A, float logp, float old, float adv) {
   float e;
   const float d = exact_diff(logp, old, &e);
-  float ratio = expf(d);
+  const Kl k = kl_of(d);  // e^d - d - 1
+  const bool near = fabsf(d) < 1.f;
+  Term t{near ? d : k.slope, near ? k.kl + e : 0.f, false};
   const bool gain = adv > 0.f, loss = adv < 0.f;
   const float x = beyond(d, e, Bound{gain ? A.up.hi : A.down.hi, gain ? A.up.lo : A.down.lo});
-  Term t;
   t.clipped = gain ? x > 0.f : loss && x < 0.f;
-  t.bounded = t.clipped ? (gain ? A.ratio_up : A.ratio_down) : ratio;
-  if (A.has_dual && loss && beyond(d, e, A.dual) > 0.f) {
-    t.clipped = true;
-    t.bounded = A.ratio_dual;
+  if (t.clipped) {
+    t.v = gain ? A.add_up.hi : A.add_down.hi;
+    t.rest = gain ? A.add_up.lo : A.add_down.lo;
   }
-  if (adv == 0.f) ratio = t.bounded = 0.f;  // not 0 * inf
-  t.ratio = ratio;
+  if (A.has_dual && loss && beyond(d, e, A.dual) > 0.f) t = Term{A.add_dual.hi, A.add_dual.lo, true};
+  if (adv == 0.f) t.v = t.rest = 0.f;  // not 0 * inf
   return t;
 }
 
-// A thread's tokens of a chunk: lo + tid + k * threads.  Masked ones are loaded, not used.
+// A thread's tokens of a chunk, lo + tid + k * threads; FULL: all of them exist.  Masked ones are
+// loaded, not used.
 struct Tokens {
   float logp[kPerThread], old[kPerThread], adv[kPerThread], ref[kPerThread], ent[kPerThread];
-  bool in[kPerThread], on[kPerThread];
+  bool on[kPerThread];
 };
-template <bool ENT>
+template <bool FULL>
+__device__ __forceinline__ bool exists(const Chunk& c, int k) {
+  return FULL || c.lo + (int)threadIdx.x + k * kPolicyThreads < c.hi;
+}
+template <bool FULL, bool ENT>
 __device__ __forceinline__ void load_tokens(const PolicyArgs& A, const Chunk& c, Tokens& t) {
   const int64_t at = (int64_t)c.lo + threadIdx.x;
-  const int left = c.hi - c.lo - (int)threadIdx.x;
   const float *logp = A.logp + at, *old = A.old_logp + at, *ref = A.ref_logp + at, *ent = A.entropy + at;
   const float* adv = A.per_token ? A.adv + at : A.adv + c.seg;
   const uint8_t* mask = A.mask + at;
   const bool per_token = A.per_token, has_ref = A.ref_logp, has_ent = ENT && A.entropy, has_mask = A.mask;
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
-    t.in[k] = t.on[k] = k * kPolicyThreads < left;
+    t.on[k] = exists<FULL>(c, k);
     t.logp[k] = t.old[k] = t.adv[k] = t.ref[k] = t.ent[k] = 0.f;
-    if (t.in[k]) {
+    if (FULL || t.on[k]) {
       t.logp[k] = logp[k * kPolicyThreads];
       t.old[k] = old[k * kPolicyThreads];
       t.adv[k] = adv[per_token ? k * kPolicyThreads : 0];
@@ -180,61 +207,74 @@ __device__ __forceinline__ void load_tokens(const PolicyArgs& A, const Chunk& c,
   }
 }
 
-// A sum kept as hi + lo, with the rounding errors of the additions in lo.
-struct Sum2 {
-  float hi, lo;
-};
-__device__ __forceinline__ Sum2 add(const Sum2& a, const Sum2& b) {
-  const float s = a.hi + b.hi, bb = s - a.hi;
-  const float e = (a.hi - (s - bb)) + (b.hi - bb) + a.lo + b.lo;
-  return Sum2{s, fabsf(s) <= 3.4e38f ? e : 0.f};
-}
 __device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     v = add(v, Sum2{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// The block's record of its chunk, complete in thread 0.
-__device__ __forceinline__ Record chunk_record(const PolicyArgs& A, const Chunk& c) {
-  __shared__ Record part[kPolicyThreads / 32];
-  const int tid = threadIdx.x;
+// A thread's share of its chunk's sums.
+struct Partial {
+  Sum2 policy;
+  float kl, ent;
+  uint32_t counts;
+};
+template <bool FULL>
+__device__ __forceinline__ Partial sum_tokens(const PolicyArgs& A, const Chunk& c) {
   Tokens x;
-  load_tokens<true>(A, c, x);
-  float policy = 0.f, kl = 0.f, h = 0.f;
-  uint32_t counts = 0;
+  load_tokens<FULL, true>(A, c, x);
+  Partial r{{0.f, 0.f}, 0.f, 0.f, 0u};
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
-    if (c.lo + k * kPolicyThreads >= c.hi) break;  // the same for the whole block
+    if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;  // the same for the whole block
     const Term t = term_of(A, x.logp[k], x.old[k], x.adv[k]);
+    const float v = A.ref_logp ? kl_of(x.ref[k] - x.logp[k]).kl : 0.f;
     if (x.on[k]) {
-      policy = fmaf(-x.adv[k], t.bounded, policy);
-      h += x.ent[k];
-      counts += t.clipped ? 0x10001u : 1u;
-    }
-    if (A.ref_logp) {
-      const float v = kl_of(x.ref[k] - x.logp[k]).kl;
-      if (x.on[k]) kl += v;
+      const float a = -x.adv[k], p = a * t.v, y = a + p;
+      // the errors of the product, of the sum (|v| <= 1 but for far ratios), and the rest
+      r.policy = add(r.policy, Sum2{y, fmaf(a, t.rest, fmaf(a, t.v, -p) + (p - (y - a)))});
+      r.kl += v;
+      r.ent += x.ent[k];
+      r.counts += t.clipped ? 0x10001u : 1u;
     }
   }
-  Record r{warp_sum(policy), warp_sum(kl), warp_sum(h), __reduce_add_sync(0xffffffffu, counts)};
-  if ((tid & 31) == 0) part[tid >> 5] = r;
+  return r;
+}
+
+// The block's record of its chunk, complete in thread 0.  The threads' sums meet in shared memory,
+// where one warp per quantity adds them: trees in every warp took a third of the time.
+__device__ __forceinline__ Record chunk_record(const PolicyArgs& A, const Chunk& c) {
+  __shared__ float s_hi[kPolicyThreads], s_lo[kPolicyThreads], s_kl[kPolicyThreads], s_h[kPolicyThreads];
+  __shared__ float s_out[2];
+  __shared__ uint32_t s_counts[kPolicyThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Partial mine = c.hi - c.lo == kPolicyChunk ? sum_tokens<true>(A, c) : sum_tokens<false>(A, c);
+  s_hi[tid] = mine.policy.hi;
+  s_lo[tid] = mine.policy.lo;
+  s_kl[tid] = mine.kl;
+  s_h[tid] = mine.ent;
+  const uint32_t counts = __reduce_add_sync(0xffffffffu, mine.counts);
+  if (lane == 0) s_counts[warp] = counts;
   __syncthreads();
-  if (tid == 0) {
+  Record r{{0.f, 0.f}, 0.f, 0.f, 0u, c.seg};
+  if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kPolicyThreads / 32; ++w) {
-      r.policy += part[w].policy;
-      r.kl += part[w].kl;
-      r.ent += part[w].ent;
-      r.counts += part[w].counts;
-    }
+    for (int w = 0; w < kPolicyThreads / 32; ++w) r.policy = add(r.policy, Sum2{s_hi[32 * w + lane], s_lo[32 * w + lane]});
+    r.policy = warp_sum(r.policy);
+  } else if (warp <= 2) {
+    const float* from = warp == 1 ? s_kl : s_h;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPolicyThreads / 32; ++w) v += from[32 * w + lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) s_out[warp - 1] = v;
   }
+  __syncthreads();
+  r.kl = s_out[0];
+  r.ent = s_out[1];
+#pragma unroll
+  for (int w = 0; w < kPolicyThreads / 32; ++w) r.counts += s_counts[w];
   return r;
 }
 
@@ -242,23 +282,17 @@ __device__ __forceinline__ Record chunk_record(const PolicyArgs& A, const Chunk&
 // the segments' weights, and the weighted sums of the records in a fixed order.  Up to
 // BATCH * THREADS records are held in registers between the two passes over them.
 template <int THREADS, int BATCH>
-__device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, const int* segs, int blocks, int N,
-                                       int* live) {
+__device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, int blocks, int N, int* live) {
   __shared__ Sum2 part[3][THREADS / 32];
   __shared__ int total, beyond_bound;
   const int tid = threadIdx.x;
   Record r[BATCH];
-  int seg[BATCH];
   auto load = [&](int first) {
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int b = first + k * THREADS;
-      r[k] = Record{0.f, 0.f, 0.f, 0u};
-      seg[k] = 0;
-      if (b < blocks) {
-        r[k] = rec[b];
-        seg[k] = segs[b];
-      }
+      r[k].counts = 0;
+      if (b < blocks) r[k] = rec[b];
     }
   };
   int sum_live = 0, sum_beyond = 0;
@@ -267,7 +301,7 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, c
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int n = r[k].counts & 0xffff;
-      if (n) atomicAdd(&live[seg[k]], n);
+      if (n) atomicAdd(&live[r[k].seg], n);
       sum_live += n;
       sum_beyond += r[k].counts >> 16;
     }
@@ -292,10 +326,10 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, c
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (!r[k].counts) continue;
-      const float w = weight(seg[k]);
-      p = add(p, Sum2{w * r[k].policy, 0.f});
-      q = add(q, Sum2{w * r[k].kl, 0.f});
-      h = add(h, Sum2{w * r[k].ent, 0.f});
+      const float w = weight(r[k].seg);
+      p = add(p, times(w, r[k].policy));
+      q = add(q, times(w, Sum2{r[k].kl, 0.f}));
+      h = add(h, times(w, Sum2{r[k].ent, 0.f}));
     }
   }
   p = warp_sum(p);
@@ -314,7 +348,7 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, c
   q = warp_sum(in ? part[1][tid] : zero);
   h = warp_sum(in ? part[2][tid] : zero);
   if (tid == 0) {
-    const double dp = (double)p.hi + p.lo, dq = (double)q.hi + q.lo, dh = (double)h.hi + h.lo;
+    const double dp = value(p), dq = value(q), dh = value(h);
     A.loss[0] = (float)(dp + A.kl_coef * dq - A.entropy_coef * dh);
     A.stats[0] = (float)dp;
     A.stats[1] = (float)dq;
@@ -323,24 +357,16 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, c
   }
 }
 
-// The workspace: the records of `blocks` blocks, then their segments.
-__device__ __forceinline__ int* segs_of(const PolicyArgs& A, int blocks) {
-  return reinterpret_cast<int*>(static_cast<Record*>(A.records) + blocks);
-}
-
 template <int CAP>
 __global__ void __launch_bounds__(kPolicyThreads, 6) policy_fwd_kernel(const PolicyArgs A,
                                                                     const __grid_constant__ SegTable<CAP> seg,
                                                                     const __grid_constant__ BlockIndex index) {
   const Chunk c = chunk_of(seg, index, blockIdx.x);
   const Record r = chunk_record(A, c);
-  if (threadIdx.x == 0) {
-    static_cast<Record*>(A.records)[blockIdx.x] = r;
-    segs_of(A, gridDim.x)[blockIdx.x] = c.seg;
-  }
+  if (threadIdx.x == 0) static_cast<Record*>(A.records)[blockIdx.x] = r;
 }
 
-constexpr int kFinishThreads = 1024;
+constexpr int kFinishThreads = 512;
 
 // Launched while the records are still being made: everything before the wait overlaps with that.
 __global__ void __launch_bounds__(kFinishThreads) policy_finish_kernel(const PolicyArgs A, int blocks, int N) {
@@ -348,7 +374,7 @@ __global__ void __launch_bounds__(kFinishThreads) policy_finish_kernel(const Pol
   for (int n = threadIdx.x; n < N; n += kFinishThreads) live[n] = 0;
   __syncthreads();
   cudaGridDependencySynchronize();
-  finish<kFinishThreads, 6>(A, static_cast<const Record*>(A.records), segs_of(A, blocks), blocks, N, live);
+  finish<kFinishThreads, 8>(A, static_cast<const Record*>(A.records), blocks, N, live);
 }
 
 // The whole forward as one cluster of gridDim.x <= kClusterBlocks blocks.
@@ -356,41 +382,45 @@ __global__ void __launch_bounds__(kPolicyThreads, 6) policy_cluster_kernel(const
                                                                         const __grid_constant__ SegTable<kSmallSegs> seg,
                                                                         const __grid_constant__ BlockIndex index) {
   __shared__ Record rec[kClusterBlocks];
-  __shared__ int segs[kClusterBlocks], live[kClusterBlocks];  // no more segments than blocks
+  __shared__ int live[kClusterBlocks];  // no more segments than blocks
   cg::cluster_group cluster = cg::this_cluster();
   const Chunk c = chunk_of(seg, index, blockIdx.x);
   const Record r = chunk_record(A, c);
   if (threadIdx.x == 0) {
     *cluster.map_shared_rank(&rec[blockIdx.x], 0) = r;
-    *cluster.map_shared_rank(&segs[blockIdx.x], 0) = c.seg;
     if (blockIdx.x == 0)
       for (int n = 0; n < kClusterBlocks; ++n) live[n] = 0;
   }
   cluster.sync();
-  if (blockIdx.x == 0) finish<kPolicyThreads, 1>(A, rec, segs, gridDim.x, seg.N, live);
+  if (blockIdx.x == 0) finish<kPolicyThreads, 1>(A, rec, gridDim.x, seg.N, live);
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kPolicyThreads, 6) policy_bwd_kernel(const PolicyArgs A,
-                                                                    const __grid_constant__ SegTable<CAP> seg,
-                                                                    const __grid_constant__ BlockIndex index) {
-  const Chunk c = chunk_of(seg, index, blockIdx.x);
-  if (c.lo >= c.hi) return;
+template <bool FULL>
+__device__ __forceinline__ void token_gradients(const PolicyArgs& A, const Chunk& c) {
   Tokens x;
-  load_tokens<false>(A, c, x);
+  load_tokens<FULL, false>(A, c, x);
   const float w = A.dloss[0] * A.weights[c.seg], wh = -(float)A.entropy_coef * w, b = (float)A.kl_coef;
   float *dlogp = A.dlogp + c.lo + threadIdx.x, *dent = A.dentropy ? A.dentropy + c.lo + threadIdx.x : nullptr;
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
-    if (c.lo + k * kPolicyThreads >= c.hi) break;
+    if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;
     const Term t = term_of(A, x.logp[k], x.old[k], x.adv[k]);
-    float g = t.clipped ? 0.f : -x.adv[k] * t.ratio;
+    float g = t.clipped ? 0.f : -x.adv[k] * (1.f + (t.v + t.rest));
     if (A.ref_logp) g = fmaf(-b, kl_of(x.ref[k] - x.logp[k]).slope, g);
-    if (x.in[k]) {
+    if (exists<FULL>(c, k)) {
       dlogp[k * kPolicyThreads] = x.on[k] ? g * w : 0.f;
       if (dent) dent[k * kPolicyThreads] = x.on[k] ? wh : 0.f;
     }
   }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kPolicyThreads, 6) policy_bwd_kernel(const PolicyArgs A,
+                                                                       const __grid_constant__ SegTable<CAP> seg,
+                                                                       const __grid_constant__ BlockIndex index) {
+  const Chunk c = chunk_of(seg, index, blockIdx.x);
+  if (c.hi - c.lo == kPolicyChunk) token_gradients<true>(A, c);
+  else if (c.lo < c.hi) token_gradients<false>(A, c);
 }
 
 template <int CAP>
@@ -443,6 +473,6 @@ cudaError_t launch_policy(bool backward, const PolicyArgs& a, int N, const int32
                          : launch_policy_c<kMaxSegs>(backward, a, N, off, blocks, st);
 }
 
-size_t policy_workspace_bytes(int N, const int32_t* off) { return (size_t)policy_blocks(N, off) * (sizeof(Record) + sizeof(int)); }
+size_t policy_workspace_bytes(int N, const int32_t* off) { return (size_t)policy_blocks(N, off) * sizeof(Record); }
 
 }  // namespace dkv
