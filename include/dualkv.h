@@ -467,7 +467,8 @@ int dualkv_selftest_kernel(int which, uint64_t limit_ns, void* stream);
  */
 int dualkv_plan_cache_info(int* n_plans, int64_t* device_bytes);
 
-/* Frees the plan cache, status words and timing events.  Not safe while launches are pending. */
+/* Frees the plan cache, status words and timing events.  Not safe while launches are pending; a
+ * CUDA graph that holds calls of this library must not be replayed after it. */
 void dualkv_release(void);
 
 #ifdef __cplusplus

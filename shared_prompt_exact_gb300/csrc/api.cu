@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -498,14 +499,24 @@ bool rows_overlap(const Rows& a, const Rows& b) {
 }
 
 // Whether an output shares a byte with an input or with another output.
-bool outputs_overlap(const std::vector<Rows>& outs, const std::vector<Rows>& ins) {
-  for (size_t i = 0; i < outs.size(); ++i) {
+bool outputs_overlap(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  for (const Rows* o = outs.begin(); o != outs.end(); ++o) {
     for (const Rows& r : ins)
-      if (rows_overlap(outs[i], r)) return true;
-    for (size_t j = 0; j < i; ++j)
-      if (rows_overlap(outs[i], outs[j])) return true;
+      if (rows_overlap(*o, r)) return true;
+    for (const Rows* other = outs.begin(); other != o; ++other)
+      if (rows_overlap(*o, *other)) return true;
   }
   return false;
+}
+
+// Runs an entry point's body; nothing that it might throw (a lock, an allocation) passes the C boundary.
+template <typename F>
+int guarded(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return DUALKV_ERR_CUDA;
+  }
 }
 
 constexpr int64_t kMaxRowStride = int64_t(1) << 31;  // elements: rows x stride x 4 bytes stays far inside 64 bits
@@ -538,18 +549,16 @@ int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int
   if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
     return DUALKV_ERR_WORKSPACE;
   const uint64_t uT = (uint64_t)T, wbytes = (uint64_t)D * (weight_dtype == DUALKV_F32 ? 4 : 2);
-  std::vector<Rows> ins = {Rows{q, (uint64_t)q_stride * 2, (uint64_t)wq * 2, uT},
-                           Rows{k, (uint64_t)k_stride * 2, (uint64_t)wk * 2, uT},
-                           flat(q_weight, wbytes), flat(k_weight, wbytes), flat(inv_freq, (uint64_t)rope_dim * 2),
-                           flat(dq_out, uT * wq * 2), flat(dk_out, uT * wk * 2)};
-  std::vector<Rows> outs = {Rows{q_out, (uint64_t)q_out_stride * 2, (uint64_t)wq * 2, uT},
-                            Rows{k_out, (uint64_t)k_out_stride * 2, (uint64_t)wk * 2, uT}};
-  if (need) {
-    outs.push_back(flat(dq_weight, (uint64_t)D * 4));
-    outs.push_back(flat(dk_weight, (uint64_t)D * 4));
-    outs.push_back(flat(workspace, need));
-  }
-  if (outputs_overlap(outs, ins)) return DUALKV_ERR_INVALID;
+  const Rows none{};
+  if (outputs_overlap({Rows{q_out, (uint64_t)q_out_stride * 2, (uint64_t)wq * 2, uT},
+                       Rows{k_out, (uint64_t)k_out_stride * 2, (uint64_t)wk * 2, uT},
+                       need ? flat(dq_weight, (uint64_t)D * 4) : none, need ? flat(dk_weight, (uint64_t)D * 4) : none,
+                       need ? flat(workspace, need) : none},
+                      {Rows{q, (uint64_t)q_stride * 2, (uint64_t)wq * 2, uT},
+                       Rows{k, (uint64_t)k_stride * 2, (uint64_t)wk * 2, uT}, flat(q_weight, wbytes),
+                       flat(k_weight, wbytes), flat(inv_freq, (uint64_t)rope_dim * 2), flat(dq_out, uT * wq * 2),
+                       flat(dk_out, uT * wk * 2)}))
+    return DUALKV_ERR_INVALID;
   typedef __nv_bfloat16 bf;
   RopeArgs a{static_cast<const bf*>(q), static_cast<const bf*>(k), q_stride, k_stride, static_cast<const bf*>(dq_out),
              static_cast<const bf*>(dk_out), static_cast<bf*>(q_out), static_cast<bf*>(k_out), q_out_stride,
@@ -597,13 +606,10 @@ int logp_impl(bool backward, const void* logits, int64_t row_stride, int dtype, 
     if (dlogits_stride < V || dlogits_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
     if (!aligned_to(dlogits, esz)) return DUALKV_ERR_ALIGN;
     const Rows out{dlogits, (uint64_t)dlogits_stride * esz, (uint64_t)V * esz, uM};
-    std::vector<Rows> ins = {flat(tokens, un * 8), flat(lse, uM * 4), flat(dlogp, un * 4)};
-    if (dentropy) {
-      ins.push_back(flat(entropy, un * 4));
-      ins.push_back(flat(dentropy, un * 4));
-    }
-    if (dlogits != logits || dlogits_stride != row_stride) ins.push_back(in);  // in place, or apart
-    if (outputs_overlap({out}, ins)) return DUALKV_ERR_INVALID;
+    const bool in_place = dlogits == logits && dlogits_stride == row_stride;
+    if (outputs_overlap({out}, {in_place ? Rows{} : in, flat(tokens, un * 8), flat(lse, uM * 4), flat(dlogp, un * 4),
+                                flat(dentropy ? entropy : nullptr, un * 4), flat(dentropy, un * 4)}))
+      return DUALKV_ERR_INVALID;
   }
   LogpArgs a{logits, row_stride, V, scale, tokens, logp, entropy, lse, dlogp, dentropy, dlogits, dlogits_stride, nullptr};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -642,22 +648,25 @@ int policy_impl(bool backward, const float* logp, const float* old_logp, const f
                         (const void*)advantages, (const void*)loss, (const void*)stats, (const void*)weights,
                         (const void*)dloss, (const void*)dlogp, (const void*)dentropy})
     if (!aligned_to(p, 4)) return DUALKV_ERR_ALIGN;
-  std::vector<Rows> ins = {flat(logp, n * 4), flat(old_logp, n * 4), flat(ref_logp, n * 4),
-                           flat(advantages, (per_token ? n : (uint64_t)N) * 4), flat(mask, n)};
-  std::vector<Rows> outs;
+  Rows out[4] = {};
   if (!backward) {
     if (!loss || !stats || (n > 0 && entropy_coef != 0.0 && !entropy)) return DUALKV_ERR_INVALID;
     const size_t need = policy_workspace_bytes(N, R_offsets);
     if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < need) return DUALKV_ERR_WORKSPACE;
-    ins.push_back(flat(entropy, n * 4));
-    outs = {flat(loss, 4), flat(stats, 16), flat(weights, (uint64_t)N * 4), flat(workspace, need)};
+    out[0] = flat(loss, 4);
+    out[1] = flat(stats, 16);
+    out[2] = flat(weights, (uint64_t)N * 4);
+    out[3] = flat(workspace, need);
   } else {
     if (!dloss || (n > 0 && !dlogp)) return DUALKV_ERR_INVALID;
-    ins.push_back(flat(dloss, 4));
-    ins.push_back(flat(weights, (uint64_t)N * 4));
-    outs = {flat(dlogp, n * 4), flat(dentropy, n * 4)};
+    out[0] = flat(dlogp, n * 4);
+    out[1] = flat(dentropy, n * 4);
   }
-  if (outputs_overlap(outs, ins)) return DUALKV_ERR_INVALID;
+  if (outputs_overlap({out[0], out[1], out[2], out[3]},
+                      {flat(logp, n * 4), flat(old_logp, n * 4), flat(ref_logp, n * 4),
+                       flat(advantages, (per_token ? n : (uint64_t)N) * 4), flat(mask, n), flat(entropy, n * 4),
+                       flat(dloss, 4), flat(backward ? weights : nullptr, (uint64_t)N * 4)}))
+    return DUALKV_ERR_INVALID;
   if (backward && n == 0) return DUALKV_OK;
   PolicyArgs a{};
   a.logp = logp;
@@ -979,9 +988,11 @@ int dualkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t 
                         const void* k_weight, int weight_dtype, float weight_offset, float eps, const float* inv_freq,
                         int rope_dim, int interleaved, int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D,
                         void* q_out, void* k_out, void* stream) {
-  return rope_impl(false, q, q_stride, k, k_stride, nullptr, nullptr, q_weight, k_weight, weight_dtype, weight_offset,
-                   eps, inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, q_out, (int64_t)Hq * D, k_out,
-                   (int64_t)Hkv * D, nullptr, nullptr, nullptr, 0, stream);
+  return guarded([&] {
+    return rope_impl(false, q, q_stride, k, k_stride, nullptr, nullptr, q_weight, k_weight, weight_dtype, weight_offset,
+                     eps, inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, q_out, (int64_t)Hq * D, k_out,
+                     (int64_t)Hkv * D, nullptr, nullptr, nullptr, 0, stream);
+  });
 }
 
 size_t dualkv_qk_norm_rope_bwd_workspace_bytes(int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D) {
@@ -995,24 +1006,30 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
                             int N, const int32_t* R_offsets, int Hq, int Hkv, int D, void* dq, int64_t dq_stride,
                             void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight, void* workspace,
                             size_t workspace_bytes, void* stream) {
-  return rope_impl(true, q, q_stride, k, k_stride, dq_out, dk_out, q_weight, k_weight, weight_dtype, weight_offset, eps,
-                   inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dq_stride, dk, dk_stride,
-                   dq_weight, dk_weight, workspace, workspace_bytes, stream);
+  return guarded([&] {
+    return rope_impl(true, q, q_stride, k, k_stride, dq_out, dk_out, q_weight, k_weight, weight_dtype, weight_offset, eps,
+                     inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq, Hkv, D, dq, dq_stride, dk, dk_stride,
+                     dq_weight, dk_weight, workspace, workspace_bytes, stream);
+  });
 }
 
 int dualkv_token_logprobs(const void* logits, int64_t row_stride, int dtype, int V, float scale, const int64_t* tokens,
                           int P, int N, const int32_t* R_offsets, float* logp, float* entropy, float* lse, void* stream) {
-  return logp_impl(false, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, logp, entropy, lse, nullptr,
-                   nullptr, nullptr, 0, stream);
+  return guarded([&] {
+    return logp_impl(false, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, logp, entropy, lse, nullptr,
+                     nullptr, nullptr, 0, stream);
+  });
 }
 
 int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype, int V, float scale,
                               const int64_t* tokens, int P, int N, const int32_t* R_offsets, const float* lse,
                               const float* entropy, const float* dlogp, const float* dentropy, void* dlogits,
                               int64_t dlogits_stride, void* stream) {
-  return logp_impl(true, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, nullptr,
-                   const_cast<float*>(entropy), const_cast<float*>(lse), dlogp, dentropy, dlogits, dlogits_stride,
-                   stream);
+  return guarded([&] {
+    return logp_impl(true, logits, row_stride, dtype, V, scale, tokens, P, N, R_offsets, nullptr,
+                     const_cast<float*>(entropy), const_cast<float*>(lse), dlogp, dentropy, dlogits, dlogits_stride,
+                     stream);
+  });
 }
 
 size_t dualkv_policy_loss_workspace_bytes(int N, const int32_t* R_offsets) {
@@ -1024,18 +1041,22 @@ int dualkv_policy_loss(const float* logp, const float* old_logp, const float* re
                        double clip_low, double clip_high, double dual_clip, double kl_coef, double entropy_coef,
                        int reduction, float* loss, float* stats, float* weights, void* workspace,
                        size_t workspace_bytes, void* stream) {
-  return policy_impl(false, logp, old_logp, ref_logp, entropy, advantages, per_token, mask, N, R_offsets, clip_low,
-                     clip_high, dual_clip, kl_coef, entropy_coef, reduction, loss, stats, weights, workspace,
-                     workspace_bytes, nullptr, nullptr, nullptr, stream);
+  return guarded([&] {
+    return policy_impl(false, logp, old_logp, ref_logp, entropy, advantages, per_token, mask, N, R_offsets, clip_low,
+                       clip_high, dual_clip, kl_coef, entropy_coef, reduction, loss, stats, weights, workspace,
+                       workspace_bytes, nullptr, nullptr, nullptr, stream);
+  });
 }
 
 int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float* ref_logp, const float* advantages,
                            int per_token, const uint8_t* mask, int N, const int32_t* R_offsets, double clip_low,
                            double clip_high, double dual_clip, double kl_coef, double entropy_coef, const float* dloss,
                            const float* weights, float* dlogp, float* dentropy, void* stream) {
-  return policy_impl(true, logp, old_logp, ref_logp, nullptr, advantages, per_token, mask, N, R_offsets, clip_low,
-                     clip_high, dual_clip, kl_coef, entropy_coef, DUALKV_LOSS_TOKEN_MEAN, nullptr, nullptr,
-                     const_cast<float*>(weights), nullptr, 0, dloss, dlogp, dentropy, stream);
+  return guarded([&] {
+    return policy_impl(true, logp, old_logp, ref_logp, nullptr, advantages, per_token, mask, N, R_offsets, clip_low,
+                       clip_high, dual_clip, kl_coef, entropy_coef, DUALKV_LOSS_TOKEN_MEAN, nullptr, nullptr,
+                       const_cast<float*>(weights), nullptr, 0, dloss, dlogp, dentropy, stream);
+  });
 }
 
 int dualkv_check_status(void* stream) {

@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kLogpThreads, 4) logp_fwd_kernel(const LogpArg
   if (parts > 1) {
     __shared__ Running joined[kMaxParts];
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();  // the first block has to run before its memory is written
     if (tid == 0) *cluster.map_shared_rank(&joined[rank], 0) = r;
     cluster.sync();
     if (rank) return;

@@ -32,6 +32,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "kernels.h"
 #include "segs.cuh"
 
@@ -384,8 +386,10 @@ __global__ void __launch_bounds__(kPolicyThreads, 6) policy_cluster_kernel(const
   __shared__ Record rec[kClusterBlocks];
   __shared__ int live[kClusterBlocks];  // no more segments than blocks
   cg::cluster_group cluster = cg::this_cluster();
+  auto started = cluster.barrier_arrive();  // the first block has to run before its memory is written
   const Chunk c = chunk_of(seg, index, blockIdx.x);
   const Record r = chunk_record(A, c);
+  cluster.barrier_wait(std::move(started));
   if (threadIdx.x == 0) {
     *cluster.map_shared_rank(&rec[blockIdx.x], 0) = r;
     if (blockIdx.x == 0)

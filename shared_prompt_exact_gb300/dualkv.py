@@ -387,16 +387,19 @@ def offsets(R_offsets: Sequence[int]):
 
 
 # ------------------------------------------------------------------ per-token operators
-_WEIGHT_DTYPES = {torch.bfloat16: DUALKV_BF16, torch.float32: DUALKV_F32}
+_DTYPE_CODES = {torch.bfloat16: DUALKV_BF16, torch.float32: DUALKV_F32}
+_BF16, _F32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int64,)
+_MASK_DTYPES = (torch.bool, torch.uint8)
+_Tensor = torch.Tensor
 
 
-def _check_tensor(where, name, t, shape, dtypes, device, rows=False):
-    """A CUDA tensor on the calling thread's current device with this shape and one of these dtypes: contiguous, or
-    (rows) only contiguous within a row of its first dimension."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_cuda
-            and t.get_device() == device and (t.is_contiguous() or (rows and _rows_contiguous(t)))):
-        return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _arg(where, name, t, shape, dtypes, device, rows=False):
+    """Address of a CUDA tensor on the calling thread's current device, with this shape and one of these dtypes,
+    contiguous or (rows) only contiguous within a row of its first dimension.  Raises if it is none."""
+    if (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == device
+            and (t.is_contiguous() or (rows and _rows_contiguous(t)))):
+        return t.data_ptr()
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{where}: {name} must be a CUDA tensor")
     if t.get_device() != device:
         raise ValueError(f"{where}: {name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
@@ -405,6 +408,11 @@ def _check_tensor(where, name, t, shape, dtypes, device, rows=False):
     if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)} for this call, got {tuple(t.shape)}")
     raise ValueError(f"{where}: {name} must be contiguous" + (" within its rows" if rows else ""))
+
+
+def _opt(where, name, t, shape, dtypes, device):
+    """The same for a tensor that may be missing."""
+    return None if t is None else _arg(where, name, t, shape, dtypes, device)
 
 
 def _rows_contiguous(t):
@@ -430,34 +438,36 @@ def _stream_of(stream, device):
     return _stream(stream)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 def _layout_rows(where, P, N, R_offsets):
-    N = int(N)
+    """Packed rows of a layout."""
+    P, N = int(P), int(N)
     if N < 1 or len(R_offsets) != N + 1:
         raise ValueError(f"{where}: R_offsets must hold N + 1 = {N + 1} entries, got {len(R_offsets)}")
-    return int(P) + int(R_offsets[N])
+    if not 0 <= P < 1 << 31:
+        raise ValueError(f"{where}: P must be a count of tokens, got {P}")
+    return P + int(R_offsets[N])
 
 
-def _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D):
-    """Checks shared by the forward and the backward; returns (T, device, the C call's weight dtype)."""
+def _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq,
+               Hkv, D):
+    """Checks shared by the forward and the backward; returns (rows, device, q and k as the C call takes them, the
+    arguments from the weights to D)."""
     T = _layout_rows(where, P, N, R_offsets)
     dev = torch.cuda.current_device()
-    bf = (torch.bfloat16,)
-    _check_tensor(where, "q", q, (T, Hq, D), bf, dev, rows=True)
-    _check_tensor(where, "k", k, (T, Hkv, D), bf, dev, rows=True)
+    qk = (_arg(where, "q", q, (T, Hq, D), _BF16, dev, True), _row_stride(q),
+          _arg(where, "k", k, (T, Hkv, D), _BF16, dev, True), _row_stride(k))
     if (q_weight is None) != (k_weight is None):
         raise ValueError(f"{where}: q_weight and k_weight go together")
-    wd = DUALKV_F32
+    qw = kw = None
+    code = DUALKV_F32
     if q_weight is not None:
-        _check_tensor(where, "q_weight", q_weight, (D,), tuple(_WEIGHT_DTYPES), dev)
-        _check_tensor(where, "k_weight", k_weight, (D,), (q_weight.dtype,), dev)
-        wd = _WEIGHT_DTYPES[q_weight.dtype]
-    if int(rope_dim):
-        _check_tensor(where, "inv_freq", inv_freq, (int(rope_dim) // 2,), (torch.float32,), dev)
-    return T, dev, wd
+        qw = _arg(where, "q_weight", q_weight, (D,), _DTYPE_CODES, dev)
+        kw = _arg(where, "k_weight", k_weight, (D,), (q_weight.dtype,), dev)
+        code = _DTYPE_CODES[q_weight.dtype]
+    rope_dim = int(rope_dim)
+    f = _arg(where, "inv_freq", inv_freq, (rope_dim // 2,), _F32, dev) if rope_dim else None
+    return T, dev, qk, (qw, kw, code, float(weight_offset), float(eps), f, rope_dim, 1 if interleaved else 0, int(P),
+                        int(N), _offsets(R_offsets), int(Hq), int(Hkv), int(D))
 
 
 def dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P, N, R_offsets,
@@ -465,13 +475,10 @@ def dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, 
     """Per-head RMS norm and position rotation of packed q [T, Hq, D] and k [T, Hkv, D] (rows may be strided, as
     columns of a fused projection are) into the contiguous q_out, k_out that dualkv_fwd reads."""
     where = "dualkv_qk_norm_rope"
-    T, dev, wd = _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D)
-    _check_tensor(where, "q_out", q_out, (T, Hq, D), (torch.bfloat16,), dev)
-    _check_tensor(where, "k_out", k_out, (T, Hkv, D), (torch.bfloat16,), dev)
-    rc = load().dualkv_qk_norm_rope(_at(q), _row_stride(q), _at(k), _row_stride(k), _at(q_weight), _at(k_weight), wd,
-                                    float(weight_offset), float(eps), _at(inv_freq), int(rope_dim),
-                                    1 if interleaved else 0, int(P), int(N), _offsets(R_offsets), int(Hq), int(Hkv),
-                                    int(D), _at(q_out), _at(k_out), _stream_of(stream, dev))
+    T, dev, qk, args = _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P,
+                                  N, R_offsets, Hq, Hkv, D)
+    rc = load().dualkv_qk_norm_rope(*qk, *args, _arg(where, "q_out", q_out, (T, Hq, D), _BF16, dev),
+                                    _arg(where, "k_out", k_out, (T, Hkv, D), _BF16, dev), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -485,55 +492,40 @@ def dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_off
                             stream=None) -> None:
     """Gradients of dualkv_qk_norm_rope: dq, dk (rows may be strided) and, with weights, dq_weight, dk_weight."""
     where = "dualkv_qk_norm_rope_bwd"
-    T, dev, wd = _check_rope(where, q, k, q_weight, k_weight, inv_freq, rope_dim, P, N, R_offsets, Hq, Hkv, D)
-    bf = (torch.bfloat16,)
-    _check_tensor(where, "dq_out", dq_out, (T, Hq, D), bf, dev)
-    _check_tensor(where, "dk_out", dk_out, (T, Hkv, D), bf, dev)
-    _check_tensor(where, "dq", dq, (T, Hq, D), bf, dev, rows=True)
-    _check_tensor(where, "dk", dk, (T, Hkv, D), bf, dev, rows=True)
+    T, dev, qk, args = _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P,
+                                  N, R_offsets, Hq, Hkv, D)
+    up = (_arg(where, "dq_out", dq_out, (T, Hq, D), _BF16, dev), _arg(where, "dk_out", dk_out, (T, Hkv, D), _BF16, dev))
+    out = (_arg(where, "dq", dq, (T, Hq, D), _BF16, dev, True), _row_stride(dq),
+           _arg(where, "dk", dk, (T, Hkv, D), _BF16, dev, True), _row_stride(dk))
+    gw = (None, None)
     if q_weight is not None:
-        _check_tensor(where, "dq_weight", dq_weight, (D,), (torch.float32,), dev)
-        _check_tensor(where, "dk_weight", dk_weight, (D,), (torch.float32,), dev)
-    workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
-    rc = load().dualkv_qk_norm_rope_bwd(_at(q), _row_stride(q), _at(k), _row_stride(k), _at(dq_out), _at(dk_out),
-                                        _at(q_weight), _at(k_weight), wd, float(weight_offset), float(eps),
-                                        _at(inv_freq), int(rope_dim), 1 if interleaved else 0, int(P), int(N),
-                                        _offsets(R_offsets), int(Hq), int(Hkv), int(D), _at(dq), _row_stride(dq),
-                                        _at(dk), _row_stride(dk), _at(dq_weight), _at(dk_weight), _at(workspace),
-                                        workspace_bytes, _stream_of(stream, dev))
+        gw = (_arg(where, "dq_weight", dq_weight, (D,), _F32, dev), _arg(where, "dk_weight", dk_weight, (D,), _F32, dev))
+    rc = load().dualkv_qk_norm_rope_bwd(*qk, *up, *args, *out, *gw,
+                                        *_workspace_args(where, workspace, workspace_bytes, dev), _stream_of(stream, dev))
     _raise(rc, where)
 
 
-def _check_logits(where, logits, tokens, P, N, R_offsets):
-    """Checks shared by the forward and the backward; returns (rows, tokens, device)."""
-    n = _layout_rows(where, 0, N, R_offsets)
-    M = n + (1 if int(P) > 0 else 0)
+def _logits_args(where, logits, tokens, scale, P, N, R_offsets):
+    """Checks shared by the forward and the backward; returns (rows, tokens, device, the arguments up to R_offsets)."""
+    n = _layout_rows(where, P, N, R_offsets) - int(P)
+    M = n + 1 if int(P) > 0 else n
     dev = torch.cuda.current_device()
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+    if not isinstance(logits, _Tensor) or logits.dim() != 2:
         raise ValueError(f"{where}: logits must be a tensor of rows")
-    _check_tensor(where, "logits", logits, (M, logits.shape[1]), tuple(_WEIGHT_DTYPES), dev, rows=True)
-    _check_tensor(where, "tokens", tokens, (n,), (torch.int64,), dev)
-    return M, n, dev
-
-
-def _check_floats(where, dev, shape, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _check_tensor(where, name, t, shape, (torch.float32,), dev)
+    V = logits.shape[1]
+    return M, n, dev, (_arg(where, "logits", logits, (M, V), _DTYPE_CODES, dev, True), _row_stride(logits),
+                       _DTYPE_CODES[logits.dtype], V, float(scale), _arg(where, "tokens", tokens, (n,), _I64, dev),
+                       int(P), int(N), _offsets(R_offsets))
 
 
 def dualkv_token_logprobs(logits, tokens, scale, P, N, R_offsets, logp, entropy, lse, stream=None) -> None:
     """Log-probabilities (and, unless None, entropies) of the response tokens from the logits of packed rows
     P - 1 .. T - 1 (all rows if P = 0); lse, unless None, gets each row's log-sum-exp."""
     where = "dualkv_token_logprobs"
-    M, n, dev = _check_logits(where, logits, tokens, P, N, R_offsets)
-    if logp is None:
-        raise ValueError(f"{where}: logp is missing")
-    _check_floats(where, dev, (n,), logp=logp, entropy=entropy)
-    _check_floats(where, dev, (M,), lse=lse)
-    rc = load().dualkv_token_logprobs(_at(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype], logits.shape[1],
-                                      float(scale), _at(tokens), int(P), int(N), _offsets(R_offsets), _at(logp),
-                                      _at(entropy), _at(lse), _stream_of(stream, dev))
+    M, n, dev, args = _logits_args(where, logits, tokens, scale, P, N, R_offsets)
+    rc = load().dualkv_token_logprobs(*args, _arg(where, "logp", logp, (n,), _F32, dev),
+                                      _opt(where, "entropy", entropy, (n,), _F32, dev),
+                                      _opt(where, "lse", lse, (M,), _F32, dev), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -541,33 +533,37 @@ def dualkv_token_logprobs_bwd(logits, tokens, scale, P, N, R_offsets, lse, entro
                               stream=None) -> None:
     """Gradient of the logits from dlogp (and, unless None, dentropy); dlogits may be logits itself."""
     where = "dualkv_token_logprobs_bwd"
-    M, n, dev = _check_logits(where, logits, tokens, P, N, R_offsets)
-    if lse is None or dlogp is None or (dentropy is not None and entropy is None):
-        raise ValueError(f"{where}: lse and dlogp are needed, and entropy with dentropy")
-    _check_floats(where, dev, (n,), dlogp=dlogp, dentropy=dentropy, entropy=entropy)
-    _check_floats(where, dev, (M,), lse=lse)
-    _check_tensor(where, "dlogits", dlogits, logits.shape, (logits.dtype,), dev, rows=True)
-    rc = load().dualkv_token_logprobs_bwd(_at(logits), _row_stride(logits), _WEIGHT_DTYPES[logits.dtype],
-                                          logits.shape[1], float(scale), _at(tokens), int(P), int(N),
-                                          _offsets(R_offsets), _at(lse), _at(entropy), _at(dlogp), _at(dentropy),
-                                          _at(dlogits), _row_stride(dlogits), _stream_of(stream, dev))
+    M, n, dev, args = _logits_args(where, logits, tokens, scale, P, N, R_offsets)
+    if dentropy is not None and entropy is None:
+        raise ValueError(f"{where}: dentropy needs entropy")
+    rc = load().dualkv_token_logprobs_bwd(*args, _arg(where, "lse", lse, (M,), _F32, dev),
+                                          _opt(where, "entropy", entropy, (n,), _F32, dev),
+                                          _arg(where, "dlogp", dlogp, (n,), _F32, dev),
+                                          _opt(where, "dentropy", dentropy, (n,), _F32, dev),
+                                          _arg(where, "dlogits", dlogits, logits.shape, (logits.dtype,), dev, True),
+                                          _row_stride(dlogits), _stream_of(stream, dev))
     _raise(rc, where)
 
 
-def _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction, per_token):
-    """Checks shared by the forward and the backward; returns (tokens, device, per-token advantages)."""
+def _policy_args(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, clip_low, clip_high, dual_clip, kl_coef,
+                 entropy_coef, reduction, per_token):
+    """Checks shared by the forward and the backward; returns (tokens, device, the log-probabilities, the arguments
+    from the advantages to the coefficients)."""
     n = _layout_rows(where, 0, N, R_offsets)
     dev = torch.cuda.current_device()
     if reduction not in LOSS_REDUCTIONS:
         raise ValueError(f"{where}: reduction must be one of {tuple(LOSS_REDUCTIONS)}, got {reduction!r}")
-    if logp is None or old_logp is None or advantages is None or (float(kl_coef) != 0.0 and ref_logp is None):
-        raise ValueError(f"{where}: logp, old_logp and advantages are needed, and ref_logp with kl_coef")
-    _check_floats(where, dev, (n,), logp=logp, old_logp=old_logp, ref_logp=ref_logp)
+    kl_coef = float(kl_coef)
+    if kl_coef != 0.0 and ref_logp is None:
+        raise ValueError(f"{where}: kl_coef needs ref_logp")
+    shape = (n,)
+    probs = (_arg(where, "logp", logp, shape, _F32, dev), _arg(where, "old_logp", old_logp, shape, _F32, dev),
+             _opt(where, "ref_logp", ref_logp, shape, _F32, dev))
+    N = int(N)
     per_token = _per_token(where, advantages, N, n, R_offsets, per_token)
-    _check_floats(where, dev, (n if per_token else int(N),), advantages=advantages)
-    if mask is not None:
-        _check_tensor(where, "mask", mask, (n,), (torch.bool, torch.uint8), dev)
-    return n, dev, per_token
+    adv = _arg(where, "advantages", advantages, shape if per_token else (N,), _F32, dev)
+    return n, dev, probs, (adv, per_token, _opt(where, "mask", mask, shape, _MASK_DTYPES, dev), N, _offsets(R_offsets),
+                           float(clip_low), float(clip_high), float(dual_clip), kl_coef, float(entropy_coef))
 
 
 def _per_token(where, advantages, N, n, R_offsets, per_token):
@@ -575,11 +571,11 @@ def _per_token(where, advantages, N, n, R_offsets, per_token):
     A length that fits both ways in a layout where it makes a difference has to be told."""
     if per_token is not None:
         return 1 if per_token else 0
-    if not isinstance(advantages, torch.Tensor) or advantages.dim() != 1:
+    if not isinstance(advantages, _Tensor) or advantages.dim() != 1:
         raise ValueError(f"{where}: advantages must be a tensor of one dimension")
-    if n == int(N) and any(int(R_offsets[i]) != i for i in range(n)):
+    if n == N and any(int(R_offsets[i]) != i for i in range(n)):
         raise ValueError(f"{where}: {n} advantages for {n} segments of {n} tokens in all: pass per_token")
-    return 1 if advantages.shape[0] != int(N) else 0
+    return 1 if advantages.shape[0] != N else 0
 
 
 def dualkv_policy_loss_workspace_bytes(N, R_offsets) -> int:
@@ -592,20 +588,15 @@ def dualkv_policy_loss(logp, old_logp, ref_logp, entropy, advantages, mask, N, R
     """Clipped policy loss with a KL term and an entropy bonus over packed response tokens.  advantages: [N], or one
     per token (per_token, by default told from the length)."""
     where = "dualkv_policy_loss"
-    n, dev, per_token = _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction,
-                                      per_token)
+    n, dev, probs, args = _policy_args(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, clip_low,
+                                       clip_high, dual_clip, kl_coef, entropy_coef, reduction, per_token)
     if float(entropy_coef) != 0.0 and entropy is None:
         raise ValueError(f"{where}: entropy_coef needs entropy")
-    _check_floats(where, dev, (n,), entropy=entropy)
-    _check_tensor(where, "loss", loss, (1,), (torch.float32,), dev)
-    _check_tensor(where, "stats", stats, (4,), (torch.float32,), dev)
-    _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
-    workspace_bytes = _workspace_bytes(where, workspace, workspace_bytes, dev)
-    rc = load().dualkv_policy_loss(_at(logp), _at(old_logp), _at(ref_logp), _at(entropy), _at(advantages), per_token,
-                                   _at(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
-                                   float(dual_clip), float(kl_coef), float(entropy_coef), LOSS_REDUCTIONS[reduction],
-                                   _at(loss), _at(stats), _at(weights), _at(workspace), workspace_bytes,
-                                   _stream_of(stream, dev))
+    rc = load().dualkv_policy_loss(*probs, _opt(where, "entropy", entropy, (n,), _F32, dev), *args,
+                                   LOSS_REDUCTIONS[reduction], _arg(where, "loss", loss, (1,), _F32, dev),
+                                   _arg(where, "stats", stats, (4,), _F32, dev),
+                                   _arg(where, "weights", weights, (int(N),), _F32, dev),
+                                   *_workspace_args(where, workspace, workspace_bytes, dev), _stream_of(stream, dev))
     _raise(rc, where)
 
 
@@ -614,36 +605,29 @@ def dualkv_policy_loss_bwd(logp, old_logp, ref_logp, advantages, mask, N, R_offs
                            per_token=None) -> None:
     """Gradients of dualkv_policy_loss: dlogp and, unless None, dentropy (the reduction is in weights)."""
     where = "dualkv_policy_loss_bwd"
-    n, dev, per_token = _check_policy(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, kl_coef, reduction,
-                                      per_token)
-    if dlogp is None:
-        raise ValueError(f"{where}: dlogp is missing")
-    _check_floats(where, dev, (n,), dlogp=dlogp, dentropy=dentropy)
-    if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
+    n, dev, probs, args = _policy_args(where, logp, old_logp, ref_logp, advantages, mask, N, R_offsets, clip_low,
+                                       clip_high, dual_clip, kl_coef, entropy_coef, reduction, per_token)
+    if not isinstance(dloss, _Tensor) or dloss.numel() != 1:
         raise ValueError(f"{where}: dloss must be a tensor of one value")
-    _check_tensor(where, "dloss", dloss, dloss.shape, (torch.float32,), dev)
-    _check_tensor(where, "weights", weights, (int(N),), (torch.float32,), dev)
-    rc = load().dualkv_policy_loss_bwd(_at(logp), _at(old_logp), _at(ref_logp), _at(advantages), per_token,
-                                       _at(mask), int(N), _offsets(R_offsets), float(clip_low), float(clip_high),
-                                       float(dual_clip), float(kl_coef), float(entropy_coef), _at(dloss), _at(weights),
-                                       _at(dlogp), _at(dentropy), _stream_of(stream, dev))
+    rc = load().dualkv_policy_loss_bwd(*probs, *args, _arg(where, "dloss", dloss, dloss.shape, _F32, dev),
+                                       _arg(where, "weights", weights, (int(N),), _F32, dev),
+                                       _arg(where, "dlogp", dlogp, (n,), _F32, dev),
+                                       _opt(where, "dentropy", dentropy, (n,), _F32, dev), _stream_of(stream, dev))
     _raise(rc, where)
 
 
-def _workspace_bytes(where, workspace, workspace_bytes, device):
-    """Bytes of a workspace tensor (0 for None); no more than it holds may be claimed."""
+def _workspace_args(where, workspace, workspace_bytes, device):
+    """(address, bytes) of a workspace tensor, (None, 0) for None; no more than it holds may be claimed."""
     if workspace is None:
-        return 0
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        return None, 0
+    if not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor")
     if workspace.get_device() != device:
         raise ValueError(f"{where}: workspace is on cuda:{workspace.get_device()}, the current device is cuda:{device}")
     held = workspace.numel() * workspace.element_size()
-    if workspace_bytes is None:
-        return held
-    if int(workspace_bytes) > held:
+    if workspace_bytes is not None and int(workspace_bytes) > held:
         raise ValueError(f"{where}: workspace holds {held} bytes, not {workspace_bytes}")
-    return int(workspace_bytes)
+    return workspace.data_ptr(), held if workspace_bytes is None else int(workspace_bytes)
 
 
 def dualkv_build_index(P, N, R_offsets):
