@@ -15,7 +15,7 @@
 // Policy terms of either sign cancel in the sum, so each is summed as -A and -A (ratio - 1): -A is
 // exact, ratio - 1 comes from the same series as the KL term, and the sums keep their rounding
 // errors beside them.  fp64 would do the same, but its adds run at two lanes per clock and SM
-// here: with fp64 trees a call on 4M tokens took 172 us instead of 39.
+// here: with fp64 trees a call on 4M tokens took 172 us instead of 33.
 //
 // A block takes up to kPolicyChunk tokens of ONE segment, all of whose loads are issued before
 // the first is used, and makes one record of sums; a single block then turns the records into
@@ -25,16 +25,18 @@
 // memory; more write them to the workspace for a second launch.
 //
 // Up to some 100,000 tokens a call is launch latency (6 to 9 us in a graph).  At 4.04M tokens
-// (1,024 responses, every input in use) the forward takes 39 us, 2.2 TB/s, 7 of them the join, and
-// is bound by issue (about 200 instructions a token and warp) and memory latency together; the
-// gradients take 28 us, 3.6 TB/s.  Four tokens a thread in chunks of 1,024 beat eight in 2,048
-// (40 against 46 us cold): more resident threads outweigh fewer blocks.
+// (1,024 responses, every input in use) the forward takes 33 us, 2.6 TB/s, 6 of them the join,
+// and the gradients 24 us, 4.2 TB/s.  The sums are bound by the comparisons and selects around the
+// bounds (the ALU pipe is 68 % busy) and memory latency together; the arithmetic is on f32x2
+// pairs of tokens, which took a tenth off both.  Four tokens a thread in chunks of 1,024 beat
+// eight in 2,048 (40 against 46 us cold): more resident threads outweigh fewer blocks.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <utility>
 
 #include "kernels.h"
+#include "ptx.cuh"
 #include "segs.cuh"
 
 namespace dkv {
@@ -120,60 +122,92 @@ __device__ __forceinline__ Chunk chunk_of(const SegTable<CAP>& s, const BlockInd
   return Chunk{lo, (int)begin, (int)(begin + kPolicyChunk < end ? begin + kPolicyChunk : end)};
 }
 
+// Arithmetic below is on pairs of tokens (f32x2).
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 pick(bool x, bool y, float a, float b) { return make_float2(x ? a : b, y ? a : b); }
+
 // a - b as the rounded difference and what rounding took away (finite even where the difference is not).
-__device__ __forceinline__ float exact_diff(float a, float b, float* err) {
-  const float d = a - b, bb = d - a;
-  const float e = (a - (d - bb)) - (b + bb);
-  *err = fmaxf(e, -1e30f);  // not NaN
+__device__ __forceinline__ float2 exact_diff(float2 a, float2 b, float2* err) {
+  const float2 d = fsub2(a, b), bb = fsub2(d, a);
+  const float2 e = fsub2(fsub2(a, fsub2(d, bb)), fadd2(b, bb));
+  *err = make_float2(fmaxf(e.x, -1e30f), fmaxf(e.y, -1e30f));  // not NaN
   return d;
 }
 // The sign of (d + e) - t: d - t.hi is exact where the two are close, and elsewhere larger than the rest.
-__device__ __forceinline__ float beyond(float d, float e, const Bound& t) { return (d - t.hi) + (e - t.lo); }
-
-// e^x - x - 1 and e^x - 1: by the series of the former below |x| = 1, where differences would cancel.
-struct Kl {
-  float kl, slope;
-};
-__device__ __forceinline__ Kl kl_of(float x) {
-  if (!(fabsf(x) < 1.f)) {
-    const float q = expf(x) - 1.f;
-    return Kl{q - x, q};
-  }
-  float p = 1.f / 39916800.f;
-  p = fmaf(p, x, 1.f / 3628800.f);
-  p = fmaf(p, x, 1.f / 362880.f);
-  p = fmaf(p, x, 1.f / 40320.f);
-  p = fmaf(p, x, 1.f / 5040.f);
-  p = fmaf(p, x, 1.f / 720.f);
-  p = fmaf(p, x, 1.f / 120.f);
-  p = fmaf(p, x, 1.f / 24.f);
-  p = fmaf(p, x, 1.f / 6.f);
-  p = fmaf(p, x, 0.5f) * x * x;
-  return Kl{p, p + x};
+__device__ __forceinline__ float2 beyond(float2 d, float2 e, float2 hi, float2 lo) {
+  return fadd2(fsub2(d, hi), fsub2(e, lo));
 }
 
-// A token's bounded ratio less 1, as v + rest, and whether it is a bound.  The difference from 1 is
-// kept apart because policy terms of either sign cancel: -A (1 + v + rest) is then summed from -A,
-// which is exact, and two products of small factors.
-struct Term {
-  float v, rest;
-  bool clipped;
+// e^x - x - 1 for |x| < 1 (its series; the difference itself would cancel).
+__device__ __forceinline__ float2 series(float2 x) {
+  float2 p = both(1.f / 39916800.f);
+  p = ffma2(p, x, both(1.f / 3628800.f));
+  p = ffma2(p, x, both(1.f / 362880.f));
+  p = ffma2(p, x, both(1.f / 40320.f));
+  p = ffma2(p, x, both(1.f / 5040.f));
+  p = ffma2(p, x, both(1.f / 720.f));
+  p = ffma2(p, x, both(1.f / 120.f));
+  p = ffma2(p, x, both(1.f / 24.f));
+  p = ffma2(p, x, both(1.f / 6.f));
+  p = ffma2(p, x, both(0.5f));
+  return fmul2(fmul2(p, x), x);
+}
+__device__ __forceinline__ bool far(float2 x) { return !(fmaxf(fabsf(x.x), fabsf(x.y)) < 1.f); }
+
+// e^x - x - 1 and e^x - 1.
+struct Kl {
+  float2 kl, slope;
 };
-__device__ __forceinline__ Term term_of(const PolicyArgs& A, float logp, float old, float adv) {
-  float e;
-  const float d = exact_diff(logp, old, &e);
-  const Kl k = kl_of(d);  // e^d - d - 1
-  const bool near = fabsf(d) < 1.f;
-  Term t{near ? d : k.slope, near ? k.kl + e : 0.f, false};
-  const bool gain = adv > 0.f, loss = adv < 0.f;
-  const float x = beyond(d, e, Bound{gain ? A.up.hi : A.down.hi, gain ? A.up.lo : A.down.lo});
-  t.clipped = gain ? x > 0.f : loss && x < 0.f;
-  if (t.clipped) {
-    t.v = gain ? A.add_up.hi : A.add_down.hi;
-    t.rest = gain ? A.add_up.lo : A.add_down.lo;
+__device__ __forceinline__ Kl kl_of(float2 x) {
+  Kl r;
+  r.kl = series(x);
+  r.slope = fadd2(r.kl, x);
+  if (far(x)) {
+    auto direct = [](float v, float& kl, float& slope) {
+      if (fabsf(v) < 1.f) return;
+      slope = expf(v) - 1.f;
+      kl = slope - v;
+    };
+    direct(x.x, r.kl.x, r.slope.x);
+    direct(x.y, r.kl.y, r.slope.y);
   }
-  if (A.has_dual && loss && beyond(d, e, A.dual) > 0.f) t = Term{A.add_dual.hi, A.add_dual.lo, true};
-  if (adv == 0.f) t.v = t.rest = 0.f;  // not 0 * inf
+  return r;
+}
+
+// Two tokens' bounded ratios less 1, as v + rest, and whether they are bounds.  The difference from
+// 1 is kept apart because policy terms of either sign cancel: A (1 + v + rest) is then summed from
+// A, which is exact, and two products of small factors.
+struct Term {
+  float2 v, rest;
+  bool clipped_x, clipped_y;
+};
+__device__ __forceinline__ Term term_of(const PolicyArgs& A, float2 logp, float2 old, float2 adv) {
+  float2 e;
+  const float2 d = exact_diff(logp, old, &e);
+  Term t;
+  t.v = d;
+  t.rest = fadd2(series(d), e);  // e^d - 1 = d + series
+  if (far(d)) {
+    auto direct = [](float x, float a, float& v, float& rest) {
+      if (fabsf(x) < 1.f) return;
+      v = a == 0.f ? 0.f : expf(x) - 1.f;  // not 0 * inf
+      rest = 0.f;
+    };
+    direct(d.x, adv.x, t.v.x, t.rest.x);
+    direct(d.y, adv.y, t.v.y, t.rest.y);
+  }
+  const bool gx = adv.x > 0.f, gy = adv.y > 0.f, lx = adv.x < 0.f, ly = adv.y < 0.f;
+  const float2 x = beyond(d, e, pick(gx, gy, A.up.hi, A.down.hi), pick(gx, gy, A.up.lo, A.down.lo));
+  t.clipped_x = gx ? x.x > 0.f : lx && x.x < 0.f;
+  t.clipped_y = gy ? x.y > 0.f : ly && x.y < 0.f;
+  const float2 bv = pick(gx, gy, A.add_up.hi, A.add_down.hi), br = pick(gx, gy, A.add_up.lo, A.add_down.lo);
+  if (t.clipped_x) t.v.x = bv.x, t.rest.x = br.x;
+  if (t.clipped_y) t.v.y = bv.y, t.rest.y = br.y;
+  if (A.has_dual) {
+    const float2 far_up = beyond(d, e, both(A.dual.hi), both(A.dual.lo));
+    if (lx && far_up.x > 0.f) t.v.x = A.add_dual.hi, t.rest.x = A.add_dual.lo, t.clipped_x = true;
+    if (ly && far_up.y > 0.f) t.v.y = A.add_dual.hi, t.rest.y = A.add_dual.lo, t.clipped_y = true;
+  }
   return t;
 }
 
@@ -215,7 +249,7 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
     v = add(v, Sum2{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
-// A thread's share of its chunk's sums.
+// A thread's share of its chunk's sums; policy: of A ratio, whose sign the join turns.
 struct Partial {
   Sum2 policy;
   float kl, ent;
@@ -225,22 +259,31 @@ template <bool FULL>
 __device__ __forceinline__ Partial sum_tokens(const PolicyArgs& A, const Chunk& c) {
   Tokens x;
   load_tokens<FULL, true>(A, c, x);
-  Partial r{{0.f, 0.f}, 0.f, 0.f, 0u};
+  const float2 zero = both(0.f);
+  float2 hi = zero, lo = zero, kl = zero, ent = zero;
+  uint32_t counts = 0;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
+  for (int k = 0; k < kPerThread; k += 2) {
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;  // the same for the whole block
-    const Term t = term_of(A, x.logp[k], x.old[k], x.adv[k]);
-    const float v = A.ref_logp ? kl_of(x.ref[k] - x.logp[k]).kl : 0.f;
-    if (x.on[k]) {
-      const float a = -x.adv[k], p = a * t.v, y = a + p;
-      // the errors of the product, of the sum (|v| <= 1 but for far ratios), and the rest
-      r.policy = add(r.policy, Sum2{y, fmaf(a, t.rest, fmaf(a, t.v, -p) + (p - (y - a)))});
-      r.kl += v;
-      r.ent += x.ent[k];
-      r.counts += t.clipped ? 0x10001u : 1u;
-    }
+    const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
+    const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
+    const float2 p = fmul2(a, t.v);
+    float2 y = fadd2(a, p);
+    // the errors of the product, of the sum (|v| <= 1 but for far ratios), and the rest
+    float2 z = ffma2(a, t.rest, fadd2(ffma2(a, t.v, fsub2(zero, p)), fsub2(p, fsub2(y, a))));
+    float2 h = make_float2(x.ent[k], x.ent[k + 1]), v = zero;
+    if (A.ref_logp) v = kl_of(fsub2(make_float2(x.ref[k], x.ref[k + 1]), logp)).kl;
+    if (!x.on[k]) y.x = z.x = h.x = v.x = 0.f;
+    if (!x.on[k + 1]) y.y = z.y = h.y = v.y = 0.f;
+    const float2 s = fadd2(hi, y), bb = fsub2(s, hi);
+    lo = fadd2(lo, fadd2(z, fadd2(fsub2(hi, fsub2(s, bb)), fsub2(y, bb))));
+    hi = s;
+    kl = fadd2(kl, v);
+    ent = fadd2(ent, h);
+    if (x.on[k]) counts += t.clipped_x ? 0x10001u : 1u;
+    if (x.on[k + 1]) counts += t.clipped_y ? 0x10001u : 1u;
   }
-  return r;
+  return Partial{add(Sum2{hi.x, lo.x}, Sum2{hi.y, lo.y}), kl.x + kl.y, ent.x + ent.y, counts};
 }
 
 // The block's record of its chunk, complete in thread 0.  The threads' sums meet in shared memory,
@@ -350,7 +393,7 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, i
   q = warp_sum(in ? part[1][tid] : zero);
   h = warp_sum(in ? part[2][tid] : zero);
   if (tid == 0) {
-    const double dp = value(p), dq = value(q), dh = value(h);
+    const double dp = -value(p), dq = value(q), dh = value(h);
     A.loss[0] = (float)(dp + A.kl_coef * dq - A.entropy_coef * dh);
     A.stats[0] = (float)dp;
     A.stats[1] = (float)dq;
@@ -406,14 +449,22 @@ __device__ __forceinline__ void token_gradients(const PolicyArgs& A, const Chunk
   const float w = A.dloss[0] * A.weights[c.seg], wh = -(float)A.entropy_coef * w, b = (float)A.kl_coef;
   float *dlogp = A.dlogp + c.lo + threadIdx.x, *dent = A.dentropy ? A.dentropy + c.lo + threadIdx.x : nullptr;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
+  for (int k = 0; k < kPerThread; k += 2) {
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;
-    const Term t = term_of(A, x.logp[k], x.old[k], x.adv[k]);
-    float g = t.clipped ? 0.f : -x.adv[k] * (1.f + (t.v + t.rest));
-    if (A.ref_logp) g = fmaf(-b, kl_of(x.ref[k] - x.logp[k]).slope, g);
+    const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
+    const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
+    float2 g = fmul2(a, fadd2(both(1.f), fadd2(t.v, t.rest)));  // sign turned by the factor below
+    if (t.clipped_x) g.x = 0.f;
+    if (t.clipped_y) g.y = 0.f;
+    if (A.ref_logp) g = ffma2(both(b), kl_of(fsub2(make_float2(x.ref[k], x.ref[k + 1]), logp)).slope, g);
+    g = fmul2(g, both(-w));
     if (exists<FULL>(c, k)) {
-      dlogp[k * kPolicyThreads] = x.on[k] ? g * w : 0.f;
+      dlogp[k * kPolicyThreads] = x.on[k] ? g.x : 0.f;
       if (dent) dent[k * kPolicyThreads] = x.on[k] ? wh : 0.f;
+    }
+    if (exists<FULL>(c, k + 1)) {
+      dlogp[(k + 1) * kPolicyThreads] = x.on[k + 1] ? g.y : 0.f;
+      if (dent) dent[(k + 1) * kPolicyThreads] = x.on[k + 1] ? wh : 0.f;
     }
   }
 }
