@@ -1,0 +1,24 @@
+// launch.cuh -- launching a kernel that joins what the one before it on the stream makes.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace dkv {
+
+// The kernel may start while its predecessor still runs; it has to call
+// cudaGridDependencySynchronize() before it reads what that one writes.  Hides the launch
+// latency of a second, small kernel (about 2 us of 9 for the loss of 65,536 tokens).
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace dkv

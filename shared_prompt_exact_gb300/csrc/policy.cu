@@ -36,6 +36,7 @@
 #include <utility>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "segs.cuh"
 
@@ -506,16 +507,7 @@ cudaError_t launch_policy_c(bool backward, const PolicyArgs& a, int N, const int
   policy_fwd_kernel<CAP><<<blocks, kPolicyThreads, 0, st>>>(a, s, x);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kFinishThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, policy_finish_kernel, a, blocks, N);
+  return launch_behind(policy_finish_kernel, dim3(1), dim3(kFinishThreads), st, a, blocks, N);
 }
 
 int policy_blocks(int N, const int32_t* off) { return first_block(off[N], N); }

@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "segs.cuh"
 
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restri
   const int col = blockIdx.x * 32 + threadIdx.x, per = (blocks + 31) / 32;
   const int b0 = threadIdx.y * per, b1 = min(blocks, b0 + per);
   float v = 0.f;
+  cudaGridDependencySynchronize();
 #pragma unroll 8
   for (int b = b0; b < b1; ++b) v += partial[(int64_t)b * 2 * D + col];
   part[threadIdx.y][threadIdx.x] = v;
@@ -478,8 +480,7 @@ cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, c
       return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || !backward || !a.q_weight) return e;
-  rope_weight_kernel<<<2 * D / 32, dim3(32, 32), 0, st>>>(a.partial, grid, D, dqw, dkw);
-  return cudaGetLastError();
+  return launch_behind(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), st, a.partial, grid, D, dqw, dkw);
 }
 
 size_t rope_workspace_bytes(int64_t T, int D) { return (size_t)rope_grid(T) * 2 * D * sizeof(float); }
