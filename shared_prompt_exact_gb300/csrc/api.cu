@@ -545,7 +545,7 @@ int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int
     if (!aligned16(p)) return DUALKV_ERR_ALIGN;
   if (N > kMaxSegs) return DUALKV_ERR_UNSUPPORTED;
   const int64_t T = (int64_t)P + R_offsets[N];
-  const size_t need = norm && backward ? rope_workspace_bytes(T, D) : 0;
+  const size_t need = norm && backward ? rope_workspace_bytes(T, Hq, Hkv, D) : 0;
   if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
     return DUALKV_ERR_WORKSPACE;
   const uint64_t uT = (uint64_t)T, wbytes = (uint64_t)D * (weight_dtype == DUALKV_F32 ? 4 : 2);
@@ -997,7 +997,7 @@ int dualkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t 
 
 size_t dualkv_qk_norm_rope_bwd_workspace_bytes(int P, int N, const int32_t* R_offsets, int Hq, int Hkv, int D) {
   if (validate_layout(P, N, R_offsets, Hq, Hkv, D) || N > kMaxSegs) return 0;
-  return rope_workspace_bytes((int64_t)P + R_offsets[N], D);
+  return rope_workspace_bytes((int64_t)P + R_offsets[N], Hq, Hkv, D);
 }
 
 int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,

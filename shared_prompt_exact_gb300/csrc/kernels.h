@@ -179,7 +179,7 @@ struct RopeArgs {
 // One launch over all rows; the backward adds a second one that sums the weight gradients.
 cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, const int32_t* off, float* dqw,
                         float* dkw, cudaStream_t st);
-size_t rope_workspace_bytes(int64_t T, int D);
+size_t rope_workspace_bytes(int64_t T, int Hq, int Hkv, int D);
 
 // ---- token log-probabilities (logprobs.cu)
 struct LogpArgs {

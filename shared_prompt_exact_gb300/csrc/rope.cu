@@ -17,10 +17,10 @@
 // pair lie in it.  Loads run ahead of their use through shared memory
 // (cp.async); arithmetic is on f32x2 pairs, because with plain fp32 the backward
 // was bound by issue (64 % of the slots) as much as by memory.  Measured: forward
-// 228 us for 71,680 rows of 32 + 8 heads of 128 (6.4 TB/s, 0.95 of the measured
-// copy bandwidth; 331 us with loads straight into registers), backward 420 us for
-// 84,997 such rows (6.2 TB/s) and 190 us for 36,522 rows of 8 + 2 heads of 512
-// (5.9 TB/s).
+// 233 us for 71,680 rows of 32 + 8 heads of 128 (6.3 TB/s, 0.93 of the measured
+// copy bandwidth; 331 us with loads straight into registers), backward 433 us for
+// 84,997 such rows (6.0 TB/s; 868 us) and 181 us for 36,522 rows of 8 + 2 heads of
+// 512 (6.2 TB/s; 496 us, with loads of every other vector).
 //
 // Angles: p f is formed in 64-bit fixed point as a fraction of a turn, and only
 // that fraction goes to fp32; at p = 10^5 a product in fp32 would already be off
@@ -190,36 +190,56 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The copies' place in a warp's walk: rows t, t + stride, ..., in each row q's heads in nq steps
-// of S = 32 / G heads, then k's up to `steps`.  x and g are the lane's vector A in the head and in
-// its upstream gradient (backward); vector B lies m.b - m.a behind.
+// A warp's walk: rows t, t + stride, ..., in each row the steps [begin, end) of the nq that take q's
+// heads, S = 32 / G at a time, and the nk behind them that take k's.  All steps, or with few rows
+// the share of block row blockIdx.y.
+template <int D>
+struct Walk {
+  static constexpr int S = 32 / (D / 16);
+  int nq, nk, begin, end;
+  int64_t first, stride;
+  __device__ __forceinline__ Walk(const RopeArgs& A, int warp) {
+    nq = (A.Hq + S - 1) / S;
+    nk = (A.Hkv + S - 1) / S;
+    begin = (nq + nk) * (int)blockIdx.y / (int)gridDim.y;
+    end = (nq + nk) * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    first = (int64_t)blockIdx.x * kRopeWarps + warp;
+    stride = (int64_t)gridDim.x * kRopeWarps;
+  }
+};
+
+// The copies' place in the walk.  x and g are the lane's vector A in the head and in its upstream
+// gradient (backward); vector B lies m.b - m.a behind.
 template <int D, bool BWD>
 struct Ahead {
-  static constexpr int S = 32 / (D / 16);
+  static constexpr int S = Walk<D>::S;
   const __nv_bfloat16 *x, *g;
   int h, H, s;
   int64_t t;
 
-  __device__ __forceinline__ void row(const RopeArgs& A, int64_t row, int slot, int a) {
-    t = row;
-    s = 0;
-    h = slot;
-    H = A.Hq;
-    x = A.q + t * A.q_stride + slot * D + a;
-    if (BWD) g = A.dq_out + (t * A.Hq + slot) * D + a;
+  __device__ __forceinline__ void place(const RopeArgs& A, const Walk<D>& w, int slot, int a) {
+    const bool is_q = s < w.nq;
+    h = slot + (s - (is_q ? 0 : w.nq)) * S;
+    H = is_q ? A.Hq : A.Hkv;
+    x = (is_q ? A.q + t * A.q_stride : A.k + t * A.k_stride) + h * D + a;
+    if (BWD) g = (is_q ? A.dq_out : A.dk_out) + (t * H + h) * D + a;
   }
-  __device__ __forceinline__ void step(const RopeArgs& A, int nq, int steps, int64_t stride, int slot, int a) {
+  __device__ __forceinline__ void start(const RopeArgs& A, const Walk<D>& w, int slot, int a) {
+    t = w.first;
+    s = w.begin;
+    place(A, w, slot, a);
+  }
+  __device__ __forceinline__ void step(const RopeArgs& A, const Walk<D>& w, int slot, int a) {
     h += S;
     x += S * D;
     if (BWD) g += S * D;
-    if (++s == nq) {
-      h = slot;
-      H = A.Hkv;
-      x = A.k + t * A.k_stride + slot * D + a;
-      if (BWD) g = A.dk_out + (t * A.Hkv + slot) * D + a;
-    } else if (s == steps) {
-      row(A, t + stride, slot, a);
+    ++s;
+    if (s != w.nq && s != w.end) return;
+    if (s == w.end) {
+      t += w.stride;
+      s = w.begin;
     }
+    place(A, w, slot, a);
   }
 };
 
@@ -232,11 +252,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
   const bool norm = A.q_weight != nullptr;
-  const int nq = (A.Hq + S - 1) / S, nk = (A.Hkv + S - 1) / S, steps = nq + nk, db = m.b - m.a;
-  const int64_t stride = (int64_t)gridDim.x * kRopeWarps, first = (int64_t)blockIdx.x * kRopeWarps + warp;
+  const int db = m.b - m.a;
+  const Walk<D> walk(A, warp);
   uint4* mine = ring + threadIdx.x;
   Ahead<D, false> ahead;
-  ahead.row(A, first, slot, m.a);
+  ahead.start(A, walk, slot, m.a);
   auto fetch = [&](int stage) {
     if (ahead.t < A.T) {
       uint4* to = mine + 2 * stage * kRopeThreads;
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
         copy16(to, ahead.x);
         copy16(to + kRopeThreads, ahead.x + db);
       }
-      ahead.step(A, nq, steps, stride, slot, m.a);
+      ahead.step(A, walk, slot, m.a);
     }
     copies_commit();
   };
@@ -252,11 +272,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
   for (int k = 0; k < kDepth - 1; ++k) fetch(k);
   load_shared<D>(A, sh);
   int stage = 0;
-  for (int64_t t = first; t < A.T; t += stride) {
+  for (int64_t t = walk.first; t < A.T; t += walk.stride) {
     const Angles ang =
         row_angles(position_of(seg, (int)t), sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
-    auto heads = [&](int n, int H, const float* w, __nv_bfloat16* y) {
-      for (int s = 0, h = slot; s < n; ++s, h += S, y += S * D) {
+    auto heads = [&](int from, int to, int H, const float* w, __nv_bfloat16* y) {
+      y += from * S * D;
+      for (int s = from, h = slot + from * S; s < to; ++s, h += S, y += S * D) {
         fetch(stage == 0 ? kDepth - 1 : stage - 1);
         copies_wait<kDepth - 1>();
         Vec8 a = unpack8(mine[2 * stage * kRopeThreads]), b = unpack8(mine[(2 * stage + 1) * kRopeThreads]);
@@ -281,8 +302,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
         }
       }
     };
-    heads(nq, A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a);
-    heads(nk, A.Hkv, sh.w[1], A.k_out + t * A.k_out_stride + slot * D + m.a);
+    heads(walk.begin, min(walk.end, walk.nq), A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a);
+    heads(max(walk.begin - walk.nq, 0), walk.end - walk.nq, A.Hkv, sh.w[1],
+          A.k_out + t * A.k_out_stride + slot * D + m.a);
   }
 }
 
@@ -353,11 +375,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
   const bool norm = A.q_weight != nullptr;
-  const int nq = (A.Hq + S - 1) / S, nk = (A.Hkv + S - 1) / S, steps = nq + nk, db = m.b - m.a;
-  const int64_t stride = (int64_t)gridDim.x * kRopeWarps, first = (int64_t)blockIdx.x * kRopeWarps + warp;
+  const int db = m.b - m.a;
+  const Walk<D> walk(A, warp);
   uint4* mine = ring + threadIdx.x;
   Ahead<D, true> ahead;
-  ahead.row(A, first, slot, m.a);
+  ahead.start(A, walk, slot, m.a);
   auto fetch = [&](int stage) {
     if (ahead.t < A.T) {
       uint4* to = mine + 4 * stage * kRopeThreads;
@@ -372,7 +394,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
 #pragma unroll
         for (int v = 0; v < 4; ++v) to[v * kRopeThreads] = make_uint4(0, 0, 0, 0);
       }
-      ahead.step(A, nq, steps, stride, slot, m.a);
+      ahead.step(A, walk, slot, m.a);
     }
     copies_commit();
   };
@@ -381,35 +403,38 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
   load_shared<D>(A, sh);
   Vec8 qa{}, qb{}, ka{}, kb{};
   int stage = 0;
-  for (int64_t t = first; t < A.T; t += stride) {
+  for (int64_t t = walk.first; t < A.T; t += walk.stride) {
     const Angles ang =
         row_angles(position_of(seg, (int)t), sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
-    auto heads = [&](int n, int H, const float* w, __nv_bfloat16* y, Vec8& da, Vec8& db_) {
-      for (int s = 0, h = slot; s < n; ++s, h += S, y += S * D) {
+    auto heads = [&](int from, int to, int H, const float* w, __nv_bfloat16* y, Vec8& da, Vec8& db_) {
+      y += from * S * D;
+      for (int s = from, h = slot + from * S; s < to; ++s, h += S, y += S * D) {
         fetch(stage == 0 ? kDepth - 1 : stage - 1);
         copies_wait<kDepth - 1>();
-        const uint4* from = mine + 4 * stage * kRopeThreads;
+        const uint4* in = mine + 4 * stage * kRopeThreads;
         stage = stage == kDepth - 1 ? 0 : stage + 1;
-        Vec8 g = unpack8(from[0]), f = unpack8(from[kRopeThreads]);
+        Vec8 g = unpack8(in[0]), f = unpack8(in[kRopeThreads]);
         rotate(g, f, ang.cs, ang.neg, ang.sn, A.inter);  // by minus the angle
         if (norm)
-          norm_backward<D>(g, f, unpack8(from[2 * kRopeThreads]), unpack8(from[3 * kRopeThreads]), w, m, A.eps, da, db_);
+          norm_backward<D>(g, f, unpack8(in[2 * kRopeThreads]), unpack8(in[3 * kRopeThreads]), w, m, A.eps, da, db_);
         if (h < H) {
           *reinterpret_cast<uint4*>(y) = pack8(g);
           *reinterpret_cast<uint4*>(y + db) = pack8(f);
         }
       }
     };
-    heads(nq, A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a, qa, qb);
-    heads(nk, A.Hkv, sh.w[1], A.k_out + t * A.k_out_stride + slot * D + m.a, ka, kb);
+    heads(walk.begin, min(walk.end, walk.nq), A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a, qa, qb);
+    heads(max(walk.begin - walk.nq, 0), walk.end - walk.nq, A.Hkv, sh.w[1],
+          A.k_out + t * A.k_out_stride + slot * D + m.a, ka, kb);
   }
   if (norm) {
     // every lane has waited for its own copies; the ring becomes the place of the block's sums
     copies_wait<0>();
     __syncthreads();
     float* smem = reinterpret_cast<float*>(ring);
-    block_weight_grad<D>(smem, m, slot, qa, qb, A.partial + (int64_t)blockIdx.x * 2 * D);
-    block_weight_grad<D>(smem, m, slot, ka, kb, A.partial + (int64_t)blockIdx.x * 2 * D + D);
+    float* out = A.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * D;
+    block_weight_grad<D>(smem, m, slot, qa, qb, out);
+    block_weight_grad<D>(smem, m, slot, ka, kb, out + D);
   }
 }
 
@@ -434,8 +459,19 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restri
   else dkw[col - D] = v;
 }
 
+// Blocks over the rows, and over the steps of a row where the rows alone would leave most warps
+// without work: at 192 rows of 32 + 8 heads of 128 the backward takes 7.0 us in a graph with its 10
+// steps spread, 10.4 with a warp walking all of them.
+dim3 rope_grid(int64_t T, int Hq, int Hkv, int D) {
+  const int64_t need = (T + kRopeWarps - 1) / kRopeWarps;
+  const int S = 512 / D, steps = (Hq + S - 1) / S + (Hkv + S - 1) / S;
+  const int64_t spare = kRopeMaxBlocks / 2 / need;  // one round of the resident blocks
+  return dim3((unsigned)(need < kRopeMaxBlocks ? need : kRopeMaxBlocks),
+              (unsigned)(spare < 1 ? 1 : spare < steps ? spare : steps));
+}
+
 template <int D, int CAP>
-cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, int grid,
+cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, dim3 grid,
                           cudaStream_t st) {
   const SegTable<CAP> s = make_segs<CAP>(P, N, off);
   const int smem = (backward ? 4 : 2) * kDepth * kRopeThreads * (int)sizeof(uint4);
@@ -449,22 +485,17 @@ cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const 
 }
 
 template <int D>
-cudaError_t launch_rope_d(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, int grid,
+cudaError_t launch_rope_d(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, dim3 grid,
                           cudaStream_t st) {
   return N <= kSmallSegs ? launch_rope_c<D, kSmallSegs>(backward, a, P, N, off, grid, st)
                          : launch_rope_c<D, kMaxSegs>(backward, a, P, N, off, grid, st);
-}
-
-int rope_grid(int64_t T) {
-  const int64_t need = (T + kRopeWarps - 1) / kRopeWarps;
-  return (int)(need < kRopeMaxBlocks ? need : kRopeMaxBlocks);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, const int32_t* off, float* dqw,
                         float* dkw, cudaStream_t st) {
-  const int grid = rope_grid(a.T);
+  const dim3 grid = rope_grid(a.T, a.Hq, a.Hkv, D);
   cudaError_t e;
   switch (D) {
     case 64:
@@ -480,9 +511,13 @@ cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, c
       return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || !backward || !a.q_weight) return e;
-  return launch_behind(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), st, a.partial, grid, D, dqw, dkw);
+  return launch_behind(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), st, a.partial, (int)(grid.x * grid.y), D, dqw,
+                       dkw);
 }
 
-size_t rope_workspace_bytes(int64_t T, int D) { return (size_t)rope_grid(T) * 2 * D * sizeof(float); }
+size_t rope_workspace_bytes(int64_t T, int Hq, int Hkv, int D) {
+  const dim3 grid = rope_grid(T, Hq, Hkv, D);
+  return (size_t)grid.x * grid.y * 2 * D * sizeof(float);
+}
 
 }  // namespace dkv
