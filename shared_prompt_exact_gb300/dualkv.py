@@ -57,6 +57,8 @@ class DualKVError(RuntimeError):
 def load(path: Optional[str] = None):
     """Load libdualkv.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -431,10 +433,14 @@ def _row_stride(t):
     return t.stride(0) if n > 1 else t.numel() // max(n, 1)
 
 
+# the current stream's handle without an object around it, where this PyTorch has that (1 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(stream, device):
     """The stream's handle: the current one of the (current) device unless given."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     return _stream(stream)
 
 
