@@ -36,11 +36,12 @@ def logprobs(logits, tokens, scale, P, off):
         if top == -np.inf:
             lse[m] = logp[i] = -np.inf
             continue
-        lse[m] = top + np.log(np.exp(z[m] - top).sum())
-        logp[i] = z[m, tokens[i]] - lse[m]
-        p = np.exp(z[m] - lse[m])
-        on = p > 0
-        ent[i] = -(p[on] * (z[m][on] - lse[m])).sum()
+        lp = z[m] - top
+        lp = lp - np.log(np.exp(lp).sum())  # holds for rows of any offset, which top + log(sum) need not
+        lse[m] = top - lp[z[m].argmax()]
+        logp[i] = lp[tokens[i]]
+        on = lp > -np.inf
+        ent[i] = -(np.exp(lp[on]) * lp[on]).sum()
     return logp, ent, lse
 
 

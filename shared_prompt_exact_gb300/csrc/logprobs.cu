@@ -171,8 +171,8 @@ __device__ __forceinline__ float floor_of(float m) { return m == -CUDART_INF_F ?
 // Moves (s, t) from their maximum to a larger one.
 __device__ __forceinline__ void rebase(Running& r, float m, float c) {
   if (r.m != -CUDART_INF_F) {
-    const float d = (r.m - floor_of(m)) * c, f = ex2(d);
-    // d is -inf only below a maximum of +inf, whose own term makes the sums NaN
+    // the bound keeps a maximum that is the type's lowest value, or one below +inf, from leaving 0 * inf
+    const float d = fmaxf((r.m - floor_of(m)) * c, -1e30f), f = ex2(d);
     r.t = fmul2(ffma2(make_float2(d, d), r.s, r.t), make_float2(f, f));
     r.s = fmul2(r.s, make_float2(f, f));
   }
@@ -342,32 +342,89 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-// Gradient of one logit z (raw): p (k0 + k1 d), d = z scale - lse.  d is formed before the
-// scaling to base 2, so that its rounding is relative to d and not to z.
+// A row's gradient p (k0 + k1 d), d = z scale - lse, p = e^d for a raw logit z.  d is formed
+// before the scaling to base 2, so that its rounding is relative to d and not to z.
+struct RowGrad {
+  float scale, lse, k0, k1;
+  float base;  // subtracted from z first, in rows that are summed again; else 0
+};
 template <bool ENT>
-__device__ __forceinline__ float grad_of(float z, float scale, float lse, float k0, float k1) {
-  const float d = fmaf(z, scale, -lse), p = ex2(d * kLog2e);
-  return ENT ? p * fmaf(fmaxf(d, -1e30f), k1, k0) : p * k0;
+__device__ __forceinline__ float2 grad_of(float2 z, const RowGrad& r) {  // base 0
+  const float2 d = ffma2(z, make_float2(r.scale, r.scale), make_float2(-r.lse, -r.lse));
+  const float2 y = fmul2(d, make_float2(kLog2e, kLog2e)), p = make_float2(ex2(y.x), ex2(y.y));
+  const float2 k = make_float2(r.k0, r.k0);
+  if (!ENT) return fmul2(p, k);
+  return fmul2(p, ffma2(make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), make_float2(r.k1, r.k1), k));
+}
+template <bool ENT>
+__device__ __forceinline__ float grad_of(float z, const RowGrad& r) {
+  const float d = fmaf(z - r.base, r.scale, -r.lse), p = ex2(d * kLog2e);
+  return ENT ? p * fmaf(fmaxf(d, -1e30f), r.k1, r.k0) : p * r.k0;
 }
 
-// The same for pairs.
-template <bool ENT>
-__device__ __forceinline__ float2 grad_of(float2 z, float scale, float lse, float k0, float k1) {
-  const float2 d = ffma2(z, make_float2(scale, scale), make_float2(-lse, -lse));
-  const float2 y = fmul2(d, make_float2(kLog2e, kLog2e)), p = make_float2(ex2(y.x), ex2(y.y)), k = make_float2(k0, k0);
-  if (!ENT) return fmul2(p, k);
-  return fmul2(p, ffma2(make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), make_float2(k1, k1), k));
+// Slots for the keys of N segments.
+__host__ __device__ __forceinline__ int key_slots(int N) {
+  int n2 = 2;
+  while (n2 < N) n2 <<= 1;
+  return n2;
 }
+
+// The shared row's targets as keys (token, segment), ascending, those that are ignored last.
+constexpr uint64_t kNoKey = ~0ull;
+
+// Sorts n2 = 2^k keys, then sums the gradients of equal tokens: at the last key of a token `sum` gets
+// them all, added in an order that depends on the keys alone.  `sum` and `spare` hold n2 values
+// each; returns the one that has the sums.  Up to a key per thread each key counts those before it;
+// more are sorted by a bitonic network (a call with 4,095 segments: 166 us, 546 when every pair of
+// targets was compared; with 256: 11.1 us by counting, 12.8 by the network).
+template <int CAP>
+__device__ __noinline__ float* sum_targets(const LogpArgs& A, const SegTable<CAP>& seg, uint64_t* key, float* sum,
+                                           float* spare, int n2) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (n2 <= kLogpThreads) {
+    const uint64_t mine = tid < n2 ? key[tid] : kNoKey;
+    int rank = 0;
+    for (int u = 0; u < n2; ++u) rank += key[u] < mine || (key[u] == mine && u < tid);
+    __syncthreads();
+    if (tid < n2) key[rank] = mine;
+    __syncthreads();
+  }
+  for (int k = 2; k <= n2 && n2 > kLogpThreads; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = tid; i < n2; i += kLogpThreads) {
+        const int p = i ^ j;
+        if (p > i && (key[i] > key[p]) == ((i & k) == 0)) {
+          const uint64_t t = key[i];
+          key[i] = key[p];
+          key[p] = t;
+        }
+      }
+      __syncthreads();
+    }
+  for (int i = tid; i < n2; i += kLogpThreads) sum[i] = key[i] == kNoKey ? 0.f : A.dlogp[seg.off[(uint32_t)key[i]]];
+  __syncthreads();
+  for (int d = 1; d < n2; d <<= 1) {
+    for (int i = tid; i < n2; i += kLogpThreads)
+      spare[i] = sum[i] + (i >= d && (key[i] >> 32) == (key[i - d] >> 32) ? sum[i - d] : 0.f);
+    __syncthreads();
+    float* t = sum;
+    sum = spare;
+    spare = t;
+  }
+  return sum;
+}
+
+// Beyond this the fp32 lse no longer holds its row's sum (at 4096 it is off by up to 2^-12): rows
+// of logits far from 0, such as those masked throughout with the type's lowest value.
+constexpr float kLseHolds = 4096.f;
 
 // Block (row, part): one part of one row's columns.
 template <typename T, bool ENT, int CAP>
 __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArgs A, int parts,
                                                                    const __grid_constant__ SegTable<CAP> seg) {
   constexpr int P2 = RowVectors<T>::E / 2, U = kBwdBatch;
-  extern __shared__ uint32_t dyn[];
-  int* s_tok = reinterpret_cast<int*>(dyn);              // [N] the shared row's targets (-1: none)
-  float* s_g = reinterpret_cast<float*>(dyn) + seg.N;    // [N] their upstream gradients
-  float* s_v = s_g + seg.N;                              // [N] the targets' logit gradients
+  extern __shared__ uint64_t keys[];  // the shared row's targets: n2 keys, then two values for each
   const int64_t row = blockIdx.x / parts;
   const int tid = threadIdx.x;
   const bool shared_row = seg.P > 0 && row == 0;
@@ -376,20 +433,26 @@ __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArg
   int lo, hi;
   part_of(y, A.V, (int)(blockIdx.x % parts), parts, &lo, &hi);
   const float lse = A.lse[row];
+  const bool renew = fabsf(lse) > kLseHolds && lse != -CUDART_INF_F;
+  if (renew) {  // the first block takes the whole row, whose sum it has to form before anyone overwrites it
+    if (blockIdx.x % parts) return;
+    lo = 0;
+    hi = A.V;
+  }
   float g = 0.f, h = 0.f, ent = 0.f;
   int tok = -1;
   bool flows;
+  const int n2 = key_slots(seg.N);
   if (shared_row) {
     int any = -1;
     bool targets = false;  // gradients that cancel in g still reach their targets
-    for (int s = tid; s < seg.N; s += kLogpThreads) {
-      const int i = seg.off[s];
-      const int t = i < seg.off[s + 1] ? token_at(A, i) : -1;
-      const float gi = t >= 0 ? A.dlogp[i] : 0.f;
-      s_tok[s] = t;
-      s_g[s] = gi;
-      targets |= gi != 0.f;
+    for (int s = tid; s < n2; s += kLogpThreads) {
+      const int i = s < seg.N ? seg.off[s] : 0;
+      const int t = s < seg.N && i < seg.off[s + 1] ? token_at(A, i) : -1;
+      keys[s] = t >= 0 ? (uint64_t)t << 32 | (uint32_t)s : kNoKey;
       if (t >= 0) {
+        const float gi = A.dlogp[i];
+        targets |= gi != 0.f;
         g += gi;
         if (ENT) h += A.dentropy[i];
         any = i;
@@ -429,30 +492,45 @@ __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArg
     return;
   }
   const float scale = A.scale;
-  const float k1 = -scale * h, k0 = -scale * fmaf(h, ent, g);
-  auto here = [&](int t) { return t >= lo && t < hi; };  // targets in this block's columns
-  // The targets' gradients, from logits that an in-place pass is about to overwrite.  Equal
-  // targets of the shared row all get the same sum over them, in segment order.
-  float vt = 0.f;
-  if (shared_row) {
-    for (int s = tid; s < seg.N; s += kLogpThreads) {
-      const int t = s_tok[s];
-      if (!here(t)) continue;
-      float sum = 0.f;
-      for (int u = 0; u < seg.N; ++u) sum += s_tok[u] == t ? s_g[u] : 0.f;
-      s_v[s] = fmaf(scale, sum, grad_of<ENT>(to_f(x[t]), scale, lse, k0, k1));
+  RowGrad rg{scale, lse, -scale * fmaf(h, ent, g), -scale * h, 0.f};
+  if (renew) {
+    __shared__ Running sums;
+    Running r = nothing_yet();
+    const float c = scale * kLog2e;
+    for (int j = tid; j < A.V; j += kLogpThreads) {
+      const float2 z[1] = {make_float2(to_f(x[j]), -CUDART_INF_F)};
+      if (z[0].x > r.m) rebase(r, z[0].x, c);
+      accumulate<false>(r, z, c);
     }
+    r = block_join(r, c);
+    if (tid == 0) sums = r;
+    __syncthreads();
+    rg.base = sums.m;
+    rg.lse = logf(sums.s.x);
+  }
+  auto here = [&](int t) { return t >= lo && t < hi; };  // targets in this block's columns
+  // The targets' gradients, from logits that an in-place pass is about to overwrite; in the shared
+  // row one for each token, at the last of its keys.
+  float vt = 0.f;
+  float* s_v = reinterpret_cast<float*>(keys + n2);
+  auto last_key = [&](int i) {
+    return keys[i] != kNoKey && (i == n2 - 1 || (keys[i] >> 32) != (keys[i + 1] >> 32)) && here((int)(keys[i] >> 32));
+  };
+  if (shared_row) {
+    s_v = sum_targets(A, seg, keys, s_v, s_v + n2, n2);
+    for (int i = tid; i < n2; i += kLogpThreads)
+      if (last_key(i)) s_v[i] = fmaf(scale, s_v[i], grad_of<ENT>(to_f(x[keys[i] >> 32]), rg));
   } else if (tid == 0 && here(tok)) {
-    vt = fmaf(scale, g, grad_of<ENT>(to_f(x[tok]), scale, lse, k0, k1));
+    vt = fmaf(scale, g, grad_of<ENT>(to_f(x[tok]), rg));
   }
   __syncthreads();
-  if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) == 0) {
+  if (!renew && ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) == 0) {
     const uint4* xv = reinterpret_cast<const uint4*>(x + lo + v.head);
     auto grads = [&](const uint4& w) {
       float2 z[P2];
       unpack(w, z);
 #pragma unroll
-      for (int e = 0; e < P2; ++e) z[e] = grad_of<ENT>(z[e], scale, lse, k0, k1);
+      for (int e = 0; e < P2; ++e) z[e] = grad_of<ENT>(z[e], rg);
       return pack(z);
     };
     int k = tid;
@@ -466,16 +544,16 @@ __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArg
     for (; k < v.nv; k += kLogpThreads) yv[k] = grads(load_once(xv + k));
     for (k = tid; k < v.ends; k += kLogpThreads) {
       const int j = lo + v.end(k);
-      from_f(grad_of<ENT>(to_f(x[j]), scale, lse, k0, k1), y + j);
+      from_f(grad_of<ENT>(to_f(x[j]), rg), y + j);
     }
-  } else {  // rows that start at different offsets within 16 bytes
+  } else {  // rows that start at different offsets within 16 bytes, or are summed again
 #pragma unroll 4
-    for (int j = lo + tid; j < hi; j += kLogpThreads) from_f(grad_of<ENT>(to_f(x[j]), scale, lse, k0, k1), y + j);
+    for (int j = lo + tid; j < hi; j += kLogpThreads) from_f(grad_of<ENT>(to_f(x[j]), rg), y + j);
   }
   __syncthreads();
   if (shared_row) {
-    for (int s = tid; s < seg.N; s += kLogpThreads)
-      if (here(s_tok[s])) from_f(s_v[s], y + s_tok[s]);
+    for (int i = tid; i < n2; i += kLogpThreads)
+      if (last_key(i)) from_f(s_v[i], y + (keys[i] >> 32));
   } else if (tid == 0 && here(tok)) {
     from_f(vt, y + tok);
   }
@@ -517,10 +595,10 @@ cudaError_t launch_logp_c(bool backward, const LogpArgs& a, int P, int N, const 
     cfg.numAttrs = parts > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, logp_fwd_kernel<T, ENT, CAP>, a, parts, s);
   }
-  cfg.dynamicSmemBytes = P > 0 ? (size_t)N * 12 : 0;
+  cfg.dynamicSmemBytes = P > 0 ? (size_t)key_slots(N) * 16 : 0;
   if (cfg.dynamicSmemBytes > 32768) {  // beyond 48 KB with the kernel's static arrays
     const cudaError_t e = cudaFuncSetAttribute(logp_bwd_kernel<T, ENT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxSegs * 12);
+                                               key_slots(kMaxSegs) * 16);
     if (e != cudaSuccess) return e;
   }
   return cudaLaunchKernelEx(&cfg, logp_bwd_kernel<T, ENT, CAP>, a, parts, s);

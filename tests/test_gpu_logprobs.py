@@ -66,7 +66,8 @@ def _check_forward(got, logits, tok, scale, P, off):
         if top == -np.inf:
             assert lse[m] == logp[i] == -np.inf and (ent is None or ent[i] == 0.0)
             continue
-        p = np.exp(z[m] - want[2][m])
+        p = np.exp(z[m] - top)
+        p /= p.sum()
         y = np.where(p > 0, np.maximum(z[m] - top, -1e30), 0.0)
         A, A2 = (p * np.abs(y)).sum(), (p * y * y).sum()
         base = 2 * A + K + 4 * abs(top)
@@ -384,3 +385,78 @@ def test_rows_split_over_blocks(rows, dtype):
     lse2 = torch.cat((flse, torch.zeros(1, device="cuda")))
     dsub = torch.cat((d[pick], torch.zeros_like(d[:1])))
     _check_backward(dsub, sub, ftok, 1.0, 1, [0, len(pick)], lse2, got[1][pick], dlogp[pick], dent[pick])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [40, 70003])
+def test_rows_far_from_zero(V, dtype):
+    # masked throughout with the type's lowest value (uniform probabilities), or far above or below 0:
+    # an fp32 lse is too coarse there to normalise with
+    P, off = 1, [0, 4]
+    logits, tok, dlogp, dent = _inputs(P, off, V, dtype, 0, 13, ignored=0.0)
+    lowest = torch.finfo(dtype).min
+    logits[0] = lowest
+    logits[1, : V // 2] = lowest
+    logits[2] += 3e4 if dtype == F32 else 2.0 ** 14
+    logits[3] -= 1e5 if dtype == F32 else 2.0 ** 15
+    got = dk.token_logprobs(logits, tok, P, off, entropy=True)
+    _check_forward(got, logits, tok, 1.0, P, off)
+    z = _np(logits)
+    lse = opl.logprobs(z, tok.tolist(), 1.0, P, off)[2]  # fp64
+    want = np.zeros_like(z)
+    tol = np.zeros_like(z)
+    step = 2.0 ** -8 if dtype == BF else U
+    for i in range(4):  # row i predicts token i
+        top = z[i].max()
+        y = np.maximum(z[i] - top, -1e4)
+        d = y - np.log(np.exp(y).sum())
+        p, g, h = np.exp(d), float(dlogp[i]), float(dent[i])
+        H = -(p * np.where(p > 0, d, 0.0)).sum()
+        want[i] = -g * p - h * p * (np.where(p > 0, d, 0.0) + H)
+        want[i, tok[i]] += g
+        # the row's sum (as the forward's) moves d as well: u (K + V/128 + 100); the given entropy its own error
+        A = (p * np.abs(np.where(p > 0, d, 0.0))).sum()
+        K = 100 + V / 128
+        c = abs(g) + abs(h) * (np.abs(d) * (p > 0) + abs(H))
+        tol[i] = step * np.abs(want[i]) + p * U * ((3 * np.abs(d) + 2 * A + K + 10) * c + abs(h) * (1 + A) ** 2 * (K + 8))
+        tol[i, tok[i]] += 8 * U * abs(g)
+    for entropy in (False, True):
+        kw = dict(entropy=got[1], dentropy=dent) if entropy else {}
+        for inplace in (False, True):
+            x = logits.clone()
+            out = dk.token_logprobs_backward(x, tok, got[2], dlogp, P, off, inplace=inplace, **kw)
+            if entropy:
+                err = np.abs(_np(out)[:4] - want[:4])
+                assert np.all(err <= tol[:4] + 2.0 ** -125), float(np.max(err - tol[:4]))
+            else:
+                sums = _np(out)[:4].sum(1)  # a softmax gradient sums to 0
+                assert np.all(np.abs(sums) <= step * np.abs(_np(out)[:4]).sum(1) + U * (K + 100))
+            assert not out[4].any()
+
+
+def test_calls_of_two_threads():
+    import threading
+    P, off, V = 3, [0, 40, 90], 5003
+    logits, tok, dlogp, dent = _inputs(P, off, V, BF, 0, 14)
+    want = dk.token_logprobs(logits, tok, P, off, entropy=True)
+    grad = dk.token_logprobs_backward(logits, tok, want[2], dlogp, P, off, entropy=want[1], dentropy=dent)
+    x = dict(logp=want[0], old=want[0] - 0.1 * dent, adv=torch.tensor([1.0, -1.0], device="cuda"))
+    loss = dk.policy_loss(x["logp"], x["old"], x["adv"], off)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        for _ in range(20):
+            got = dk.token_logprobs(logits, tok, P, off, entropy=True, stream=stream)
+            g = dk.token_logprobs_backward(logits, tok, got[2], dlogp, P, off, entropy=got[1], dentropy=dent, stream=stream)
+            l3 = dk.policy_loss(x["logp"], x["old"], x["adv"], off, stream=stream)
+            stream.synchronize()
+            wrong.extend(k for k, (a, b) in enumerate(zip(want + (grad,) + loss, got + (g,) + l3)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

@@ -183,6 +183,32 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_a_graph():
             assert torch.equal(a, b)
 
 
+def test_rows_past_32_bit_offsets():
+    # rows 65,536 values apart: the last ones lie beyond 2^31 values and 2^32 bytes
+    T, Hq, Hkv, D, width = 33_001, 2, 1, 64, 65_536
+    row = torch.empty(T, width, dtype=BF, device="cuda")
+    cols = torch.randn(T, 4 * D, device="cuda").to(BF)
+    row[:, 1024:1024 + 4 * D] = cols
+    q, k = row[:, 1024:1024 + 2 * D].view(T, Hq, D), row[:, 1024 + 2 * D:1024 + 3 * D].view(T, Hkv, D)
+    qc, kc = cols[:, :2 * D].contiguous().view(T, Hq, D), cols[:, 2 * D:3 * D].contiguous().view(T, Hkv, D)
+    P, off = 1, [0, T - 1]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = [1 + 0.1 * torch.randn(D, generator=g, device="cuda") for _ in range(2)]
+    f = _inv_freq(D, 1e4)
+    got, want = dk.qk_norm_rope(q, k, P, off, f, *w), dk.qk_norm_rope(qc, kc, P, off, f, *w)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    dq, dkk = (torch.randn(T, H, D, generator=g, device="cuda").to(BF) for H in (Hq, Hkv))
+    want = dk.qk_norm_rope_backward(qc, kc, dq, dkk, P, off, f, *w)
+    out = torch.empty(T, width, dtype=BF, device="cuda")
+    o = [out[:, 2048:2048 + 2 * D].view(T, Hq, D), out[:, 2048 + 2 * D:2048 + 3 * D].view(T, Hkv, D)]
+    dw = [torch.empty(D, device="cuda") for _ in range(2)]
+    ws = torch.empty(dk.dualkv_qk_norm_rope_bwd_workspace_bytes(P, 1, off, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+    dk.dualkv_qk_norm_rope_bwd(q, k, dq, dkk, *w, 0.0, 1e-6, f, D, False, P, 1, off, Hq, Hkv, D, *o, *dw, ws)
+    for a, b in zip(o + dw, want):
+        assert torch.equal(a, b)
+
+
 def test_binding_refuses_what_does_not_fit():
     P, off, Hq, Hkv, D = 4, [0, 3], 2, 1, 64
     q, k, qw, kw, f, dq_out, dk_out = _inputs(P, off, Hq, Hkv, D, D, BF, False, 1)
