@@ -160,7 +160,7 @@ cudaError_t launch_pack(int kind, const void* src, void* dst, const int32_t* d_o
                         int row_elems, int num_sms, cudaStream_t st);
 
 // ---- per-head norm and rotation of q and k (rope.cu)
-constexpr int kRopeMaxBlocks = 152 * 4;  // two rounds of the resident blocks
+constexpr int kRopeMaxBlocks = 152 * 8;  // four rounds of the resident blocks
 
 struct RopeArgs {
   const __nv_bfloat16 *q, *k;            // projections' rows, head h of row t at t * stride + h * D
@@ -170,7 +170,7 @@ struct RopeArgs {
   int64_t q_out_stride, k_out_stride;
   const void *q_weight, *k_weight;       // D values each; both null: no norm
   const float* inv_freq;                 // half values
-  float* partial;                        // backward: [block][2][D] weight gradients
+  float* partial;                        // backward: [block][D] weight gradients, q's blocks first
   int64_t T;
   int Hq, Hkv, half;                     // half = rope_dim / 2
   float w0, eps;

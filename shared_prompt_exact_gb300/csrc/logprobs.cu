@@ -473,13 +473,14 @@ __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArg
   } else {
     int open;
     const int i = predicted(seg, row, &open);
-    if (i >= 0) tok = token_at(A, i);
-    if (tok >= 0) {
+    if (i >= 0) {  // all at once; an ignored token's values count for nothing
       g = A.dlogp[i];
       if (ENT) {
         h = A.dentropy[i];
         ent = A.entropy[i];
       }
+      tok = token_at(A, i);
+      if (tok < 0) g = h = 0.f;
     }
     flows = g != 0.f || h != 0.f;
   }
@@ -523,6 +524,8 @@ __global__ void __launch_bounds__(kLogpThreads, 5) logp_bwd_kernel(const LogpArg
   } else if (tid == 0 && here(tok)) {
     vt = fmaf(scale, g, grad_of<ENT>(to_f(x[tok]), rg));
   }
+  // needed in place only, but the other calls keep it too: without it the block's warps drift apart
+  // and 10,479 rows of 131,072 bf16 take 826 us instead of 779
   __syncthreads();
   if (!renew && ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) == 0) {
     const uint4* xv = reinterpret_cast<const uint4*>(x + lo + v.head);

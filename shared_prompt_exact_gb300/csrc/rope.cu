@@ -17,10 +17,10 @@
 // pair lie in it.  Loads run ahead of their use through shared memory
 // (cp.async); arithmetic is on f32x2 pairs, because with plain fp32 the backward
 // was bound by issue (64 % of the slots) as much as by memory.  Measured: forward
-// 233 us for 71,680 rows of 32 + 8 heads of 128 (6.3 TB/s, 0.93 of the measured
-// copy bandwidth; 331 us with loads straight into registers), backward 433 us for
-// 84,997 such rows (6.0 TB/s; 868 us) and 181 us for 36,522 rows of 8 + 2 heads of
-// 512 (6.2 TB/s; 496 us, with loads of every other vector).
+// 226 us for 71,680 rows of 32 + 8 heads of 128 (6.5 TB/s, 0.96 of the measured
+// copy bandwidth; 331 us with loads straight into registers), backward 398 us for
+// 84,997 such rows (6.6 TB/s; 868 us) and 187 us for 36,522 rows of 8 + 2 heads of
+// 512 (6.0 TB/s; 496 us, with loads of every other vector).
 //
 // Angles: p f is formed in 64-bit fixed point as a fraction of a turn, and only
 // that fraction goes to fp32; at p = 10^5 a product in fp32 would already be off
@@ -42,7 +42,8 @@ constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
 // Steps in a lane's ring: the one in use and those that its copies run ahead.  Three keep 32 KB
 // (forward) and 64 KB (backward) per SM in flight; with 4 to 6 and grids of 304 to 1216 blocks the
-// times below moved by less than 4 %, two blocks per SM in each case.
+// times above moved by less than 4 %.  Two blocks per SM: three leave the backward 80 registers, and
+// it then spills (464 us instead of 404).
 constexpr int kDepth = 3;
 
 // Eight consecutive values as four f32x2 pairs: (0, 2), (4, 6), (1, 3), (5, 7).  That order costs
@@ -129,17 +130,8 @@ struct Angles {
   Vec8 cs, sn, neg;
 };
 
-// The warp's cosines and sines of one row in shared memory, then the lane's own 8 of
-// each (1 and 0 where its values are not turned).
-__device__ __forceinline__ Angles row_angles(int p, const uint64_t* freq, int half, float* wc, float* ws, int lane,
-                                             const LaneMap& m, bool inter) {
-  __syncwarp();
-  for (int j = lane; j < half; j += 32) {
-    const int turns = (int)(uint32_t)(((uint64_t)(uint32_t)p * freq[j]) >> 32);
-    const int at = inter ? j : vec8_at(j);
-    sincospif((float)turns * 4.656612873077393e-10f, ws + at, wc + at);  // 2^-31: half turns
-  }
-  __syncwarp();
+// The lane's own cosines and sines of its warp's row (1 and 0 where its values are not turned).
+__device__ __forceinline__ Angles lane_angles(const float* wc, const float* ws, const LaneMap& m) {
   Angles r{load8(wc + m.ja, wc + m.jb), load8(ws + m.ja, ws + m.jb), {}};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -150,6 +142,19 @@ __device__ __forceinline__ Angles row_angles(int p, const uint64_t* freq, int ha
     r.neg.v[e] = make_float2(-r.sn.v[e].x, -r.sn.v[e].y);
   }
   return r;
+}
+
+// The warp's cosines and sines of one row in shared memory, then the lane's own of them.
+__device__ __forceinline__ Angles row_angles(int p, const uint64_t* freq, int half, float* wc, float* ws, int lane,
+                                             const LaneMap& m, bool inter) {
+  __syncwarp();
+  for (int j = lane; j < half; j += 32) {
+    const int turns = (int)(uint32_t)(((uint64_t)(uint32_t)p * freq[j]) >> 32);
+    const int at = inter ? j : vec8_at(j);
+    sincospif((float)turns * 4.656612873077393e-10f, ws + at, wc + at);  // 2^-31: half turns
+  }
+  __syncwarp();
+  return lane_angles(wc, ws, m);
 }
 
 // (u, v) <- (u c - v s, v c + u s)
@@ -190,19 +195,24 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's walk: rows t, t + stride, ..., in each row the steps [begin, end) of the nq that take q's
-// heads, S = 32 / G at a time, and the nk behind them that take k's.  All steps, or with few rows
-// the share of block row blockIdx.y.
+// A warp's walk: rows t, t + stride, ..., in each row the steps [begin, end) of those that take q's
+// heads, S = 32 / G at a time, and those behind them that take k's.  Block rows (blockIdx.y) share a
+// row's steps: the first `qparts` of them q's; with `both` there is one for all steps.
 template <int D>
 struct Walk {
   static constexpr int S = 32 / (D / 16);
-  int nq, nk, begin, end;
+  int nq, begin, end;
   int64_t first, stride;
-  __device__ __forceinline__ Walk(const RopeArgs& A, int warp) {
+  __device__ __forceinline__ Walk(const RopeArgs& A, int qparts, bool both, int warp) {
     nq = (A.Hq + S - 1) / S;
-    nk = (A.Hkv + S - 1) / S;
-    begin = (nq + nk) * (int)blockIdx.y / (int)gridDim.y;
-    end = (nq + nk) * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    const int nk = (A.Hkv + S - 1) / S, y = (int)blockIdx.y, kparts = (int)gridDim.y - qparts;
+    if (both) {
+      begin = (nq + nk) * y / (int)gridDim.y;
+      end = (nq + nk) * (y + 1) / (int)gridDim.y;
+    } else {
+      begin = y < qparts ? nq * y / qparts : nq + nk * (y - qparts) / kparts;
+      end = y < qparts ? nq * (y + 1) / qparts : nq + nk * (y + 1 - qparts) / kparts;
+    }
     first = (int64_t)blockIdx.x * kRopeWarps + warp;
     stride = (int64_t)gridDim.x * kRopeWarps;
   }
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
   const bool norm = A.q_weight != nullptr;
   const int db = m.b - m.a;
-  const Walk<D> walk(A, warp);
+  const Walk<D> walk(A, 0, true, warp);
   uint4* mine = ring + threadIdx.x;
   Ahead<D, false> ahead;
   ahead.start(A, walk, slot, m.a);
@@ -367,16 +377,16 @@ __device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m,
 }
 
 template <int D, int CAP>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs A,
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs A, int qparts,
                                                                     const __grid_constant__ SegTable<CAP> seg) {
   constexpr int G = D / 16, S = 32 / G;
   extern __shared__ uint4 ring[];  // [kDepth][4][threads]
   __shared__ RopeShared<D> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
   const LaneMap m = lane_map<D>(i, A.half, A.inter);
-  const bool norm = A.q_weight != nullptr;
+  const bool norm = A.q_weight != nullptr, is_q = (int)blockIdx.y < qparts;
   const int db = m.b - m.a;
-  const Walk<D> walk(A, warp);
+  const Walk<D> walk(A, qparts, false, warp);
   uint4* mine = ring + threadIdx.x;
   Ahead<D, true> ahead;
   ahead.start(A, walk, slot, m.a);
@@ -401,77 +411,93 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
 #pragma unroll
   for (int k = 0; k < kDepth - 1; ++k) fetch(k);
   load_shared<D>(A, sh);
-  Vec8 qa{}, qb{}, ka{}, kb{};
+  Vec8 da{}, db_{};
   int stage = 0;
+  const int from = walk.begin - (is_q ? 0 : walk.nq), to = walk.end - (is_q ? 0 : walk.nq), H = is_q ? A.Hq : A.Hkv;
+  const float* w = sh.w[!is_q];
+  __nv_bfloat16* out = (is_q ? A.q_out : A.k_out) + (from * S + slot) * D + m.a;
+  const int64_t out_stride = is_q ? A.q_out_stride : A.k_out_stride;
   for (int64_t t = walk.first; t < A.T; t += walk.stride) {
     const Angles ang =
         row_angles(position_of(seg, (int)t), sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
-    auto heads = [&](int from, int to, int H, const float* w, __nv_bfloat16* y, Vec8& da, Vec8& db_) {
-      y += from * S * D;
-      for (int s = from, h = slot + from * S; s < to; ++s, h += S, y += S * D) {
-        fetch(stage == 0 ? kDepth - 1 : stage - 1);
-        copies_wait<kDepth - 1>();
-        const uint4* in = mine + 4 * stage * kRopeThreads;
-        stage = stage == kDepth - 1 ? 0 : stage + 1;
-        Vec8 g = unpack8(in[0]), f = unpack8(in[kRopeThreads]);
-        rotate(g, f, ang.cs, ang.neg, ang.sn, A.inter);  // by minus the angle
-        if (norm)
-          norm_backward<D>(g, f, unpack8(in[2 * kRopeThreads]), unpack8(in[3 * kRopeThreads]), w, m, A.eps, da, db_);
-        if (h < H) {
-          *reinterpret_cast<uint4*>(y) = pack8(g);
-          *reinterpret_cast<uint4*>(y + db) = pack8(f);
-        }
+    __nv_bfloat16* y = out + t * out_stride;
+    for (int s = from; s < to; ++s) {
+      fetch(stage == 0 ? kDepth - 1 : stage - 1);
+      copies_wait<kDepth - 1>();
+      const uint4* in = mine + 4 * stage * kRopeThreads;
+      stage = stage == kDepth - 1 ? 0 : stage + 1;
+      Vec8 g = unpack8(in[0]), f = unpack8(in[kRopeThreads]);
+      rotate(g, f, ang.cs, ang.neg, ang.sn, A.inter);  // by minus the angle
+      if (norm)
+        norm_backward<D>(g, f, unpack8(in[2 * kRopeThreads]), unpack8(in[3 * kRopeThreads]), w, m, A.eps, da, db_);
+      if (s * S + slot < H) {
+        *reinterpret_cast<uint4*>(y) = pack8(g);
+        *reinterpret_cast<uint4*>(y + db) = pack8(f);
       }
-    };
-    heads(walk.begin, min(walk.end, walk.nq), A.Hq, sh.w[0], A.q_out + t * A.q_out_stride + slot * D + m.a, qa, qb);
-    heads(max(walk.begin - walk.nq, 0), walk.end - walk.nq, A.Hkv, sh.w[1],
-          A.k_out + t * A.k_out_stride + slot * D + m.a, ka, kb);
+      y += S * D;
+    }
   }
   if (norm) {
     // every lane has waited for its own copies; the ring becomes the place of the block's sums
     copies_wait<0>();
     __syncthreads();
-    float* smem = reinterpret_cast<float*>(ring);
-    float* out = A.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * D;
-    block_weight_grad<D>(smem, m, slot, qa, qb, out);
-    block_weight_grad<D>(smem, m, slot, ka, kb, out + D);
+    block_weight_grad<D>(reinterpret_cast<float*>(ring), m, slot, da, db_,
+                         A.partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * D);
   }
 }
 
 // Weight gradients: column d of the blocks' partial sums, added in block order.
-// A block of 32 x 32 threads takes 32 columns; its rows of threads take contiguous
-// shares of the blocks, which are then added in order.
-__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restrict__ partial, int blocks, int D,
-                                                           float* __restrict__ dqw, float* __restrict__ dkw) {
+// A block of 32 x 32 threads takes 32 columns of q's or k's; its rows of threads take
+// contiguous shares of the blocks, which are then added in order.
+__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restrict__ partial, int qblocks, int kblocks,
+                                                           int D, float* __restrict__ dqw, float* __restrict__ dkw) {
   __shared__ float part[32][33];
-  const int col = blockIdx.x * 32 + threadIdx.x, per = (blocks + 31) / 32;
+  const int c = blockIdx.x * 32 + threadIdx.x, col = c % D;
+  const bool is_q = c < D;
+  const int blocks = is_q ? qblocks : kblocks, per = (blocks + 31) / 32;
   const int b0 = threadIdx.y * per, b1 = min(blocks, b0 + per);
+  if (!is_q) partial += (int64_t)qblocks * D;
   float v = 0.f;
   cudaGridDependencySynchronize();
 #pragma unroll 8
-  for (int b = b0; b < b1; ++b) v += partial[(int64_t)b * 2 * D + col];
+  for (int b = b0; b < b1; ++b) v += partial[(int64_t)b * D + col];
   part[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y) return;
 #pragma unroll
   for (int k = 1; k < 32; ++k) v += part[k][threadIdx.x];
-  if (col < D) dqw[col] = v;
-  else dkw[col - D] = v;
+  (is_q ? dqw : dkw)[col] = v;
 }
 
-// Blocks over the rows, and over the steps of a row where the rows alone would leave most warps
-// without work: at 192 rows of 32 + 8 heads of 128 the backward takes 7.0 us in a graph with its 10
-// steps spread, 10.4 with a warp walking all of them.
-dim3 rope_grid(int64_t T, int Hq, int Hkv, int D) {
+// Blocks over the rows (x) and over the steps of a row (y): as many block rows as it takes to give
+// the resident warps work when rows are few (192 rows of 32 + 8 heads of 128: the backward takes 8 us
+// in a graph, 10.4 with a warp walking all 10 steps of its row).  In the backward the first qparts of them take q's heads
+// and the others k's, so that a lane sums one tensor's weight gradients and needs 16 registers less for
+// them (410 against 422 us at 84,997 rows; the grid of four rounds took it to 398).
+constexpr int kRopeResident = 152 * 2;
+struct RopeGrid {
+  dim3 grid;
+  int qparts;
+};
+RopeGrid rope_grid(bool backward, int64_t T, int Hq, int Hkv, int D) {
   const int64_t need = (T + kRopeWarps - 1) / kRopeWarps;
-  const int S = 512 / D, steps = (Hq + S - 1) / S + (Hkv + S - 1) / S;
-  const int64_t spare = kRopeMaxBlocks / 2 / need;  // one round of the resident blocks
-  return dim3((unsigned)(need < kRopeMaxBlocks ? need : kRopeMaxBlocks),
-              (unsigned)(spare < 1 ? 1 : spare < steps ? spare : steps));
+  const int S = 512 / D, nq = (Hq + S - 1) / S, nk = (Hkv + S - 1) / S;
+  int64_t spare = kRopeResident / need;
+  if (spare < 1) spare = 1;
+  RopeGrid g;
+  g.grid = dim3((unsigned)(need < kRopeMaxBlocks ? need : kRopeMaxBlocks));
+  if (!backward) {
+    g.qparts = 0;
+    g.grid.y = (unsigned)(spare < nq + nk ? spare : nq + nk);
+  } else {
+    g.qparts = (int)(spare < nq ? spare : nq);
+    g.grid.y = (unsigned)(g.qparts + (spare < nk ? spare : nk));
+  }
+  return g;
 }
 
 template <int D, int CAP>
-cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, dim3 grid,
+cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, const RopeGrid& g,
                           cudaStream_t st) {
   const SegTable<CAP> s = make_segs<CAP>(P, N, off);
   const int smem = (backward ? 4 : 2) * kDepth * kRopeThreads * (int)sizeof(uint4);
@@ -479,45 +505,45 @@ cudaError_t launch_rope_c(bool backward, const RopeArgs& a, int P, int N, const 
     const cudaError_t e = cudaFuncSetAttribute(rope_bwd_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  if (backward) rope_bwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
-  else rope_fwd_kernel<D, CAP><<<grid, kRopeThreads, smem, st>>>(a, s);
+  if (backward) rope_bwd_kernel<D, CAP><<<g.grid, kRopeThreads, smem, st>>>(a, g.qparts, s);
+  else rope_fwd_kernel<D, CAP><<<g.grid, kRopeThreads, smem, st>>>(a, s);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_rope_d(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, dim3 grid,
+cudaError_t launch_rope_d(bool backward, const RopeArgs& a, int P, int N, const int32_t* off, const RopeGrid& g,
                           cudaStream_t st) {
-  return N <= kSmallSegs ? launch_rope_c<D, kSmallSegs>(backward, a, P, N, off, grid, st)
-                         : launch_rope_c<D, kMaxSegs>(backward, a, P, N, off, grid, st);
+  return N <= kSmallSegs ? launch_rope_c<D, kSmallSegs>(backward, a, P, N, off, g, st)
+                         : launch_rope_c<D, kMaxSegs>(backward, a, P, N, off, g, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(bool backward, int D, const RopeArgs& a, int P, int N, const int32_t* off, float* dqw,
                         float* dkw, cudaStream_t st) {
-  const dim3 grid = rope_grid(a.T, a.Hq, a.Hkv, D);
+  const RopeGrid g = rope_grid(backward, a.T, a.Hq, a.Hkv, D);
   cudaError_t e;
   switch (D) {
     case 64:
-      e = launch_rope_d<64>(backward, a, P, N, off, grid, st);
+      e = launch_rope_d<64>(backward, a, P, N, off, g, st);
       break;
     case 128:
-      e = launch_rope_d<128>(backward, a, P, N, off, grid, st);
+      e = launch_rope_d<128>(backward, a, P, N, off, g, st);
       break;
     case 512:
-      e = launch_rope_d<512>(backward, a, P, N, off, grid, st);
+      e = launch_rope_d<512>(backward, a, P, N, off, g, st);
       break;
     default:
       return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || !backward || !a.q_weight) return e;
-  return launch_behind(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), st, a.partial, (int)(grid.x * grid.y), D, dqw,
-                       dkw);
+  const int qblocks = (int)(g.grid.x * g.qparts), kblocks = (int)(g.grid.x * g.grid.y) - qblocks;
+  return launch_behind(rope_weight_kernel, dim3(2 * D / 32), dim3(32, 32), st, a.partial, qblocks, kblocks, D, dqw, dkw);
 }
 
 size_t rope_workspace_bytes(int64_t T, int Hq, int Hkv, int D) {
-  const dim3 grid = rope_grid(T, Hq, Hkv, D);
-  return (size_t)grid.x * grid.y * 2 * D * sizeof(float);
+  const dim3 grid = rope_grid(true, T, Hq, Hkv, D).grid;
+  return (size_t)grid.x * grid.y * D * sizeof(float);
 }
 
 }  // namespace dkv
