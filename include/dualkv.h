@@ -215,7 +215,8 @@ int dualkv_fold(const void* g_rep, void* g_packed, int P, int N, const int32_t* 
  *   y = n with each pair j < rope_dim/2 turned by the angle position * inv_freq[j]:
  *       (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin), where (a, b) is
  *       (j, j + rope_dim/2), or (2j, 2j + 1) if interleaved; values from rope_dim on are kept.
- * Computed in fp32 (angles in fp64) and rounded to bf16 once, at the end.
+ * Computed in fp32 (angles as fractions of a turn in 64-bit fixed point) and rounded to bf16 once,
+ * at the end; the squares have to stay within fp32's range (|x| below 1e18).
  *
  *   q, k            device bf16: head h of row t at [t * stride + h * D].  q_stride >= Hq * D
  *                   and k_stride >= Hkv * D in elements, multiples of 8, so q and k may be

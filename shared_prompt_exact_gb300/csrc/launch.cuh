@@ -6,7 +6,8 @@ namespace dkv {
 
 // The kernel may start while its predecessor still runs; it has to call
 // cudaGridDependencySynchronize() before it reads what that one writes.  Hides the launch
-// latency of a second, small kernel (about 2 us of 9 for the loss of 65,536 tokens).
+// latency of a second, small kernel: the loss of 4.04M tokens takes 33.5 us instead of 36.7
+// outside a graph (within one, 0.1 us less).
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};

@@ -24,12 +24,12 @@
 // to kClusterBlocks blocks run as one cluster whose first block joins the records from its shared
 // memory; more write them to the workspace for a second launch.
 //
-// Up to some 100,000 tokens a call is launch latency (6 to 9 us in a graph).  At 4.04M tokens
-// (1,024 responses, every input in use) the forward takes 33 us, 2.6 TB/s, 6 of them the join,
-// and the gradients 24 us, 4.2 TB/s.  The sums are bound by the comparisons and selects around the
-// bounds (the ALU pipe is 68 % busy) and memory latency together; the arithmetic is on f32x2
-// pairs of tokens, which took a tenth off both.  Four tokens a thread in chunks of 1,024 beat
-// eight in 2,048 (40 against 46 us cold): more resident threads outweigh fewer blocks.
+// Up to some 100,000 tokens a call is launch latency (in a graph 4.5 to 5.3 us, the gradients 2 to
+// 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 33 us, 2.6 TB/s,
+// 6 of them the join, and the gradients 24 us, 4.2 TB/s.  The sums are bound by the comparisons and
+// selects around the bounds (the ALU pipe is 68 % busy) and memory latency together; the arithmetic
+// is on f32x2 pairs of tokens, which took a tenth off both.  Four tokens a thread in chunks of
+// 1,024 beat eight in 2,048 (40 against 46 us cold): more resident threads outweigh fewer blocks.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

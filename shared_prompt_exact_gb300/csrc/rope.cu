@@ -197,7 +197,7 @@ __device__ __forceinline__ void copies_wait() {
 
 // A warp's walk: rows t, t + stride, ..., in each row the steps [begin, end) of those that take q's
 // heads, S = 32 / G at a time, and those behind them that take k's.  Block rows (blockIdx.y) share a
-// row's steps: the first `qparts` of them q's; with `both` there is one for all steps.
+// row's steps: the first `qparts` of them q's and the others k's, or (`both`) all of them all steps.
 template <int D>
 struct Walk {
   static constexpr int S = 32 / (D / 16);
@@ -471,9 +471,10 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restri
 
 // Blocks over the rows (x) and over the steps of a row (y): as many block rows as it takes to give
 // the resident warps work when rows are few (192 rows of 32 + 8 heads of 128: the backward takes 8 us
-// in a graph, 10.4 with a warp walking all 10 steps of its row).  In the backward the first qparts of them take q's heads
-// and the others k's, so that a lane sums one tensor's weight gradients and needs 16 registers less for
-// them (410 against 422 us at 84,997 rows; the grid of four rounds took it to 398).
+// in a graph, 10.4 with a warp walking all 10 steps of its row).  In the backward the first qparts of
+// them take q's heads and the others k's, so that a lane sums one tensor's weight gradients and
+// needs 16 registers less for them (410 against 422 us at 84,997 rows; the grid of four rounds took
+// it to 398).
 constexpr int kRopeResident = 152 * 2;
 struct RopeGrid {
   dim3 grid;
