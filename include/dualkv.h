@@ -313,7 +313,7 @@ int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype,
  *   advantages  device fp32, [N], or [R_offsets[N]] if per_token
  *   mask        device bytes [R_offsets[N]], 0: not live, nothing of the token's other
  *               inputs is used; NULL: all are live
- *   clip_low    in [0, 1); clip_high >= 0; dual_clip 0 or > 1
+ *   clip_low    in [0, 1); clip_high >= 0; dual_clip 0 or > 1; these and the coefficients up to 1e30
  *   loss        device fp32 [1], written
  *   stats       device fp32 [4], written: the weighted sums of policy, kl (0 without
  *               ref_logp) and entropy (0 without entropy), and the share of live tokens

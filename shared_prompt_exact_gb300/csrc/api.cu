@@ -528,7 +528,7 @@ int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int
               float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
   if (validate_layout(P, N, R_offsets, Hq, Hkv, D)) return DUALKV_ERR_INVALID;
   const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
-  if (wq > INT32_MAX) return DUALKV_ERR_INVALID;
+  if (wq > INT32_MAX / 2) return DUALKV_ERR_INVALID;
   if (!q || !k || !q_out || !k_out || (backward && (!dq_out || !dk_out))) return DUALKV_ERR_INVALID;
   for (int64_t s : {q_stride, q_out_stride})
     if (s < wq || s > kMaxRowStride || s % 8) return DUALKV_ERR_INVALID;
@@ -637,9 +637,10 @@ int policy_impl(bool backward, const float* logp, const float* old_logp, const f
                 float* dlogp, float* dentropy, void* stream) {
   const int rc_layout = check_segments(1, N, R_offsets);  // a batch without tokens is one with loss 0
   if (rc_layout) return rc_layout;
-  if (!(clip_low >= 0.0 && clip_low < 1.0) || !(clip_high >= 0.0) || !std::isfinite(clip_high)) return DUALKV_ERR_INVALID;
-  if (dual_clip != 0.0 && (!(dual_clip > 1.0) || !std::isfinite(dual_clip))) return DUALKV_ERR_INVALID;
-  if (!std::isfinite(kl_coef) || !std::isfinite(entropy_coef)) return DUALKV_ERR_INVALID;
+  constexpr double kMost = 1e30;  // the kernels hold these in fp32
+  if (!(clip_low >= 0.0 && clip_low < 1.0) || !(clip_high >= 0.0 && clip_high <= kMost)) return DUALKV_ERR_INVALID;
+  if (dual_clip != 0.0 && !(dual_clip > 1.0 && dual_clip <= kMost)) return DUALKV_ERR_INVALID;
+  if (!(std::fabs(kl_coef) <= kMost) || !(std::fabs(entropy_coef) <= kMost)) return DUALKV_ERR_INVALID;
   if (reduction < 0 || reduction > DUALKV_LOSS_SEQ_SUM) return DUALKV_ERR_INVALID;
   const uint64_t n = (uint64_t)R_offsets[N];
   if (n > 0 && (!logp || !old_logp || !advantages || (kl_coef != 0.0 && !ref_logp))) return DUALKV_ERR_INVALID;

@@ -126,7 +126,7 @@ def test_policy_refusals(lib, backward):
     nan = float("nan")
     for kw in (dict(N=0), dict(off=None), dict(off=[0, 3, 2]), dict(off=[1, 2, 3]), dict(lp=0), dict(old=0), dict(ref=0),
                dict(adv=0), dict(w=0), dict(lo=1.0), dict(lo=-0.1), dict(lo=nan), dict(hi=-1.0), dict(hi=nan), dict(dual=1.0),
-               dict(dual=nan), dict(kl=nan), dict(ec=float("inf"))):
+               dict(dual=nan), dict(kl=nan), dict(ec=float("inf")), dict(hi=1e31), dict(dual=1e31), dict(kl=-1e31)):
         assert _policy(lib, backward, **kw) == dk.DUALKV_ERR_INVALID, kw
     for kw in (dict(lp=0x100002), dict(adv=0x104001), dict(w=0x108003)):
         assert _policy(lib, backward, **kw) == dk.DUALKV_ERR_ALIGN, kw
