@@ -175,39 +175,41 @@ __device__ __forceinline__ Kl kl_of(float2 x) {
   return r;
 }
 
-// Two tokens' bounded ratios less 1, as v + rest, and whether they are bounds.  The difference from
-// 1 is kept apart because policy terms of either sign cancel: A (1 + v + rest) is then summed from
-// A, which is exact, and two products of small factors.
+// Two tokens' bounded ratios as base + v + rest, and whether they are bounds.  base is 1 for a bound
+// and a ratio near 1: policy terms of either sign cancel, and A (1 + v + rest) is then summed from A,
+// which is exact, and two products of small factors.  A ratio that is far from 1 has base 0.
 struct Term {
-  float2 v, rest;
+  float2 base, v, rest;
   bool clipped_x, clipped_y;
 };
 __device__ __forceinline__ Term term_of(const PolicyArgs& A, float2 logp, float2 old, float2 adv) {
   float2 e;
   const float2 d = exact_diff(logp, old, &e);
   Term t;
+  t.base = both(1.f);
   t.v = d;
   t.rest = fadd2(series(d), e);  // e^d - 1 = d + series
   if (far(d)) {
-    auto direct = [](float x, float a, float& v, float& rest) {
+    auto direct = [](float x, float err, float a, float& base, float& v, float& rest) {
       if (fabsf(x) < 1.f) return;
-      v = a == 0.f ? 0.f : expf(x) - 1.f;  // not 0 * inf
-      rest = 0.f;
+      base = 0.f;
+      v = a == 0.f ? 0.f : expf(x);  // not 0 * inf
+      rest = fabsf(x) < 80.f ? v * err : 0.f;
     };
-    direct(d.x, adv.x, t.v.x, t.rest.x);
-    direct(d.y, adv.y, t.v.y, t.rest.y);
+    direct(d.x, e.x, adv.x, t.base.x, t.v.x, t.rest.x);
+    direct(d.y, e.y, adv.y, t.base.y, t.v.y, t.rest.y);
   }
   const bool gx = adv.x > 0.f, gy = adv.y > 0.f, lx = adv.x < 0.f, ly = adv.y < 0.f;
   const float2 x = beyond(d, e, pick(gx, gy, A.up.hi, A.down.hi), pick(gx, gy, A.up.lo, A.down.lo));
   t.clipped_x = gx ? x.x > 0.f : lx && x.x < 0.f;
   t.clipped_y = gy ? x.y > 0.f : ly && x.y < 0.f;
   const float2 bv = pick(gx, gy, A.add_up.hi, A.add_down.hi), br = pick(gx, gy, A.add_up.lo, A.add_down.lo);
-  if (t.clipped_x) t.v.x = bv.x, t.rest.x = br.x;
-  if (t.clipped_y) t.v.y = bv.y, t.rest.y = br.y;
+  if (t.clipped_x) t.base.x = 1.f, t.v.x = bv.x, t.rest.x = br.x;
+  if (t.clipped_y) t.base.y = 1.f, t.v.y = bv.y, t.rest.y = br.y;
   if (A.has_dual) {
-    const float2 far_up = beyond(d, e, both(A.dual.hi), both(A.dual.lo));
-    if (lx && far_up.x > 0.f) t.v.x = A.add_dual.hi, t.rest.x = A.add_dual.lo, t.clipped_x = true;
-    if (ly && far_up.y > 0.f) t.v.y = A.add_dual.hi, t.rest.y = A.add_dual.lo, t.clipped_y = true;
+    const float2 up = beyond(d, e, both(A.dual.hi), both(A.dual.lo));
+    if (lx && up.x > 0.f) t.base.x = 1.f, t.v.x = A.add_dual.hi, t.rest.x = A.add_dual.lo, t.clipped_x = true;
+    if (ly && up.y > 0.f) t.base.y = 1.f, t.v.y = A.add_dual.hi, t.rest.y = A.add_dual.lo, t.clipped_y = true;
   }
   return t;
 }
@@ -268,10 +270,10 @@ __device__ __forceinline__ Partial sum_tokens(const PolicyArgs& A, const Chunk& 
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;  // the same for the whole block
     const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
     const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
-    const float2 p = fmul2(a, t.v);
-    float2 y = fadd2(a, p);
-    // the errors of the product, of the sum (|v| <= 1 but for far ratios), and the rest
-    float2 z = ffma2(a, t.rest, fadd2(ffma2(a, t.v, fsub2(zero, p)), fsub2(p, fsub2(y, a))));
+    const float2 p = fmul2(a, t.v), ab = fmul2(a, t.base);
+    float2 y = fadd2(ab, p);
+    // the errors of the product, of the sum (|v| <= 1 but for bounds above 2), and the rest
+    float2 z = ffma2(a, t.rest, fadd2(ffma2(a, t.v, fsub2(zero, p)), fsub2(p, fsub2(y, ab))));
     float2 h = make_float2(x.ent[k], x.ent[k + 1]), v = zero;
     if (A.ref_logp) v = kl_of(fsub2(make_float2(x.ref[k], x.ref[k + 1]), logp)).kl;
     if (!x.on[k]) y.x = z.x = h.x = v.x = 0.f;
@@ -454,7 +456,7 @@ __device__ __forceinline__ void token_gradients(const PolicyArgs& A, const Chunk
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;
     const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
     const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
-    float2 g = fmul2(a, fadd2(both(1.f), fadd2(t.v, t.rest)));  // sign turned by the factor below
+    float2 g = fmul2(a, fadd2(t.base, fadd2(t.v, t.rest)));  // sign turned by the factor below
     if (t.clipped_x) g.x = 0.f;
     if (t.clipped_y) g.y = 0.f;
     if (A.ref_logp) g = ffma2(both(b), kl_of(fsub2(make_float2(x.ref[k], x.ref[k + 1]), logp)).slope, g);
