@@ -77,6 +77,13 @@ __device__ __forceinline__ Vec8 load8(const float* p, const float* q) {  // 4 fl
   return Vec8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
+// Place of value d of n in shared memory: the first four of every Vec8, then the last four, so that
+// neighbouring lanes read neighbouring 16 bytes.
+__device__ __forceinline__ int split_at(int d, int n) {
+  const int p = vec8_at(d) & 7;
+  return (p < 4 ? 0 : n / 2) + (d >> 3) * 4 + (p & 3);
+}
+
 // Where a lane's vectors A and B lie in a head, and the angles that turn them: 4 from ja
 // and 4 from jb on (both of no use where the lane's values are not turned).  In both layouts
 // neighbouring lanes read neighbouring vectors.
@@ -88,7 +95,7 @@ struct LaneMap {
 template <int D>
 __device__ __forceinline__ LaneMap lane_map(int i, int half, bool inter) {
   if (inter) return LaneMap{8 * i, D / 2 + 8 * i, 4 * i, D / 4 + 4 * i, 4 * i < half, D / 4 + 4 * i < half};
-  if (8 * i < half) return LaneMap{8 * i, half + 8 * i, 8 * i, 8 * i + 4, true, true};
+  if (8 * i < half) return LaneMap{8 * i, half + 8 * i, 4 * i, half / 2 + 4 * i, true, true};
   return LaneMap{half + 8 * i, D / 2 + 8 * i, 0, 0, false, false};  // behind the turned 2 half values
 }
 
@@ -101,8 +108,8 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
   return (uint64_t)__double2ull_rd(t * 18446744073709551616.0);  // t < 1; 2^64 itself saturates
 }
 
-// What a block keeps in shared memory: frequencies, effective weights w + w0 of q and k in
-// Vec8 order, and every warp's cosines and sines.
+// What a block keeps in shared memory: frequencies, effective weights w + w0 of q and k (split_at),
+// and every warp's cosines and sines.
 template <int D>
 struct RopeShared {
   alignas(16) float w[2][D];
@@ -118,7 +125,7 @@ __device__ __forceinline__ void load_shared(const RopeArgs& A, RopeShared<D>& s)
     for (int d = threadIdx.x; d < 2 * D; d += kRopeThreads) {
       const void* w = d < D ? A.q_weight : A.k_weight;
       const int e = d % D;
-      s.w[d / D][vec8_at(e)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
+      s.w[d / D][split_at(e, D)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
                                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]));
     }
   }
@@ -150,7 +157,7 @@ __device__ __forceinline__ Angles row_angles(int p, const uint64_t* freq, int ha
   __syncwarp();
   for (int j = lane; j < half; j += 32) {
     const int turns = (int)(uint32_t)(((uint64_t)(uint32_t)p * freq[j]) >> 32);
-    const int at = inter ? j : vec8_at(j);
+    const int at = inter ? j : split_at(j, half);
     sincospif((float)turns * 4.656612873077393e-10f, ws + at, wc + at);  // 2^-31: half turns
   }
   __syncwarp();
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
           for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
           const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
           const float2 rr = make_float2(r, r);
-          const Vec8 wa = load8(w + m.a, w + m.a + 4), wb = load8(w + m.b, w + m.b + 4);
+          const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
@@ -324,7 +331,7 @@ template <int D>
 __device__ __forceinline__ void norm_backward(Vec8& g, Vec8& f, const Vec8& a, const Vec8& b, const float* w,
                                               const LaneMap& m, float eps, Vec8& da, Vec8& db) {
   constexpr int G = D / 16;
-  const Vec8 wa = load8(w + m.a, w + m.a + 4), wb = load8(w + m.b, w + m.b + 4);
+  const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
   float2 ss = make_float2(0.f, 0.f), ux = ss;
   Vec8 ua, ub;
 #pragma unroll
@@ -361,9 +368,9 @@ __device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m,
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-    if (slot == 0) {
-      smem[warp * D + m.a + e] = a;
-      smem[warp * D + m.b + e] = b;
+    if (slot == 0) {  // value e of every vector together: neighbouring lanes write neighbouring words
+      smem[warp * D + e * (D / 8) + m.a / 8] = a;
+      smem[warp * D + e * (D / 8) + m.b / 8] = b;
     }
   }
   __syncthreads();
@@ -371,7 +378,7 @@ __device__ __forceinline__ void block_weight_grad(float* smem, const LaneMap& m,
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < kRopeWarps; ++k) v += smem[k * D + d];
-    out[d] = v;
+    out[d % (D / 8) * 8 + d / (D / 8)] = v;
   }
   __syncthreads();
 }
