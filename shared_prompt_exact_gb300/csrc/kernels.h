@@ -160,8 +160,6 @@ cudaError_t launch_pack(int kind, const void* src, void* dst, const int32_t* d_o
                         int row_elems, int num_sms, cudaStream_t st);
 
 // ---- per-head norm and rotation of q and k (rope.cu)
-constexpr int kRopeMaxBlocks = 152 * 8;  // four rounds of the resident blocks
-
 struct RopeArgs {
   const __nv_bfloat16 *q, *k;            // projections' rows, head h of row t at t * stride + h * D
   int64_t q_stride, k_stride;            // elements

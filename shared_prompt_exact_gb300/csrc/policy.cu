@@ -25,7 +25,7 @@
 // memory; more write them to the workspace for a second launch.
 //
 // Up to some 100,000 tokens a call is launch latency (in a graph 4.5 to 5.3 us, the gradients 2 to
-// 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 33 us, 2.6 TB/s,
+// 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 32 us, 2.6 TB/s,
 // 6 of them the join, and the gradients 24 us, 4.2 TB/s.  The sums are bound by the comparisons and
 // selects around the bounds (the ALU pipe is 68 % busy) and memory latency together; the arithmetic
 // is on f32x2 pairs of tokens, which took a tenth off both.  Four tokens a thread in chunks of
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kFinishThreads) policy_finish_kernel(const Pol
   for (int n = threadIdx.x; n < N; n += kFinishThreads) live[n] = 0;
   __syncthreads();
   cudaGridDependencySynchronize();
-  finish<kFinishThreads, 8>(A, static_cast<const Record*>(A.records), blocks, N, live);
+  finish<kFinishThreads, 10>(A, static_cast<const Record*>(A.records), blocks, N, live);
 }
 
 // The whole forward as one cluster of gridDim.x <= kClusterBlocks blocks.

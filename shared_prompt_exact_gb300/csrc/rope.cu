@@ -17,10 +17,10 @@
 // pair lie in it.  Loads run ahead of their use through shared memory
 // (cp.async); arithmetic is on f32x2 pairs, because with plain fp32 the backward
 // was bound by issue (64 % of the slots) as much as by memory.  Measured: forward
-// 226 us for 71,680 rows of 32 + 8 heads of 128 (6.5 TB/s, 0.96 of the measured
-// copy bandwidth; 331 us with loads straight into registers), backward 398 us for
-// 84,997 such rows (6.6 TB/s; 868 us) and 187 us for 36,522 rows of 8 + 2 heads of
-// 512 (6.0 TB/s; 496 us, with loads of every other vector).
+// 227 us for 71,680 rows of 32 + 8 heads of 128 (6.5 TB/s, 0.95 of the measured
+// copy bandwidth; 331 us with loads straight into registers), backward 392 us for
+// 84,997 such rows (6.7 TB/s; 868 us) and 180 us for 36,522 rows of 8 + 2 heads of
+// 512 (6.2 TB/s; 496 us, with loads of every other vector).
 //
 // Angles: p f is formed in 64-bit fixed point as a fraction of a turn, and only
 // that fraction goes to fp32; at p = 10^5 a product in fp32 would already be off
@@ -41,8 +41,8 @@ namespace {
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
 // Steps in a lane's ring: the one in use and those that its copies run ahead.  Three keep 32 KB
-// (forward) and 64 KB (backward) per SM in flight; with 4 to 6 and grids of 304 to 1216 blocks the
-// times above moved by less than 4 %.  Two blocks per SM: three leave the backward 80 registers, and
+// (forward) and 64 KB (backward) per SM in flight; with 4 to 6 and grids of 608 to 2432 blocks the
+// times above moved by less than 4 % (304 blocks: 7 % more).  Two blocks per SM: three leave the backward 80 registers, and
 // it then spills (464 us instead of 404).
 constexpr int kDepth = 3;
 
@@ -480,9 +480,11 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restri
 // the resident warps work when rows are few (192 rows of 32 + 8 heads of 128: the backward takes 8 us
 // in a graph, 10.4 with a warp walking all 10 steps of its row).  In the backward the first qparts of
 // them take q's heads and the others k's, so that a lane sums one tensor's weight gradients and
-// needs 16 registers less for them (410 against 422 us at 84,997 rows; the grid of four rounds took
-// it to 398).
+// needs 16 registers less for them (410 against 422 us at 84,997 rows).
 constexpr int kRopeResident = 152 * 2;
+// Most blocks over the rows: 912 for the backward, whose blocks end with a sum (1,824: the same time),
+// 1,824 for the forward (912: 1 % more).
+constexpr int kRopeFwdBlocks = 152 * 12, kRopeBwdBlocks = 152 * 6;
 struct RopeGrid {
   dim3 grid;
   int qparts;
@@ -492,8 +494,9 @@ RopeGrid rope_grid(bool backward, int64_t T, int Hq, int Hkv, int D) {
   const int S = 512 / D, nq = (Hq + S - 1) / S, nk = (Hkv + S - 1) / S;
   int64_t spare = kRopeResident / need;
   if (spare < 1) spare = 1;
+  const int most = backward ? kRopeBwdBlocks : kRopeFwdBlocks;
   RopeGrid g;
-  g.grid = dim3((unsigned)(need < kRopeMaxBlocks ? need : kRopeMaxBlocks));
+  g.grid = dim3((unsigned)(need < most ? need : most));
   if (!backward) {
     g.qparts = 0;
     g.grid.y = (unsigned)(spare < nq + nk ? spare : nq + nk);
