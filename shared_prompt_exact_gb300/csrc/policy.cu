@@ -15,7 +15,7 @@
 // Policy terms of either sign cancel in the sum, so each is summed as -A and -A (ratio - 1): -A is
 // exact, ratio - 1 comes from the same series as the KL term, and the sums keep their rounding
 // errors beside them.  fp64 would do the same, but its adds run at two lanes per clock and SM
-// here: with fp64 trees a call on 4M tokens took 172 us instead of 33.
+// here: with fp64 trees a call on 4M tokens took 172 us instead of 32.
 //
 // A block takes up to kPolicyChunk tokens of ONE segment, all of whose loads are issued before
 // the first is used, and makes one record of sums; a single block then turns the records into
@@ -26,7 +26,7 @@
 //
 // Up to some 100,000 tokens a call is launch latency (in a graph 4.5 to 5.3 us, the gradients 2 to
 // 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 32 us, 2.6 TB/s,
-// 6 of them the join, and the gradients 24 us, 4.2 TB/s.  The sums are bound by the comparisons and
+// 6 of them the join, and the gradients 23 us, 4.5 TB/s.  The sums are bound by the comparisons and
 // selects around the bounds (the ALU pipe is 68 % busy) and memory latency together; the arithmetic
 // is on f32x2 pairs of tokens, which took a tenth off both.  Four tokens a thread in chunks of
 // 1,024 beat eight in 2,048 (40 against 46 us cold): more resident threads outweigh fewer blocks.
@@ -178,10 +178,12 @@ __device__ __forceinline__ Kl kl_of(float2 x) {
 // Two tokens' bounded ratios as base + v + rest, and whether they are bounds.  base is 1 for a bound
 // and a ratio near 1: policy terms of either sign cancel, and A (1 + v + rest) is then summed from A,
 // which is exact, and two products of small factors.  A ratio that is far from 1 has base 0.
+// Without BOUNDED the ratio is left unbounded (the backward only needs to know).
 struct Term {
   float2 base, v, rest;
   bool clipped_x, clipped_y;
 };
+template <bool BOUNDED>
 __device__ __forceinline__ Term term_of(const PolicyArgs& A, float2 logp, float2 old, float2 adv) {
   float2 e;
   const float2 d = exact_diff(logp, old, &e);
@@ -203,14 +205,21 @@ __device__ __forceinline__ Term term_of(const PolicyArgs& A, float2 logp, float2
   const float2 x = beyond(d, e, pick(gx, gy, A.up.hi, A.down.hi), pick(gx, gy, A.up.lo, A.down.lo));
   t.clipped_x = gx ? x.x > 0.f : lx && x.x < 0.f;
   t.clipped_y = gy ? x.y > 0.f : ly && x.y < 0.f;
-  const float2 bv = pick(gx, gy, A.add_up.hi, A.add_down.hi), br = pick(gx, gy, A.add_up.lo, A.add_down.lo);
-  if (t.clipped_x) t.base.x = 1.f, t.v.x = bv.x, t.rest.x = br.x;
-  if (t.clipped_y) t.base.y = 1.f, t.v.y = bv.y, t.rest.y = br.y;
+  bool far_x = false, far_y = false;
   if (A.has_dual) {
     const float2 up = beyond(d, e, both(A.dual.hi), both(A.dual.lo));
-    if (lx && up.x > 0.f) t.base.x = 1.f, t.v.x = A.add_dual.hi, t.rest.x = A.add_dual.lo, t.clipped_x = true;
-    if (ly && up.y > 0.f) t.base.y = 1.f, t.v.y = A.add_dual.hi, t.rest.y = A.add_dual.lo, t.clipped_y = true;
+    far_x = lx && up.x > 0.f;
+    far_y = ly && up.y > 0.f;
   }
+  if (BOUNDED) {
+    const float2 bv = pick(gx, gy, A.add_up.hi, A.add_down.hi), br = pick(gx, gy, A.add_up.lo, A.add_down.lo);
+    if (t.clipped_x) t.base.x = 1.f, t.v.x = bv.x, t.rest.x = br.x;
+    if (t.clipped_y) t.base.y = 1.f, t.v.y = bv.y, t.rest.y = br.y;
+    if (far_x) t.base.x = 1.f, t.v.x = A.add_dual.hi, t.rest.x = A.add_dual.lo;
+    if (far_y) t.base.y = 1.f, t.v.y = A.add_dual.hi, t.rest.y = A.add_dual.lo;
+  }
+  t.clipped_x |= far_x;
+  t.clipped_y |= far_y;
   return t;
 }
 
@@ -269,7 +278,7 @@ __device__ __forceinline__ Partial sum_tokens(const PolicyArgs& A, const Chunk& 
   for (int k = 0; k < kPerThread; k += 2) {
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;  // the same for the whole block
     const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
-    const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
+    const Term t = term_of<true>(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
     const float2 p = fmul2(a, t.v), ab = fmul2(a, t.base);
     float2 y = fadd2(ab, p);
     // the errors of the product, of the sum (|v| <= 1 but for bounds above 2), and the rest
@@ -455,7 +464,7 @@ __device__ __forceinline__ void token_gradients(const PolicyArgs& A, const Chunk
   for (int k = 0; k < kPerThread; k += 2) {
     if (!FULL && c.lo + k * kPolicyThreads >= c.hi) break;
     const float2 logp = make_float2(x.logp[k], x.logp[k + 1]), a = make_float2(x.adv[k], x.adv[k + 1]);
-    const Term t = term_of(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
+    const Term t = term_of<false>(A, logp, make_float2(x.old[k], x.old[k + 1]), a);
     float2 g = fmul2(a, fadd2(t.base, fadd2(t.v, t.rest)));  // sign turned by the factor below
     if (t.clipped_x) g.x = 0.f;
     if (t.clipped_y) g.y = 0.f;
