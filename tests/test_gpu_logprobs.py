@@ -460,3 +460,23 @@ def test_calls_of_two_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("V", [65, 70003])
+def test_forward_without_log_sums(V):
+    # scoring alone needs neither lse nor entropies
+    P, off = 2, [0, 3, 5]
+    logits, tok, _, _ = _inputs(P, off, V, BF, 0, 15)
+    want = dk.token_logprobs(logits, tok, P, off)
+    logp = torch.full((5,), float("nan"), device="cuda")
+    dk.dualkv_token_logprobs(logits, tok, 1.0, P, 2, off, logp, None, None)
+    assert torch.equal(logp, want[0])
+
+
+def test_tensors_of_another_device_are_refused():
+    # the binding compares with the calling thread's current device (here: a device that these are not on)
+    t = torch.zeros(3, device="cuda")
+    with pytest.raises(ValueError, match="current device"):
+        dk._arg("call", "t", t, (3,), (F32,), t.get_device() + 1)
+    with pytest.raises(ValueError, match="current device"):
+        dk._workspace_args("call", t, None, t.get_device() + 1)

@@ -100,6 +100,7 @@ CASES = [
     ("rotation-only", 8, [0, 9, 30], 4, 2, 128, 128, False, None, 0.0, True),
     ("rotation-only-part", 8, [0, 9, 30], 3, 3, 64, 48, True, None, 0.0, False),
     ("many-segments", 3, [0] + np.cumsum(np.arange(300) % 3).tolist(), 2, 2, 64, 64, False, BF, 0.0, False),
+    ("most-segments", 2, [0] + np.cumsum(np.arange(4095) % 2).tolist(), 2, 1, 64, 32, True, torch.float32, 0.0, True),
     ("many-rows", 3001, [0, 4000, 9001], 3, 1, 64, 64, False, BF, 0.0, False),
 ]
 
