@@ -233,7 +233,7 @@ int dualkv_fold(const void* g_rep, void* g_packed, int P, int N, const int32_t* 
  *   dq_weight, dk_weight  device fp32 [D], written; sums over rows and heads in a fixed order
  *                   (not written without weights)
  *   workspace       device, 256-byte aligned, >= dualkv_qk_norm_rope_bwd_workspace_bytes()
- *                   (0 for invalid input); not needed without weights
+ *                   (0 for invalid input); not needed without weights; calls that may overlap need one each
  * No output may share memory with an input or with another output (columns of one fused
  * buffer with equal strides may interleave): DUALKV_ERR_INVALID.
  * These calls keep nothing between calls and may be captured into a CUDA graph.
@@ -265,8 +265,8 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
  *               dlogp[i] (1[v = tokens[i]] - p_v) - dentropy[i] p_v (z_v - lse + entropy[i])
  * (the prompt's last row sums over the segments).  Statistics are fp32.
  *
- *   logits      device, bf16 or fp32 (dtype DUALKV_BF16 / DUALKV_F32), [M, V], rows row_stride >= V
- *               elements apart; only element alignment is needed.  -inf marks masked entries;
+ *   logits      device, bf16 or fp32 (dtype DUALKV_BF16 / DUALKV_F32), [M, V], V up to 2^30, rows
+ *               row_stride >= V elements apart; only element alignment is needed.  -inf marks masked entries;
  *               a NaN or +inf makes its row's results NaN; a row that is -inf throughout has
  *               lse = logp = -inf, entropy 0 and gradient 0
  *   scale       > 0, an inverse temperature

@@ -519,6 +519,7 @@ int guarded(F&& body) noexcept {
   }
 }
 
+constexpr int kMaxVocab = 1 << 30;  // the kernels step through a row with an int
 constexpr int64_t kMaxRowStride = int64_t(1) << 31;  // elements: rows x stride x 4 bytes stays far inside 64 bits
 
 int rope_impl(bool backward, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
@@ -588,7 +589,7 @@ int logp_impl(bool backward, const void* logits, int64_t row_stride, int dtype, 
   if (rc_layout) return rc_layout;
   const int64_t n = R_offsets[N], M = n + (P > 0 ? 1 : 0);
   if (dtype != DUALKV_BF16 && dtype != DUALKV_F32) return DUALKV_ERR_INVALID;
-  if (V < 1 || row_stride < V || row_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
+  if (V < 1 || V > kMaxVocab || row_stride < V || row_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
   if (!(scale > 0.f) || !std::isfinite(scale)) return DUALKV_ERR_INVALID;
   if (!logits || (n > 0 && !tokens)) return DUALKV_ERR_INVALID;
   const uint64_t esz = dtype == DUALKV_F32 ? 4 : 2, un = (uint64_t)n, uM = (uint64_t)M;

@@ -3,6 +3,7 @@ case below is refused before any device work; no pointer is dereferenced."""
 import ctypes
 
 import pytest
+import torch
 
 from shared_prompt_exact_gb300 import build as pbuild
 from shared_prompt_exact_gb300 import dualkv as dk
@@ -144,3 +145,12 @@ def test_policy_outputs_and_workspace(lib):
         assert _policy(lib, True, **kw) == bad, kw
     assert lib.dualkv_policy_loss_workspace_bytes(2, dk.offsets(OK_OFF)) > 0
     assert lib.dualkv_policy_loss_workspace_bytes(2, dk.offsets([0, 3, 1])) == 0
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_logprobs_vocabulary_limit(lib, backward):
+    far = dict(x=1 << 44, dx=1 << 45, xs=1 << 31, dxs=1 << 31)
+    for V in ((1 << 30) + 1, (1 << 31) - 1):
+        assert _logp(lib, backward, V=V, **far) == dk.DUALKV_ERR_INVALID
+    if not torch.cuda.is_available():  # the largest passes the checks, and there is no device to run it
+        assert _logp(lib, backward, V=1 << 30, **far) == dk.DUALKV_ERR_CUDA
