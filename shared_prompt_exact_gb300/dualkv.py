@@ -395,12 +395,31 @@ _MASK_DTYPES = (torch.bool, torch.uint8)
 _Tensor = torch.Tensor
 
 
-def _arg(where, name, t, shape, dtypes, device, rows=False):
-    """Address of a CUDA tensor on the calling thread's current device, with this shape and one of these dtypes,
-    contiguous or (rows) only contiguous within a row of its first dimension.  Raises if it is none."""
+def _arg(where, name, t, shape, dtypes, device):
+    """Address of a contiguous CUDA tensor on the calling thread's current device, with this shape and one of these
+    dtypes.  Raises if it is none."""
     if (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == device
-            and (t.is_contiguous() or (rows and _rows_contiguous(t)))):
+            and t.is_contiguous()):
         return t.data_ptr()
+    _refuse(where, name, t, shape, dtypes, device, "must be contiguous")
+
+
+def _opt(where, name, t, shape, dtypes, device):
+    """The same for a tensor that may be missing."""
+    return None if t is None else _arg(where, name, t, shape, dtypes, device)
+
+
+def _rows(where, name, t, shape, inner, dtypes, device):
+    """Address and row stride (in elements) of a CUDA tensor that is contiguous within each row of its first
+    dimension: `inner` are the strides behind that one.  A single row has the stride that its width gives."""
+    if isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == device:
+        strides = t.stride()
+        if strides[1:] == inner or all(n == 1 or a == b for n, a, b in zip(shape[1:], strides[1:], inner)):
+            return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1] * inner[0]
+    _refuse(where, name, t, shape, dtypes, device, "must be contiguous within its rows")
+
+
+def _refuse(where, name, t, shape, dtypes, device, layout):
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{where}: {name} must be a CUDA tensor")
     if t.get_device() != device:
@@ -409,28 +428,7 @@ def _arg(where, name, t, shape, dtypes, device, rows=False):
         raise ValueError(f"{where}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)} for this call, got {tuple(t.shape)}")
-    raise ValueError(f"{where}: {name} must be contiguous" + (" within its rows" if rows else ""))
-
-
-def _opt(where, name, t, shape, dtypes, device):
-    """The same for a tensor that may be missing."""
-    return None if t is None else _arg(where, name, t, shape, dtypes, device)
-
-
-def _rows_contiguous(t):
-    """Whether each slice of t along its first dimension is contiguous."""
-    width = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != width:
-            return False
-        width *= n
-    return True
-
-
-def _row_stride(t):
-    """Elements between the rows of t's first dimension (a single row has the stride that its width gives)."""
-    n = t.shape[0]
-    return t.stride(0) if n > 1 else t.numel() // max(n, 1)
+    raise ValueError(f"{where}: {name} {layout}")
 
 
 # the current stream's handle without an object around it, where this PyTorch has that (1 us per call)
@@ -460,8 +458,8 @@ def _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, ro
     arguments from the weights to D)."""
     T = _layout_rows(where, P, N, R_offsets)
     dev = torch.cuda.current_device()
-    qk = (_arg(where, "q", q, (T, Hq, D), _BF16, dev, True), _row_stride(q),
-          _arg(where, "k", k, (T, Hkv, D), _BF16, dev, True), _row_stride(k))
+    inner = (D, 1)
+    qk = _rows(where, "q", q, (T, Hq, D), inner, _BF16, dev) + _rows(where, "k", k, (T, Hkv, D), inner, _BF16, dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError(f"{where}: q_weight and k_weight go together")
     qw = kw = None
@@ -501,8 +499,8 @@ def dualkv_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, weight_off
     T, dev, qk, args = _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P,
                                   N, R_offsets, Hq, Hkv, D)
     up = (_arg(where, "dq_out", dq_out, (T, Hq, D), _BF16, dev), _arg(where, "dk_out", dk_out, (T, Hkv, D), _BF16, dev))
-    out = (_arg(where, "dq", dq, (T, Hq, D), _BF16, dev, True), _row_stride(dq),
-           _arg(where, "dk", dk, (T, Hkv, D), _BF16, dev, True), _row_stride(dk))
+    out = (_rows(where, "dq", dq, (T, Hq, D), (D, 1), _BF16, dev)
+           + _rows(where, "dk", dk, (T, Hkv, D), (D, 1), _BF16, dev))
     gw = (None, None)
     if q_weight is not None:
         gw = (_arg(where, "dq_weight", dq_weight, (D,), _F32, dev), _arg(where, "dk_weight", dk_weight, (D,), _F32, dev))
@@ -519,9 +517,8 @@ def _logits_args(where, logits, tokens, scale, P, N, R_offsets):
     if not isinstance(logits, _Tensor) or logits.dim() != 2:
         raise ValueError(f"{where}: logits must be a tensor of rows")
     V = logits.shape[1]
-    return M, n, dev, (_arg(where, "logits", logits, (M, V), _DTYPE_CODES, dev, True), _row_stride(logits),
-                       _DTYPE_CODES[logits.dtype], V, float(scale), _arg(where, "tokens", tokens, (n,), _I64, dev),
-                       int(P), int(N), _offsets(R_offsets))
+    return M, n, dev, (*_rows(where, "logits", logits, (M, V), (1,), _DTYPE_CODES, dev), _DTYPE_CODES[logits.dtype], V,
+                       float(scale), _arg(where, "tokens", tokens, (n,), _I64, dev), int(P), int(N), _offsets(R_offsets))
 
 
 def dualkv_token_logprobs(logits, tokens, scale, P, N, R_offsets, logp, entropy, lse, stream=None) -> None:
@@ -546,8 +543,8 @@ def dualkv_token_logprobs_bwd(logits, tokens, scale, P, N, R_offsets, lse, entro
                                           _opt(where, "entropy", entropy, (n,), _F32, dev),
                                           _arg(where, "dlogp", dlogp, (n,), _F32, dev),
                                           _opt(where, "dentropy", dentropy, (n,), _F32, dev),
-                                          _arg(where, "dlogits", dlogits, logits.shape, (logits.dtype,), dev, True),
-                                          _row_stride(dlogits), _stream_of(stream, dev))
+                                          *_rows(where, "dlogits", dlogits, logits.shape, (1,), (logits.dtype,), dev),
+                                          _stream_of(stream, dev))
     _raise(rc, where)
 
 
