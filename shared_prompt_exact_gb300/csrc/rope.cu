@@ -326,10 +326,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_fwd_kernel(const RopeArg
 }
 
 // One head's input gradient from the gradient turned back (g, f) and the head (a, b), in place; adds
-// the lane's weight gradients to (da, db).
+// the lane's weight gradients to (da, db).  `head`: whether the lane's slot has a head in this step; one
+// without adds nothing (its zeros alone would not see to that: with eps = 0 their norm is 0 * inf).
 template <int D>
 __device__ __forceinline__ void norm_backward(Vec8& g, Vec8& f, const Vec8& a, const Vec8& b, const float* w,
-                                              const LaneMap& m, float eps, Vec8& da, Vec8& db) {
+                                              const LaneMap& m, float eps, bool head, Vec8& da, Vec8& db) {
   constexpr int G = D / 16;
   const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
   float2 ss = make_float2(0.f, 0.f), ux = ss;
@@ -341,7 +342,7 @@ __device__ __forceinline__ void norm_backward(Vec8& g, Vec8& f, const Vec8& a, c
     ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
     ux = ffma2(ub.v[e], b.v[e], ffma2(ua.v[e], a.v[e], ux));
   }
-  const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + eps);
+  const float mean = group_sum<G>(ss) * (1.f / D) + eps, r = head ? rsqrtf(mean) : 0.f;
   const float k = -group_sum<G>(ux) * (1.f / D) * r * r * r;  // dx = r u - x r^3 mean(u x)
   const float2 rr = make_float2(r, r), kk = make_float2(k, k);
 #pragma unroll
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
           copy16(to + 2 * kRopeThreads, ahead.x);
           copy16(to + 3 * kRopeThreads, ahead.x + db);
         }
-      } else {  // an idle slot adds nothing to the weight gradients
+      } else {  // an idle slot's gradient is 0
 #pragma unroll
         for (int v = 0; v < 4; ++v) to[v * kRopeThreads] = make_uint4(0, 0, 0, 0);
       }
@@ -433,11 +434,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
       copies_wait<kDepth - 1>();
       const uint4* in = mine + 4 * stage * kRopeThreads;
       stage = stage == kDepth - 1 ? 0 : stage + 1;
+      const bool head = s * S + slot < H;
       Vec8 g = unpack8(in[0]), f = unpack8(in[kRopeThreads]);
       rotate(g, f, ang.cs, ang.neg, ang.sn, A.inter);  // by minus the angle
       if (norm)
-        norm_backward<D>(g, f, unpack8(in[2 * kRopeThreads]), unpack8(in[3 * kRopeThreads]), w, m, A.eps, da, db_);
-      if (s * S + slot < H) {
+        norm_backward<D>(g, f, unpack8(in[2 * kRopeThreads]), unpack8(in[3 * kRopeThreads]), w, m, A.eps, head, da, db_);
+      if (head) {
         *reinterpret_cast<uint4*>(y) = pack8(g);
         *reinterpret_cast<uint4*>(y + db) = pack8(f);
       }
