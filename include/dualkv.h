@@ -301,6 +301,7 @@ int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype,
  *            at most -A dual_clip unless dual_clip is 0, and 0 if A = 0
  *   kl     = exp(x) - x - 1
  *   loss   = sum_n w_n sum over live tokens of segment n of (policy + kl_coef kl - entropy_coef entropy)
+ *            (a term whose coefficient is 0 is not part of it, whatever its values)
  * and w_n, 0 for a segment without a live token, is
  *   DUALKV_LOSS_TOKEN_MEAN  1 / (live tokens of the batch)
  *   DUALKV_LOSS_SEQ_MEAN    1 / (N * live tokens of segment n)

@@ -409,7 +409,9 @@ __device__ __forceinline__ void finish(const PolicyArgs& A, const Record* rec, i
   h = warp_sum(in ? part[2][tid] : zero);
   if (tid == 0) {
     const double dp = -value(p), dq = value(q), dh = value(h);
-    A.loss[0] = (float)(dp + A.kl_coef * dq - A.entropy_coef * dh);
+    // a term without a coefficient is a statistic alone: 0 * inf or 0 * NaN must not reach the loss
+    const double kl = A.kl_coef != 0.0 ? A.kl_coef * dq : 0.0, ent = A.entropy_coef != 0.0 ? A.entropy_coef * dh : 0.0;
+    A.loss[0] = (float)(dp + kl - ent);
     A.stats[0] = (float)dp;
     A.stats[1] = (float)dq;
     A.stats[2] = (float)dh;

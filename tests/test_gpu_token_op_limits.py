@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_policy as tp
 import test_gpu_rope as tr
 from oracle import rope as orp
 from shared_prompt_exact_gb300 import build as pbuild
@@ -10,6 +11,7 @@ from shared_prompt_exact_gb300 import dualkv as dk
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
+INF = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -32,3 +34,28 @@ def test_norm_without_eps(monkeypatch, Hq, Hkv, D, wdtype):
         tr._check_forward(tr._np(y[i]), tr._np(x), tr._np(w), 0.0, pos, fn, False)
         assert bool(torch.isfinite(g[2 + i]).all())
         tr._check_backward(tr._np(g[i]), tr._np(g[2 + i]), tr._np(x), tr._np(dy), tr._np(w), 0.0, pos, fn, False)
+
+
+@pytest.mark.parametrize("off", [[0, 40, 90], [0, 3000, 3001, 30000]], ids=["one-cluster", "two-launches"])
+@pytest.mark.parametrize("entropies", [INF, float("nan")])
+def test_terms_without_a_coefficient_stay_out_of_the_loss(off, entropies):
+    # KL and entropies may be passed for the statistics alone; what they hold then does not reach the loss
+    x = tp._inputs(off, 41, False, 0.2)
+    x["mask"][:3] = True
+    x["ref"][0] = -INF                  # what token_logprobs returns for a masked target
+    x["ref"][1] = x["logp"][1] + 100.0  # e^100 is beyond fp32
+    x["ent"][2] = entropies
+    args = dict(mask=x["mask"], reduction="seq_mean")
+    want = dk.policy_loss(x["logp"], x["old"], x["adv"], off, **args)
+    loss, stats, w = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["ref"], x["ent"], **args)
+    assert bool(torch.isfinite(want[0]).all()) and torch.equal(loss, want[0]) and torch.equal(w, want[2])
+    assert torch.equal(stats[[0, 3]], want[1][[0, 3]])
+    assert float(stats[1]) == INF and not bool(torch.isfinite(stats[2]))
+    # each for itself with the other's coefficient set
+    e_only = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["ref"], x["old"], entropy_coef=0.5, **args)
+    assert bool(torch.isfinite(e_only[0]).all()) and float(e_only[1][1]) == INF
+    kl_only = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["old"], x["ent"], kl_coef=0.5, **args)
+    assert bool(torch.isfinite(kl_only[0]).all()) and not bool(torch.isfinite(kl_only[1][2]))
+    # with a coefficient they do
+    both = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["ref"], x["ent"], kl_coef=0.5, **args)
+    assert float(both[0]) == INF
