@@ -457,9 +457,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
 
 // Weight gradients: column d of the blocks' partial sums, added in block order.
 // A block of 32 x 32 threads takes 32 columns of q's or k's; its rows of threads take
-// contiguous shares of the blocks, which are then added in order.
-__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* __restrict__ partial, int qblocks, int kblocks,
-                                                           int D, float* __restrict__ dqw, float* __restrict__ dkw) {
+// contiguous shares of the blocks, which are then added in order.  It may start before `partial` is
+// complete, so that is not __restrict__.
+__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* partial, int qblocks, int kblocks, int D,
+                                                           float* dqw, float* dkw) {
   __shared__ float part[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x, col = c % D;
   const bool is_q = c < D;
