@@ -269,6 +269,7 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
  *               row_stride >= V elements apart; only element alignment is needed.  -inf marks masked entries;
  *               a NaN or +inf makes its row's results NaN; a row that is -inf throughout has
  *               lse = logp = -inf, entropy 0 and gradient 0
+ *               (an lse of any other row is finite: beyond fp32's range it ends at the type's limits)
  *   scale       > 0, an inverse temperature
  *   tokens      device int64 [R_offsets[N]], 0 .. V - 1; negative: ignored.  One past the
  *               vocabulary is ignored and reported by dualkv_check_status()

@@ -24,6 +24,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <cfloat>
+
 #include "kernels.h"
 #include "ptx.cuh"
 #include "segs.cuh"
@@ -327,7 +329,12 @@ __global__ void __launch_bounds__(kLogpThreads, 4) logp_fwd_kernel(const LogpArg
   } else if (tid == 0) {
     write(mine);
   }
-  if (tid == 0 && A.lse) A.lse[row] = none ? -CUDART_INF_F : fmaf(r.m, A.scale, ln_sum);
+  // scale * max may pass fp32's range in a row of the type's lowest or largest values: its lse stays finite, so
+  // that -inf means a row without entries and nothing else
+  if (tid == 0 && A.lse) {
+    const float lse = fmaf(r.m, A.scale, ln_sum);
+    A.lse[row] = none ? -CUDART_INF_F : isinf(lse) ? copysignf(FLT_MAX, lse) : lse;
+  }
 }
 
 __device__ __forceinline__ float block_sum(float v) {

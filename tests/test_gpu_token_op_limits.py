@@ -3,13 +3,16 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_logprobs as tl
 import test_gpu_policy as tp
 import test_gpu_rope as tr
+from oracle import policy as opl
 from oracle import rope as orp
 from shared_prompt_exact_gb300 import build as pbuild
 from shared_prompt_exact_gb300 import dualkv as dk
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
 BF, F32 = torch.bfloat16, torch.float32
 INF = float("inf")
 
@@ -59,3 +62,80 @@ def test_terms_without_a_coefficient_stay_out_of_the_loss(off, entropies):
     # with a coefficient they do
     both = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["ref"], x["ent"], kl_coef=0.5, **args)
     assert float(both[0]) == INF
+
+
+def _gradients_from_the_logits(logits, tok, scale, P, off, dlogp, dent):
+    """fp64 gradient of the logits with each row's own sum, and its tolerance per value.
+
+    With p, d = z - lse, A, A2 and K as in test_gpu_logprobs: the kernel normalises with the forward's lse, off by
+    u (2 A + K + 4 |lse| + 4 |max z|), in rows whose lse is at most 64 from 0, and with a sum of its own, off by
+    u (2 A + K), in all others; the entropy that it is given is off by u ((1 + A + A2) (K + 8) + 4 |H|).  The rest as
+    there; scales are exact in fp32 here."""
+    z, tok = tl._np(logits) * scale, torch.as_tensor(tok).tolist()
+    M, V = z.shape
+    want, tol = np.zeros_like(z), np.zeros_like(z)
+    K = 100 + V / 128
+    step = 2.0 ** -8 if logits.dtype == BF else U
+    for m in range(M):
+        mine = [i for i, r in enumerate(opl.predictor(P, off)) if r == m and tok[i] >= 0]
+        if not mine:
+            continue
+        top = z[m].max()
+        y = np.maximum(z[m] - top, -1e4)
+        s = np.exp(y).sum()
+        d, lse = y - np.log(s), top + np.log(s)
+        p = np.exp(d)
+        dp = np.where(p > 0, d, 0.0)
+        H = -(p * dp).sum()
+        A, A2 = (p * np.abs(dp)).sum(), (p * dp * dp).sum()
+        g, h = dlogp[mine].sum(), dent[mine].sum() if dent is not None else 0.0
+        ga, ha = np.abs(dlogp[mine]).sum(), np.abs(dent[mine]).sum() if dent is not None else 0.0
+        want[m] = -g * p - h * p * (dp + H)
+        for i in mine:
+            want[m, tok[i]] += dlogp[i]
+        want[m] *= scale
+        sum_off = 2 * A + K + (8 * max(abs(lse), abs(top)) if abs(lse) <= 64.001 else 0.0)
+        c = ga + ha * (np.abs(dp) + abs(H))
+        # p moves by its own relative error, and with it (by ha p) the factor d + H
+        e = p * ((3 * np.abs(dp) + sum_off + 10) * (c + ha) + ha * ((1 + A + A2) * (K + 8) + 4 * abs(H)))
+        tol[m] = step * np.abs(want[m]) + scale * U * e + 2.0 ** -125 * np.maximum(1.0, c)
+        for i in mine:
+            tol[m, tok[i]] += scale * U * (len(off) + 4) * ga
+    return want, tol
+
+
+@pytest.mark.parametrize("scale", [0.75, 1.25])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [40, 70003])
+def test_rows_of_the_lowest_value_at_any_scale(V, dtype, scale):
+    # scale times the type's lowest value passes fp32's range: the log-sum stays finite, -inf keeps its one meaning
+    P, off = 1, [0, 5]
+    logits, tok, dlogp, dent = tl._inputs(P, off, V, dtype, 0, 61, ignored=0.0)
+    most = torch.finfo(dtype).max
+    logits[0] = -most              # uniform probabilities
+    logits[1, : V // 2] = -most
+    logits[2] = -INF               # a row without any entry
+    logits[3] = most
+    logits[4] = -most
+    logits[4, int(tok[4])] = most  # one sure entry
+    lp, ent, lse = (tl._np(t) for t in dk.token_logprobs(logits, tok, P, off, scale=scale, entropy=True))
+    bound = float(np.finfo(np.float32).max)
+    for m, p in ((0, 1 / V), (3, 1 / V), (4, 1.0)):
+        K = 100 + V / 128
+        assert abs(lp[m] - np.log(p)) <= U * (K + 4 * abs(np.log(p)))
+        assert abs(ent[m] + np.log(p)) <= U * (2 * (K + 8) + 4 * abs(np.log(p)))
+        want = np.clip(tl._np(logits[m]).max() * scale, -bound, bound)
+        assert np.isfinite(lse[m]) and abs(lse[m] - want) <= 2 * U * abs(want)
+    assert lp[2] == lse[2] == -INF and ent[2] == 0.0
+    keep = [0, 1, 3, 4]
+    full = dk.token_logprobs(logits, tok, P, off, scale=scale, entropy=True)
+    for inplace in (False, True):
+        x = logits.clone()
+        out = dk.token_logprobs_backward(x, tok, full[2], dlogp, P, off, scale=scale, entropy=full[1], dentropy=dent,
+                                         inplace=inplace)
+        some = torch.cat((logits[keep], logits[:1]))  # the last row predicts nothing
+        want, tol = _gradients_from_the_logits(some, tok[keep], scale, P, [0, 4], tl._np(dlogp)[keep],
+                                               tl._np(dent)[keep])
+        err = np.abs(tl._np(out)[keep] - want[:4])
+        assert np.all(err <= tol[:4]), float(np.max(err - tol[:4]))
+        assert not out[2].any() and not out[5].any()
