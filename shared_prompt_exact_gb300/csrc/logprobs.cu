@@ -41,6 +41,10 @@ constexpr int kFwdBatch = 8, kBwdBatch = 4;  // vectors that a thread has in fli
 constexpr int kMaxParts = 8;                 // blocks of a forward cluster
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Bound on exponents that are multiplied with their power, which is 0 long before (from -126 in base 2 on), so that
+// a masked entry adds 0 and not 0 * inf: near enough to 0 that its products with a row's sum or an upstream
+// gradient stay finite too.
+constexpr float kFloor = -1e4f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -174,7 +178,7 @@ __device__ __forceinline__ float floor_of(float m) { return m == -CUDART_INF_F ?
 __device__ __forceinline__ void rebase(Running& r, float m, float c) {
   if (r.m != -CUDART_INF_F) {
     // the bound keeps a maximum that is the type's lowest value, or one below +inf, from leaving 0 * inf
-    const float d = fmaxf((r.m - floor_of(m)) * c, -1e30f), f = ex2(d);
+    const float d = fmaxf((r.m - floor_of(m)) * c, kFloor), f = ex2(d);
     r.t = fmul2(ffma2(make_float2(d, d), r.s, r.t), make_float2(f, f));
     r.s = fmul2(r.s, make_float2(f, f));
   }
@@ -200,7 +204,7 @@ __device__ __forceinline__ void accumulate(Running& r, const float2 (&z)[K], flo
     const float2 x = make_float2(ex2(y.x), ex2(y.y));
     r.s = fadd2(r.s, x);
     if (ENT) {
-      y = make_float2(fmaxf(y.x, -1e30f), fmaxf(y.y, -1e30f));  // a masked logit adds 0, not 0 * inf
+      y = make_float2(fmaxf(y.x, kFloor), fmaxf(y.y, kFloor));  // a masked logit adds 0, not 0 * inf
       r.t = ffma2(x, y, r.t);
     }
   }
@@ -361,12 +365,12 @@ __device__ __forceinline__ float2 grad_of(float2 z, const RowGrad& r) {  // base
   const float2 y = fmul2(d, make_float2(kLog2e, kLog2e)), p = make_float2(ex2(y.x), ex2(y.y));
   const float2 k = make_float2(r.k0, r.k0);
   if (!ENT) return fmul2(p, k);
-  return fmul2(p, ffma2(make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), make_float2(r.k1, r.k1), k));
+  return fmul2(p, ffma2(make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor)), make_float2(r.k1, r.k1), k));
 }
 template <bool ENT>
 __device__ __forceinline__ float grad_of(float z, const RowGrad& r) {
   const float d = fmaf(z - r.base, r.scale, -r.lse), p = ex2(d * kLog2e);
-  return ENT ? p * fmaf(fmaxf(d, -1e30f), r.k1, r.k0) : p * r.k0;
+  return ENT ? p * fmaf(fmaxf(d, kFloor), r.k1, r.k0) : p * r.k0;
 }
 
 // Slots for the keys of N segments.

@@ -139,3 +139,19 @@ def test_rows_of_the_lowest_value_at_any_scale(V, dtype, scale):
         err = np.abs(tl._np(out)[keep] - want[:4])
         assert np.all(err <= tol[:4]), float(np.max(err - tol[:4]))
         assert not out[2].any() and not out[5].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [40, 70003])
+def test_masked_entries_under_large_gradients(V, dtype):
+    # a masked entry's gradient is 0 whatever flows into its row (0 times a large factor, not 0 times infinity)
+    P, off = 1, [0, 4, 7]
+    logits, tok, dlogp, dent = tl._inputs(P, off, V, dtype, 0, 71, ignored=0.0)
+    tok %= V // 2
+    logits[:, V // 2:] = -INF
+    logits[1, V // 4: V // 2] = torch.finfo(dtype).min
+    got = dk.token_logprobs(logits, tok, P, off, entropy=True)
+    dent *= 1e12
+    d = dk.token_logprobs_backward(logits, tok, got[2], dlogp, P, off, entropy=got[1], dentropy=dent)
+    assert bool(torch.isfinite(d).all()) and not d[:, V // 2:].any()
+    tl._check_backward(d, logits, tok, 1.0, P, off, got[2], got[1], dlogp, dent)
