@@ -68,8 +68,8 @@ def _gradients_from_the_logits(logits, tok, scale, P, off, dlogp, dent):
     """fp64 gradient of the logits with each row's own sum, and its tolerance per value.
 
     With p, d = z - lse, A, A2 and K as in test_gpu_logprobs: the kernel normalises with the forward's lse, off by
-    u (2 A + K + 4 |lse| + 4 |max z|), in rows whose lse is at most 64 from 0, and with a sum of its own, off by
-    u (2 A + K), in all others; the entropy that it is given is off by u ((1 + A + A2) (K + 8) + 4 |H|).  The rest as
+    u (2 A + K + 4 |lse| + 4 |max z|), in rows whose lse is at most 64 (bf16: 512) from 0, and with a sum of its
+    own, off by u (2 A + K), in all others; the entropy that it is given is off by u ((1 + A + A2) (K + 8) + 4 |H|).  The rest as
     there; scales are exact in fp32 here."""
     z, tok = tl._np(logits) * scale, torch.as_tensor(tok).tolist()
     M, V = z.shape
@@ -94,7 +94,8 @@ def _gradients_from_the_logits(logits, tok, scale, P, off, dlogp, dent):
         for i in mine:
             want[m, tok[i]] += dlogp[i]
         want[m] *= scale
-        sum_off = 2 * A + K + (8 * max(abs(lse), abs(top)) if abs(lse) <= 64.001 else 0.0)
+        holds = 512.01 if logits.dtype == BF else 64.001
+        sum_off = 2 * A + K + (8 * max(abs(lse), abs(top)) if abs(lse) <= holds else 0.0)
         c = ga + ha * (np.abs(dp) + abs(H))
         # p moves by its own relative error, and with it (by ha p) the factor d + H
         e = p * ((3 * np.abs(dp) + sum_off + 10) * (c + ha) + ha * ((1 + A + A2) * (K + 8) + 4 * abs(H)))
@@ -155,3 +156,33 @@ def test_masked_entries_under_large_gradients(V, dtype):
     d = dk.token_logprobs_backward(logits, tok, got[2], dlogp, P, off, entropy=got[1], dentropy=dent)
     assert bool(torch.isfinite(d).all()) and not d[:, V // 2:].any()
     tl._check_backward(d, logits, tok, 1.0, P, off, got[2], got[1], dlogp, dent)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1.25])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [40, 4096, 70003])
+def test_gradients_of_rows_off_zero(V, dtype, scale):
+    # the rounding of an fp32 lse would be up to 2^-13 of every probability, and more than g (1 - p) at a sure target
+    P, off = 2, [0, 9, 12, 13]
+    for k, shift in enumerate((0.0, 45.0, 70.0, 200.0, -1000.0, 4000.0, 4090.0)):
+        logits, tok, dlogp, dent = tl._inputs(P, off, V, dtype, 0, 50 + k, ignored=0.0)
+        rows = torch.tensor(opl.predictor(P, off), device="cuda")
+        logits[rows[::2], tok[::2]] += 14.0 + logits.float().amax().to(dtype)  # every other target is sure
+        logits = (logits.float() + shift + 3.7 * torch.arange(len(logits), device="cuda")[:, None]).to(dtype)
+        lp, ent, lse = dk.token_logprobs(logits, tok, P, off, scale=scale, entropy=True)
+        for entropy in (False, True):
+            kw = dict(entropy=ent, dentropy=dent) if entropy else {}
+            want, tol = _gradients_from_the_logits(logits, tok, scale, P, off, tl._np(dlogp),
+                                                   tl._np(dent) if entropy else None)
+            out = dk.token_logprobs_backward(logits, tok, lse, dlogp, P, off, scale=scale, **kw)
+            err = np.abs(tl._np(out) - want)
+            assert np.all(err <= tol), (shift, float(np.max(err / np.maximum(tol, 1e-300))))
+            # rows that start elsewhere within 16 bytes, and in place: the same bits
+            full = torch.full((len(logits), V + 3), 7.0, dtype=dtype, device="cuda")
+            dk.dualkv_token_logprobs_bwd(logits, tok, scale, P, len(off) - 1, off, lse, ent, dlogp,
+                                         dent if entropy else None, full[:, 1:V + 1])
+            assert torch.equal(full[:, 1:V + 1], out) and bool((full[:, V + 1:] == 7.0).all())
+            x = logits.clone()
+            dk.token_logprobs_backward(x, tok, lse, dlogp, P, off, scale=scale, inplace=True, **kw)
+            assert torch.equal(x, out)
+    dk.dualkv_check_status()
