@@ -39,6 +39,7 @@ EXPORTS = ("dualkv_fwd", "dualkv_bwd_workspace_bytes", "dualkv_bwd", "dualkv_bui
            "dualkv_token_logprobs_bwd", "dualkv_policy_loss", "dualkv_policy_loss_bwd",
            "dualkv_policy_loss_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 32 << 20
+_TOO_FAR = 1 << 31  # counts from here on would wrap on their way into a C int
 KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope", "logprobs", "policy")
 DUALKV_BF16 = 0
 DUALKV_F32 = 1
@@ -149,8 +150,10 @@ def _offsets(R_offsets: Sequence[int]):
     so a program with one layout for many calls can convert it once (``offsets``)."""
     if isinstance(R_offsets, ctypes.Array) and R_offsets._type_ is ctypes.c_int32:
         return R_offsets
-    arr = (ctypes.c_int32 * len(R_offsets))(*[int(x) for x in R_offsets])
-    return arr
+    values = [int(x) for x in R_offsets]
+    if values and not -_TOO_FAR <= min(values) <= max(values) < _TOO_FAR:
+        raise ValueError(f"R_offsets must fit 32 bits, got {max(values, key=abs)}")
+    return (ctypes.c_int32 * len(values))(*values)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -447,9 +450,16 @@ def _layout_rows(where, P, N, R_offsets):
     P, N = int(P), int(N)
     if N < 1 or len(R_offsets) != N + 1:
         raise ValueError(f"{where}: R_offsets must hold N + 1 = {N + 1} entries, got {len(R_offsets)}")
-    if not 0 <= P < 1 << 31:
+    if not 0 <= P < _TOO_FAR:
         raise ValueError(f"{where}: P must be a count of tokens, got {P}")
     return P + int(R_offsets[N])
+
+
+def _counts(where, **counts):
+    """Refuses a count that a C int would not hold."""
+    for name, v in counts.items():
+        if not -_TOO_FAR <= v < _TOO_FAR:
+            raise ValueError(f"{where}: {name} must fit 32 bits, got {v}")
 
 
 def _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, P, N, R_offsets, Hq,
@@ -458,6 +468,8 @@ def _rope_args(where, q, k, q_weight, k_weight, weight_offset, eps, inv_freq, ro
     arguments from the weights to D)."""
     T = _layout_rows(where, P, N, R_offsets)
     dev = torch.cuda.current_device()
+    if max(Hq, Hkv, D, rope_dim) >= _TOO_FAR:
+        _counts(where, Hq=Hq, Hkv=Hkv, D=D, rope_dim=rope_dim)
     inner = (D, 1)
     qk = _rows(where, "q", q, (T, Hq, D), inner, _BF16, dev) + _rows(where, "k", k, (T, Hkv, D), inner, _BF16, dev)
     if (q_weight is None) != (k_weight is None):
@@ -487,6 +499,7 @@ def dualkv_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, inv_freq, 
 
 
 def dualkv_qk_norm_rope_bwd_workspace_bytes(P, N, R_offsets, Hq, Hkv, D) -> int:
+    _counts("dualkv_qk_norm_rope_bwd_workspace_bytes", P=P, N=N, Hq=Hq, Hkv=Hkv, D=D)
     return int(load().dualkv_qk_norm_rope_bwd_workspace_bytes(int(P), int(N), _offsets(R_offsets), int(Hq), int(Hkv),
                                                               int(D)))
 
@@ -517,6 +530,8 @@ def _logits_args(where, logits, tokens, scale, P, N, R_offsets):
     if not isinstance(logits, _Tensor) or logits.dim() != 2:
         raise ValueError(f"{where}: logits must be a tensor of rows")
     V = logits.shape[1]
+    if V >= _TOO_FAR:
+        _counts(where, V=V)
     return M, n, dev, (*_rows(where, "logits", logits, (M, V), (1,), _DTYPE_CODES, dev), _DTYPE_CODES[logits.dtype], V,
                        float(scale), _arg(where, "tokens", tokens, (n,), _I64, dev), int(P), int(N), _offsets(R_offsets))
 
@@ -582,6 +597,7 @@ def _per_token(where, advantages, N, n, R_offsets, per_token):
 
 
 def dualkv_policy_loss_workspace_bytes(N, R_offsets) -> int:
+    _counts("dualkv_policy_loss_workspace_bytes", N=N)
     return int(load().dualkv_policy_loss_workspace_bytes(int(N), _offsets(R_offsets)))
 
 
