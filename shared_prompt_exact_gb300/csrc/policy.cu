@@ -429,14 +429,19 @@ __global__ void __launch_bounds__(kPolicyThreads, 6) policy_fwd_kernel(const Pol
 }
 
 constexpr int kFinishThreads = 512;
+// Records that a thread holds between the two passes; those of larger batches are read twice.  It hardly
+// matters: 4, 8, 10 and 16 (the most without spills) took the same time within the clock's 1 us at 0.5 to 8 million
+// tokens, cold, and 4 took 89 us against 87 at 12 million.
+constexpr int kFinishBatch = 8;
 
-// Launched while the records are still being made: everything before the wait overlaps with that.
+// Starts when the blocks that make the records have exited; what comes before the wait overlaps with the rest of
+// that grid's end (nothing there triggers an earlier start).
 __global__ void __launch_bounds__(kFinishThreads) policy_finish_kernel(const PolicyArgs A, int blocks, int N) {
   __shared__ int live[kMaxSegs + 1];
   for (int n = threadIdx.x; n < N; n += kFinishThreads) live[n] = 0;
   __syncthreads();
   cudaGridDependencySynchronize();
-  finish<kFinishThreads, 10>(A, static_cast<const Record*>(A.records), blocks, N, live);
+  finish<kFinishThreads, kFinishBatch>(A, static_cast<const Record*>(A.records), blocks, N, live);
 }
 
 // The whole forward as one cluster of gridDim.x <= kClusterBlocks blocks.

@@ -186,3 +186,33 @@ def test_gradients_of_rows_off_zero(V, dtype, scale):
             dk.token_logprobs_backward(x, tok, lse, dlogp, P, off, scale=scale, inplace=True, **kw)
             assert torch.equal(x, out)
     dk.dualkv_check_status()
+
+
+@pytest.mark.parametrize("reduction", ["token_mean", "seq_mean", "seq_sum"])
+def test_loss_of_more_records_than_the_join_holds(reduction):
+    # 1,024 tokens a record: 4,096 records and more are read twice
+    for n in (4_100_000, 4_300_007, 9_000_001):
+        off = [0, 5, 5, n // 3, n]
+        x = tp._inputs(off, n, True, 0.3)
+        args = dict(clip_low=0.2, clip_high=0.28, kl_coef=0.05, entropy_coef=0.01)
+        loss, stats, w = dk.policy_loss(x["logp"], x["old"], x["adv"], off, x["ref"], x["ent"], x["mask"], reduction=reduction,
+                                        per_token=True, **args)
+        lp, old, ref, ent, A = (x[k].double() for k in ("logp", "old", "ref", "ent", "adv"))
+        seg = torch.repeat_interleave(torch.arange(4, device="cuda"), torch.tensor(np.diff(off), device="cuda"))
+        live = torch.zeros(4, dtype=torch.float64, device="cuda").index_add_(0, seg, x["mask"].double())
+        per = {"token_mean": live.sum().expand(4), "seq_mean": 4 * live, "seq_sum": torch.full_like(live, 4.0)}[reduction]
+        want_w = torch.where(live > 0, 1.0 / per, torch.zeros_like(live))
+        on = want_w[seg] * x["mask"]
+        ratio = torch.exp(lp - old)
+        pg = -torch.minimum(ratio * A, ratio.clamp(0.8, 1.28) * A)
+        d = ref - lp
+        kl = torch.expm1(d) - d
+        far = torch.where(A > 0, ratio > 1.28, ratio < 0.8) & (A != 0) & x["mask"]
+        want = torch.stack([(on * pg).sum(), (on * kl).sum(), (on * ent).sum(), far.sum() / live.sum()])
+        # tolerances as in test_gpu_policy; a weight's division and its count beyond 2^24 round twice
+        tol = U * torch.stack([24 * (on * pg.abs()).sum(), 24 * (on * (kl + (d.exp() + 1) * d.abs())).sum(),
+                               16 * (on * ent.abs()).sum(), torch.zeros_like(want[0])]) + 2 * U * want.abs()
+        assert bool(((w.double() - want_w).abs() <= 2 * U * want_w).all())
+        assert bool(((stats.double() - want).abs() <= tol).all()), ((stats.double() - want) / tol)
+        total = want[0] + 0.05 * want[1] - 0.01 * want[2]
+        assert abs(float(loss) - float(total)) <= float(tol[0] + 0.05 * tol[1] + 0.01 * tol[2] + U * total.abs())
