@@ -270,7 +270,7 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
  *               a NaN or +inf makes its row's results NaN; a row that is -inf throughout has
  *               lse = logp = -inf, entropy 0 and gradient 0
  *               (an lse of any other row is finite: beyond fp32's range it ends at the type's limits)
- *   scale       > 0, an inverse temperature
+ *   scale       > 0, an inverse temperature; scale * log2(e) has to be finite (up to 2.3e38)
  *   tokens      device int64 [R_offsets[N]], 0 .. V - 1; negative: ignored.  One past the
  *               vocabulary is ignored and reported by dualkv_check_status()
  *   logp, entropy  device fp32 [R_offsets[N]], written; 0 for a token that is ignored or not

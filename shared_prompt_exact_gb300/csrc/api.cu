@@ -590,7 +590,7 @@ int logp_impl(bool backward, const void* logits, int64_t row_stride, int dtype, 
   const int64_t n = R_offsets[N], M = n + (P > 0 ? 1 : 0);
   if (dtype != DUALKV_BF16 && dtype != DUALKV_F32) return DUALKV_ERR_INVALID;
   if (V < 1 || V > kMaxVocab || row_stride < V || row_stride > kMaxRowStride) return DUALKV_ERR_INVALID;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DUALKV_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DUALKV_ERR_INVALID;  // as the kernels use it
   if (!logits || (n > 0 && !tokens)) return DUALKV_ERR_INVALID;
   const uint64_t esz = dtype == DUALKV_F32 ? 4 : 2, un = (uint64_t)n, uM = (uint64_t)M;
   if (!aligned_to(logits, esz) || !aligned_to(tokens, 8)) return DUALKV_ERR_ALIGN;
@@ -709,7 +709,7 @@ int fwd_impl(const void* q, const void* k, const void* v, int P, int N, const in
              int D, float scale, int window, int kv_lo, int kv_hi, void* out, float* lse, void* stream) {
   if (validate_layout(P, N, R_offsets, Hq, Hkv, D)) return DUALKV_ERR_INVALID;
   if (kv_lo < 0 || kv_hi > Hkv || kv_lo >= kv_hi) return DUALKV_ERR_INVALID;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DUALKV_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DUALKV_ERR_INVALID;  // as the kernels use it
   if (!q || !k || !v || !out || !lse) return DUALKV_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse)) return DUALKV_ERR_ALIGN;
   if (!supported_fwd_d(D)) return DUALKV_ERR_UNSUPPORTED;
@@ -738,7 +738,7 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* out, const
              void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) {
   if (validate_layout(P, N, R_offsets, Hq, Hkv, D)) return DUALKV_ERR_INVALID;
   if (kv_lo < 0 || kv_hi > Hkv || kv_lo >= kv_hi) return DUALKV_ERR_INVALID;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DUALKV_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DUALKV_ERR_INVALID;  // as the kernels use it
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return DUALKV_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) || !aligned16(dout) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv))

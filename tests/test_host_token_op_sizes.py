@@ -5,6 +5,7 @@ import torch
 
 from shared_prompt_exact_gb300 import build as pbuild
 from shared_prompt_exact_gb300 import dualkv as dk
+from test_host_token_ops import _logp
 
 BF, F32 = torch.bfloat16, torch.float32
 FAR = 1 << 32
@@ -67,3 +68,10 @@ def test_heads_of_too_many_values(Hq, Hkv, D, rope_dim):
 def test_prompt_of_too_many_tokens():
     with pytest.raises(ValueError):
         dk.dualkv_qk_norm_rope_bwd_workspace_bytes(FAR + 4, 1, [0, 1], 2, 1, 64)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_scale_whose_base_2_form_overflows(backward):
+    # scale * log2(e) has to be finite: 0 * inf would make a row's largest entry NaN
+    for scale in (2.4e38, 3.4e38):
+        assert _logp(dk.load(), backward, scale=scale) == dk.DUALKV_ERR_INVALID
