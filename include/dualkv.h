@@ -219,11 +219,13 @@ int dualkv_fold(const void* g_rep, void* g_packed, int P, int N, const int32_t* 
  * at the end; the squares have to stay within fp32's range (|x| below 1e18).
  *
  *   q, k            device bf16: head h of row t at [t * stride + h * D].  q_stride >= Hq * D
- *                   and k_stride >= Hkv * D in elements, multiples of 8, so q and k may be
- *                   columns of one fused projection's rows
+ *                   and k_stride >= Hkv * D in elements, multiples of 8 up to 2^31, so q and k may be
+ *                   columns of one fused projection's rows.  All pointers of these calls are 16-byte
+ *                   aligned (DUALKV_ERR_ALIGN)
+ *   eps             >= 0; with 0 no head may be all zeros (its norm is 0 / 0), and |x| has to be above 1e-18
  *   q_weight, k_weight  device [D] of weight_dtype (DUALKV_BF16 or DUALKV_F32), or both NULL:
  *                   no norm.  weight_offset is added to them (1 where a model stores w - 1)
- *   inv_freq        device fp32 [rope_dim / 2]; rope_dim a multiple of 16, 0 .. D (0: no rotation)
+ *   inv_freq        device fp32 [rope_dim / 2], finite; rope_dim a multiple of 16, 0 .. D (0: no rotation)
  *   D               64, 128 or 512; N <= 4095 (DUALKV_ERR_UNSUPPORTED beyond)
  *   q_out, k_out    device bf16 [T, Hq, D] and [T, Hkv, D], contiguous, written
  * Backward:
@@ -266,7 +268,7 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
  * (the prompt's last row sums over the segments).  Statistics are fp32.
  *
  *   logits      device, bf16 or fp32 (dtype DUALKV_BF16 / DUALKV_F32), [M, V], V up to 2^30, rows
- *               row_stride >= V elements apart; only element alignment is needed.  -inf marks masked entries;
+ *               row_stride >= V elements apart (up to 2^31); only element alignment is needed.  -inf marks masked entries;
  *               a NaN or +inf makes its row's results NaN; a row that is -inf throughout has
  *               lse = logp = -inf, entropy 0 and gradient 0
  *               (an lse of any other row is finite: beyond fp32's range it ends at the type's limits)
@@ -308,7 +310,8 @@ int dualkv_token_logprobs_bwd(const void* logits, int64_t row_stride, int dtype,
  *   DUALKV_LOSS_SEQ_MEAN    1 / (N * live tokens of segment n)
  *   DUALKV_LOSS_SEQ_SUM     1 / N
  * Gradients: a token beyond a bound passes none through its ratio; one exactly on it does.
- * The comparisons with the bounds are exact in fp64.
+ * The comparisons with the bounds are exact in fp64.  Ratios and e^x are fp32: a difference above 88 makes an
+ * unclipped term, or its gradient, infinite (and 0 * that, as with dloss = 0, NaN).
  *
  *   logp, old_logp  device fp32 [R_offsets[N]] in packed order
  *   ref_logp    same, or NULL if kl_coef is 0;  entropy  same, or NULL if entropy_coef is 0

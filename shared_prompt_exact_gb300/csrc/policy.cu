@@ -25,11 +25,12 @@
 // memory; more write them to the workspace for a second launch.
 //
 // Up to some 100,000 tokens a call is launch latency (in a graph 4.5 to 5.3 us, the gradients 2 to
-// 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 32 us, 2.6 TB/s,
-// 6 of them the join, and the gradients 23 us, 4.5 TB/s.  The sums are bound by the comparisons and
-// selects around the bounds (the ALU pipe is 59 % busy) and memory latency together: without the terms'
-// arithmetic a cold call still takes 36 us of 40.  The arithmetic is on f32x2 pairs of tokens, which
-// took a tenth off both.  Four tokens a thread in chunks of
+// 2.5).  At 4.04M tokens (1,024 responses, every input in use) the forward takes 33 us, 2.6 TB/s,
+// 6 of them the join, and the gradients 23 us, 4.5 TB/s.  What bounds them is the shape of the work rather than
+// a unit: a block loads one chunk, whose latency only the other blocks of its SM cover, and one block joins
+// the records behind all of them.  The arithmetic is a tenth: a cold call without it takes 36 us of 40 (the ALU pipe, which
+// has the comparisons and selects around the bounds, is 59 % busy), and doing it on f32x2 pairs of
+// tokens took a tenth off both directions.  Four tokens a thread in chunks of
 // 1,024 beat eight in 2,048 (40 against 46 us cold): more resident threads outweigh fewer blocks.
 // For the same reason blocks that stay and walk several chunks, the next one's loads ahead of the sums, lose:
 // 42 against 40 us cold, the gradients 32 against 28, although they make a third of the records.

@@ -18,7 +18,7 @@
 // (cp.async); arithmetic is on f32x2 pairs, because with plain fp32 the backward
 // was bound by issue (64 % of the slots) as much as by memory.  Measured: forward
 // 222 us for 71,680 rows of 32 + 8 heads of 128 (6.6 TB/s, 0.97 of the measured
-// copy bandwidth; 331 us with loads straight into registers), backward 392 us for
+// copy bandwidth; 331 us with loads straight into registers), backward 393 us for
 // 84,997 such rows (6.7 TB/s; 868 us) and 180 us for 36,522 rows of 8 + 2 heads of
 // 512 (6.2 TB/s; 496 us, with loads of every other vector).
 //
