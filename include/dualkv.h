@@ -280,7 +280,7 @@ int dualkv_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int6
  *   lse         device fp32 [M], written, may be NULL in the forward; 0 for a row that predicts
  *               no token (such rows are not read)
  * Backward: lse (and entropy, with dentropy) as the forward wrote them (a row whose lse is beyond
- *   +-64, for bf16 +-512, where its rounding would show in the gradients, is summed again);
+ *   +-128, for bf16 +-1024, where its rounding would show in the gradients, is summed again);
  *   dlogp, dentropy  device fp32 [R_offsets[N]]; dentropy may be NULL
  *   dlogits     device, dtype, [M, V], rows dlogits_stride >= V apart, written whole (values
  *               between the rows are left as they are): zeros in rows into which nothing
