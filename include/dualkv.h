@@ -349,6 +349,102 @@ int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float
                            const float* weights, float* dlogp, float* dentropy, void* stream);
 
 /*
+ * Paged key/value cache: what a model keeps between the steps that generate the responses of
+ * a micro-batch.  A cache is two pools of pages, keys and values.  A page holds page_size
+ * consecutive tokens of every kv-head:
+ *   bits 16   k, v: device bf16 [pages, Hkv, page_size, D]; the scales are NULL
+ *   bits 4    k, v: device bytes [pages, Hkv, page_size, D / 2], value 2j of a token in the low half
+ *             of byte j; k_scale, v_scale: device bf16 [pages, Hkv, page_size, D / 32].  A value is
+ *             scale * (code - 8), codes 1 .. 15, with its group's scale (32 values of a head): a seventh of
+ *             the group's largest magnitude (in fp32) rounded up to 5 significant bits, so the value
+ *             is exact in bf16; a magnitude goes to the nearest code, from half way to the larger one.
+ *             A group with a value that is not finite has the scale NaN.  |x| up to 9e37
+ * page_size is a multiple of 16 up to 65,536; all pointers are 16-byte aligned.  A stream's tokens lie in
+ * the pages that its row of a page table (device int32 [streams, max_pages]) names: token i in slot
+ * i % page_size of page i / page_size of the row.  Entries behind a stream's last token are not read.
+ * Streams may share pages that are only read (the prompt's); no slot may be written twice in a call.
+ * A page outside the pool, or a stream longer than its row of the table, is reported by
+ * dualkv_check_status(): nothing is read or written through it (read: zeros; decode: the
+ * keys do not count).
+ */
+typedef struct dualkv_kv_cache {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int64_t pages;
+  int32_t page_size;
+  int32_t bits;
+} dualkv_kv_cache;
+
+/*
+ * New rows of S streams into the cache: per-head norm and rotation of q and k as in
+ * dualkv_qk_norm_rope, the turned q to q_out, the turned k and v into the pages.
+ * Stream s has rows row_offsets[s] .. row_offsets[s+1] of q, k, v (none, one or many), the last of its
+ * lens[s] tokens: with n of them, row j of it is token i = lens[s] - n + j at position starts[s] + i.
+ * A response behind a prompt in pages of its own has starts[s] = the prompt's length.
+ *
+ *   q, k, v         device bf16: head h of row t at [t * stride + h * D]; strides in elements, multiples
+ *                   of 8 from the row's width up to 2^31
+ *   q_weight .. interleaved   as in dualkv_qk_norm_rope
+ *   pages           device int32 [S, max_pages]; max_pages * page_size < 2^31
+ *   lens, starts    device int32 [S]: tokens that the stream holds after this call; position of
+ *                   its token 0 (positions below 2^31)
+ *   row_offsets     HOST int32 [S+1], row_offsets[0] = 0, non-decreasing; S <= 4095
+ *                   (DUALKV_ERR_UNSUPPORTED beyond).  No rows at all: nothing is done
+ *   q_out           device bf16 [row_offsets[S], Hq, D], contiguous, written
+ * Neither q_out nor the cache may share memory with an input or each other (DUALKV_ERR_INVALID).
+ */
+int dualkv_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype,
+                        float weight_offset, float eps, const float* inv_freq, int rope_dim, int interleaved,
+                        const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens,
+                        const int32_t* starts, int S, const int32_t* row_offsets, int Hq, int Hkv, int D, void* q_out,
+                        void* stream);
+
+/*
+ * The same rows (the last row_offsets[s+1] - row_offsets[s] of stream s's lens[s] tokens) back as
+ * dense keys and values, as dualkv_fwd takes them: k_out, v_out device bf16
+ * [row_offsets[S], Hkv, D], contiguous, written.
+ */
+int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens, int S,
+                      const int32_t* row_offsets, int Hkv, int D, void* k_out, void* v_out, void* stream);
+
+/*
+ * Attention of one new token per response over a shared prompt and the response's own tokens,
+ * both in the cache: the generating counterpart of dualkv_fwd.  Responses
+ * groups[g] .. groups[g+1] share prompt g.  With P the prompt's length and n = lens[b], the query of
+ * response b stands at position P + n - 1 and sees, by the rule above, the prompt's tokens (positions
+ * 0 .. P - 1) and its own n (positions P ..): out = softmax(scale q k^T) v, lse its log-sum-exp.
+ * The query's own key is expected in the cache (dualkv_cache_append, with lens counting it).
+ * A prompt is read for a whole group at once.
+ *
+ *   q               device bf16: head h of response b at [b * q_stride + h * D], q_stride as above
+ *   prompt_pages    device int32 [G, max_prompt_pages], prompt_lens device int32 [G] (0: no prompt);
+ *                   both may be NULL with max_prompt_pages = 0: no prompts
+ *   pages, lens     device int32 [B, max_pages] and [B], B = groups[G].  lens[b] = 0: the prompt
+ *                   alone; negative: the response has ended, and nothing is read for it
+ *   groups          HOST int32 [G+1], groups[0] = 0, non-decreasing; G <= 4095, B <= 8192
+ *                   (DUALKV_ERR_UNSUPPORTED beyond).  B = 0: nothing is done
+ *   scale           > 0; scale * log2(e) has to be finite
+ *   window          <= 0: all tokens; else the last `window` ones
+ *   out             device bf16 [B, Hq, D], written; lse device fp32 [Hq, B], written, may be NULL.
+ *                   A response that sees no token has out 0 and lse -inf
+ *   workspace       device, 256-byte aligned, >= dualkv_decode_workspace_bytes() (0 for invalid input);
+ *                   calls that may overlap need one each
+ * Keys and values that no query of the call sees may hold anything.  What one of a group's
+ * responses sees has to be finite for all of them to be.
+ * No output may share memory with an input or another output (DUALKV_ERR_INVALID).
+ * The lengths stay on the device: these three calls may be captured into a CUDA graph whose replays
+ * find longer streams, for as long as the tables' sizes and the host arrays fit.
+ */
+size_t dualkv_decode_workspace_bytes(int G, const int32_t* groups, int Hq, int Hkv, int D);
+int dualkv_decode(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, const int32_t* prompt_pages,
+                  int max_prompt_pages, const int32_t* prompt_lens, const int32_t* pages, int max_pages,
+                  const int32_t* lens, int G, const int32_t* groups, int Hq, int Hkv, int D, float scale, int window,
+                  void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Token-reduction factor rho = sum_n (P + R_n) / (P + sum_n R_n) (paper
  * abstract: rho = N(P+R)/(P+NR) for equal lengths).  Host only; -1 on invalid input.
  */
@@ -388,7 +484,9 @@ const char* dualkv_error_string(int code);
 #define DUALKV_KERNEL_ROPE 6 /* dualkv_qk_norm_rope and its backward */
 #define DUALKV_KERNEL_LOGPROBS 7 /* dualkv_token_logprobs and its backward */
 #define DUALKV_KERNEL_POLICY 8   /* dualkv_policy_loss and its backward */
-#define DUALKV_KERNEL_KINDS 9
+#define DUALKV_KERNEL_CACHE 9    /* dualkv_cache_append and dualkv_cache_read */
+#define DUALKV_KERNEL_DECODE 10  /* dualkv_decode */
+#define DUALKV_KERNEL_KINDS 11
 int dualkv_profile_enable(int on);
 int dualkv_profile_read(double* ms, int64_t* launches);
 

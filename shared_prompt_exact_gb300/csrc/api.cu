@@ -626,6 +626,207 @@ int logp_impl(bool backward, const void* logits, int64_t row_stride, int dtype, 
   return DUALKV_OK;
 }
 
+// ---------------------------------------------------------------- paged cache
+// A cache's fields as the kernels take them; head_rows: rows of all heads of all pages.
+int check_cache(const dualkv_kv_cache* c, int Hkv, int D, PagedKV* kv, uint64_t* head_rows) {
+  if (!c || (D != 64 && D != 128 && D != 512) || Hkv < 1 || Hkv > (1 << 16)) return DUALKV_ERR_INVALID;
+  if (c->pages < 1 || c->pages > INT32_MAX) return DUALKV_ERR_INVALID;
+  if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16) return DUALKV_ERR_INVALID;
+  if (c->bits != 16 && c->bits != 4) return DUALKV_ERR_INVALID;
+  if (!c->k || !c->v) return DUALKV_ERR_INVALID;
+  const bool scales = c->bits == 4;
+  if (scales != (c->k_scale != nullptr) || scales != (c->v_scale != nullptr)) return DUALKV_ERR_INVALID;
+  for (const void* p : {c->k, c->v, c->k_scale, c->v_scale})
+    if (!aligned16(p)) return DUALKV_ERR_ALIGN;
+  if ((uint64_t)c->pages * (uint64_t)Hkv > (uint64_t(1) << 40)) return DUALKV_ERR_INVALID;
+  *head_rows = (uint64_t)c->pages * (uint64_t)Hkv * (uint64_t)c->page_size;
+  typedef __nv_bfloat16 bf;
+  *kv = PagedKV{c->k, c->v, static_cast<bf*>(c->k_scale), static_cast<bf*>(c->v_scale), (int)c->pages, c->page_size, Hkv};
+  return DUALKV_OK;
+}
+
+// The pools (i = 0: keys, 1: values, 2 and 3: their scales) as memory ranges.
+Rows cache_range(const PagedKV& kv, uint64_t head_rows, int D, int i) {
+  const void* p[4] = {kv.k, kv.v, kv.ks, kv.vs};
+  return flat(p[i], head_rows * (uint64_t)(i < 2 ? (kv.ks ? D / 2 : 2 * D) : D / 16));
+}
+
+// Offsets from 0 on that do not decrease; the last one may be 0.
+int check_offsets(int n, const int32_t* off) {
+  if (n < 1 || !off || off[0] != 0) return DUALKV_ERR_INVALID;
+  for (int i = 0; i < n; ++i)
+    if (off[i + 1] < off[i]) return DUALKV_ERR_INVALID;
+  return n > kMaxSegs ? DUALKV_ERR_UNSUPPORTED : DUALKV_OK;
+}
+
+bool table_fits(int max_pages, int page_size) {
+  return max_pages >= 1 && (int64_t)max_pages * page_size <= INT32_MAX;
+}
+
+int status_of_device(uint32_t** status) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DUALKV_ERR_CUDA;
+  return status_word(dev, status);
+}
+
+int append_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                const void* q_weight, const void* k_weight, int weight_dtype, float weight_offset, float eps,
+                const float* inv_freq, int rope_dim, int interleaved, const dualkv_kv_cache* cache, const int32_t* pages,
+                int max_pages, const int32_t* lens, const int32_t* starts, int S, const int32_t* off, int Hq, int Hkv,
+                int D, void* q_out, void* stream) {
+  AppendArgs a{};
+  uint64_t head_rows = 0;
+  int rc = check_offsets(S, off);
+  if (rc) return rc;
+  if ((rc = check_cache(cache, Hkv, D, &a.kv, &head_rows))) return rc;
+  const int64_t T = off[S], wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if (Hq < 1 || Hq % Hkv || wq > INT32_MAX / 2) return DUALKV_ERR_INVALID;
+  if (!table_fits(max_pages, cache->page_size)) return DUALKV_ERR_INVALID;
+  if ((q_weight != nullptr) != (k_weight != nullptr)) return DUALKV_ERR_INVALID;
+  if (weight_dtype != DUALKV_BF16 && weight_dtype != DUALKV_F32) return DUALKV_ERR_INVALID;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset)) return DUALKV_ERR_INVALID;
+  if (rope_dim < 0 || rope_dim > D || rope_dim % 16 || (rope_dim && !inv_freq)) return DUALKV_ERR_INVALID;
+  if (q_stride < wq || q_stride > kMaxRowStride || q_stride % 8) return DUALKV_ERR_INVALID;
+  for (int64_t s : {k_stride, v_stride})
+    if (s < wk || s > kMaxRowStride || s % 8) return DUALKV_ERR_INVALID;
+  if (T == 0) return DUALKV_OK;
+  if (!q || !k || !v || !q_out || !pages || !lens || !starts) return DUALKV_ERR_INVALID;
+  for (const void* p : {q, k, v, q_weight, k_weight, (const void*)inv_freq, (const void*)q_out})
+    if (!aligned16(p)) return DUALKV_ERR_ALIGN;
+  for (const void* p : {(const void*)pages, (const void*)lens, (const void*)starts})
+    if (!aligned_to(p, 4)) return DUALKV_ERR_ALIGN;
+  const uint64_t uT = (uint64_t)T, uS = (uint64_t)S, wbytes = (uint64_t)D * (weight_dtype == DUALKV_F32 ? 4 : 2);
+  auto rows = [&](const void* p, int64_t stride, int64_t w) {
+    return Rows{p, (uint64_t)stride * 2, (uint64_t)w * 2, uT};
+  };
+  if (outputs_overlap({flat(q_out, uT * wq * 2), cache_range(a.kv, head_rows, D, 0), cache_range(a.kv, head_rows, D, 1),
+                       cache_range(a.kv, head_rows, D, 2), cache_range(a.kv, head_rows, D, 3)},
+                      {rows(q, q_stride, wq), rows(k, k_stride, wk), rows(v, v_stride, wk), flat(q_weight, wbytes),
+                       flat(k_weight, wbytes), flat(inv_freq, (uint64_t)rope_dim * 2),
+                       flat(pages, uS * (uint64_t)max_pages * 4), flat(lens, uS * 4), flat(starts, uS * 4)}))
+    return DUALKV_ERR_INVALID;
+  typedef __nv_bfloat16 bf;
+  a.q = static_cast<const bf*>(q);
+  a.k = static_cast<const bf*>(k);
+  a.v = static_cast<const bf*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<bf*>(q_out);
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.inv_freq = inv_freq;
+  a.table = pages;
+  a.lens = lens;
+  a.starts = starts;
+  a.max_pages = max_pages;
+  a.T = T;
+  a.Hq = Hq;
+  a.half = rope_dim / 2;
+  a.w0 = weight_offset;
+  a.eps = eps;
+  a.weight_f32 = weight_dtype == DUALKV_F32;
+  a.inter = interleaved != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if ((rc = status_of_device(&a.status))) return rc;
+  return timed(DUALKV_KERNEL_CACHE, st, [&] { return launch_append(D, a, S, off, st); }) == cudaSuccess ? DUALKV_OK
+                                                                                                      : DUALKV_ERR_CUDA;
+}
+
+int read_impl(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens, int S,
+              const int32_t* off, int Hkv, int D, void* k_out, void* v_out, void* stream) {
+  ReadArgs a{};
+  uint64_t head_rows = 0;
+  int rc = check_offsets(S, off);
+  if (rc) return rc;
+  if ((rc = check_cache(cache, Hkv, D, &a.kv, &head_rows))) return rc;
+  if ((int64_t)Hkv * D > INT32_MAX / 2 || !table_fits(max_pages, cache->page_size)) return DUALKV_ERR_INVALID;
+  const uint64_t uT = (uint64_t)off[S], uS = (uint64_t)S, bytes = uT * (uint64_t)Hkv * (uint64_t)D * 2;
+  if (uT == 0) return DUALKV_OK;
+  if (!pages || !lens || !k_out || !v_out) return DUALKV_ERR_INVALID;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned_to(pages, 4) || !aligned_to(lens, 4)) return DUALKV_ERR_ALIGN;
+  if (outputs_overlap({flat(k_out, bytes), flat(v_out, bytes)},
+                      {cache_range(a.kv, head_rows, D, 0), cache_range(a.kv, head_rows, D, 1),
+                       cache_range(a.kv, head_rows, D, 2), cache_range(a.kv, head_rows, D, 3),
+                       flat(pages, uS * (uint64_t)max_pages * 4), flat(lens, uS * 4)}))
+    return DUALKV_ERR_INVALID;
+  a.table = pages;
+  a.lens = lens;
+  a.max_pages = max_pages;
+  a.T = off[S];
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if ((rc = status_of_device(&a.status))) return rc;
+  return timed(DUALKV_KERNEL_CACHE, st, [&] { return launch_read(D, a, S, off, st); }) == cudaSuccess ? DUALKV_OK
+                                                                                                    : DUALKV_ERR_CUDA;
+}
+
+// Groups and heads of a decode call.
+int check_decode(int G, const int32_t* groups, int Hq, int Hkv, int D) {
+  const int rc = check_offsets(G, groups);
+  if (rc) return rc;
+  if ((D != 64 && D != 128 && D != 512) || Hkv < 1 || Hkv > (1 << 16) || Hq < 1 || Hq % Hkv || Hq > (1 << 16))
+    return DUALKV_ERR_INVALID;
+  return groups[G] > kMaxResponses ? DUALKV_ERR_UNSUPPORTED : DUALKV_OK;
+}
+
+int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, const int32_t* prompt_pages,
+                int max_prompt_pages, const int32_t* prompt_lens, const int32_t* pages, int max_pages,
+                const int32_t* lens, int G, const int32_t* groups, int Hq, int Hkv, int D, float scale, int window,
+                void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  DecodeArgs a{};
+  uint64_t head_rows = 0;
+  int rc = check_decode(G, groups, Hq, Hkv, D);
+  if (rc) return rc;
+  if ((rc = check_cache(cache, Hkv, D, &a.kv, &head_rows))) return rc;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DUALKV_ERR_INVALID;
+  const int64_t wq = (int64_t)Hq * D;
+  if (q_stride < wq || q_stride > kMaxRowStride || q_stride % 8) return DUALKV_ERR_INVALID;
+  if (!table_fits(max_pages, cache->page_size)) return DUALKV_ERR_INVALID;
+  const bool prompts = prompt_pages != nullptr;
+  if (prompts != (prompt_lens != nullptr)) return DUALKV_ERR_INVALID;
+  if (prompts ? !table_fits(max_prompt_pages, cache->page_size) : max_prompt_pages != 0) return DUALKV_ERR_INVALID;
+  const uint64_t B = (uint64_t)groups[G], uG = (uint64_t)G;
+  if (B == 0) return DUALKV_OK;
+  if (!q || !pages || !lens || !out) return DUALKV_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(out)) return DUALKV_ERR_ALIGN;
+  for (const void* p : {(const void*)prompt_pages, (const void*)prompt_lens, (const void*)pages, (const void*)lens,
+                        (const void*)lse})
+    if (!aligned_to(p, 4)) return DUALKV_ERR_ALIGN;
+  const size_t need = decode_workspace_bytes((int)B, Hq, Hkv, D);
+  if (need && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < need)) return DUALKV_ERR_WORKSPACE;
+  if (outputs_overlap({flat(out, B * wq * 2), flat(lse, B * Hq * 4), flat(workspace, need)},
+                      {Rows{q, (uint64_t)q_stride * 2, (uint64_t)wq * 2, B}, cache_range(a.kv, head_rows, D, 0),
+                       cache_range(a.kv, head_rows, D, 1), cache_range(a.kv, head_rows, D, 2),
+                       cache_range(a.kv, head_rows, D, 3), flat(prompt_pages, uG * (uint64_t)max_prompt_pages * 4),
+                       flat(prompt_lens, uG * 4), flat(pages, B * (uint64_t)max_pages * 4), flat(lens, B * 4)}))
+    return DUALKV_ERR_INVALID;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.prompt_table = prompt_pages;
+  a.prompt_lens = prompt_lens;
+  a.table = pages;
+  a.lens = lens;
+  a.max_prompt_pages = max_prompt_pages;
+  a.max_pages = max_pages;
+  a.G = G;
+  a.B = (int)B;
+  a.Hq = Hq;
+  a.window = window < 0 ? 0 : window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.workspace = workspace;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if ((rc = status_of_device(&a.status))) return rc;
+  return timed(DUALKV_KERNEL_DECODE, st, [&] { return launch_decode(D, a, groups, st); }) == cudaSuccess ? DUALKV_OK
+                                                                                                       : DUALKV_ERR_CUDA;
+}
+
 Bound bound_of(double v) {
   const float hi = (float)v;
   return Bound{hi, (float)(v - (double)hi)};
@@ -1058,6 +1259,38 @@ int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float
     return policy_impl(true, logp, old_logp, ref_logp, nullptr, advantages, per_token, mask, N, R_offsets, clip_low,
                        clip_high, dual_clip, kl_coef, entropy_coef, DUALKV_LOSS_TOKEN_MEAN, nullptr, nullptr,
                        const_cast<float*>(weights), nullptr, 0, dloss, dlogp, dentropy, stream);
+  });
+}
+
+int dualkv_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype,
+                        float weight_offset, float eps, const float* inv_freq, int rope_dim, int interleaved,
+                        const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens,
+                        const int32_t* starts, int S, const int32_t* row_offsets, int Hq, int Hkv, int D, void* q_out,
+                        void* stream) {
+  return guarded([&] {
+    return append_impl(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, weight_dtype, weight_offset, eps,
+                       inv_freq, rope_dim, interleaved, cache, pages, max_pages, lens, starts, S, row_offsets, Hq, Hkv,
+                       D, q_out, stream);
+  });
+}
+
+int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens, int S,
+                      const int32_t* row_offsets, int Hkv, int D, void* k_out, void* v_out, void* stream) {
+  return guarded([&] { return read_impl(cache, pages, max_pages, lens, S, row_offsets, Hkv, D, k_out, v_out, stream); });
+}
+
+size_t dualkv_decode_workspace_bytes(int G, const int32_t* groups, int Hq, int Hkv, int D) {
+  return check_decode(G, groups, Hq, Hkv, D) ? 0 : decode_workspace_bytes(groups[G], Hq, Hkv, D);
+}
+
+int dualkv_decode(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, const int32_t* prompt_pages,
+                  int max_prompt_pages, const int32_t* prompt_lens, const int32_t* pages, int max_pages,
+                  const int32_t* lens, int G, const int32_t* groups, int Hq, int Hkv, int D, float scale, int window,
+                  void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return decode_impl(q, q_stride, cache, prompt_pages, max_prompt_pages, prompt_lens, pages, max_pages, lens, G,
+                       groups, Hq, Hkv, D, scale, window, out, lse, workspace, workspace_bytes, stream);
   });
 }
 

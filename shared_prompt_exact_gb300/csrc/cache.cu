@@ -1,0 +1,344 @@
+// cache.cu -- new rows of keys and values into a paged cache, and rows of it back.
+//
+// append: for row t of stream s, the (t - off[s])-th of the n_s rows of this call, with lens[s]
+// tokens held afterwards:
+//   index i = lens[s] - n_s + (t - off[s]),  position p = starts[s] + i
+//   q, k: per-head norm and rotation by p f_j as in rope.cu;  q -> q_out,  k and v -> (page i / ps, slot i % ps)
+//   4 bits, for each 32 values of a head:
+//     step = max |x| / 7 rounded up to 5 significant bits (so (code - 8) step is exact in bf16)
+//     n = x / step rounded to the nearest, ties away from zero;  code = n + 8
+//     a group with a value that is not finite gets the scale NaN
+// read: the same rows back in bf16.
+//
+// Both touch each value once and are bound by HBM bandwidth (few rows: by latency).  The walk over
+// rows and heads, the loads ahead through shared memory and the arithmetic are rope.cu's: one warp per
+// row, q's heads first, then k's, then v's.  Keys are quantised from fp32, before any rounding to bf16.
+#include <cuda_bf16.h>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+#include "segs.cuh"
+
+namespace dkv {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kDepth = 3;  // steps in a lane's ring, as in rope.cu
+
+// Where row t of the call goes: its position, and its page and slot (page < 0: nowhere).
+struct Place {
+  uint32_t pos;
+  int page, slot;
+};
+template <int CAP>
+__device__ __forceinline__ int index_of(const SegTable<CAP>& seg, const int32_t* lens, int t, int& s) {
+  s = seg_of(seg, t);
+  return lens[s] - (seg.off[s + 1] - t);
+}
+template <int CAP>
+__device__ __forceinline__ void find_page(const PagedKV& kv, const SegTable<CAP>& seg, const int32_t* table,
+                                          int max_pages, int t, int s, int index, uint32_t* status, Place& at) {
+  at.page = -1;
+  at.slot = 0;
+  if (index < t - seg.off[s]) {  // the stream is said to hold fewer tokens than this call has of it
+    if (status) atomicOr(status, kDevErrBounds);
+    return;
+  }
+  const int place = index / kv.ps;
+  at.slot = index - place * kv.ps;
+  at.page = page_at(kv, table + (int64_t)s * max_pages, max_pages, place, status);
+}
+
+// What a block of the append keeps in shared memory.
+template <int D, int BITS>
+struct AppendShared {
+  alignas(16) float w[2][D];
+  alignas(16) float cs[kWarps][D / 2];
+  alignas(16) float sn[kWarps][D / 2];
+  uint64_t freq[D / 2];
+  alignas(16) float k[BITS == 4 ? kWarps : 1][BITS == 4 ? 512 : 4];  // a step's keys in their order
+  uint4 ring[kDepth][2][kThreads];
+};
+
+// Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.
+__device__ __forceinline__ uint2 quantise16(const float (&x)[16], __nv_bfloat16& scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);  // NaN above infinity above all
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const uint32_t bits = (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0x7ffffu) & ~0x7ffffu;
+  scale = top < 0x7f800000u ? __ushort_as_bfloat16((unsigned short)(bits >> 16))
+                            : __ushort_as_bfloat16((unsigned short)0x7fc0u);
+  const float step = top != 0u && top < 0x7f800000u ? __uint_as_float(bits) : 1.f;
+  uint32_t out[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float n = floorf(__fdiv_rn(fabsf(x[e]), step) + 0.5f);
+    const int code = 8 + (top < 0x7f800000u ? (int)copysignf(n, x[e]) : 0);
+    out[e >> 3] |= (uint32_t)(code & 15) << (4 * (e & 7));
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// The rotation of the lane's values that are turned; the others pass as they are, infinities among them.
+__device__ __forceinline__ void turn(Vec8& a, Vec8& b, const Angles& g, const LaneMap& m, bool inter) {
+  if (!inter) {
+    if (m.ta) rotate(a, b, g.cs, g.sn, g.neg, false);
+    return;
+  }
+  if (m.ta) {
+    turn2(a.v[0], a.v[2], g.cs.v[0], g.sn.v[0], g.neg.v[0]);
+    turn2(a.v[1], a.v[3], g.cs.v[1], g.sn.v[1], g.neg.v[1]);
+  }
+  if (m.tb) {
+    turn2(b.v[0], b.v[2], g.cs.v[2], g.sn.v[2], g.neg.v[2]);
+    turn2(b.v[1], b.v[3], g.cs.v[3], g.sn.v[3], g.neg.v[3]);
+  }
+}
+
+__device__ __forceinline__ void natural8(const Vec8& v, float* to) {
+  *reinterpret_cast<float4*>(to) = make_float4(v.v[0].x, v.v[2].x, v.v[0].y, v.v[2].y);
+  *reinterpret_cast<float4*>(to + 4) = make_float4(v.v[1].x, v.v[3].x, v.v[1].y, v.v[3].y);
+}
+
+// 16 values from natural order into a row of the 4-bit pools.
+template <int D>
+__device__ __forceinline__ void store_codes(const float (&x)[16], void* codes, __nv_bfloat16* scales, int64_t row, int i,
+                                            bool live) {
+  __nv_bfloat16 scale;
+  const uint2 c = quantise16(x, scale);
+  if (!live) return;
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + row * (D / 2) + 8 * i) = c;
+  if ((i & 1) == 0) scales[row * (D / kGroup) + i / 2] = scale;
+}
+
+template <int D, int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
+                                                             const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int G = D / 16, S = 32 / G;
+  extern __shared__ uint4 dynamic[];
+  AppendShared<D, BITS>& sh = *reinterpret_cast<AppendShared<D, BITS>*>(dynamic);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G, i = lane % G;
+  const LaneMap m = lane_map<D>(i, A.half, A.inter);
+  // a lane's two vectors of a value head: 16 consecutive values in 4 bits, else as its neighbours'
+  const int va = BITS == 4 ? 16 * i : 8 * i, vb = BITS == 4 ? 16 * i + 8 : D / 2 + 8 * i;
+  const bool norm = A.q_weight != nullptr;
+  const int Hkv = A.kv.Hkv, nq = (A.Hq + S - 1) / S, nk = (Hkv + S - 1) / S, steps = nq + 2 * nk;
+  // block rows (blockIdx.y) share a row's steps
+  const int begin = steps * (int)blockIdx.y / (int)gridDim.y, end = steps * ((int)blockIdx.y + 1) / (int)gridDim.y;
+  const int64_t first = (int64_t)blockIdx.x * kWarps + warp, stride = (int64_t)gridDim.x * kWarps;
+
+  int64_t at = first;
+  int s_at = begin;
+  auto fetch = [&](int stage) {
+    if (at < A.T) {
+      const int part = s_at < nq ? 0 : s_at < nq + nk ? 1 : 2;
+      const int h = slot + (s_at - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * S;
+      const __nv_bfloat16* x = (part == 0 ? A.q + at * A.q_stride : part == 1 ? A.k + at * A.k_stride : A.v + at * A.v_stride) + h * D;
+      if (h < (part == 0 ? A.Hq : Hkv)) {
+        copy16(&sh.ring[stage][0][threadIdx.x], x + (part == 2 ? va : m.a));
+        copy16(&sh.ring[stage][1][threadIdx.x], x + (part == 2 ? vb : m.b));
+      }
+      if (++s_at == end) {
+        s_at = begin;
+        at += stride;
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+  for (int j = threadIdx.x; j < A.half; j += kThreads) sh.freq[j] = turn_fraction(A.inv_freq[j]);
+  if (norm) {
+    for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
+      const void* w = d < D ? A.q_weight : A.k_weight;
+      const int e = d % D;
+      sh.w[d / D][split_at(e, D)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
+                                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]));
+    }
+  }
+  __syncthreads();
+
+  int stage = 0;
+  for (int64_t t = first; t < A.T; t += stride) {
+    int s;
+    const int index = index_of(seg, A.lens, (int)t, s);
+    Place at_row;
+    at_row.pos = (uint32_t)A.starts[s] + (uint32_t)index;
+    find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at_row);
+    const Angles ang = row_angles((int)at_row.pos, sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
+    for (int step = begin; step < end; ++step) {
+      const int part = step < nq ? 0 : step < nq + nk ? 1 : 2;
+      const int h = slot + (step - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * S;
+      fetch(stage == 0 ? kDepth - 1 : stage - 1);
+      copies_wait<kDepth - 1>();
+      const uint4 ra = sh.ring[stage][0][threadIdx.x], rb = sh.ring[stage][1][threadIdx.x];
+      stage = stage == kDepth - 1 ? 0 : stage + 1;
+      const bool live = part == 0 ? h < A.Hq : h < Hkv && at_row.page >= 0;
+      const int64_t row = part == 0 ? t * A.Hq + h : cache_row(A.kv, at_row.page, h, at_row.slot);
+      if (part == 2) {
+        if (BITS == 16) {
+          if (live) {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.v) + row * D;
+            *reinterpret_cast<uint4*>(y + va) = ra;
+            *reinterpret_cast<uint4*>(y + vb) = rb;
+          }
+        } else {
+          float x[16];
+          natural8(unpack8(ra), x);
+          natural8(unpack8(rb), x + 8);
+          store_codes<D>(x, A.kv.v, A.kv.vs, row, i, live);
+        }
+        continue;
+      }
+      Vec8 a = unpack8(ra), b = unpack8(rb);
+      if (norm) {
+        const float* w = sh.w[part];
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
+        const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
+        const float2 rr = make_float2(r, r);
+        const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
+          b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
+        }
+      }
+      turn(a, b, ang, m, A.inter);
+      if (part == 0 || BITS == 16) {
+        if (live) {
+          __nv_bfloat16* y = (part == 0 ? A.q_out : static_cast<__nv_bfloat16*>(A.kv.k)) + row * D;
+          *reinterpret_cast<uint4*>(y + m.a) = pack8(a);
+          *reinterpret_cast<uint4*>(y + m.b) = pack8(b);
+        }
+      } else {  // groups of 32 lie across lanes: through shared memory into the values' order
+        float* keys = sh.k[BITS == 4 ? warp : 0];
+        natural8(a, keys + slot * D + m.a);
+        natural8(b, keys + slot * D + m.b);
+        __syncwarp();
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(keys + 16 * lane + e);
+        __syncwarp();
+        store_codes<D>(x, A.kv.k, A.kv.ks, row, i, live);
+      }
+    }
+  }
+}
+
+// A warp takes a row: first its keys, then its values, 8 values a lane and step.
+template <int D, int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int V = D / 8;  // vectors of a head
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  if (t >= A.T) return;
+  int s;
+  const int index = index_of(seg, A.lens, (int)t, s);
+  Place at;
+  find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at);
+  const int n = A.kv.Hkv * V;
+  uint4* out[2] = {reinterpret_cast<uint4*>(A.k_out) + t * n, reinterpret_cast<uint4*>(A.v_out) + t * n};
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const void* pool = which ? A.kv.v : A.kv.k;
+    const __nv_bfloat16* scales = which ? A.kv.vs : A.kv.ks;
+#pragma unroll 4
+    for (int u = lane; u < n; u += 32) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (at.page >= 0) {
+        const int64_t row = cache_row(A.kv, at.page, u / V, at.slot);
+        if (BITS == 16) {
+          y = static_cast<const uint4*>(pool)[row * V + u % V];
+        } else {
+          const uint32_t w = static_cast<const uint32_t*>(pool)[row * V + u % V];
+          const __nv_bfloat162 sc = __bfloat162bfloat162(scales[row * (D / kGroup) + u % V / 4]);
+          const __nv_bfloat162 off = __hmul2(sc, __float2bfloat162_rn(-24.f));
+          // codes 0 and 4, 1 and 5, ...
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 d = decode2(w >> (4 * e), sc, off);
+            p[e] = *reinterpret_cast<const uint32_t*>(&d);
+          }
+          y = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                         __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+        }
+      }
+      out[which][u] = y;
+    }
+  }
+}
+
+template <int D, int BITS, int CAP>
+cudaError_t append_c(const AppendArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  const SegTable<CAP> seg = make_segs<CAP>(0, S, off);
+  constexpr int smem = (int)sizeof(AppendShared<D, BITS>);
+  const cudaError_t e =
+      cudaFuncSetAttribute(append_kernel<D, BITS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int heads = 512 / D, steps = (a.Hq + heads - 1) / heads + 2 * ((a.kv.Hkv + heads - 1) / heads);
+  const int64_t need = (a.T + kWarps - 1) / kWarps;
+  int64_t spare = 304 / need;
+  if (spare < 1) spare = 1;
+  const dim3 grid((unsigned)(need < 1824 ? need : 1824), (unsigned)(spare < steps ? spare : steps));
+  append_kernel<D, BITS, CAP><<<grid, kThreads, smem, st>>>(a, seg);
+  return cudaGetLastError();
+}
+
+template <int D, int BITS, int CAP>
+cudaError_t read_c(const ReadArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  const SegTable<CAP> seg = make_segs<CAP>(0, S, off);
+  read_kernel<D, BITS, CAP><<<(unsigned)((a.T + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, seg);
+  return cudaGetLastError();
+}
+
+template <int D, int CAP>
+cudaError_t append_d(const AppendArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  return a.kv.ks ? append_c<D, 4, CAP>(a, S, off, st) : append_c<D, 16, CAP>(a, S, off, st);
+}
+template <int D, int CAP>
+cudaError_t read_d(const ReadArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  return a.kv.ks ? read_c<D, 4, CAP>(a, S, off, st) : read_c<D, 16, CAP>(a, S, off, st);
+}
+
+}  // namespace
+
+cudaError_t launch_append(int D, const AppendArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  if (a.T <= 0) return cudaSuccess;
+  const bool few = S <= kSmallSegs;
+  switch (D) {
+    case 64:
+      return few ? append_d<64, kSmallSegs>(a, S, off, st) : append_d<64, kMaxSegs>(a, S, off, st);
+    case 128:
+      return few ? append_d<128, kSmallSegs>(a, S, off, st) : append_d<128, kMaxSegs>(a, S, off, st);
+    case 512:
+      return few ? append_d<512, kSmallSegs>(a, S, off, st) : append_d<512, kMaxSegs>(a, S, off, st);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_read(int D, const ReadArgs& a, int S, const int32_t* off, cudaStream_t st) {
+  if (a.T <= 0) return cudaSuccess;
+  const bool few = S <= kSmallSegs;
+  switch (D) {
+    case 64:
+      return few ? read_d<64, kSmallSegs>(a, S, off, st) : read_d<64, kMaxSegs>(a, S, off, st);
+    case 128:
+      return few ? read_d<128, kSmallSegs>(a, S, off, st) : read_d<128, kMaxSegs>(a, S, off, st);
+    case 512:
+      return few ? read_d<512, kSmallSegs>(a, S, off, st) : read_d<512, kMaxSegs>(a, S, off, st);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace dkv

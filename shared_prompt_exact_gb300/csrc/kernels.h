@@ -218,4 +218,56 @@ struct PolicyArgs {
 cudaError_t launch_policy(bool backward, const PolicyArgs& a, int N, const int32_t* off, cudaStream_t st);
 size_t policy_workspace_bytes(int N, const int32_t* off);
 
+// ---- paged key/value cache (cache.cu)
+struct PagedKV {
+  void *k, *v;              // [pages, Hkv, ps, D] bf16, or codes [pages, Hkv, ps, D / 2]
+  __nv_bfloat16 *ks, *vs;   // scales [pages, Hkv, ps, D / 32] of the codes; null: bf16
+  int pages, ps, Hkv;
+};
+struct AppendArgs {
+  const __nv_bfloat16 *q, *k, *v;       // rows, head h of row t at t * stride + h * D
+  int64_t q_stride, k_stride, v_stride;  // elements
+  __nv_bfloat16* q_out;                  // contiguous
+  const void *q_weight, *k_weight;       // D values each; both null: no norm
+  const float* inv_freq;                 // half values
+  PagedKV kv;
+  const int32_t *table, *lens, *starts;  // [streams, max_pages], [streams], [streams]
+  int max_pages;
+  int64_t T;
+  int Hq, half;
+  float w0, eps;
+  bool weight_f32, inter;
+  uint32_t* status;
+};
+cudaError_t launch_append(int D, const AppendArgs& a, int S, const int32_t* off, cudaStream_t st);
+
+struct ReadArgs {
+  PagedKV kv;
+  const int32_t *table, *lens;
+  int max_pages;
+  int64_t T;
+  __nv_bfloat16 *k_out, *v_out;  // contiguous
+  uint32_t* status;
+};
+cudaError_t launch_read(int D, const ReadArgs& a, int S, const int32_t* off, cudaStream_t st);
+
+// ---- attention of one token per response over the cache (decode.cu)
+constexpr int kMaxResponses = 8192;
+struct DecodeArgs {
+  const __nv_bfloat16* q;  // head h of response b at b * q_stride + h * D
+  int64_t q_stride;        // elements
+  PagedKV kv;
+  const int32_t *prompt_table, *prompt_lens;  // [G, max_prompt_pages], [G]; null: no prompts
+  const int32_t *table, *lens;                // [B, max_pages], [B]
+  int max_prompt_pages, max_pages;
+  int G, B, Hq, window;
+  float scale_log2;  // softmax scale * log2(e)
+  __nv_bfloat16* out;
+  float* lse;        // may be null
+  void* workspace;
+  uint32_t* status;
+};
+cudaError_t launch_decode(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st);
+size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D);
+
 }  // namespace dkv

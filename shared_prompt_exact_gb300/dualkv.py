@@ -37,10 +37,11 @@ EXPORTS = ("dualkv_fwd", "dualkv_bwd_workspace_bytes", "dualkv_bwd", "dualkv_bui
            "dualkv_selftest_kernel", "dualkv_plan_cache_info", "dualkv_qk_norm_rope",
            "dualkv_qk_norm_rope_bwd", "dualkv_qk_norm_rope_bwd_workspace_bytes", "dualkv_token_logprobs",
            "dualkv_token_logprobs_bwd", "dualkv_policy_loss", "dualkv_policy_loss_bwd",
-           "dualkv_policy_loss_workspace_bytes")
+           "dualkv_policy_loss_workspace_bytes", "dualkv_cache_append", "dualkv_cache_read", "dualkv_decode",
+           "dualkv_decode_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 _TOO_FAR = 1 << 31  # counts from here on would wrap on their way into a C int
-KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope", "logprobs", "policy")
+KERNEL_KINDS = ("fwd", "prep", "dkv", "reduce", "dq", "pack", "rope", "logprobs", "policy", "cache", "decode")
 DUALKV_BF16 = 0
 DUALKV_F32 = 1
 LOSS_REDUCTIONS = {"token_mean": 0, "seq_mean": 1, "seq_sum": 2}
@@ -53,6 +54,13 @@ class DualKVError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
         super().__init__(f"{where}: {error_string(code)} (code {code})")
+
+
+class _CacheStruct(ctypes.Structure):
+    """dualkv_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("bits", ctypes.c_int32)]
 
 
 def load(path: Optional[str] = None):
@@ -135,6 +143,17 @@ def load(path: Optional[str] = None):
         lib.dualkv_policy_loss.restype = ci
         lib.dualkv_policy_loss_bwd.argtypes = [vp, vp, vp, vp, ci, vp, ci, i32p, cd, cd, cd, cd, cd, vp, vp, vp, vp, vp]
         lib.dualkv_policy_loss_bwd.restype = ci
+        cache = ctypes.POINTER(_CacheStruct)
+        lib.dualkv_cache_append.argtypes = ([vp, i64, vp, i64, vp, i64, vp, vp, ci, cf, cf, vp, ci, ci, cache, vp, ci, vp, vp,
+                                             ci, i32p, ci, ci, ci, vp, vp])
+        lib.dualkv_cache_append.restype = ci
+        lib.dualkv_cache_read.argtypes = [cache, vp, ci, vp, ci, i32p, ci, ci, vp, vp, vp]
+        lib.dualkv_cache_read.restype = ci
+        lib.dualkv_decode_workspace_bytes.argtypes = [ci, i32p, ci, ci, ci]
+        lib.dualkv_decode_workspace_bytes.restype = ctypes.c_size_t
+        lib.dualkv_decode.argtypes = [vp, i64, cache, vp, ci, vp, vp, ci, vp, ci, i32p, ci, ci, ci, cf, ci, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
+        lib.dualkv_decode.restype = ci
         lib.dualkv_release.argtypes = []
         lib.dualkv_release.restype = None
         _lib = lib
@@ -635,6 +654,159 @@ def dualkv_policy_loss_bwd(logp, old_logp, ref_logp, advantages, mask, N, R_offs
     _raise(rc, where)
 
 
+# ------------------------------------------------------------------ paged key/value cache
+CACHE_GROUP = 32  # values that share a scale in a 4-bit cache
+_I32, _U8 = (torch.int32,), (torch.uint8,)
+
+
+class KVCache:
+    """A paged cache of keys and values: bf16 pools [pages, Hkv, page_size, D], or 4-bit codes, two to a byte
+    (uint8 [pages, Hkv, page_size, D / 2]), with bf16 scales [pages, Hkv, page_size, D / 32].  It wraps tensors
+    that the caller owns; ``KVCache.empty`` allocates them."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "bits", "pages", "Hkv", "page_size", "D", "device", "_c")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not isinstance(k, _Tensor) or not k.is_cuda or k.dim() != 4:
+            raise ValueError("KVCache: k must be a CUDA tensor [pages, heads, page size, values]")
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("KVCache: k_scale and v_scale go together")
+        dev, shape = k.get_device(), k.shape
+        pages, Hkv, ps, width = shape
+        dtypes = _BF16 if k_scale is None else _U8
+        struct = _CacheStruct(_arg("KVCache", "k", k, shape, dtypes, dev), _arg("KVCache", "v", v, shape, dtypes, dev),
+                              None, None, pages, ps, 16)
+        if k_scale is not None:
+            groups = (pages, Hkv, ps, 2 * width // CACHE_GROUP)
+            struct.k_scale = _arg("KVCache", "k_scale", k_scale, groups, _BF16, dev)
+            struct.v_scale = _arg("KVCache", "v_scale", v_scale, groups, _BF16, dev)
+            struct.bits, width = 4, 2 * width
+        self.k, self.v, self.k_scale, self.v_scale, self.device, self._c = k, v, k_scale, v_scale, dev, struct
+        self.bits, self.pages, self.Hkv, self.page_size, self.D = struct.bits, pages, Hkv, ps, width
+
+    @classmethod
+    def empty(cls, pages, Hkv, page_size, D, bits=16, device="cuda"):
+        """A cache of uninitialised pages."""
+        if bits not in (16, 4):
+            raise ValueError(f"KVCache: bits must be 16 or 4, got {bits}")
+        shape = (pages, Hkv, page_size)
+        if bits == 16:
+            return cls(*(torch.empty(*shape, D, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        if D % CACHE_GROUP:
+            raise ValueError(f"KVCache: D must be a multiple of {CACHE_GROUP}, got {D}")
+        return cls(*(torch.empty(*shape, D // 2, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.empty(*shape, D // CACHE_GROUP, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+
+def _cache_arg(where, cache, Hkv, D, device):
+    if not isinstance(cache, KVCache):
+        raise ValueError(f"{where}: cache must be a KVCache")
+    if cache.Hkv != Hkv or cache.D != D:
+        raise ValueError(f"{where}: cache holds {cache.Hkv} heads of {cache.D}, not {Hkv} of {D}")
+    if cache.device != device:
+        raise ValueError(f"{where}: cache is on cuda:{cache.device}, the current device is cuda:{device}")
+    return cache._c
+
+
+def _table(where, name, pages, streams, device):
+    """Address and width of a page table."""
+    if not isinstance(pages, _Tensor) or pages.dim() != 2 or pages.shape[1] >= _TOO_FAR:
+        raise ValueError(f"{where}: {name} must be a tensor [streams, most pages]")
+    width = pages.shape[1]
+    return _arg(where, name, pages, (streams, width), _I32, device), width
+
+
+def _last_offset(where, name, n, offsets):
+    """Rows that `offsets` (n + 1 entries) describe."""
+    if n < 1 or len(offsets) != n + 1:
+        raise ValueError(f"{where}: {name} must hold {n + 1} entries, got {len(offsets)}")
+    last = int(offsets[n])
+    if last < 0:
+        raise ValueError(f"{where}: {name} must not decrease, got {last} as the last")
+    return last
+
+
+def dualkv_cache_append(q, k, v, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, cache, pages, lens,
+                        starts, S, row_offsets, Hq, Hkv, D, q_out, stream=None) -> None:
+    """Norm and rotation of new rows q [T, Hq, D], k [T, Hkv, D] of S streams (rows may be strided, as columns of a
+    fused projection are): q into q_out, k and v into the pages that `pages` [S, most pages] names.  lens: tokens of each
+    stream after this call; starts: position of its token 0."""
+    where = "dualkv_cache_append"
+    S, rope_dim = int(S), int(rope_dim)
+    T = _last_offset(where, "row_offsets", S, row_offsets)
+    dev = torch.cuda.current_device()
+    if max(Hq, Hkv, D, rope_dim) >= _TOO_FAR:
+        _counts(where, Hq=Hq, Hkv=Hkv, D=D, rope_dim=rope_dim)
+    inner = (D, 1)
+    qkv = (_rows(where, "q", q, (T, Hq, D), inner, _BF16, dev) + _rows(where, "k", k, (T, Hkv, D), inner, _BF16, dev)
+           + _rows(where, "v", v, (T, Hkv, D), inner, _BF16, dev))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError(f"{where}: q_weight and k_weight go together")
+    qw = kw = None
+    code = DUALKV_F32
+    if q_weight is not None:
+        qw = _arg(where, "q_weight", q_weight, (D,), _DTYPE_CODES, dev)
+        kw = _arg(where, "k_weight", k_weight, (D,), (q_weight.dtype,), dev)
+        code = _DTYPE_CODES[q_weight.dtype]
+    f = _arg(where, "inv_freq", inv_freq, (rope_dim // 2,), _F32, dev) if rope_dim else None
+    table, width = _table(where, "pages", pages, S, dev)
+    rc = load().dualkv_cache_append(*qkv, qw, kw, code, float(weight_offset), float(eps), f, rope_dim,
+                                    1 if interleaved else 0, _cache_arg(where, cache, Hkv, D, dev), table, width,
+                                    _arg(where, "lens", lens, (S,), _I32, dev),
+                                    _arg(where, "starts", starts, (S,), _I32, dev), S, _offsets(row_offsets), int(Hq),
+                                    int(Hkv), int(D), _arg(where, "q_out", q_out, (T, Hq, D), _BF16, dev),
+                                    _stream_of(stream, dev))
+    _raise(rc, where)
+
+
+def dualkv_cache_read(cache, pages, lens, S, row_offsets, Hkv, D, k_out, v_out, stream=None) -> None:
+    """The last rows of each stream (as many as row_offsets gives it) back as dense keys and values [T, Hkv, D]."""
+    where = "dualkv_cache_read"
+    S = int(S)
+    T = _last_offset(where, "row_offsets", S, row_offsets)
+    dev = torch.cuda.current_device()
+    table, width = _table(where, "pages", pages, S, dev)
+    shape = (T, Hkv, D)
+    rc = load().dualkv_cache_read(_cache_arg(where, cache, Hkv, D, dev), table, width,
+                                  _arg(where, "lens", lens, (S,), _I32, dev), S, _offsets(row_offsets), int(Hkv), int(D),
+                                  _arg(where, "k_out", k_out, shape, _BF16, dev),
+                                  _arg(where, "v_out", v_out, shape, _BF16, dev), _stream_of(stream, dev))
+    _raise(rc, where)
+
+
+def dualkv_decode_workspace_bytes(G, groups, Hq, Hkv, D) -> int:
+    _counts("dualkv_decode_workspace_bytes", G=G, Hq=Hq, Hkv=Hkv, D=D)
+    _last_offset("dualkv_decode_workspace_bytes", "groups", int(G), groups)
+    return int(load().dualkv_decode_workspace_bytes(int(G), _offsets(groups), int(Hq), int(Hkv), int(D)))
+
+
+def dualkv_decode(q, cache, prompt_pages, prompt_lens, pages, lens, G, groups, Hq, Hkv, D, scale, window, out, lse, workspace,
+                  workspace_bytes=None, stream=None) -> None:
+    """Attention of one new token per response, q [B, Hq, D] (rows may be strided), over the prompt that its group
+    shares and its own tokens.  groups: responses before each group's first, B in all; prompt_pages and prompt_lens may
+    be None (no prompts), lse may be."""
+    where = "dualkv_decode"
+    G = int(G)
+    B = _last_offset(where, "groups", G, groups)
+    dev = torch.cuda.current_device()
+    if max(Hq, Hkv, D, abs(window)) >= _TOO_FAR:
+        _counts(where, Hq=Hq, Hkv=Hkv, D=D, window=window)
+    if (prompt_pages is None) != (prompt_lens is None):
+        raise ValueError(f"{where}: prompt_pages and prompt_lens go together")
+    prompts = (None, 0, None)
+    if prompt_pages is not None:
+        prompts = (*_table(where, "prompt_pages", prompt_pages, G, dev),
+                   _arg(where, "prompt_lens", prompt_lens, (G,), _I32, dev))
+    table, width = _table(where, "pages", pages, B, dev)
+    rc = load().dualkv_decode(*_rows(where, "q", q, (B, Hq, D), (D, 1), _BF16, dev),
+                              _cache_arg(where, cache, Hkv, D, dev), *prompts, table, width,
+                              _arg(where, "lens", lens, (B,), _I32, dev), G, _offsets(groups), int(Hq), int(Hkv), int(D),
+                              float(scale), int(window), _arg(where, "out", out, (B, Hq, D), _BF16, dev),
+                              _opt(where, "lse", lse, (Hq, B), _F32, dev),
+                              *_workspace_args(where, workspace, workspace_bytes, dev), _stream_of(stream, dev))
+    _raise(rc, where)
+
+
 def _workspace_args(where, workspace, workspace_bytes, device):
     """(address, bytes) of a workspace tensor, (None, 0) for None; no more than it holds may be claimed."""
     if workspace is None:
@@ -836,3 +1008,40 @@ def policy_loss_backward(logp, old_logp, advantages, R_offsets, dloss, weights, 
                                kl_coef, entropy_coef, "token_mean", dloss, weights, dlogp, dentropy,
                                per_token=per_token)
     return dlogp, dentropy
+
+
+def cache_append(q, k, v, cache, pages, lens, starts, row_offsets, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                 weight_offset=0.0, interleaved=False, stream=None):
+    """Allocate q_out and run dualkv_cache_append; rope_dim is twice the length of inv_freq (None: no rotation)."""
+    (T, Hq, D), Hkv = q.shape, k.shape[1]
+    rope_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    with _allocating_on(stream):
+        q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+        dualkv_cache_append(q, k, v, q_weight, k_weight, weight_offset, eps, inv_freq, rope_dim, interleaved, cache, pages,
+                            lens, starts, len(row_offsets) - 1, row_offsets, Hq, Hkv, D, q_out)
+    return q_out
+
+
+def cache_read(cache, pages, lens, row_offsets, stream=None):
+    """Allocate k and v and run dualkv_cache_read: (k, v), as dualkv.forward takes them."""
+    S = len(row_offsets) - 1
+    with _allocating_on(stream):
+        k, v = (torch.empty(int(row_offsets[S]), cache.Hkv, cache.D, dtype=torch.bfloat16, device=cache.k.device)
+                for _ in range(2))
+        dualkv_cache_read(cache, pages, lens, S, row_offsets, cache.Hkv, cache.D, k, v)
+    return k, v
+
+
+def decode(q, cache, prompt_pages, prompt_lens, pages, lens, groups, window=0, scale=None, workspace=None, stream=None):
+    """Allocate out, lse (and the workspace if not given) and run dualkv_decode: (out [B, Hq, D], lse [Hq, B])."""
+    (B, Hq, D), G = q.shape, len(groups) - 1
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    with _allocating_on(stream):
+        out = torch.empty(B, Hq, D, dtype=q.dtype, device=q.device)
+        lse = torch.empty(Hq, B, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            nbytes = dualkv_decode_workspace_bytes(G, groups, Hq, cache.Hkv, D)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        dualkv_decode(q, cache, prompt_pages, prompt_lens, pages, lens, G, groups, Hq, cache.Hkv, D, scale, window, out, lse,
+                      workspace)
+    return out, lse
