@@ -361,7 +361,7 @@ int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float
  *             A group with a value that is not finite has the scale NaN.  |x| up to 9e37
  * page_size is a multiple of 16 up to 65,536; all pointers are 16-byte aligned.  A stream's tokens lie in
  * the pages that its row of a page table (device int32 [streams, max_pages]) names: token i in slot
- * i % page_size of page i / page_size of the row.  Entries behind a stream's last token are not read.
+ * i % page_size of page i / page_size of the row.  Entries behind a stream's last token are not used.
  * Streams may share pages that are only read (the prompt's); no slot may be written twice in a call.
  * A page outside the pool, or a stream longer than its row of the table, is reported by
  * dualkv_check_status(): nothing is read or written through it (read: zeros; decode: the
@@ -424,7 +424,8 @@ int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int ma
  *                   both may be NULL with max_prompt_pages = 0: no prompts
  *   pages, lens     device int32 [B, max_pages] and [B], B = groups[G].  lens[b] = 0: the prompt
  *                   alone; negative: the response has ended, and nothing is read for it
- *   groups          HOST int32 [G+1], groups[0] = 0, non-decreasing; G <= 4095, B <= 8192
+ *   groups          HOST int32 [G+1], groups[0] = 0, non-decreasing; G <= 4095, B <= 8192,
+ *                   and the tables' tokens times the queries that see them below 2^38
  *                   (DUALKV_ERR_UNSUPPORTED beyond).  B = 0: nothing is done
  *   scale           > 0; scale * log2(e) has to be finite
  *   window          <= 0: all tokens; else the last `window` ones

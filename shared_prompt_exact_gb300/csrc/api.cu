@@ -791,6 +791,12 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   if (prompts ? !table_fits(max_prompt_pages, cache->page_size) : max_prompt_pages != 0) return DUALKV_ERR_INVALID;
   const uint64_t B = (uint64_t)groups[G], uG = (uint64_t)G;
   if (B == 0) return DUALKV_OK;
+  // the kernels count tiles of 16 tokens, once for every 8 queries that share them, in 32 bits
+  const uint64_t GQ = (uint64_t)(Hq / Hkv), page_tiles = (uint64_t)cache->page_size / 16;
+  uint64_t tiles = B * ((GQ + 7) / 8) * (uint64_t)max_pages * page_tiles;
+  for (int g = 0; g < G; ++g)
+    tiles += ((uint64_t)(groups[g + 1] - groups[g]) * GQ + 7) / 8 * (uint64_t)max_prompt_pages * page_tiles;
+  if (tiles >= uint64_t(1) << 31) return DUALKV_ERR_UNSUPPORTED;
   if (!q || !pages || !lens || !out) return DUALKV_ERR_INVALID;
   if (!aligned16(q) || !aligned16(out)) return DUALKV_ERR_ALIGN;
   for (const void* p : {(const void*)prompt_pages, (const void*)prompt_lens, (const void*)pages, (const void*)lens,

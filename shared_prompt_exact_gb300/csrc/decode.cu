@@ -3,12 +3,28 @@
 // For response b of group g (prompt of P tokens, own n = lens[b] >= 0 tokens, query at P + n - 1):
 //   x_k = scale q k over the tokens of the prompt and the response within the window
 //   m = max x, l = sum exp(x - m), out = sum exp(x - m) v / l, lse = m + log l
-// A block takes one response and head; its warps walk the keys with a running maximum, a lane
-// holding D / 32 values of the head, and join their sums at the end.
+//
+// Few queries meet many keys, so the keys' and values' bytes are the bound, each response's read once and each
+// prompt's once for its group.  A *source* is a response's own tokens or a group's prompt; its *rows* are the
+// queries that see it (the Hq / Hkv heads of a kv-head, of one response or of all of a group).  Sources are cut into tiles
+// of 16 keys, and the tiles of all sources and kv-heads are dealt out in order to the warps of one block per SM, the
+// same number to each, whatever the lengths are: a warp walks its share alone, with a running maximum and
+// sum per row, and leaves a partial result (sum, maximum, weighted values) for every source that it meets.  A second
+// kernel joins a row's partial results, its response's and its prompt's, in a fixed order.
+// The lengths stay on the device: every block forms the same prefix sum of the sources' tiles.
+//
+// Inside a warp (mma.m16n8k16, keys as M, up to 8 NT query rows as N):
+//   S^T[keys, rows] = K Q^T        K straight from its rows in shared memory as the A operand: the order of the
+//                                  head's values in a contraction is free, so a lane takes 16 consecutive bytes
+//   O^T[values, rows] += V^T P^T   two keys' words interleaved as the A operand; P^T is the transpose of the
+//                                  packed weights (movmatrix); the order of the values is undone when O is written
+// Both accumulators have a row's numbers in the same lanes, so a change of its maximum is a product per lane.  A tile
+// comes by cp.async, keys and values by turns through the warp's own ring: no barrier but the warp's.
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "segs.cuh"
 
@@ -16,89 +32,701 @@ namespace dkv {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTile = 16;       // keys of a tile
+constexpr int kBlocks = 152;    // one per SM
+constexpr int kMostShared = 226 << 10;  // dynamic shared memory of a block, 1 KB left for the rest
+constexpr float kLowest = -3e38f;  // maximum of a row that has seen nothing: finite, so differences are too
+constexpr float kRescale = 8.f;    // a maximum moves when a weight would pass 2^8
 
-// Value d of a row of a pool.
-__device__ __forceinline__ float value_at(const void* pool, const __nv_bfloat16* scales, int64_t row, int D, int d) {
-  if (!scales) return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[row * D + d]);
-  const uint8_t c = static_cast<const uint8_t*>(pool)[row * (D / 2) + d / 2];
-  return __bfloat162float(scales[row * (D / kGroup) + d / kGroup]) * (float)((d & 1 ? c >> 4 : c & 15) - 8);
+template <int D, int BITS, int NT>
+struct Cfg {
+  static constexpr int RB = BITS == 16 ? 2 * D : D / 2;  // bytes of a row
+  static constexpr int KP = BITS == 16 ? RB + 16 : RB;   // pitches in shared memory: 16 bytes more where lanes of
+  static constexpr int VP = RB + 16;                     // several keys would meet in one bank
+  static constexpr int SB = BITS == 16 ? 0 : kTile * (D / kGroup) * 2;  // bytes of a tile's scales
+  static constexpr int SLOT = kTile * VP + SB;
+  static constexpr int WARPS = D == 512 ? (BITS == 16 ? 6 : 8) : (NT == 2 ? 12 : (BITS == 16 ? 12 : 16));
+  static constexpr int SLOTS = D == 512 ? (BITS == 16 ? 2 : 4) : (BITS == 16 ? (D == 128 ? 4 : 6) : 6);
+  static constexpr int COLS = 8 * NT;
+  static constexpr int RING = SLOTS * SLOT;  // bytes of a warp's ring
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// 16 bytes, or zeros where `bytes` is 0
+__device__ __forceinline__ void copy16z(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* p) {
+  if constexpr (WORDS == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  }
 }
 
-template <int D, int CAP>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const DecodeArgs A, const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = seg_of(seg, b), kvh = h / (A.Hq / A.kv.Hkv), n = A.lens[b];
-  const int P = A.prompt_lens && n >= 0 ? max(0, A.prompt_lens[g]) : 0;
-  const int lo = A.window > 0 ? max(0, P - A.window + n) : 0, end = P + max(n, 0);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(A.q[b * A.q_stride + h * D + lane + 32 * e]) * A.scale_log2;
-    o[e] = 0.f;
-  }
-  for (int k = lo + warp; k < end; k += kWarps) {
-    const int i = k < P ? k : k - P, max_pages = k < P ? A.max_prompt_pages : A.max_pages, place = i / A.kv.ps;
-    const int32_t* table = k < P ? A.prompt_table + (int64_t)g * max_pages : A.table + (int64_t)b * max_pages;
-    const int page = page_at(A.kv, table, max_pages, place, A.status);
-    if (page < 0) continue;
-    const int64_t row = cache_row(A.kv, page, kvh, i - place * A.kv.ps);
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], value_at(A.kv.k, A.kv.ks, row, D, lane + 32 * e), x);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    const float top = fmaxf(m, x), shift = exp2f(m - top), p = exp2f(x - top);
-    m = top;
-    l = l * shift + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * shift + p * value_at(A.kv.v, A.kv.vs, row, D, lane + 32 * e);
-  }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+// Codes e and e + 4 of word w (cache.cuh's decode2 with the shifts folded).
+template <int E>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 minus24s) {
+  const uint32_t u = ((E == 0 ? w << 3 : w >> (E == 0 ? 0 : 4 * E - 3)) & 0x00780078u) | 0x41804180u;
+  return bits(__hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, minus24s));
+}
+
+// ---------------------------------------------------------------- the deal
+// Tiles of every source in order: prompts 0 .. G - 1, then responses 0 .. B - 1; a source with more rows
+// than a warp takes at once counts its tiles once for every block of rows.  The same sequence follows for each kv-head.
+struct Deal {
+  uint64_t total;   // tiles of all kv-heads
+  uint32_t per_head, workers;
+};
+__device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int warps) {
+  Deal d;
+  d.per_head = per_head;
+  d.total = (uint64_t)per_head * (uint64_t)Hkv;
+  d.workers = (uint32_t)(d.total < (uint64_t)warps ? d.total : (uint64_t)warps);  // so that each has a tile
+  return d;
+}
+__device__ __forceinline__ uint64_t first_tile(const Deal& d, uint32_t worker) { return d.total * worker / d.workers; }
+__device__ __forceinline__ uint32_t worker_of(const Deal& d, uint64_t tile) {
+  return (uint32_t)(((tile + 1) * d.workers - 1) / d.total);
+}
+
+__device__ __forceinline__ int clamp_len(int n, int max_pages, int ps, uint32_t* status) {
+  if (n <= (int64_t)max_pages * ps) return n;
+  if (status) atomicOr(status, kDevErrBounds);
+  return max_pages * ps;
+}
+// Prompt of group g (0 without prompts) and tokens of response b (negative: ended), as far as the tables go.
+__device__ __forceinline__ int prompt_len(const DecodeArgs& A, int g, uint32_t* status) {
+  return A.prompt_lens ? max(0, clamp_len(A.prompt_lens[g], A.max_prompt_pages, A.kv.ps, status)) : 0;
+}
+__device__ __forceinline__ int response_len(const DecodeArgs& A, int b, uint32_t* status) {
+  return clamp_len(A.lens[b], A.max_pages, A.kv.ps, status);
+}
+// First position that a response of n tokens behind a prompt of P sees.
+__device__ __forceinline__ int first_position(const DecodeArgs& A, int P, int n) {
+  return A.window > 0 ? (int)max((int64_t)0, (int64_t)P + n - A.window) : 0;
+}
+// Tiles of tokens [lo, end).
+__device__ __forceinline__ int tiles_of(int lo, int end) { return lo < end ? (end + kTile - 1) / kTile - lo / kTile : 0; }
+
+struct Workspace {
+  uint32_t* cum;  // [G + B + 1] tiles before each source, of one kv-head
+  float2* ml;     // [slots] maximum (base 2) and sum
+  float* o;       // [slots][D]
+};
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+constexpr int kMostSources = kMaxSegs + kMaxResponses;
+constexpr size_t kMostWarps = kBlocks * 16, kMostCols = 16;
+__host__ __device__ inline size_t slots_of(int B, int Hq) { return 2 * (size_t)B * Hq + kMostWarps * kMostCols; }
+__host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
+  uint8_t* at = static_cast<uint8_t*>(p);
+  Workspace w;
+  w.cum = reinterpret_cast<uint32_t*>(at);
+  at += align256(sizeof(uint32_t) * (kMostSources + 1));
+  w.ml = reinterpret_cast<float2*>(at);
+  at += align256(sizeof(float2) * slots_of(B, Hq));
+  w.o = reinterpret_cast<float*>(at);
+  return w;
+}
+
+// Prefix sums of the sources' tiles into cum[0 .. G + B] (shared memory), by the whole block.
+template <int COLS, int CAP>
+__device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, uint32_t* cum, uint32_t* scratch) {
+  const int G = A.G, n = A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
+  // a prompt's entry first holds its group's fewest tokens of a response that has not ended
+  for (int g = tid; g < G; g += THREADS) cum[1 + g] = 0x7fffffffu;
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  if (top == -INFINITY) top = 0.f;
-  for (int w = 0; w < kWarps; ++w) total += sl[w] * exp2f(sm[w] - top);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float y = 0.f;
-    for (int w = 0; w < kWarps; ++w) y += so[w][d] * exp2f(sm[w] - top);
-    A.out[((int64_t)b * A.Hq + h) * D + d] = __float2bfloat16(total > 0.f ? y / total : 0.f);
+  for (int b = tid; b < A.B; b += THREADS) {
+    const int len = response_len(A, b, A.status), g = seg_of(seg, b);
+    uint32_t tiles = 0;
+    if (len >= 0) {
+      const int P = prompt_len(A, g, nullptr), lo = max(0, first_position(A, P, len) - P);
+      atomicMin(&cum[1 + g], (uint32_t)len);
+      tiles = (uint32_t)tiles_of(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
+    }
+    cum[1 + G + b] = tiles;
   }
-  if (threadIdx.x == 0 && A.lse)
+  __syncthreads();
+  for (int g = tid; g < G; g += THREADS) {
+    const uint32_t least = cum[1 + g];
+    uint32_t tiles = 0;
+    if (least != 0x7fffffffu) {
+      const int P = prompt_len(A, g, A.status), rows = (seg.off[g + 1] - seg.off[g]) * GQ;
+      tiles = (uint32_t)tiles_of(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
+    }
+    cum[1 + g] = tiles;
+  }
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+  // inclusive scan of cum[1 .. n]: every thread takes a run
+  const int per = (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);
+  uint32_t sum = 0;
+  for (int i = from; i < to; ++i) sum += cum[i];
+  const int lane = tid & 31, warp = tid >> 5;
+  uint32_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - sum;
+  for (int w = 0; w < warp; ++w) before += scratch[w];
+  for (int i = from; i < to; ++i) {
+    before += cum[i];
+    cum[i] = before;
+  }
+  __syncthreads();
+}
+
+// Source holding tile `t` of a kv-head: the largest s with cum[s] <= t.
+__device__ __forceinline__ int source_of(const uint32_t* cum, int n, uint32_t t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- a warp's walk
+template <int D, int BITS, int NT, int CAP>
+__global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
+    decode_kernel(const DecodeArgs A, const __grid_constant__ SegTable<CAP> seg) {
+  using C = Cfg<D, BITS, NT>;
+  constexpr int CPR = C::RB / 16;
+  const int warps = blockDim.x >> 5;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + warps * C::RING);
+  __shared__ uint32_t scratch[C::WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
+  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  deal_sources<C::COLS>(A, seg, cum, scratch);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= sources; i += blockDim.x) ws.cum[i] = cum[i];
+  const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
+  // neighbouring shares go to different SMs, so that a short batch spreads over all of them
+  const uint32_t worker = (uint32_t)(warp * kBlocks + blockIdx.x);
+  if (worker >= deal.workers) return;
+  uint64_t at = first_tile(deal, worker);
+  const uint64_t stop = first_tile(deal, worker + 1);
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  const uint8_t* ring_p = smem + warp * C::RING;
+  // this lane's places in a slot when it copies, and its bytes in a tile
+  const int copy_row = CPR <= 32 ? lane / CPR : 0, copy_col = CPR <= 32 ? lane % CPR : lane;
+
+  while (at < stop) {
+    // ---- the source, its rows and the tiles of it that are this warp's
+    const int kvh = (int)(at / deal.per_head);
+    const uint32_t local = (uint32_t)(at % deal.per_head);
+    const int s = source_of(cum, sources, local);
+    const bool prompt = s < A.G;
+    const int b0 = prompt ? seg.off[s] : s - A.G, group = prompt ? s : seg_of(seg, b0);
+    const int row_begin = b0 * GQ, row_end = (prompt ? seg.off[s + 1] : b0 + 1) * GQ;
+    const int blocks = (row_end - row_begin + C::COLS - 1) / C::COLS;
+    const int tiles = (int)((cum[s + 1] - cum[s]) / (uint32_t)blocks);
+    const int block = (int)(local - cum[s]) / tiles, t0 = (int)(local - cum[s]) - block * tiles;
+    const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
+    at += (uint64_t)(t1 - t0);
+    const int r0 = row_begin + block * C::COLS;
+    const int P = prompt_len(A, group, nullptr);
+    const int end = prompt ? P : response_len(A, b0, nullptr);
+    // first tile of the source: its last one ends at `end`
+    const int tile0 = (end + kTile - 1) / kTile - tiles;
+
+    // ---- first token that each of the lane's rows sees, and the first and last of those of the block's rows
+    int lo[2 * NT], lo_min = 0x7fffffff, lo_max = 0;
+#pragma unroll
+    for (int c = 0; c < 2 * NT; ++c) {
+      const int r = r0 + 8 * (c >> 1) + 2 * t + (c & 1);
+      lo[c] = 0x7fffffff;
+      if (r < row_end) {
+        const int len = prompt ? response_len(A, r / GQ, nullptr) : end;
+        if (len >= 0) {
+          lo[c] = first_position(A, P, len);
+          if (!prompt) lo[c] = max(0, lo[c] - P);
+          lo_min = min(lo_min, lo[c]);
+          lo_max = max(lo_max, lo[c]);
+        }
+      }
+    }
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+
+    // ---- the producer: half h of the walk is the keys (even) or the values (odd) of tile first + h / 2
+    const int first = max(tile0 + t0, min(lo_min, end) / kTile), last = tile0 + t1;  // tiles no row sees are skipped
+    const int halves = 2 * max(0, last - first);
+    const int max_pages = prompt ? A.max_prompt_pages : A.max_pages;
+    const int32_t* table = (prompt ? A.prompt_table : A.table) + (int64_t)(prompt ? s : b0) * max_pages;
+    int place = 0, in_page = 0, page = -1, next_page = -1;
+    if (halves) {
+      place = first * kTile / A.kv.ps;
+      in_page = first * kTile - place * A.kv.ps;
+      page = page_at(A.kv, table, max_pages, place, A.status);
+      if (place + 1 < max_pages) next_page = table[place + 1];
+    }
+    uint32_t missing = 0;  // tiles in the ring without a page
+    int issued = 0, issue_slot = 0;
+    auto issue = [&]() {
+      if (issued < halves) {
+        const int tile = first + (issued >> 1);
+        const uint32_t dst = ring + issue_slot * C::SLOT;
+        const bool values = issued & 1;
+        if (page < 0) {
+          missing |= 1u << (tile & 31);
+        } else {
+          missing &= ~(1u << (tile & 31));
+          const int64_t row = cache_row(A.kv, page, kvh, in_page);
+          const uint8_t* src = static_cast<const uint8_t*>(values ? A.kv.v : A.kv.k) + row * C::RB + lane * 16;
+          const int pitch = values ? C::VP : C::KP, key0 = tile * kTile;
+          const uint32_t to = dst + copy_row * pitch + copy_col * 16;
+          // values that no row sees may be anything: they come as zeros, which their weights 0 leave at 0
+          const bool edge = BITS == 16 && values && (key0 < lo_min || key0 + kTile > end);
+#pragma unroll
+          for (int j = 0; j < C::RB / 32; ++j) {
+            const int row_j = CPR <= 32 ? j * (32 / CPR) : j / (CPR / 32);
+            const int col_j = CPR <= 32 ? 0 : j % (CPR / 32) * 512;
+            const int key = key0 + copy_row + row_j;
+            copy16z(to + row_j * pitch + col_j, src + j * 512, edge && (key < lo_min || key >= end) ? 0 : 16);
+          }
+          if (BITS == 4 && lane < C::SB / 16)
+            copy16z(dst + kTile * C::VP + lane * 16,
+                    reinterpret_cast<const uint8_t*>(values ? A.kv.vs : A.kv.ks) + row * (D / kGroup * 2) + lane * 16, 16);
+        }
+        if (values) {
+          in_page += kTile;
+          if (in_page == A.kv.ps && tile + 1 < last) {
+            in_page = 0;
+            ++place;
+            page = next_page;
+            if ((uint32_t)page >= (uint32_t)A.kv.pages) {
+              page = -1;
+              if (A.status) atomicOr(A.status, kDevErrBounds);
+            }
+            if (place + 1 < max_pages) next_page = table[place + 1];
+          }
+        }
+        ++issued;
+        issue_slot = issue_slot == C::SLOTS - 1 ? 0 : issue_slot + 1;
+      }
+      commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::SLOTS - 1; ++k) issue();
+
+    // ---- queries as B operands, in the order in which a lane meets the keys' values
+    uint32_t q[NT][D / 16][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g, b = r / GQ;
+      const uint4* row = reinterpret_cast<const uint4*>(A.q + b * A.q_stride + (kvh * GQ + (r - b * GQ)) * D);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int chunk = BITS == 16 ? 2 * t + (j & 1) + 8 * (j >> 1)
+                                     : (D == 64 ? 2 * t + j : 4 * t + 16 * (j >> 2) + (j & 3));
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < row_end) w = row[chunk];
+        if (BITS == 4)  // values e and e + 4 together
+          w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
+                         __byte_perm(w.y, w.w, 0x7632));
+        q[nt][2 * j][0] = w.x;
+        q[nt][2 * j][1] = w.y;
+        q[nt][2 * j + 1][0] = w.z;
+        q[nt][2 * j + 1][1] = w.w;
+      }
+    }
+
+    float o[NT][D / 64][4][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kLowest;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][p][e] = 0.f;
+    }
+
+    int slot = 0;
+    for (int tile = first; tile < last; ++tile) {
+      const int key0 = tile * kTile;
+      const bool edge = key0 < lo_max || key0 + kTile > end;
+      // ---- S^T = K Q^T
+      wait<C::SLOTS - 2>();
+      __syncwarp();
+      issue();
+      const bool gone = missing >> (tile & 31) & 1;
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+      if (!gone) {
+        const uint8_t* k = ring_p + slot * C::SLOT;
+        if constexpr (BITS == 16) {
+          const uint8_t* r = k + g * C::KP + t * 32;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const int off = 16 * (j & 1) + 128 * (j >> 1);
+            const uint4 x = *reinterpret_cast<const uint4*>(r + off);
+            const uint4 y = *reinterpret_cast<const uint4*>(r + 8 * C::KP + off);
+            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(sc[nt], a0, q[nt][2 * j][0], q[nt][2 * j][1]);
+              mma16816(sc[nt], a1, q[nt][2 * j + 1][0], q[nt][2 * j + 1][1]);
+            }
+          }
+        } else {
+          constexpr int W = D == 64 ? 2 : 4;  // words that a lane takes at once: within a group of 32
+          const __nv_bfloat16* scales = reinterpret_cast<const __nv_bfloat16*>(k + kTile * C::VP);
+          const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
+#pragma unroll
+          for (int j = 0; j < D / (32 * W); ++j) {
+            uint32_t x[W], y[W];
+            load_words<W>(x, k + g * C::KP + 4 * W * t + 64 * j);
+            load_words<W>(y, k + (g + 8) * C::KP + 4 * W * t + 64 * j);
+            const int grp = D == 64 ? t >> 1 : t + 4 * j;
+            const __nv_bfloat162 sx = __bfloat162bfloat162(scales[g * (D / kGroup) + grp]);
+            const __nv_bfloat162 sy = __bfloat162bfloat162(scales[(g + 8) * (D / kGroup) + grp]);
+            const __nv_bfloat162 ox = __hmul2(sx, m24), oy = __hmul2(sy, m24);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              const uint32_t a0[4] = {decode_pair<0>(x[w], sx, ox), decode_pair<0>(y[w], sy, oy),
+                                      decode_pair<1>(x[w], sx, ox), decode_pair<1>(y[w], sy, oy)};
+              const uint32_t a1[4] = {decode_pair<2>(x[w], sx, ox), decode_pair<2>(y[w], sy, oy),
+                                      decode_pair<3>(x[w], sx, ox), decode_pair<3>(y[w], sy, oy)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(sc[nt], a0, q[nt][2 * (W * j + w)][0], q[nt][2 * (W * j + w)][1]);
+                mma16816(sc[nt], a1, q[nt][2 * (W * j + w) + 1][0], q[nt][2 * (W * j + w) + 1][1]);
+              }
+            }
+          }
+        }
+      }
+      slot = slot == C::SLOTS - 1 ? 0 : slot + 1;
+      // ---- weights: element e of sc is key g + 8 (e / 2), row 2 t + e % 2
+      uint32_t p[NT][2];
+      bool grown = false;
+      float y[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (edge) {
+            const int key = key0 + g + 8 * (e >> 1);
+            if (key < lo[2 * nt + (e & 1)] || key >= end) sc[nt][e] = -INFINITY;
+          }
+          if (gone) sc[nt][e] = -INFINITY;
+          y[nt][e] = fmaf(sc[nt][e], A.scale_log2, -m[nt][e & 1]);
+        }
+        grown |= fmaxf(fmaxf(y[nt][0], y[nt][1]), fmaxf(y[nt][2], y[nt][3])) > kRescale;
+      }
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(sc[nt][c], sc[nt][c + 2]) * A.scale_log2;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top = fmaxf(m[nt][c], top);
+            const float f = ex2_approx(m[nt][c] - top);
+            m[nt][c] = top;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+              for (int pp = 0; pp < 4; ++pp) {
+                o[nt][i][pp][c] *= f;
+                o[nt][i][pp][c + 2] *= f;
+              }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(sc[nt][e], A.scale_log2, -m[nt][e & 1]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[nt][e] = ex2_approx(y[nt][e]);
+        l[nt][0] += y[nt][0] + y[nt][2];
+        l[nt][1] += y[nt][1] + y[nt][3];
+        p[nt][0] = transpose8x8(pack_bf16x2(y[nt][0], y[nt][1]));
+        p[nt][1] = transpose8x8(pack_bf16x2(y[nt][2], y[nt][3]));
+      }
+      // ---- O^T += V^T P^T; this lane's keys are 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      wait<C::SLOTS - 2>();
+      __syncwarp();
+      issue();
+      if (!gone) {
+        const uint8_t* v = ring_p + slot * C::SLOT;
+        if constexpr (BITS == 16) {
+          const uint8_t* r = v + 2 * t * C::VP + 16 * g;
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            uint32_t a[4][4];
+            load_words<4>(a[0], r + 128 * i);
+            load_words<4>(a[1], r + C::VP + 128 * i);
+            load_words<4>(a[2], r + 8 * C::VP + 128 * i);
+            load_words<4>(a[3], r + 9 * C::VP + 128 * i);
+#pragma unroll
+            for (int pp = 0; pp < 4; ++pp) {
+              const uint32_t f[4] = {__byte_perm(a[0][pp], a[1][pp], 0x5410), __byte_perm(a[0][pp], a[1][pp], 0x7632),
+                                     __byte_perm(a[2][pp], a[3][pp], 0x5410), __byte_perm(a[2][pp], a[3][pp], 0x7632)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i][pp], f, p[nt][0], p[nt][1]);
+            }
+          }
+        } else {
+          constexpr int W = D / 64;  // words of a row in each lane
+          const __nv_bfloat16* scales = reinterpret_cast<const __nv_bfloat16*>(v + kTile * C::VP);
+          const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
+          uint32_t a[4][W];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) load_words<W>(a[k], v + (2 * t + (k & 1) + 8 * (k >> 1)) * C::VP + 4 * W * g);
+          __nv_bfloat162 s2[2], o2[2];
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            if (w % 4 == 0) {  // a group of 32 values is four words
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                __nv_bfloat16 sk[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int key = 2 * t + x + 8 * k;
+                  sk[x] = scales[key * (D / kGroup) + (W * g + w) / 4];
+                  if (edge && (key0 + key < lo_min || key0 + key >= end)) sk[x] = __ushort_as_bfloat16(0);
+                }
+                s2[k] = __halves2bfloat162(sk[0], sk[1]);
+                o2[k] = __hmul2(s2[k], m24);
+              }
+            }
+            const uint32_t x0 = __byte_perm(a[0][w], a[1][w], 0x5410), x1 = __byte_perm(a[0][w], a[1][w], 0x7632);
+            const uint32_t y0 = __byte_perm(a[2][w], a[3][w], 0x5410), y1 = __byte_perm(a[2][w], a[3][w], 0x7632);
+#define DKV_PV(E)                                                                                             \
+  {                                                                                                           \
+    const uint32_t f[4] = {decode_pair<E>(x0, s2[0], o2[0]), decode_pair<E>(x1, s2[0], o2[0]),                \
+                           decode_pair<E>(y0, s2[1], o2[1]), decode_pair<E>(y1, s2[1], o2[1])};               \
+    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][w][E], f, p[nt][0], p[nt][1]);           \
+  }
+            DKV_PV(0)
+            DKV_PV(1)
+            DKV_PV(2)
+            DKV_PV(3)
+#undef DKV_PV
+          }
+        }
+      }
+      slot = slot == C::SLOTS - 1 ? 0 : slot + 1;
+    }
+    __syncwarp();
+
+    // ---- the partial result: the source's own places if its first tile is here, else this warp's
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[nt][c];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int col = 8 * nt + 2 * t + c, r = r0 + col;
+        if (r >= row_end) continue;
+        const int b = r / GQ;
+        const size_t rows = (size_t)A.B * A.Hq;
+        const size_t to = t0 == 0 ? (prompt ? rows : 0) + (size_t)b * A.Hq + kvh * GQ + (r - b * GQ)
+                                  : 2 * rows + (size_t)worker * C::COLS + col;
+        if (g == 0) ws.ml[to] = make_float2(m[nt][c], sum);
+        float* out = ws.o + to * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const auto& x = o[nt][i];
+          // bf16: values 2 pp and 2 pp + 1 of the chunk; 4 bits: pp and pp + 4 of the word
+          float4* dst = reinterpret_cast<float4*>(out + (BITS == 16 ? 8 * g + 64 * i : 8 * (D / 64 * g + i)));
+          if (BITS == 16) {
+            dst[0] = make_float4(x[0][c], x[0][c + 2], x[1][c], x[1][c + 2]);
+            dst[1] = make_float4(x[2][c], x[2][c + 2], x[3][c], x[3][c + 2]);
+          } else {
+            dst[0] = make_float4(x[0][c], x[1][c], x[2][c], x[3][c]);
+            dst[1] = make_float4(x[0][c + 2], x[1][c + 2], x[2][c + 2], x[3][c + 2]);
+          }
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------- the join
+// A source's partial results for one row: the first in the row's own place, the others in those of the warps behind.
+struct Parts {
+  size_t own;
+  uint32_t first;  // worker of the first one
+  int n;
+};
+__device__ __forceinline__ Parts parts_of(const Deal& d, const uint32_t* cum, int s, int blocks, int block, int kvh, size_t own) {
+  Parts p{own, 0, 0};
+  const uint32_t tiles = (cum[s + 1] - cum[s]) / (uint32_t)blocks;
+  if (!tiles) return p;
+  const uint64_t from = (uint64_t)kvh * d.per_head + cum[s] + (uint64_t)block * tiles;
+  p.first = worker_of(d, from);
+  p.n = (int)(worker_of(d, from + tiles - 1) - p.first) + 1;
+  return p;
+}
+
+constexpr int kJoinWarps = 4;
+
+// `share` warps of a block take a row's partial results by turns, and the first of them joins their sums.  The kernel may
+// start before the partial results are complete, so nothing that reads them is __restrict__.
+template <int D, int CAP>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    join_kernel(const DecodeArgs A, int share, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int E = D / 32;
+  __shared__ float so[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % share;
+  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
+  const bool live = row < (int64_t)A.B * A.Hq;
+  const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row % A.Hq) : 0;
+  const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, group = seg_of(seg, b);
+  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  cudaGridDependencySynchronize();
+  float top = kLowest, total = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const uint32_t per_head = ws.cum[A.G + A.B];
+  if (live && per_head && A.lens[b] >= 0) {
+    const Deal d = make_deal(per_head, A.kv.Hkv, warps);
+    const size_t rows = (size_t)A.B * A.Hq;
+    const int in_prompt = (b - seg.off[group]) * GQ + h % GQ, in_own = h % GQ;
+    const Parts p[2] = {parts_of(d, ws.cum, group, ((seg.off[group + 1] - seg.off[group]) * GQ + cols - 1) / cols,
+                                 in_prompt / cols, kvh, rows + (size_t)row),
+                        parts_of(d, ws.cum, A.G + b, (GQ + cols - 1) / cols, in_own / cols, kvh, (size_t)row)};
+    const int n = p[0].n + p[1].n;
+    auto place = [&](int i) -> size_t {
+      const bool second = i >= p[0].n;
+      const Parts& q = second ? p[1] : p[0];
+      if (second) i -= p[0].n;
+      return i == 0 ? q.own : 2 * rows + (size_t)(q.first + i) * cols + (second ? in_own : in_prompt) % cols;
+    };
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, ws.ml[place(i)].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    for (int i = lane; i < n; i += 32) {
+      const float2 v = ws.ml[place(i)];
+      total += v.y * ex2_approx(v.x - top);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+#pragma unroll 4
+    for (int i = part; i < n; i += share) {
+      const size_t at = place(i);
+      const float f = ex2_approx(ws.ml[at].x - top);
+      const float2* v = reinterpret_cast<const float2*>(ws.o + at * D);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 x = v[lane + 16 * e];
+        acc[e] = fmaf(x.x, f, acc[e]);
+        acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+      }
+    }
+  }
+  if (share > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][32 * e + lane] = acc[e];
+    __syncthreads();
+    if (part) return;
+    for (int w = 1; w < share; ++w)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += so[warp + w][32 * e + lane];
+  }
+  if (!live) return;
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[lane + 16 * e] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && A.lse)
     A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <int CAP>
-cudaError_t launch_c(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+template <int D, int BITS, int NT, int CAP>
+cudaError_t launch_t(const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+  using C = Cfg<D, BITS, NT>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
-  const dim3 grid((unsigned)a.B, (unsigned)a.Hq);
-  switch (D) {
-    case 64:
-      decode_kernel<64, CAP><<<grid, kWarps * 32, 0, st>>>(a, seg);
-      break;
-    case 128:
-      decode_kernel<128, CAP><<<grid, kWarps * 32, 0, st>>>(a, seg);
-      break;
-    default:
-      decode_kernel<512, CAP><<<grid, kWarps * 32, 0, st>>>(a, seg);
+  // many sources take the place of some warps' rings
+  const int cum = (a.G + a.B + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
+  const int warps = room < C::WARPS ? room : C::WARPS, smem = warps * C::RING + cum;
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, BITS, NT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, BITS, NT, CAP><<<kBlocks, warps * 32, smem, st>>>(a, seg);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.B * a.Hq;
+  const int share = rows >= 2432 ? 1 : kJoinWarps, per = kJoinWarps / share;
+  return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinWarps * 32), st, a, share,
+                       (int)C::COLS, kBlocks * warps, seg);
+}
+
+template <int D, int BITS>
+cudaError_t launch_b(const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+  const bool few = a.G <= kSmallSegs;
+  if constexpr (D != 512) {
+    if (a.Hq / a.kv.Hkv > 8)
+      return few ? launch_t<D, BITS, 2, kSmallSegs>(a, groups, st) : launch_t<D, BITS, 2, kMaxSegs>(a, groups, st);
   }
-  return cudaGetLastError();
+  return few ? launch_t<D, BITS, 1, kSmallSegs>(a, groups, st) : launch_t<D, BITS, 1, kMaxSegs>(a, groups, st);
 }
 
 }  // namespace
 
 cudaError_t launch_decode(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
-  return a.G <= kSmallSegs ? launch_c<kSmallSegs>(D, a, groups, st) : launch_c<kMaxSegs>(D, a, groups, st);
+  const bool four = a.kv.ks != nullptr;
+  switch (D) {
+    case 64:
+      return four ? launch_b<64, 4>(a, groups, st) : launch_b<64, 16>(a, groups, st);
+    case 128:
+      return four ? launch_b<128, 4>(a, groups, st) : launch_b<128, 16>(a, groups, st);
+    case 512:
+      return four ? launch_b<512, 4>(a, groups, st) : launch_b<512, 16>(a, groups, st);
+    default:
+      return cudaErrorInvalidValue;
+  }
 }
 
-size_t decode_workspace_bytes(int, int, int, int) { return 256; }
+size_t decode_workspace_bytes(int B, int Hq, int, int D) {
+  const Workspace w = carve(nullptr, B, Hq);
+  return reinterpret_cast<size_t>(w.o) + sizeof(float) * slots_of(B, Hq) * (size_t)D;
+}
 
 }  // namespace dkv

@@ -116,6 +116,7 @@ def test_decode_refusals(lib):
         assert _decode(lib, **kw) == dk.DUALKV_ERR_WORKSPACE, kw
     assert _decode(lib, G=4096, off=[0] * 4096 + [1]) == dk.DUALKV_ERR_UNSUPPORTED
     assert _decode(lib, G=1, off=[0, 8193]) == dk.DUALKV_ERR_UNSUPPORTED
+    assert _decode(lib, mp=(1 << 27) - 1, ps=16, G=1, off=[0, 4096]) == dk.DUALKV_ERR_UNSUPPORTED
     assert _decode(lib, off=[0, 0, 0], q=0, out=0, ws=0) == dk.DUALKV_OK
     assert lib.dualkv_decode_workspace_bytes(2, off, 4, 3, 64) == 0 and lib.dualkv_decode_workspace_bytes(2, off, 4, 2, 96) == 0
 
