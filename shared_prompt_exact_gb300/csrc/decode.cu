@@ -32,7 +32,6 @@ namespace dkv {
 
 namespace {
 
-constexpr int kTile = 16;       // keys of a tile
 constexpr int kBlocks = 152;    // one per SM
 constexpr int kMostShared = 226 << 10;  // dynamic shared memory of a block, 1 KB left for the rest
 constexpr float kLowest = -3e38f;  // maximum of a row that has seen nothing: finite, so differences are too
@@ -43,10 +42,13 @@ struct Cfg {
   static constexpr int RB = BITS == 16 ? 2 * D : D / 2;  // bytes of a row
   static constexpr int KP = BITS == 16 ? RB + 16 : RB;   // pitches in shared memory: 16 bytes more where lanes of
   static constexpr int VP = RB + 16;                     // several keys would meet in one bank
-  static constexpr int SB = BITS == 16 ? 0 : kTile * (D / kGroup) * 2;  // bytes of a tile's scales
-  static constexpr int SLOT = kTile * VP + SB;
+  static constexpr int SP = BITS == 16 ? 0 : D / kGroup * 2;  // bytes of a key's scales
+  // keys of a tile: 16 for each sub-tile, which lies in one page
+  static constexpr int KT = D == 512 ? (BITS == 16 ? 1 : 2) : (BITS == 16 ? (D == 128 ? 2 : 4) : 4);
+  static constexpr int TILE = 16 * KT;
+  static constexpr int SLOT = TILE * (VP + SP);  // keys or values of a tile, and their scales
   static constexpr int WARPS = D == 512 ? (BITS == 16 ? 6 : 8) : (NT == 2 ? 12 : (BITS == 16 ? 12 : 16));
-  static constexpr int SLOTS = D == 512 ? (BITS == 16 ? 2 : 4) : (BITS == 16 ? (D == 128 ? 4 : 6) : 6);
+  static constexpr int SLOTS = D == 64 && BITS == 4 ? 4 : 2;
   static constexpr int COLS = 8 * NT;
   static constexpr int RING = SLOTS * SLOT;  // bytes of a warp's ring
 };
@@ -63,9 +65,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// 16 bytes, or zeros where `bytes` is 0
-__device__ __forceinline__ void copy16z(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -136,7 +137,10 @@ __device__ __forceinline__ int first_position(const DecodeArgs& A, int P, int n)
   return A.window > 0 ? (int)max((int64_t)0, (int64_t)P + n - A.window) : 0;
 }
 // Tiles of tokens [lo, end).
-__device__ __forceinline__ int tiles_of(int lo, int end) { return lo < end ? (end + kTile - 1) / kTile - lo / kTile : 0; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int lo, int end) {
+  return lo < end ? (end + TILE - 1) / TILE - lo / TILE : 0;
+}
 
 struct Workspace {
   uint32_t* cum;  // [G + B + 1] tiles before each source, of one kv-head
@@ -159,7 +163,7 @@ __host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
 }
 
 // Prefix sums of the sources' tiles into cum[0 .. G + B] (shared memory), by the whole block.
-template <int COLS, int CAP>
+template <int COLS, int TILE, int CAP>
 __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, uint32_t* cum, uint32_t* scratch) {
   const int G = A.G, n = A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
   // a prompt's entry first holds its group's fewest tokens of a response that has not ended
@@ -171,7 +175,7 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
     if (len >= 0) {
       const int P = prompt_len(A, g, nullptr), lo = max(0, first_position(A, P, len) - P);
       atomicMin(&cum[1 + g], (uint32_t)len);
-      tiles = (uint32_t)tiles_of(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
+      tiles = (uint32_t)tiles_of<TILE>(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
     }
     cum[1 + G + b] = tiles;
   }
@@ -181,7 +185,7 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
     uint32_t tiles = 0;
     if (least != 0x7fffffffu) {
       const int P = prompt_len(A, g, A.status), rows = (seg.off[g + 1] - seg.off[g]) * GQ;
-      tiles = (uint32_t)tiles_of(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
+      tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
     }
     cum[1 + g] = tiles;
   }
@@ -225,7 +229,8 @@ template <int D, int BITS, int NT, int CAP>
 __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     decode_kernel(const DecodeArgs A, const __grid_constant__ SegTable<CAP> seg) {
   using C = Cfg<D, BITS, NT>;
-  constexpr int CPR = C::RB / 16;
+  constexpr int TILE = C::TILE, KT = C::KT;
+  constexpr int LG = 32 / KT, CPR = C::RB / 16;  // lanes that copy a sub-tile; 16-byte chunks of a row
   const int warps = blockDim.x >> 5;
   extern __shared__ __align__(16) uint8_t smem[];
   uint32_t* cum = reinterpret_cast<uint32_t*>(smem + warps * C::RING);
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  deal_sources<C::COLS>(A, seg, cum, scratch);
+  deal_sources<C::COLS, C::TILE>(A, seg, cum, scratch);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= sources; i += blockDim.x) ws.cum[i] = cum[i];
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
@@ -243,9 +248,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   uint64_t at = first_tile(deal, worker);
   const uint64_t stop = first_tile(deal, worker + 1);
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
-  const uint8_t* ring_p = smem + warp * C::RING;
-  // this lane's places in a slot when it copies, and its bytes in a tile
-  const int copy_row = CPR <= 32 ? lane / CPR : 0, copy_col = CPR <= 32 ? lane % CPR : lane;
+  uint8_t* ring_p = smem + warp * C::RING;
+  // what this lane copies: every LG-th chunk of sub-tile `mine`
+  const int mine = lane / LG, li = lane % LG;
+  const int copy_row = 16 * mine + (CPR <= LG ? li / CPR : 0), copy_col = CPR <= LG ? li % CPR : li;
+  const int step_places = TILE / A.kv.ps, step_slots = TILE % A.kv.ps;
 
   while (at < stop) {
     // ---- the source, its rows and the tiles of it that are this warp's
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     const int P = prompt_len(A, group, nullptr);
     const int end = prompt ? P : response_len(A, b0, nullptr);
     // first tile of the source: its last one ends at `end`
-    const int tile0 = (end + kTile - 1) / kTile - tiles;
+    const int tile0 = (end + TILE - 1) / TILE - tiles;
 
     // ---- first token that each of the lane's rows sees, and the first and last of those of the block's rows
     int lo[2 * NT], lo_min = 0x7fffffff, lo_max = 0;
@@ -285,66 +292,67 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     lo_min = __reduce_min_sync(0xffffffffu, lo_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
 
-    // ---- the producer: half h of the walk is the keys (even) or the values (odd) of tile first + h / 2
-    const int first = max(tile0 + t0, min(lo_min, end) / kTile), last = tile0 + t1;  // tiles no row sees are skipped
-    const int halves = 2 * max(0, last - first);
+    // ---- the producer: keys and values of tiles [first, last) by turns, SLOTS - 1 ahead
+    const int first = max(tile0 + t0, min(lo_min, end) / TILE), last = tile0 + t1;  // tiles no row sees are skipped
     const int max_pages = prompt ? A.max_prompt_pages : A.max_pages;
     const int32_t* table = (prompt ? A.prompt_table : A.table) + (int64_t)(prompt ? s : b0) * max_pages;
-    int place = 0, in_page = 0, page = -1, next_page = -1;
-    if (halves) {
-      place = first * kTile / A.kv.ps;
-      in_page = first * kTile - place * A.kv.ps;
-      page = page_at(A.kv, table, max_pages, place, A.status);
-      if (place + 1 < max_pages) next_page = table[place + 1];
-    }
-    uint32_t missing = 0;  // tiles in the ring without a page
-    int issued = 0, issue_slot = 0;
-    auto issue = [&]() {
-      if (issued < halves) {
-        const int tile = first + (issued >> 1);
-        const uint32_t dst = ring + issue_slot * C::SLOT;
-        const bool values = issued & 1;
-        if (page < 0) {
-          missing |= 1u << (tile & 31);
-        } else {
-          missing &= ~(1u << (tile & 31));
-          const int64_t row = cache_row(A.kv, page, kvh, in_page);
-          const uint8_t* src = static_cast<const uint8_t*>(values ? A.kv.v : A.kv.k) + row * C::RB + lane * 16;
-          const int pitch = values ? C::VP : C::KP, key0 = tile * kTile;
-          const uint32_t to = dst + copy_row * pitch + copy_col * 16;
-          // values that no row sees may be anything: they come as zeros, which their weights 0 leave at 0
-          const bool edge = BITS == 16 && values && (key0 < lo_min || key0 + kTile > end);
+    // this lane's sub-tile: its place in the table, its first slot in the page, and the page (loaded a tile ahead)
+    int token = first * TILE + 16 * mine, place = token / A.kv.ps, in_page = token - place * A.kv.ps;
+    int page = first < last && token < end ? table[place] : -1;
+    int64_t row = 0;       // of the pools, where the last issued keys' sub-tile starts
+    bool has_page = false;
+    uint32_t missing = 0;  // tiles in the ring that have a token without a page
+    int tile_k = first, tile_v = first, issue_slot = 0;
+    auto copy_rows = [&](const void* pool, const __nv_bfloat16* scales, int pitch) {
+      const uint32_t dst = ring + issue_slot * C::SLOT;
+      const uint8_t* src = static_cast<const uint8_t*>(pool) + row * C::RB + li * 16;
+      const uint32_t to = dst + copy_row * pitch + copy_col * 16;
 #pragma unroll
-          for (int j = 0; j < C::RB / 32; ++j) {
-            const int row_j = CPR <= 32 ? j * (32 / CPR) : j / (CPR / 32);
-            const int col_j = CPR <= 32 ? 0 : j % (CPR / 32) * 512;
-            const int key = key0 + copy_row + row_j;
-            copy16z(to + row_j * pitch + col_j, src + j * 512, edge && (key < lo_min || key >= end) ? 0 : 16);
-          }
-          if (BITS == 4 && lane < C::SB / 16)
-            copy16z(dst + kTile * C::VP + lane * 16,
-                    reinterpret_cast<const uint8_t*>(values ? A.kv.vs : A.kv.ks) + row * (D / kGroup * 2) + lane * 16, 16);
+      for (int j = 0; j < C::RB / LG; ++j) {
+        const int row_j = CPR <= LG ? j * (LG / CPR) : j / (CPR / LG), col_j = CPR <= LG ? 0 : j % (CPR / LG) * LG * 16;
+        copy16(to + row_j * pitch + col_j, src + j * LG * 16);
+      }
+      if (BITS == 4) {
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(scales) + row * C::SP + li * 16;
+#pragma unroll
+        for (int j = 0; j < (C::SP + LG - 1) / LG; ++j)
+          if (li + j * LG < C::SP) copy16(dst + TILE * C::VP + 16 * mine * C::SP + (li + j * LG) * 16, sc + j * LG * 16);
+      }
+    };
+    auto issue_keys = [&]() {
+      if (tile_k < last) {
+        has_page = (uint32_t)page < (uint32_t)A.kv.pages;
+        const uint32_t bit = 1u << (tile_k & 31);
+        missing = __any_sync(0xffffffffu, !has_page && token < end) ? missing | bit : missing & ~bit;
+        row = cache_row(A.kv, page, kvh, in_page);
+        if (has_page) copy_rows(A.kv.k, A.kv.ks, C::KP);
+        token += TILE;
+        place += step_places;
+        in_page += step_slots;
+        if (in_page >= A.kv.ps) {
+          in_page -= A.kv.ps;
+          ++place;
         }
-        if (values) {
-          in_page += kTile;
-          if (in_page == A.kv.ps && tile + 1 < last) {
-            in_page = 0;
-            ++place;
-            page = next_page;
-            if ((uint32_t)page >= (uint32_t)A.kv.pages) {
-              page = -1;
-              if (A.status) atomicOr(A.status, kDevErrBounds);
-            }
-            if (place + 1 < max_pages) next_page = table[place + 1];
-          }
-        }
-        ++issued;
-        issue_slot = issue_slot == C::SLOTS - 1 ? 0 : issue_slot + 1;
+        ++tile_k;
+        page = tile_k < last && token < end ? table[place] : -1;
       }
       commit();
+      issue_slot = issue_slot == C::SLOTS - 1 ? 0 : issue_slot + 1;
     };
+    auto issue_values = [&]() {  // of the tile whose keys were issued last
+      if (tile_v < last) {
+        if (has_page) copy_rows(A.kv.v, A.kv.vs, C::VP);
+        ++tile_v;
+      }
+      commit();
+      issue_slot = issue_slot == C::SLOTS - 1 ? 0 : issue_slot + 1;
+    };
+    issue_keys();
 #pragma unroll
-    for (int k = 0; k < C::SLOTS - 1; ++k) issue();
+    for (int k = 1; k < C::SLOTS / 2; ++k) {
+      issue_values();
+      issue_keys();
+    }
 
     // ---- queries as B operands, in the order in which a lane meets the keys' values
     uint32_t q[NT][D / 16][2];
@@ -383,91 +391,107 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
 
     int slot = 0;
     for (int tile = first; tile < last; ++tile) {
-      const int key0 = tile * kTile;
-      const bool edge = key0 < lo_max || key0 + kTile > end;
+      const int key0 = tile * TILE;
+      bool edge = key0 < lo_max || key0 + TILE > end;
       // ---- S^T = K Q^T
       wait<C::SLOTS - 2>();
       __syncwarp();
-      issue();
-      const bool gone = missing >> (tile & 31) & 1;
-      float sc[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-      if (!gone) {
+      issue_values();
+      uint32_t gone = 0;  // sub-tiles without a page: their keys do not count
+      if (missing >> (tile & 31) & 1) {
+        const int at_key = key0 + 16 * lane;
+        const bool bad = lane < KT && at_key < end && page_at(A.kv, table, max_pages, at_key / A.kv.ps, A.status) < 0;
+        gone = __ballot_sync(0xffffffffu, bad);
+        edge = true;
+      }
+      float sc[KT][NT][4];
+      {
         const uint8_t* k = ring_p + slot * C::SLOT;
-        if constexpr (BITS == 16) {
-          const uint8_t* r = k + g * C::KP + t * 32;
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            const int off = 16 * (j & 1) + 128 * (j >> 1);
-            const uint4 x = *reinterpret_cast<const uint4*>(r + off);
-            const uint4 y = *reinterpret_cast<const uint4*>(r + 8 * C::KP + off);
-            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+        for (int u = 0; u < KT; ++u) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16816(sc[nt], a0, q[nt][2 * j][0], q[nt][2 * j][1]);
-              mma16816(sc[nt], a1, q[nt][2 * j + 1][0], q[nt][2 * j + 1][1]);
-            }
-          }
-        } else {
-          constexpr int W = D == 64 ? 2 : 4;  // words that a lane takes at once: within a group of 32
-          const __nv_bfloat16* scales = reinterpret_cast<const __nv_bfloat16*>(k + kTile * C::VP);
-          const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < D / (32 * W); ++j) {
-            uint32_t x[W], y[W];
-            load_words<W>(x, k + g * C::KP + 4 * W * t + 64 * j);
-            load_words<W>(y, k + (g + 8) * C::KP + 4 * W * t + 64 * j);
-            const int grp = D == 64 ? t >> 1 : t + 4 * j;
-            const __nv_bfloat162 sx = __bfloat162bfloat162(scales[g * (D / kGroup) + grp]);
-            const __nv_bfloat162 sy = __bfloat162bfloat162(scales[(g + 8) * (D / kGroup) + grp]);
-            const __nv_bfloat162 ox = __hmul2(sx, m24), oy = __hmul2(sy, m24);
+            for (int e = 0; e < 4; ++e) sc[u][nt][e] = 0.f;
+          if constexpr (BITS == 16) {
+            const uint8_t* r = k + (16 * u + g) * C::KP + t * 32;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-              const uint32_t a0[4] = {decode_pair<0>(x[w], sx, ox), decode_pair<0>(y[w], sy, oy),
-                                      decode_pair<1>(x[w], sx, ox), decode_pair<1>(y[w], sy, oy)};
-              const uint32_t a1[4] = {decode_pair<2>(x[w], sx, ox), decode_pair<2>(y[w], sy, oy),
-                                      decode_pair<3>(x[w], sx, ox), decode_pair<3>(y[w], sy, oy)};
+            for (int j = 0; j < D / 32; ++j) {
+              const int off = 16 * (j & 1) + 128 * (j >> 1);
+              const uint4 x = *reinterpret_cast<const uint4*>(r + off);
+              const uint4 y = *reinterpret_cast<const uint4*>(r + 8 * C::KP + off);
+              const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma16816(sc[nt], a0, q[nt][2 * (W * j + w)][0], q[nt][2 * (W * j + w)][1]);
-                mma16816(sc[nt], a1, q[nt][2 * (W * j + w) + 1][0], q[nt][2 * (W * j + w) + 1][1]);
+                mma16816(sc[u][nt], a0, q[nt][2 * j][0], q[nt][2 * j][1]);
+                mma16816(sc[u][nt], a1, q[nt][2 * j + 1][0], q[nt][2 * j + 1][1]);
+              }
+            }
+          } else {
+            constexpr int W = D == 64 ? 2 : 4;  // words that a lane takes at once: within a group of 32
+            const uint8_t* r = k + (16 * u + g) * C::KP + 4 * W * t;
+            const __nv_bfloat16* scales =
+                reinterpret_cast<const __nv_bfloat16*>(k + TILE * C::VP + (16 * u + g) * C::SP) + (D == 64 ? t >> 1 : t);
+            const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
+#pragma unroll
+            for (int j = 0; j < D / (32 * W); ++j) {
+              uint32_t x[W], y[W];
+              load_words<W>(x, r + 64 * j);
+              load_words<W>(y, r + 8 * C::KP + 64 * j);
+              const __nv_bfloat162 sx = __bfloat162bfloat162(scales[4 * j]);
+              const __nv_bfloat162 sy = __bfloat162bfloat162(scales[4 * j + 8 * (D / kGroup)]);
+              const __nv_bfloat162 ox = __hmul2(sx, m24), oy = __hmul2(sy, m24);
+#pragma unroll
+              for (int w = 0; w < W; ++w) {
+                const uint32_t a0[4] = {decode_pair<0>(x[w], sx, ox), decode_pair<0>(y[w], sy, oy),
+                                        decode_pair<1>(x[w], sx, ox), decode_pair<1>(y[w], sy, oy)};
+                const uint32_t a1[4] = {decode_pair<2>(x[w], sx, ox), decode_pair<2>(y[w], sy, oy),
+                                        decode_pair<3>(x[w], sx, ox), decode_pair<3>(y[w], sy, oy)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma16816(sc[u][nt], a0, q[nt][2 * (W * j + w)][0], q[nt][2 * (W * j + w)][1]);
+                  mma16816(sc[u][nt], a1, q[nt][2 * (W * j + w) + 1][0], q[nt][2 * (W * j + w) + 1][1]);
+                }
               }
             }
           }
         }
       }
       slot = slot == C::SLOTS - 1 ? 0 : slot + 1;
-      // ---- weights: element e of sc is key g + 8 (e / 2), row 2 t + e % 2
-      uint32_t p[NT][2];
-      bool grown = false;
-      float y[NT][4];
+      // ---- weights: element e of sc is key g + 8 (e / 2) of its sub-tile, row 2 t + e % 2
+      if (edge) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int u = 0; u < KT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (edge) {
-            const int key = key0 + g + 8 * (e >> 1);
-            if (key < lo[2 * nt + (e & 1)] || key >= end) sc[nt][e] = -INFINITY;
-          }
-          if (gone) sc[nt][e] = -INFINITY;
-          y[nt][e] = fmaf(sc[nt][e], A.scale_log2, -m[nt][e & 1]);
-        }
-        grown |= fmaxf(fmaxf(y[nt][0], y[nt][1]), fmaxf(y[nt][2], y[nt][3])) > kRescale;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 16 * u + g + 8 * (e >> 1);
+              if (key < lo[2 * nt + (e & 1)] || key >= end || (gone >> u & 1)) sc[u][nt][e] = -INFINITY;
+            }
       }
+      float top[NT][2];
+      bool grown = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+#pragma unroll
+          for (int u = 1; u < KT; ++u) top[nt][c] = fmax3(top[nt][c], sc[u][nt][c], sc[u][nt][c + 2]);
+          grown |= fmaf(top[nt][c], A.scale_log2, -m[nt][c]) > kRescale;
+        }
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(sc[nt][c], sc[nt][c + 2]) * A.scale_log2;
+            float x = top[nt][c] * A.scale_log2;
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            top = fmaxf(m[nt][c], top);
-            const float f = ex2_approx(m[nt][c] - top);
-            m[nt][c] = top;
+            for (int i = 4; i < 32; i <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+            x = fmaxf(m[nt][c], x);
+            const float f = ex2_approx(m[nt][c] - x);
+            m[nt][c] = x;
             l[nt][c] *= f;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
@@ -477,27 +501,44 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
                 o[nt][i][pp][c + 2] *= f;
               }
           }
+      }
+      uint32_t p[KT][NT][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[nt][e] = fmaf(sc[nt][e], A.scale_log2, -m[nt][e & 1]);
+      for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[u][nt][e] = ex2_approx(fmaf(sc[u][nt][e], A.scale_log2, -m[nt][e & 1]));
+          l[nt][0] += sc[u][nt][0] + sc[u][nt][2];
+          l[nt][1] += sc[u][nt][1] + sc[u][nt][3];
+          p[u][nt][0] = transpose8x8(pack_bf16x2(sc[u][nt][0], sc[u][nt][1]));
+          p[u][nt][1] = transpose8x8(pack_bf16x2(sc[u][nt][2], sc[u][nt][3]));
         }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[nt][e] = ex2_approx(y[nt][e]);
-        l[nt][0] += y[nt][0] + y[nt][2];
-        l[nt][1] += y[nt][1] + y[nt][3];
-        p[nt][0] = transpose8x8(pack_bf16x2(y[nt][0], y[nt][1]));
-        p[nt][1] = transpose8x8(pack_bf16x2(y[nt][2], y[nt][3]));
-      }
-      // ---- O^T += V^T P^T; this lane's keys are 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      // ---- O^T += V^T P^T; this lane's keys are 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each sub-tile
       wait<C::SLOTS - 2>();
       __syncwarp();
-      issue();
-      if (!gone) {
-        const uint8_t* v = ring_p + slot * C::SLOT;
+      issue_keys();
+      uint8_t* v = ring_p + slot * C::SLOT;
+      if (edge) {
+        // values that no row sees may be anything: 0 (in 4 bits: their scales), which weights of 0 leave at 0
+#pragma unroll 1
+        for (int k = 0; k < TILE; ++k) {
+          const int key = key0 + k;
+          if (key >= lo_min && key < end && !(gone >> (k >> 4) & 1)) continue;
+          if (BITS == 16) {
+            for (int c = lane; c < CPR; c += 32) *reinterpret_cast<uint4*>(v + k * C::VP + 16 * c) = make_uint4(0, 0, 0, 0);
+          } else if (lane < C::SP / 2) {
+            reinterpret_cast<uint16_t*>(v + TILE * C::VP + k * C::SP)[lane] = 0;
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int u = 0; u < KT; ++u) {
+        const uint8_t* r = v + (16 * u + 2 * t) * C::VP;
         if constexpr (BITS == 16) {
-          const uint8_t* r = v + 2 * t * C::VP + 16 * g;
+          r += 16 * g;
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
             uint32_t a[4][4];
@@ -510,30 +551,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
               const uint32_t f[4] = {__byte_perm(a[0][pp], a[1][pp], 0x5410), __byte_perm(a[0][pp], a[1][pp], 0x7632),
                                      __byte_perm(a[2][pp], a[3][pp], 0x5410), __byte_perm(a[2][pp], a[3][pp], 0x7632)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i][pp], f, p[nt][0], p[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i][pp], f, p[u][nt][0], p[u][nt][1]);
             }
           }
         } else {
           constexpr int W = D / 64;  // words of a row in each lane
-          const __nv_bfloat16* scales = reinterpret_cast<const __nv_bfloat16*>(v + kTile * C::VP);
+          const __nv_bfloat16* scales =
+              reinterpret_cast<const __nv_bfloat16*>(v + TILE * C::VP + (16 * u + 2 * t) * C::SP) + W * g / 4;
           const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f);
           uint32_t a[4][W];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) load_words<W>(a[k], v + (2 * t + (k & 1) + 8 * (k >> 1)) * C::VP + 4 * W * g);
+          for (int k = 0; k < 4; ++k) load_words<W>(a[k], r + ((k & 1) + 8 * (k >> 1)) * C::VP + 4 * W * g);
           __nv_bfloat162 s2[2], o2[2];
 #pragma unroll
           for (int w = 0; w < W; ++w) {
             if (w % 4 == 0) {  // a group of 32 values is four words
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                __nv_bfloat16 sk[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const int key = 2 * t + x + 8 * k;
-                  sk[x] = scales[key * (D / kGroup) + (W * g + w) / 4];
-                  if (edge && (key0 + key < lo_min || key0 + key >= end)) sk[x] = __ushort_as_bfloat16(0);
-                }
-                s2[k] = __halves2bfloat162(sk[0], sk[1]);
+                s2[k] = __halves2bfloat162(scales[8 * k * (D / kGroup) + w / 4], scales[(8 * k + 1) * (D / kGroup) + w / 4]);
                 o2[k] = __hmul2(s2[k], m24);
               }
             }
@@ -543,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   {                                                                                                           \
     const uint32_t f[4] = {decode_pair<E>(x0, s2[0], o2[0]), decode_pair<E>(x1, s2[0], o2[0]),                \
                            decode_pair<E>(y0, s2[1], o2[1]), decode_pair<E>(y1, s2[1], o2[1])};               \
-    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][w][E], f, p[nt][0], p[nt][1]);           \
+    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][w][E], f, p[u][nt][0], p[u][nt][1]);     \
   }
             DKV_PV(0)
             DKV_PV(1)
@@ -607,54 +642,78 @@ __device__ __forceinline__ Parts parts_of(const Deal& d, const uint32_t* cum, in
   return p;
 }
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
 
-// `share` warps of a block take a row's partial results by turns, and the first of them joins their sums.  The kernel may
-// start before the partial results are complete, so nothing that reads them is __restrict__.
+// The partial results of row `row`: n of them, and where the i-th lies.
+template <int CAP>
+struct RowParts {
+  Parts p[2];
+  size_t carried;  // the first warp's place for the partial results of later tiles
+  int n, cols, at[2];
+  __device__ __forceinline__ RowParts(const DecodeArgs& A, const SegTable<CAP>& seg, const uint32_t* cum, int warps,
+                                      int cols_, int b, int h) {
+    const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, group = seg_of(seg, b);
+    const int in_prompt = (b - seg.off[group]) * GQ + h % GQ, in_own = h % GQ;
+    const size_t rows = (size_t)A.B * A.Hq, row = (size_t)b * A.Hq + h;
+    const Deal d = make_deal(cum[A.G + A.B], A.kv.Hkv, warps);
+    cols = cols_;
+    p[0] = parts_of(d, cum, group, ((seg.off[group + 1] - seg.off[group]) * GQ + cols - 1) / cols, in_prompt / cols, kvh,
+                    rows + row);
+    p[1] = parts_of(d, cum, A.G + b, (GQ + cols - 1) / cols, in_own / cols, kvh, row);
+    carried = 2 * rows;
+    at[0] = in_prompt % cols;
+    at[1] = in_own % cols;
+    n = p[0].n + p[1].n;
+  }
+  __device__ __forceinline__ size_t place(int i) const {
+    const bool second = i >= p[0].n;
+    const int k = second ? i - p[0].n : i;
+    const size_t own = second ? p[1].own : p[0].own;
+    return k == 0 ? own
+                  : carried + (size_t)((second ? p[1].first : p[0].first) + k) * cols + (second ? at[1] : at[0]);
+  }
+};
+
+__device__ __forceinline__ float lse_of(float top, float total) {
+  return total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+  return x;
+}
+
+// Many rows: a warp joins one.  Both kernels may start before the partial results are complete, so nothing that
+// reads them is __restrict__.
 template <int D, int CAP>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    join_kernel(const DecodeArgs A, int share, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
+__global__ void __launch_bounds__(kJoinThreads)
+    join_rows_kernel(const DecodeArgs A, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
   constexpr int E = D / 32;
-  __shared__ float so[kJoinWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % share;
-  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
-  const bool live = row < (int64_t)A.B * A.Hq;
-  const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row % A.Hq) : 0;
-  const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, group = seg_of(seg, b);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= (int64_t)A.B * A.Hq) return;
+  const int b = (int)(row / A.Hq), h = (int)(row % A.Hq);
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   cudaGridDependencySynchronize();
   float top = kLowest, total = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const uint32_t per_head = ws.cum[A.G + A.B];
-  if (live && per_head && A.lens[b] >= 0) {
-    const Deal d = make_deal(per_head, A.kv.Hkv, warps);
-    const size_t rows = (size_t)A.B * A.Hq;
-    const int in_prompt = (b - seg.off[group]) * GQ + h % GQ, in_own = h % GQ;
-    const Parts p[2] = {parts_of(d, ws.cum, group, ((seg.off[group + 1] - seg.off[group]) * GQ + cols - 1) / cols,
-                                 in_prompt / cols, kvh, rows + (size_t)row),
-                        parts_of(d, ws.cum, A.G + b, (GQ + cols - 1) / cols, in_own / cols, kvh, (size_t)row)};
-    const int n = p[0].n + p[1].n;
-    auto place = [&](int i) -> size_t {
-      const bool second = i >= p[0].n;
-      const Parts& q = second ? p[1] : p[0];
-      if (second) i -= p[0].n;
-      return i == 0 ? q.own : 2 * rows + (size_t)(q.first + i) * cols + (second ? in_own : in_prompt) % cols;
-    };
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, ws.ml[place(i)].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    for (int i = lane; i < n; i += 32) {
-      const float2 v = ws.ml[place(i)];
-      total += v.y * ex2_approx(v.x - top);
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  if (ws.cum[A.G + A.B] && A.lens[b] >= 0) {
+    const RowParts<CAP> parts(A, seg, ws.cum, warps, cols, b, h);
+    for (int i = lane; i < parts.n; i += 32) top = fmaxf(top, ws.ml[parts.place(i)].x);
+    top = warp_max(top);
 #pragma unroll 4
-    for (int i = part; i < n; i += share) {
-      const size_t at = place(i);
-      const float f = ex2_approx(ws.ml[at].x - top);
-      const float2* v = reinterpret_cast<const float2*>(ws.o + at * D);
+    for (int i = 0; i < parts.n; ++i) {
+      const size_t at = parts.place(i);
+      const float2 ml = ws.ml[at], *v = reinterpret_cast<const float2*>(ws.o + at * D);
+      const float f = ex2_approx(ml.x - top);
+      total = fmaf(ml.y, f, total);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         const float2 x = v[lane + 16 * e];
@@ -663,22 +722,64 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       }
     }
   }
-  if (share > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][32 * e + lane] = acc[e];
-    __syncthreads();
-    if (part) return;
-    for (int w = 1; w < share; ++w)
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += so[warp + w][32 * e + lane];
-  }
-  if (!live) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D);
 #pragma unroll
   for (int e = 0; e < E; e += 2) out[lane + 16 * e] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && A.lse)
-    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+  if (lane == 0 && A.lse) A.lse[(int64_t)h * A.B + b] = lse_of(top, total);
+}
+
+// Few rows, which may have a partial result of every warp: a block joins 32 values of one (blockIdx.y: which).
+template <int D, int CAP>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_slices_kernel(const DecodeArgs A, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
+  __shared__ float weight[kJoinThreads], sum[kJoinWarps], most[kJoinWarps], part[kJoinWarps][32];
+  __shared__ size_t place[kJoinThreads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = (int)blockIdx.x / A.Hq, h = (int)blockIdx.x % A.Hq;
+  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  cudaGridDependencySynchronize();
+  float top = kLowest, total = 0.f, acc = 0.f;
+  if (ws.cum[A.G + A.B] && A.lens[b] >= 0) {  // the same for the whole block
+    const RowParts<CAP> parts(A, seg, ws.cum, warps, cols, b, h);
+    for (int i = threadIdx.x; i < parts.n; i += kJoinThreads) top = fmaxf(top, ws.ml[parts.place(i)].x);
+    top = warp_max(top);
+    if (lane == 0) most[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, most[w]);
+    for (int i0 = 0; i0 < parts.n; i0 += kJoinThreads) {
+      const int i = i0 + (int)threadIdx.x;
+      if (i < parts.n) {
+        const size_t at = parts.place(i);
+        const float2 ml = ws.ml[at];
+        const float f = ex2_approx(ml.x - top);
+        weight[threadIdx.x] = f;
+        place[threadIdx.x] = at;
+        total = fmaf(ml.y, f, total);
+      }
+      __syncthreads();
+      const int n = min(kJoinThreads, parts.n - i0);
+#pragma unroll 8
+      for (int k = warp; k < n; k += kJoinWarps)
+        acc = fmaf(ws.o[place[k] * D + 32 * blockIdx.y + lane], weight[k], acc);
+      __syncthreads();
+    }
+  }
+  total = warp_sum(total);
+  if (lane == 0) sum[warp] = total;
+  part[warp][lane] = acc;
+  __syncthreads();
+  if (warp) return;
+  total = 0.f;
+  acc = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    total += sum[w];
+    acc += part[w][lane];
+  }
+  A.out[(int64_t)blockIdx.x * D + 32 * blockIdx.y + lane] = __float2bfloat16(total > 0.f ? acc / total : 0.f);
+  if (lane == 0 && blockIdx.y == 0 && A.lse) A.lse[(int64_t)h * A.B + b] = lse_of(top, total);
 }
 
 template <int D, int BITS, int NT, int CAP>
@@ -693,9 +794,11 @@ cudaError_t launch_t(const DecodeArgs& a, const int32_t* groups, cudaStream_t st
   decode_kernel<D, BITS, NT, CAP><<<kBlocks, warps * 32, smem, st>>>(a, seg);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.B * a.Hq;
-  const int share = rows >= 2432 ? 1 : kJoinWarps, per = kJoinWarps / share;
-  return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinWarps * 32), st, a, share,
-                       (int)C::COLS, kBlocks * warps, seg);
+  if (rows > kBlocks * kJoinWarps)
+    return launch_behind(join_rows_kernel<D, CAP>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinThreads),
+                         st, a, (int)C::COLS, kBlocks * warps, seg);
+  return launch_behind(join_slices_kernel<D, CAP>, dim3((unsigned)rows, D / 32), dim3(kJoinThreads), st, a, (int)C::COLS,
+                       kBlocks * warps, seg);
 }
 
 template <int D, int BITS>
