@@ -829,8 +829,18 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
   if ((rc = status_of_device(&a.status))) return rc;
-  return timed(DUALKV_KERNEL_DECODE, st, [&] { return launch_decode(D, a, groups, st); }) == cudaSuccess ? DUALKV_OK
-                                                                                                       : DUALKV_ERR_CUDA;
+  CUtensorMap tk = {}, tv = {};
+  if (D != 512 && prompts && G <= kBigGroups && head_rows <= INT32_MAX) {
+    for (int g = 0; g < G; ++g) a.big |= (uint64_t)(groups[g + 1] - groups[g]) * GQ >= kBigRows;
+    if (a.big && cache->bits == 16) {
+      if ((rc = ensure_encode())) return rc;
+      if (make_tmap(&tk, cache->k, (int64_t)head_rows, 1, D, 16) || make_tmap(&tv, cache->v, (int64_t)head_rows, 1, D, 16))
+        return DUALKV_ERR_CUDA;
+    }
+  }
+  return timed(DUALKV_KERNEL_DECODE, st, [&] { return launch_decode(D, a, tk, tv, groups, st); }) == cudaSuccess
+             ? DUALKV_OK
+             : DUALKV_ERR_CUDA;
 }
 
 Bound bound_of(double v) {

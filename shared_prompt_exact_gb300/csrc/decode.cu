@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
+#include "decode.cuh"
 #include "kernels.h"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -32,9 +33,6 @@ namespace dkv {
 
 namespace {
 
-constexpr int kBlocks = 152;    // one per SM
-constexpr int kMostShared = 226 << 10;  // dynamic shared memory of a block, 1 KB left for the rest
-constexpr float kLowest = -3e38f;  // maximum of a row that has seen nothing: finite, so differences are too
 constexpr float kRescale = 8.f;    // a maximum moves when a weight would pass 2^8
 
 template <int D, int BITS, int NT>
@@ -101,129 +99,6 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, __nv_bfloat162 s, __
   return bits(__hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, minus24s));
 }
 
-// ---------------------------------------------------------------- the deal
-// Tiles of every source in order: prompts 0 .. G - 1, then responses 0 .. B - 1; a source with more rows
-// than a warp takes at once counts its tiles once for every block of rows.  The same sequence follows for each kv-head.
-struct Deal {
-  uint64_t total;   // tiles of all kv-heads
-  uint32_t per_head, workers;
-};
-__device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int warps) {
-  Deal d;
-  d.per_head = per_head;
-  d.total = (uint64_t)per_head * (uint64_t)Hkv;
-  d.workers = (uint32_t)(d.total < (uint64_t)warps ? d.total : (uint64_t)warps);  // so that each has a tile
-  return d;
-}
-__device__ __forceinline__ uint64_t first_tile(const Deal& d, uint32_t worker) { return d.total * worker / d.workers; }
-__device__ __forceinline__ uint32_t worker_of(const Deal& d, uint64_t tile) {
-  return (uint32_t)(((tile + 1) * d.workers - 1) / d.total);
-}
-
-__device__ __forceinline__ int clamp_len(int n, int max_pages, int ps, uint32_t* status) {
-  if (n <= (int64_t)max_pages * ps) return n;
-  if (status) atomicOr(status, kDevErrBounds);
-  return max_pages * ps;
-}
-// Prompt of group g (0 without prompts) and tokens of response b (negative: ended), as far as the tables go.
-__device__ __forceinline__ int prompt_len(const DecodeArgs& A, int g, uint32_t* status) {
-  return A.prompt_lens ? max(0, clamp_len(A.prompt_lens[g], A.max_prompt_pages, A.kv.ps, status)) : 0;
-}
-__device__ __forceinline__ int response_len(const DecodeArgs& A, int b, uint32_t* status) {
-  return clamp_len(A.lens[b], A.max_pages, A.kv.ps, status);
-}
-// First position that a response of n tokens behind a prompt of P sees.
-__device__ __forceinline__ int first_position(const DecodeArgs& A, int P, int n) {
-  return A.window > 0 ? (int)max((int64_t)0, (int64_t)P + n - A.window) : 0;
-}
-// Tiles of tokens [lo, end).
-template <int TILE>
-__device__ __forceinline__ int tiles_of(int lo, int end) {
-  return lo < end ? (end + TILE - 1) / TILE - lo / TILE : 0;
-}
-
-struct Workspace {
-  uint32_t* cum;  // [G + B + 1] tiles before each source, of one kv-head
-  float2* ml;     // [slots] maximum (base 2) and sum
-  float* o;       // [slots][D]
-};
-__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-constexpr int kMostSources = kMaxSegs + kMaxResponses;
-constexpr size_t kMostWarps = kBlocks * 16, kMostCols = 16;
-__host__ __device__ inline size_t slots_of(int B, int Hq) { return 2 * (size_t)B * Hq + kMostWarps * kMostCols; }
-__host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
-  uint8_t* at = static_cast<uint8_t*>(p);
-  Workspace w;
-  w.cum = reinterpret_cast<uint32_t*>(at);
-  at += align256(sizeof(uint32_t) * (kMostSources + 1));
-  w.ml = reinterpret_cast<float2*>(at);
-  at += align256(sizeof(float2) * slots_of(B, Hq));
-  w.o = reinterpret_cast<float*>(at);
-  return w;
-}
-
-// Prefix sums of the sources' tiles into cum[0 .. G + B] (shared memory), by the whole block.
-template <int COLS, int TILE, int CAP>
-__device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, uint32_t* cum, uint32_t* scratch) {
-  const int G = A.G, n = A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
-  // a prompt's entry first holds its group's fewest tokens of a response that has not ended
-  for (int g = tid; g < G; g += THREADS) cum[1 + g] = 0x7fffffffu;
-  __syncthreads();
-  for (int b = tid; b < A.B; b += THREADS) {
-    const int len = response_len(A, b, A.status), g = seg_of(seg, b);
-    uint32_t tiles = 0;
-    if (len >= 0) {
-      const int P = prompt_len(A, g, nullptr), lo = max(0, first_position(A, P, len) - P);
-      atomicMin(&cum[1 + g], (uint32_t)len);
-      tiles = (uint32_t)tiles_of<TILE>(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
-    }
-    cum[1 + G + b] = tiles;
-  }
-  __syncthreads();
-  for (int g = tid; g < G; g += THREADS) {
-    const uint32_t least = cum[1 + g];
-    uint32_t tiles = 0;
-    if (least != 0x7fffffffu) {
-      const int P = prompt_len(A, g, A.status), rows = (seg.off[g + 1] - seg.off[g]) * GQ;
-      tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
-    }
-    cum[1 + g] = tiles;
-  }
-  if (tid == 0) cum[0] = 0;
-  __syncthreads();
-  // inclusive scan of cum[1 .. n]: every thread takes a run
-  const int per = (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);
-  uint32_t sum = 0;
-  for (int i = from; i < to; ++i) sum += cum[i];
-  const int lane = tid & 31, warp = tid >> 5;
-  uint32_t incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  uint32_t before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += scratch[w];
-  for (int i = from; i < to; ++i) {
-    before += cum[i];
-    cum[i] = before;
-  }
-  __syncthreads();
-}
-
-// Source holding tile `t` of a kv-head: the largest s with cum[s] <= t.
-__device__ __forceinline__ int source_of(const uint32_t* cum, int n, uint32_t t) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cum[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // ---------------------------------------------------------------- a warp's walk
 template <int D, int BITS, int NT, int CAP>
 __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
@@ -238,15 +113,17 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  deal_sources<C::COLS, C::TILE>(A, seg, cum, scratch);
+  deal_sources<C::COLS, C::TILE, false>(A, seg, cum, scratch, nullptr);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= sources; i += blockDim.x) ws.cum[i] = cum[i];
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
   // neighbouring shares go to different SMs, so that a short batch spreads over all of them
   const uint32_t worker = (uint32_t)(warp * kBlocks + blockIdx.x);
-  if (worker >= deal.workers) return;
-  uint64_t at = first_tile(deal, worker);
-  const uint64_t stop = first_tile(deal, worker + 1);
+  uint64_t at = 0, stop = 0;
+  if (worker < deal.workers) {
+    at = first_tile(deal, worker);
+    stop = first_tile(deal, worker + 1);
+  }
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
   uint8_t* ring_p = smem + warp * C::RING;
   // what this lane copies: every LG-th chunk of sub-tile `mine`
@@ -605,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
         const int b = r / GQ;
         const size_t rows = (size_t)A.B * A.Hq;
         const size_t to = t0 == 0 ? (prompt ? rows : 0) + (size_t)b * A.Hq + kvh * GQ + (r - b * GQ)
-                                  : 2 * rows + (size_t)worker * C::COLS + col;
+                                  : own_slots(A.B, A.Hq) + (size_t)worker * C::COLS + col;
         if (g == 0) ws.ml[to] = make_float2(m[nt][c], sum);
         float* out = ws.o + to * D;
 #pragma unroll
@@ -623,55 +500,54 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
         }
       }
   }
+  // the kernel of the large groups' prompts may still run: the join, which waits for this one, needs both
+  if (warp == 0) cudaGridDependencySynchronize();
 }
 
 // ---------------------------------------------------------------- the join
-// A source's partial results for one row: the first in the row's own place, the others in those of the warps behind.
+// A source's partial results for one row: the first in the row's own slot, the others in those of the workers behind.
 struct Parts {
-  size_t own;
-  uint32_t first;  // worker of the first one
-  int n;
+  size_t own, carried;  // slots of the first and (n > 1) of the one before the second
+  int n, stride;
 };
-__device__ __forceinline__ Parts parts_of(const Deal& d, const uint32_t* cum, int s, int blocks, int block, int kvh, size_t own) {
-  Parts p{own, 0, 0};
+__device__ __forceinline__ Parts parts_of(const uint32_t* cum, int n_sources, int Hkv, int workers, int s, int rows, int row,
+                                          int kvh, size_t own, size_t carried, int cols) {
+  Parts p{own, 0, 0, cols};
+  const int blocks = (rows + cols - 1) / cols;
   const uint32_t tiles = (cum[s + 1] - cum[s]) / (uint32_t)blocks;
   if (!tiles) return p;
-  const uint64_t from = (uint64_t)kvh * d.per_head + cum[s] + (uint64_t)block * tiles;
-  p.first = worker_of(d, from);
-  p.n = (int)(worker_of(d, from + tiles - 1) - p.first) + 1;
+  const Deal d = make_deal(cum[n_sources], Hkv, workers);
+  const uint64_t from = (uint64_t)kvh * d.per_head + cum[s] + (uint64_t)(row / cols) * tiles;
+  const uint32_t first = worker_of(d, from);
+  p.n = (int)(worker_of(d, from + tiles - 1) - first) + 1;
+  p.carried = carried + (size_t)first * cols + row % cols;
   return p;
 }
 
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
 
-// The partial results of row `row`: n of them, and where the i-th lies.
-template <int CAP>
+// The partial results of one row: n of them, and where the i-th lies.
 struct RowParts {
   Parts p[2];
-  size_t carried;  // the first warp's place for the partial results of later tiles
-  int n, cols, at[2];
-  __device__ __forceinline__ RowParts(const DecodeArgs& A, const SegTable<CAP>& seg, const uint32_t* cum, int warps,
-                                      int cols_, int b, int h) {
-    const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, group = seg_of(seg, b);
-    const int in_prompt = (b - seg.off[group]) * GQ + h % GQ, in_own = h % GQ;
-    const size_t rows = (size_t)A.B * A.Hq, row = (size_t)b * A.Hq + h;
-    const Deal d = make_deal(cum[A.G + A.B], A.kv.Hkv, warps);
-    cols = cols_;
-    p[0] = parts_of(d, cum, group, ((seg.off[group + 1] - seg.off[group]) * GQ + cols - 1) / cols, in_prompt / cols, kvh,
-                    rows + row);
-    p[1] = parts_of(d, cum, A.G + b, (GQ + cols - 1) / cols, in_own / cols, kvh, row);
-    carried = 2 * rows;
-    at[0] = in_prompt % cols;
-    at[1] = in_own % cols;
+  int n;
+  template <int CAP>
+  __device__ __forceinline__ RowParts(const DecodeArgs& A, const SegTable<CAP>& seg, const Workspace& ws, int warps, int cols,
+                                      int b, int h) {
+    const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, g = seg_of(seg, b), sources = A.G + A.B;
+    const int rows = (seg.off[g + 1] - seg.off[g]) * GQ, in_prompt = (b - seg.off[g]) * GQ + h % GQ;
+    const size_t row = (size_t)b * A.Hq + h, own = own_slots(A.B, A.Hq);
+    p[0] = big_group(A, seg.off[g + 1] - seg.off[g])
+               ? parts_of(ws.big_cum, A.G, A.kv.Hkv, kBlocks, g, rows, in_prompt, kvh, own / 2 + row, own + kWarpSlots, 128)
+               : parts_of(ws.cum, sources, A.kv.Hkv, warps, g, rows, in_prompt, kvh, own / 2 + row, own, cols);
+    p[1] = parts_of(ws.cum, sources, A.kv.Hkv, warps, A.G + b, GQ, h % GQ, kvh, row, own, cols);
     n = p[0].n + p[1].n;
   }
   __device__ __forceinline__ size_t place(int i) const {
     const bool second = i >= p[0].n;
+    const Parts& q = second ? p[1] : p[0];
     const int k = second ? i - p[0].n : i;
-    const size_t own = second ? p[1].own : p[0].own;
-    return k == 0 ? own
-                  : carried + (size_t)((second ? p[1].first : p[0].first) + k) * cols + (second ? at[1] : at[0]);
+    return k == 0 ? q.own : q.carried + (size_t)k * q.stride;
   }
 };
 
@@ -704,8 +580,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   float top = kLowest, total = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (ws.cum[A.G + A.B] && A.lens[b] >= 0) {
-    const RowParts<CAP> parts(A, seg, ws.cum, warps, cols, b, h);
+  if (A.lens[b] >= 0) {
+    const RowParts parts(A, seg, ws, warps, cols, b, h);
     for (int i = lane; i < parts.n; i += 32) top = fmaxf(top, ws.ml[parts.place(i)].x);
     top = warp_max(top);
 #pragma unroll 4
@@ -740,8 +616,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   cudaGridDependencySynchronize();
   float top = kLowest, total = 0.f, acc = 0.f;
-  if (ws.cum[A.G + A.B] && A.lens[b] >= 0) {  // the same for the whole block
-    const RowParts<CAP> parts(A, seg, ws.cum, warps, cols, b, h);
+  if (A.lens[b] >= 0) {  // the same for the whole block
+    const RowParts parts(A, seg, ws, warps, cols, b, h);
     for (int i = threadIdx.x; i < parts.n; i += kJoinThreads) top = fmaxf(top, ws.ml[parts.place(i)].x);
     top = warp_max(top);
     if (lane == 0) most[warp] = top;
@@ -783,7 +659,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int D, int BITS, int NT, int CAP>
-cudaError_t launch_t(const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
+                     cudaStream_t st) {
   using C = Cfg<D, BITS, NT>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
   // many sources take the place of some warps' rings
@@ -791,8 +668,22 @@ cudaError_t launch_t(const DecodeArgs& a, const int32_t* groups, cudaStream_t st
   const int warps = room < C::WARPS ? room : C::WARPS, smem = warps * C::RING + cum;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, BITS, NT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, BITS, NT, CAP><<<kBlocks, warps * 32, smem, st>>>(a, seg);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.big) {
+    if constexpr (D != 512) {
+      if ((e = launch_prompt(D, a, tk, tv, groups, st)) != cudaSuccess) return e;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kBlocks);
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute behind;
+  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &behind;
+  cfg.numAttrs = a.big ? 1 : 0;
+  if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, BITS, NT, CAP>, a, seg)) != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.B * a.Hq;
   if (rows > kBlocks * kJoinWarps)
     return launch_behind(join_rows_kernel<D, CAP>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinThreads),
@@ -802,26 +693,28 @@ cudaError_t launch_t(const DecodeArgs& a, const int32_t* groups, cudaStream_t st
 }
 
 template <int D, int BITS>
-cudaError_t launch_b(const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+cudaError_t launch_b(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
+                     cudaStream_t st) {
   const bool few = a.G <= kSmallSegs;
   if constexpr (D != 512) {
     if (a.Hq / a.kv.Hkv > 8)
-      return few ? launch_t<D, BITS, 2, kSmallSegs>(a, groups, st) : launch_t<D, BITS, 2, kMaxSegs>(a, groups, st);
+      return few ? launch_t<D, BITS, 2, kSmallSegs>(a, tk, tv, groups, st) : launch_t<D, BITS, 2, kMaxSegs>(a, tk, tv, groups, st);
   }
-  return few ? launch_t<D, BITS, 1, kSmallSegs>(a, groups, st) : launch_t<D, BITS, 1, kMaxSegs>(a, groups, st);
+  return few ? launch_t<D, BITS, 1, kSmallSegs>(a, tk, tv, groups, st) : launch_t<D, BITS, 1, kMaxSegs>(a, tk, tv, groups, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st) {
+cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
+                          cudaStream_t st) {
   const bool four = a.kv.ks != nullptr;
   switch (D) {
     case 64:
-      return four ? launch_b<64, 4>(a, groups, st) : launch_b<64, 16>(a, groups, st);
+      return four ? launch_b<64, 4>(a, tk, tv, groups, st) : launch_b<64, 16>(a, tk, tv, groups, st);
     case 128:
-      return four ? launch_b<128, 4>(a, groups, st) : launch_b<128, 16>(a, groups, st);
+      return four ? launch_b<128, 4>(a, tk, tv, groups, st) : launch_b<128, 16>(a, tk, tv, groups, st);
     case 512:
-      return four ? launch_b<512, 4>(a, groups, st) : launch_b<512, 16>(a, groups, st);
+      return four ? launch_b<512, 4>(a, tk, tv, groups, st) : launch_b<512, 16>(a, tk, tv, groups, st);
     default:
       return cudaErrorInvalidValue;
   }

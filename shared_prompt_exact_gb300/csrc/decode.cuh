@@ -1,0 +1,157 @@
+// decode.cuh -- what the kernels of dualkv_decode share: the deal of tiles to workers and the workspace.
+#pragma once
+#include <stdint.h>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "segs.cuh"
+
+namespace dkv {
+
+namespace {
+
+constexpr int kBlocks = 152;    // one per SM
+constexpr int kMostShared = 226 << 10;  // dynamic shared memory of a block, 1 KB left for the rest
+constexpr float kLowest = -3e38f;  // maximum of a row that has seen nothing: finite, so differences are too
+
+// ---------------------------------------------------------------- the deal
+// Tiles of every source in order: prompts 0 .. G - 1, then responses 0 .. B - 1; a source with more rows
+// than are taken at once counts its tiles once for every block of rows.  The same sequence follows for each kv-head.
+struct Deal {
+  uint64_t total;   // tiles of all kv-heads
+  uint32_t per_head, workers;
+};
+__device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int warps) {
+  Deal d;
+  d.per_head = per_head;
+  d.total = (uint64_t)per_head * (uint64_t)Hkv;
+  d.workers = (uint32_t)(d.total < (uint64_t)warps ? d.total : (uint64_t)warps);  // so that each has a tile
+  return d;
+}
+__device__ __forceinline__ uint64_t first_tile(const Deal& d, uint32_t worker) { return d.total * worker / d.workers; }
+__device__ __forceinline__ uint32_t worker_of(const Deal& d, uint64_t tile) {
+  return (uint32_t)(((tile + 1) * d.workers - 1) / d.total);
+}
+
+__device__ __forceinline__ int clamp_len(int n, int max_pages, int ps, uint32_t* status) {
+  if (n <= (int64_t)max_pages * ps) return n;
+  if (status) atomicOr(status, kDevErrBounds);
+  return max_pages * ps;
+}
+// Prompt of group g (0 without prompts) and tokens of response b (negative: ended), as far as the tables go.
+__device__ __forceinline__ int prompt_len(const DecodeArgs& A, int g, uint32_t* status) {
+  return A.prompt_lens ? max(0, clamp_len(A.prompt_lens[g], A.max_prompt_pages, A.kv.ps, status)) : 0;
+}
+__device__ __forceinline__ int response_len(const DecodeArgs& A, int b, uint32_t* status) {
+  return clamp_len(A.lens[b], A.max_pages, A.kv.ps, status);
+}
+// First position that a response of n tokens behind a prompt of P sees.
+__device__ __forceinline__ int first_position(const DecodeArgs& A, int P, int n) {
+  return A.window > 0 ? (int)max((int64_t)0, (int64_t)P + n - A.window) : 0;
+}
+// Tiles of tokens [lo, end).
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int lo, int end) {
+  return lo < end ? (end + TILE - 1) / TILE - lo / TILE : 0;
+}
+
+struct Workspace {
+  uint32_t* cum;      // [G + B + 1] tiles before each source, of one kv-head
+  uint32_t* big_cum;  // [G + 1] the same of prompt.cu's prompts
+  float2* ml;         // [slots] maximum (base 2) and sum
+  float* o;           // [slots][D]
+};
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+// Slots of partial results: the rows' own ones of the responses and of the prompts; then those for what a worker
+// goes on with that another one began: 16 for a warp, 128 for a block of prompt.cu.
+constexpr size_t kWarpSlots = (size_t)kBlocks * 16 * 16, kBlockSlots = (size_t)kBlocks * 128;
+__host__ __device__ inline size_t own_slots(int B, int Hq) { return 2 * (size_t)B * Hq; }
+__host__ __device__ inline size_t slots_of(int B, int Hq) { return own_slots(B, Hq) + kWarpSlots + kBlockSlots; }
+__host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
+  uint8_t* at = static_cast<uint8_t*>(p);
+  Workspace w;
+  w.cum = reinterpret_cast<uint32_t*>(at);
+  at += align256(sizeof(uint32_t) * (kMaxSegs + kMaxResponses + 1));
+  w.big_cum = reinterpret_cast<uint32_t*>(at);
+  at += align256(sizeof(uint32_t) * (kBigGroups + 1));
+  w.ml = reinterpret_cast<float2*>(at);
+  at += align256(sizeof(float2) * slots_of(B, Hq));
+  w.o = reinterpret_cast<float*>(at);
+  return w;
+}
+
+// Whether a prompt is left to prompt.cu's kernel, which takes 128 of its rows at once.
+__device__ __forceinline__ bool big_group(const DecodeArgs& A, int responses) {
+  return A.big && responses * (A.Hq / A.kv.Hkv) >= kBigRows;
+}
+
+// Prefix sums of the sources' tiles into cum[0 .. n] (shared memory), by the whole block.  BIG: of the prompts that
+// big_group names alone, n = G, with the fewest tokens of a response that has not ended (or INT_MAX) into
+// least_of; else of the other prompts and of all responses, n = G + B.
+template <int COLS, int TILE, bool BIG, int CAP>
+__device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, uint32_t* cum, uint32_t* scratch,
+                                             int* least_of) {
+  const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
+  // a prompt's entry first holds its group's fewest tokens of a response that has not ended
+  for (int g = tid; g < G; g += THREADS) cum[1 + g] = 0x7fffffffu;
+  __syncthreads();
+  for (int b = tid; b < A.B; b += THREADS) {
+    const int len = response_len(A, b, A.status), g = seg_of(seg, b);
+    uint32_t tiles = 0;
+    if (len >= 0) {
+      const int P = prompt_len(A, g, nullptr), lo = max(0, first_position(A, P, len) - P);
+      atomicMin(&cum[1 + g], (uint32_t)len);
+      tiles = (uint32_t)tiles_of<TILE>(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
+    }
+    if (!BIG) cum[1 + G + b] = tiles;
+  }
+  __syncthreads();
+  for (int g = tid; g < G; g += THREADS) {
+    const uint32_t least = cum[1 + g];
+    uint32_t tiles = 0;
+    if (BIG) least_of[g] = (int)least;
+    if (least != 0x7fffffffu && big_group(A, seg.off[g + 1] - seg.off[g]) == BIG) {
+      const int P = prompt_len(A, g, A.status), rows = (seg.off[g + 1] - seg.off[g]) * GQ;
+      tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
+    }
+    cum[1 + g] = tiles;
+  }
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+  // inclusive scan of cum[1 .. n]: every thread takes a run
+  const int per = (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);
+  uint32_t sum = 0;
+  for (int i = from; i < to; ++i) sum += cum[i];
+  const int lane = tid & 31, warp = tid >> 5;
+  uint32_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - sum;
+  for (int w = 0; w < warp; ++w) before += scratch[w];
+  for (int i = from; i < to; ++i) {
+    before += cum[i];
+    cum[i] = before;
+  }
+  __syncthreads();
+}
+
+// Source holding tile `t` of a kv-head: the largest s with cum[s] <= t.
+__device__ __forceinline__ int source_of(const uint32_t* cum, int n, uint32_t t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+}  // namespace
+
+}  // namespace dkv

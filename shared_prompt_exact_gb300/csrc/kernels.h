@@ -266,8 +266,16 @@ struct DecodeArgs {
   float* lse;        // may be null
   void* workspace;
   uint32_t* status;
+  bool big;          // some prompts go to launch_prompt: of groups with kBigRows rows (responses x Hq / Hkv) or more
 };
-cudaError_t launch_decode(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st);
+// A group's prompt is worth the tensor cores' large tiles from here on.
+constexpr int kBigRows = 32;
+constexpr int kBigGroups = 2048;  // most groups of a call whose prompts may go there
+// tk, tv: views (make_tmap, boxes of 16 rows) of the bf16 pools, used where a.big and the cache holds bf16
+cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
+                          cudaStream_t st);
+cudaError_t launch_prompt(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
+                          cudaStream_t st);
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D);
 
 }  // namespace dkv
