@@ -830,7 +830,7 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   std::lock_guard<std::mutex> lock(g_mu);
   if ((rc = status_of_device(&a.status))) return rc;
   CUtensorMap tk = {}, tv = {};
-  if (D != 512 && prompts && G <= kBigGroups && head_rows <= INT32_MAX) {
+  if (D != 512 && prompts && G <= kBigGroups && B <= kBigResponses && head_rows <= INT32_MAX) {
     for (int g = 0; g < G; ++g) a.big |= (uint64_t)(groups[g + 1] - groups[g]) * GQ >= kBigRows;
     if (a.big && cache->bits == 16) {
       if ((rc = ensure_encode())) return rc;

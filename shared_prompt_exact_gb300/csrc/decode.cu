@@ -108,22 +108,21 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   constexpr int LG = 32 / KT, CPR = C::RB / 16;  // lanes that copy a sub-tile; 16-byte chunks of a row
   const int warps = blockDim.x >> 5;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + warps * C::RING);
+  const Sources src{reinterpret_cast<uint32_t*>(smem + warps * C::RING),
+                    reinterpret_cast<int*>(smem + warps * C::RING) + A.G + A.B + 1, nullptr};
+  const uint32_t* cum = src.cum;
   __shared__ uint32_t scratch[C::WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  deal_sources<C::COLS, C::TILE, false>(A, seg, cum, scratch, nullptr);
+  deal_sources<C::COLS, C::TILE, false>(A, seg, src, scratch);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= sources; i += blockDim.x) ws.cum[i] = cum[i];
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
   // neighbouring shares go to different SMs, so that a short batch spreads over all of them
   const uint32_t worker = (uint32_t)(warp * kBlocks + blockIdx.x);
-  uint64_t at = 0, stop = 0;
-  if (worker < deal.workers) {
-    at = first_tile(deal, worker);
-    stop = first_tile(deal, worker + 1);
-  }
+  uint64_t at = first_tile(deal, worker);
+  const uint64_t stop = first_tile(deal, worker + 1);
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
   uint8_t* ring_p = smem + warp * C::RING;
   // what this lane copies: every LG-th chunk of sub-tile `mine`
@@ -133,11 +132,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
 
   while (at < stop) {
     // ---- the source, its rows and the tiles of it that are this warp's
-    const int kvh = (int)(at / deal.per_head);
-    const uint32_t local = (uint32_t)(at % deal.per_head);
+    const int kvh = (int)divide(at, deal.per_head);
+    const uint32_t local = (uint32_t)(at - (uint64_t)kvh * deal.per_head);
     const int s = source_of(cum, sources, local);
     const bool prompt = s < A.G;
-    const int b0 = prompt ? seg.off[s] : s - A.G, group = prompt ? s : seg_of(seg, b0);
+    const int b0 = prompt ? seg.off[s] : s - A.G;
     const int row_begin = b0 * GQ, row_end = (prompt ? seg.off[s + 1] : b0 + 1) * GQ;
     const int blocks = (row_end - row_begin + C::COLS - 1) / C::COLS;
     const int tiles = (int)((cum[s + 1] - cum[s]) / (uint32_t)blocks);
@@ -145,8 +144,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
     at += (uint64_t)(t1 - t0);
     const int r0 = row_begin + block * C::COLS;
-    const int P = prompt_len(A, group, nullptr);
-    const int end = prompt ? P : response_len(A, b0, nullptr);
+    const int end = src.len[s];
     // first tile of the source: its last one ends at `end`
     const int tile0 = (end + TILE - 1) / TILE - tiles;
 
@@ -157,10 +155,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       const int r = r0 + 8 * (c >> 1) + 2 * t + (c & 1);
       lo[c] = 0x7fffffff;
       if (r < row_end) {
-        const int len = prompt ? response_len(A, r / GQ, nullptr) : end;
+        const int len = prompt ? src.len[A.G + r / GQ] : end;
         if (len >= 0) {
-          lo[c] = first_position(A, P, len);
-          if (!prompt) lo[c] = max(0, lo[c] - P);
+          lo[c] = prompt ? first_position(A, end, len) : first_own(A, len);
           lo_min = min(lo_min, lo[c]);
           lo_max = max(lo_max, lo[c]);
         }
@@ -176,6 +173,25 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     // this lane's sub-tile: its place in the table, its first slot in the page, and the page (loaded a tile ahead)
     int token = first * TILE + 16 * mine, place = token / A.kv.ps, in_page = token - place * A.kv.ps;
     int page = first < last && token < end ? table[place] : -1;
+    // ---- queries as B operands, in the order in which a lane meets the keys' values (the loads first: they
+    // are on their way while the first keys are asked for)
+    uint32_t q[NT][D / 16][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g, b = r / GQ;
+      const uint4* row = reinterpret_cast<const uint4*>(A.q + b * A.q_stride + (kvh * GQ + (r - b * GQ)) * D);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int chunk = BITS == 16 ? 2 * t + (j & 1) + 8 * (j >> 1)
+                                     : (D == 64 ? 2 * t + j : 4 * t + 16 * (j >> 2) + (j & 3));
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < row_end) w = row[chunk];
+        q[nt][2 * j][0] = w.x;
+        q[nt][2 * j][1] = w.y;
+        q[nt][2 * j + 1][0] = w.z;
+        q[nt][2 * j + 1][1] = w.w;
+      }
+    }
     int64_t row = 0;       // of the pools, where the last issued keys' sub-tile starts
     bool has_page = false;
     uint32_t missing = 0;  // tiles in the ring that have a token without a page
@@ -231,26 +247,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       issue_keys();
     }
 
-    // ---- queries as B operands, in the order in which a lane meets the keys' values
-    uint32_t q[NT][D / 16][2];
+    if (BITS == 4) {  // values e and e + 4 of each 8 together
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g, b = r / GQ;
-      const uint4* row = reinterpret_cast<const uint4*>(A.q + b * A.q_stride + (kvh * GQ + (r - b * GQ)) * D);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int chunk = BITS == 16 ? 2 * t + (j & 1) + 8 * (j >> 1)
-                                     : (D == 64 ? 2 * t + j : 4 * t + 16 * (j >> 2) + (j & 3));
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < row_end) w = row[chunk];
-        if (BITS == 4)  // values e and e + 4 together
-          w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
-                         __byte_perm(w.y, w.w, 0x7632));
-        q[nt][2 * j][0] = w.x;
-        q[nt][2 * j][1] = w.y;
-        q[nt][2 * j + 1][0] = w.z;
-        q[nt][2 * j + 1][1] = w.w;
-      }
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t(&x)[2] = q[nt][2 * j], (&y)[2] = q[nt][2 * j + 1];
+          const uint32_t w[4] = {__byte_perm(x[0], y[0], 0x5410), __byte_perm(x[0], y[0], 0x7632),
+                                 __byte_perm(x[1], y[1], 0x5410), __byte_perm(x[1], y[1], 0x7632)};
+          x[0] = w[0];
+          x[1] = w[1];
+          y[0] = w[2];
+          y[1] = w[3];
+        }
     }
 
     float o[NT][D / 64][4][4], m[NT][2], l[NT][2];
@@ -399,15 +408,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       uint8_t* v = ring_p + slot * C::SLOT;
       if (edge) {
         // values that no row sees may be anything: 0 (in 4 bits: their scales), which weights of 0 leave at 0
-#pragma unroll 1
-        for (int k = 0; k < TILE; ++k) {
+        for (int k = lane; k < TILE; k += 32) {
           const int key = key0 + k;
           if (key >= lo_min && key < end && !(gone >> (k >> 4) & 1)) continue;
-          if (BITS == 16) {
-            for (int c = lane; c < CPR; c += 32) *reinterpret_cast<uint4*>(v + k * C::VP + 16 * c) = make_uint4(0, 0, 0, 0);
-          } else if (lane < C::SP / 2) {
-            reinterpret_cast<uint16_t*>(v + TILE * C::VP + k * C::SP)[lane] = 0;
-          }
+          uint8_t* z = BITS == 16 ? v + k * C::VP : v + TILE * C::VP + k * C::SP;
+#pragma unroll 4
+          for (int c = 0; c < (BITS == 16 ? C::RB : C::SP) / 4; ++c) reinterpret_cast<uint32_t*>(z)[c] = 0;
         }
         __syncwarp();
       }
@@ -565,97 +571,58 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Many rows: a warp joins one.  Both kernels may start before the partial results are complete, so nothing that
-// reads them is __restrict__.
+// `share` warps of a block take a row's partial results by turns, and the first of them adds up what they have.  The
+// kernel may start before the partial results are complete, so nothing that reads them is __restrict__.
 template <int D, int CAP>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_rows_kernel(const DecodeArgs A, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
+    join_kernel(const DecodeArgs A, int share, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)A.B * A.Hq) return;
-  const int b = (int)(row / A.Hq), h = (int)(row % A.Hq);
+  __shared__ float2 sums[kJoinWarps][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % share;
+  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
+  const bool live = row < (int64_t)A.B * A.Hq;
+  const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
+  const bool ended = !live || A.lens[b] < 0;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   cudaGridDependencySynchronize();
-  float top = kLowest, total = 0.f, acc[E];
+  float top = kLowest, total = 0.f;
+  float2 acc[E / 2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  if (A.lens[b] >= 0) {
+  for (int e = 0; e < E / 2; ++e) acc[e] = make_float2(0.f, 0.f);
+  if (!ended) {
     const RowParts parts(A, seg, ws, warps, cols, b, h);
     for (int i = lane; i < parts.n; i += 32) top = fmaxf(top, ws.ml[parts.place(i)].x);
     top = warp_max(top);
+    for (int i = lane; i < parts.n; i += 32) {
+      const float2 ml = ws.ml[parts.place(i)];
+      total = fmaf(ml.y, ex2_approx(ml.x - top), total);
+    }
+    total = warp_sum(total);
 #pragma unroll 4
-    for (int i = 0; i < parts.n; ++i) {
+    for (int i = part; i < parts.n; i += share) {
       const size_t at = parts.place(i);
-      const float2 ml = ws.ml[at], *v = reinterpret_cast<const float2*>(ws.o + at * D);
-      const float f = ex2_approx(ml.x - top);
-      total = fmaf(ml.y, f, total);
+      const float f = ex2_approx(ws.ml[at].x - top);
+      const float2* v = reinterpret_cast<const float2*>(ws.o + at * D);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 x = v[lane + 16 * e];
-        acc[e] = fmaf(x.x, f, acc[e]);
-        acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
-      }
+      for (int e = 0; e < E / 2; ++e) acc[e] = ffma2(v[lane + 32 * e], make_float2(f, f), acc[e]);
     }
   }
+  if (share > 1) {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) sums[warp][lane + 32 * e] = acc[e];
+    __syncthreads();
+    if (part) return;
+    for (int w = 1; w < share; ++w)
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) acc[e] = fadd2(acc[e], sums[warp + w][lane + 32 * e]);
+  }
+  if (!live) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) out[lane + 16 * e] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && A.lse) A.lse[(int64_t)h * A.B + b] = lse_of(top, total);
-}
-
-// Few rows, which may have a partial result of every warp: a block joins 32 values of one (blockIdx.y: which).
-template <int D, int CAP>
-__global__ void __launch_bounds__(kJoinThreads)
-    join_slices_kernel(const DecodeArgs A, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
-  __shared__ float weight[kJoinThreads], sum[kJoinWarps], most[kJoinWarps], part[kJoinWarps][32];
-  __shared__ size_t place[kJoinThreads];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = (int)blockIdx.x / A.Hq, h = (int)blockIdx.x % A.Hq;
-  const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  cudaGridDependencySynchronize();
-  float top = kLowest, total = 0.f, acc = 0.f;
-  if (A.lens[b] >= 0) {  // the same for the whole block
-    const RowParts parts(A, seg, ws, warps, cols, b, h);
-    for (int i = threadIdx.x; i < parts.n; i += kJoinThreads) top = fmaxf(top, ws.ml[parts.place(i)].x);
-    top = warp_max(top);
-    if (lane == 0) most[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, most[w]);
-    for (int i0 = 0; i0 < parts.n; i0 += kJoinThreads) {
-      const int i = i0 + (int)threadIdx.x;
-      if (i < parts.n) {
-        const size_t at = parts.place(i);
-        const float2 ml = ws.ml[at];
-        const float f = ex2_approx(ml.x - top);
-        weight[threadIdx.x] = f;
-        place[threadIdx.x] = at;
-        total = fmaf(ml.y, f, total);
-      }
-      __syncthreads();
-      const int n = min(kJoinThreads, parts.n - i0);
-#pragma unroll 8
-      for (int k = warp; k < n; k += kJoinWarps)
-        acc = fmaf(ws.o[place[k] * D + 32 * blockIdx.y + lane], weight[k], acc);
-      __syncthreads();
-    }
-  }
-  total = warp_sum(total);
-  if (lane == 0) sum[warp] = total;
-  part[warp][lane] = acc;
-  __syncthreads();
-  if (warp) return;
-  total = 0.f;
-  acc = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    total += sum[w];
-    acc += part[w][lane];
-  }
-  A.out[(int64_t)blockIdx.x * D + 32 * blockIdx.y + lane] = __float2bfloat16(total > 0.f ? acc / total : 0.f);
-  if (lane == 0 && blockIdx.y == 0 && A.lse) A.lse[(int64_t)h * A.B + b] = lse_of(top, total);
+  for (int e = 0; e < E / 2; ++e) out[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
+  if (lane == 0 && A.lse)
+    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 template <int D, int BITS, int NT, int CAP>
@@ -664,7 +631,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   using C = Cfg<D, BITS, NT>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
   // many sources take the place of some warps' rings
-  const int cum = (a.G + a.B + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
+  const int cum = (2 * (a.G + a.B) + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
   const int warps = room < C::WARPS ? room : C::WARPS, smem = warps * C::RING + cum;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, BITS, NT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -684,12 +651,12 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   cfg.attrs = &behind;
   cfg.numAttrs = a.big ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, BITS, NT, CAP>, a, seg)) != cudaSuccess) return e;
+  // as many warps to a row as it can have partial results to spare, on average
   const int64_t rows = (int64_t)a.B * a.Hq;
-  if (rows > kBlocks * kJoinWarps)
-    return launch_behind(join_rows_kernel<D, CAP>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinThreads),
-                         st, a, (int)C::COLS, kBlocks * warps, seg);
-  return launch_behind(join_slices_kernel<D, CAP>, dim3((unsigned)rows, D / 32), dim3(kJoinThreads), st, a, (int)C::COLS,
-                       kBlocks * warps, seg);
+  const int64_t most = 2 + ((int64_t)kBlocks * warps * (a.Hq / a.kv.Hkv) + (a.big ? kBlocks * 128 : 0)) / rows;
+  const int share = most > 24 ? 8 : most > 12 ? 4 : most > 6 ? 2 : 1, per = kJoinWarps / share;
+  return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), st, a, share,
+                       (int)C::COLS, kBlocks * warps, seg);
 }
 
 template <int D, int BITS>

@@ -19,20 +19,24 @@ constexpr float kLowest = -3e38f;  // maximum of a row that has seen nothing: fi
 // Tiles of every source in order: prompts 0 .. G - 1, then responses 0 .. B - 1; a source with more rows
 // than are taken at once counts its tiles once for every block of rows.  The same sequence follows for each kv-head.
 struct Deal {
-  uint64_t total;   // tiles of all kv-heads
-  uint32_t per_head, workers;
+  uint64_t total, chunk;  // tiles of all kv-heads, and those of one worker: worker w has w chunk .. (w + 1) chunk - 1
+  uint32_t per_head;
 };
-__device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int warps) {
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {  // in 32 bits where that does
+  return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+__device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int workers) {
   Deal d;
   d.per_head = per_head;
   d.total = (uint64_t)per_head * (uint64_t)Hkv;
-  d.workers = (uint32_t)(d.total < (uint64_t)warps ? d.total : (uint64_t)warps);  // so that each has a tile
+  d.chunk = divide(d.total + (uint64_t)workers - 1, (uint64_t)workers);
   return d;
 }
-__device__ __forceinline__ uint64_t first_tile(const Deal& d, uint32_t worker) { return d.total * worker / d.workers; }
-__device__ __forceinline__ uint32_t worker_of(const Deal& d, uint64_t tile) {
-  return (uint32_t)(((tile + 1) * d.workers - 1) / d.total);
+__device__ __forceinline__ uint64_t first_tile(const Deal& d, uint32_t worker) {
+  const uint64_t at = d.chunk * worker;
+  return at < d.total ? at : d.total;
 }
+__device__ __forceinline__ uint32_t worker_of(const Deal& d, uint64_t tile) { return (uint32_t)divide(tile, d.chunk); }
 
 __device__ __forceinline__ int clamp_len(int n, int max_pages, int ps, uint32_t* status) {
   if (n <= (int64_t)max_pages * ps) return n;
@@ -86,33 +90,41 @@ __device__ __forceinline__ bool big_group(const DecodeArgs& A, int responses) {
   return A.big && responses * (A.Hq / A.kv.Hkv) >= kBigRows;
 }
 
-// Prefix sums of the sources' tiles into cum[0 .. n] (shared memory), by the whole block.  BIG: of the prompts that
-// big_group names alone, n = G, with the fewest tokens of a response that has not ended (or INT_MAX) into
-// least_of; else of the other prompts and of all responses, n = G + B.
+// What a block knows of the sources, in shared memory.
+struct Sources {
+  uint32_t* cum;  // [n + 1] tiles before each source, of one kv-head
+  int* len;       // [n] tokens of the prompts (0 .. G - 1) and of the responses (negative: ended)
+  int* least;     // BIG: [G] fewest tokens of a group's response that has not ended, or INT_MAX
+};
+
+// First token of its own that a response of n tokens sees.
+__device__ __forceinline__ int first_own(const DecodeArgs& A, int n) { return A.window > 0 ? max(0, n - A.window) : 0; }
+
+// Fills in the above, by the whole block.  BIG: tiles of the prompts that big_group names alone, n = G; else of the
+// other prompts and of all responses, n = G + B.  Lengths are kept of all sources either way.
 template <int COLS, int TILE, bool BIG, int CAP>
-__device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, uint32_t* cum, uint32_t* scratch,
-                                             int* least_of) {
+__device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
+                                             uint32_t* scratch) {
   const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
-  // a prompt's entry first holds its group's fewest tokens of a response that has not ended
-  for (int g = tid; g < G; g += THREADS) cum[1 + g] = 0x7fffffffu;
+  uint32_t* cum = src.cum;
+  for (int g = tid; g < G; g += THREADS) {
+    cum[1 + g] = 0x7fffffffu;
+    src.len[g] = prompt_len(A, g, A.status);
+  }
   __syncthreads();
   for (int b = tid; b < A.B; b += THREADS) {
-    const int len = response_len(A, b, A.status), g = seg_of(seg, b);
-    uint32_t tiles = 0;
-    if (len >= 0) {
-      const int P = prompt_len(A, g, nullptr), lo = max(0, first_position(A, P, len) - P);
-      atomicMin(&cum[1 + g], (uint32_t)len);
-      tiles = (uint32_t)tiles_of<TILE>(lo, len) * (uint32_t)((GQ + COLS - 1) / COLS);
-    }
-    if (!BIG) cum[1 + G + b] = tiles;
+    const int len = response_len(A, b, A.status);
+    src.len[G + b] = len;
+    if (len >= 0) atomicMin(&cum[1 + seg_of(seg, b)], (uint32_t)len);
+    if (!BIG) cum[1 + G + b] = (uint32_t)tiles_of<TILE>(first_own(A, len), len) * (uint32_t)((GQ + COLS - 1) / COLS);
   }
   __syncthreads();
   for (int g = tid; g < G; g += THREADS) {
     const uint32_t least = cum[1 + g];
     uint32_t tiles = 0;
-    if (BIG) least_of[g] = (int)least;
+    if (BIG) src.least[g] = (int)least;
     if (least != 0x7fffffffu && big_group(A, seg.off[g + 1] - seg.off[g]) == BIG) {
-      const int P = prompt_len(A, g, A.status), rows = (seg.off[g + 1] - seg.off[g]) * GQ;
+      const int P = src.len[g], rows = (seg.off[g + 1] - seg.off[g]) * GQ;
       tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
     }
     cum[1 + g] = tiles;

@@ -270,7 +270,8 @@ struct DecodeArgs {
 };
 // A group's prompt is worth the tensor cores' large tiles from here on.
 constexpr int kBigRows = 32;
-constexpr int kBigGroups = 2048;  // most groups of a call whose prompts may go there
+constexpr int kBigGroups = 512;    // most groups of a call whose prompts may go there: their lengths are in shared memory
+constexpr int kBigResponses = 4096;  // and most responses
 // tk, tv: views (make_tmap, boxes of 16 rows) of the bf16 pools, used where a.big and the cache holds bf16
 cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
                           cudaStream_t st);

@@ -74,8 +74,9 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PromptCtl ctl;
-  uint32_t* cum = reinterpret_cast<uint32_t*>(smem + C::RINGS);
-  int* least_of = reinterpret_cast<int*>(cum + A.G + 1);
+  const Sources src{reinterpret_cast<uint32_t*>(smem + C::RINGS), reinterpret_cast<int*>(smem + C::RINGS) + 2 * A.G + 1,
+                    reinterpret_cast<int*>(smem + C::RINGS) + A.G + 1};
+  const uint32_t* cum = src.cum;
   const uint32_t warp = warp_id(), lane = lane_id();
   const int GQ = A.Hq / A.kv.Hkv, ps = A.kv.ps;
   FailState fs{&ctl.abort_flag, A.status, kLaunchWaitLimitNs};
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  deal_sources<128, 128, true>(A, seg, cum, ctl.scratch, least_of);  // ends with a barrier
+  deal_sources<128, 128, true>(A, seg, src, ctl.scratch);  // ends with a barrier
   tc_fence_after();
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
   const uint32_t tmem = ctl.tmem_base;
@@ -115,15 +116,11 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= A.G; i += C::THREADS) ws.big_cum[i] = cum[i];
   const Deal deal = make_deal(cum[A.G], A.kv.Hkv, kBlocks);
-  uint64_t begin = 0, stop = 0;
-  if (blockIdx.x < deal.workers) {
-    begin = first_tile(deal, blockIdx.x);
-    stop = first_tile(deal, blockIdx.x + 1);
-  }
+  const uint64_t begin = first_tile(deal, blockIdx.x), stop = first_tile(deal, blockIdx.x + 1);
   auto next_segment = [&](uint64_t& at) {
     Segment s;
-    s.kvh = (int)(at / deal.per_head);
-    const uint32_t local = (uint32_t)(at % deal.per_head);
+    s.kvh = (int)divide(at, deal.per_head);
+    const uint32_t local = (uint32_t)(at - (uint64_t)s.kvh * deal.per_head);
     s.g = source_of(cum, A.G, local);
     const int begin_row = seg.off[s.g] * GQ;
     s.row_end = seg.off[s.g + 1] * GQ;
@@ -133,8 +130,8 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
     at += (uint64_t)(t1 - t0);
     s.r0 = begin_row + block * C::BM;
-    s.P = prompt_len(A, s.g, nullptr);
-    s.lo = first_position(A, s.P, least_of[s.g]);
+    s.P = src.len[s.g];
+    s.lo = first_position(A, s.P, src.least[s.g]);
     const int tile0 = (s.P + C::BN - 1) / C::BN - tiles;
     s.first = tile0 + t0;
     s.last = tile0 + t1;
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
           *reinterpret_cast<uint4*>(smem + (c >> 3) * C::BM * 128 + sw128_offset(row, c & 7)) = x;
         }
         if (r < s.row_end) {
-          const int len = response_len(A, b_of, nullptr);
+          const int len = src.len[A.G + b_of];
           if (len >= 0) lo = first_position(A, s.P, len);
         }
         fence_async();
@@ -492,7 +489,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
                      cudaStream_t st) {
   using C = PromptCfg<D, BITS>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
-  const int smem = C::RINGS + 1024 + (2 * a.G + 1) * (int)sizeof(uint32_t);
+  const int smem = C::RINGS + 1024 + (3 * a.G + a.B + 1) * (int)sizeof(uint32_t);
   const cudaError_t e =
       cudaFuncSetAttribute(prompt_kernel<D, BITS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
