@@ -821,6 +821,8 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   a.G = G;
   a.B = (int)B;
   a.Hq = Hq;
+  a.by_ps = FastDiv(cache->page_size);
+  a.by_heads = FastDiv(Hq / Hkv);
   a.window = window < 0 ? 0 : window;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16*>(out);

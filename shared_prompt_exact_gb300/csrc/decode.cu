@@ -116,8 +116,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   deal_sources<C::COLS, C::TILE, false>(A, seg, src, scratch);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= sources; i += blockDim.x) ws.cum[i] = cum[i];
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
   // neighbouring shares go to different SMs, so that a short batch spreads over all of them
   const uint32_t worker = (uint32_t)(warp * kBlocks + blockIdx.x);
@@ -128,7 +126,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   // what this lane copies: every LG-th chunk of sub-tile `mine`
   const int mine = lane / LG, li = lane % LG;
   const int copy_row = 16 * mine + (CPR <= LG ? li / CPR : 0), copy_col = CPR <= LG ? li % CPR : li;
-  const int step_places = TILE / A.kv.ps, step_slots = TILE % A.kv.ps;
+  const int step_places = A.by_ps(TILE), step_slots = TILE - step_places * A.kv.ps;
 
   while (at < stop) {
     // ---- the source, its rows and the tiles of it that are this warp's
@@ -142,6 +140,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     const int tiles = (int)((cum[s + 1] - cum[s]) / (uint32_t)blocks);
     const int block = (int)(local - cum[s]) / tiles, t0 = (int)(local - cum[s]) - block * tiles;
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
+    const int parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - worker) + 1;
     at += (uint64_t)(t1 - t0);
     const int r0 = row_begin + block * C::COLS;
     const int end = src.len[s];
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       const int r = r0 + 8 * (c >> 1) + 2 * t + (c & 1);
       lo[c] = 0x7fffffff;
       if (r < row_end) {
-        const int len = prompt ? src.len[A.G + r / GQ] : end;
+        const int len = prompt ? src.len[A.G + A.by_heads(r)] : end;
         if (len >= 0) {
           lo[c] = prompt ? first_position(A, end, len) : first_own(A, len);
           lo_min = min(lo_min, lo[c]);
@@ -171,14 +170,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     const int max_pages = prompt ? A.max_prompt_pages : A.max_pages;
     const int32_t* table = (prompt ? A.prompt_table : A.table) + (int64_t)(prompt ? s : b0) * max_pages;
     // this lane's sub-tile: its place in the table, its first slot in the page, and the page (loaded a tile ahead)
-    int token = first * TILE + 16 * mine, place = token / A.kv.ps, in_page = token - place * A.kv.ps;
+    int token = first * TILE + 16 * mine, place = A.by_ps(token), in_page = token - place * A.kv.ps;
     int page = first < last && token < end ? table[place] : -1;
     // ---- queries as B operands, in the order in which a lane meets the keys' values (the loads first: they
     // are on their way while the first keys are asked for)
     uint32_t q[NT][D / 16][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g, b = r / GQ;
+      const int r = r0 + 8 * nt + g, b = A.by_heads(r);
       const uint4* row = reinterpret_cast<const uint4*>(A.q + b * A.q_stride + (kvh * GQ + (r - b * GQ)) * D);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       uint32_t gone = 0;  // sub-tiles without a page: their keys do not count
       if (missing >> (tile & 31) & 1) {
         const int at_key = key0 + 16 * lane;
-        const bool bad = lane < KT && at_key < end && page_at(A.kv, table, max_pages, at_key / A.kv.ps, A.status) < 0;
+        const bool bad = lane < KT && at_key < end && page_at(A.kv, table, max_pages, A.by_ps(at_key), A.status) < 0;
         gone = __ballot_sync(0xffffffffu, bad);
         edge = true;
       }
@@ -485,11 +484,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int col = 8 * nt + 2 * t + c, r = r0 + col;
         if (r >= row_end) continue;
-        const int b = r / GQ;
+        const int b = A.by_heads(r);
         const size_t rows = (size_t)A.B * A.Hq;
         const size_t to = t0 == 0 ? (prompt ? rows : 0) + (size_t)b * A.Hq + kvh * GQ + (r - b * GQ)
                                   : own_slots(A.B, A.Hq) + (size_t)worker * C::COLS + col;
-        if (g == 0) ws.ml[to] = make_float2(m[nt][c], sum);
+        if (g == 0) ws.partial[to] = Partial{m[nt][c], sum, worker, parts};
         float* out = ws.o + to * D;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
@@ -511,51 +510,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
 }
 
 // ---------------------------------------------------------------- the join
-// A source's partial results for one row: the first in the row's own slot, the others in those of the workers behind.
-struct Parts {
-  size_t own, carried;  // slots of the first and (n > 1) of the one before the second
-  int n, stride;
-};
-__device__ __forceinline__ Parts parts_of(const uint32_t* cum, int n_sources, int Hkv, int workers, int s, int rows, int row,
-                                          int kvh, size_t own, size_t carried, int cols) {
-  Parts p{own, 0, 0, cols};
-  const int blocks = (rows + cols - 1) / cols;
-  const uint32_t tiles = (cum[s + 1] - cum[s]) / (uint32_t)blocks;
-  if (!tiles) return p;
-  const Deal d = make_deal(cum[n_sources], Hkv, workers);
-  const uint64_t from = (uint64_t)kvh * d.per_head + cum[s] + (uint64_t)(row / cols) * tiles;
-  const uint32_t first = worker_of(d, from);
-  p.n = (int)(worker_of(d, from + tiles - 1) - first) + 1;
-  p.carried = carried + (size_t)first * cols + row % cols;
-  return p;
-}
-
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 constexpr int kJoinThreads = kJoinWarps * 32;
-
-// The partial results of one row: n of them, and where the i-th lies.
-struct RowParts {
-  Parts p[2];
-  int n;
-  template <int CAP>
-  __device__ __forceinline__ RowParts(const DecodeArgs& A, const SegTable<CAP>& seg, const Workspace& ws, int warps, int cols,
-                                      int b, int h) {
-    const int GQ = A.Hq / A.kv.Hkv, kvh = h / GQ, g = seg_of(seg, b), sources = A.G + A.B;
-    const int rows = (seg.off[g + 1] - seg.off[g]) * GQ, in_prompt = (b - seg.off[g]) * GQ + h % GQ;
-    const size_t row = (size_t)b * A.Hq + h, own = own_slots(A.B, A.Hq);
-    p[0] = big_group(A, seg.off[g + 1] - seg.off[g])
-               ? parts_of(ws.big_cum, A.G, A.kv.Hkv, kBlocks, g, rows, in_prompt, kvh, own / 2 + row, own + kWarpSlots, 128)
-               : parts_of(ws.cum, sources, A.kv.Hkv, warps, g, rows, in_prompt, kvh, own / 2 + row, own, cols);
-    p[1] = parts_of(ws.cum, sources, A.kv.Hkv, warps, A.G + b, GQ, h % GQ, kvh, row, own, cols);
-    n = p[0].n + p[1].n;
-  }
-  __device__ __forceinline__ size_t place(int i) const {
-    const bool second = i >= p[0].n;
-    const Parts& q = second ? p[1] : p[0];
-    const int k = second ? i - p[0].n : i;
-    return k == 0 ? q.own : q.carried + (size_t)k * q.stride;
-  }
-};
 
 __device__ __forceinline__ float lse_of(float top, float total) {
   return total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
@@ -575,54 +531,83 @@ __device__ __forceinline__ float warp_sum(float x) {
 // kernel may start before the partial results are complete, so nothing that reads them is __restrict__.
 template <int D, int CAP>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const DecodeArgs A, int share, int cols, int warps, const __grid_constant__ SegTable<CAP> seg) {
-  constexpr int E = D / 32;
+    join_kernel(const DecodeArgs A, int share, int cols, const __grid_constant__ SegTable<CAP> seg) {
+  constexpr int E = D / 64, BATCH = D == 512 ? 2 : 8;  // float2s of a lane; partial results on their way at once
   __shared__ float2 sums[kJoinWarps][D / 2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % share;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & (share - 1);
   const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
   const bool live = row < (int64_t)A.B * A.Hq;
   const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
-  const bool ended = !live || A.lens[b] < 0;
+  const int GQ = A.Hq / A.kv.Hkv, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  // which sources the row sees, as the kernels that left the partial results decided
+  const int len = response_len(A, b, nullptr), P = prompt_len(A, g, nullptr);
+  const bool sees_own = live && len > 0, sees_prompt = live && len >= 0 && first_position(A, P, len) < P;
+  const bool big = big_group(A, seg.off[g + 1] - seg.off[g]);
+  const size_t own = own_slots(A.B, A.Hq);
   cudaGridDependencySynchronize();
+  const Partial none{kLowest, 0.f, 0, 0};
+  const Partial p0 = sees_prompt ? ws.partial[own / 2 + row] : none, p1 = sees_own ? ws.partial[row] : none;
+  const int n = p0.parts + p1.parts, in_group = (b - seg.off[g]) * GQ + j;
+  // slots of the workers behind a source's first one
+  const size_t behind0 = big ? own + kWarpSlots + (size_t)p0.worker * 128 + (in_group & 127)
+                             : own + (size_t)p0.worker * cols + (in_group & (cols - 1));
+  const size_t behind1 = own + (size_t)p1.worker * cols + (j & (cols - 1));
+  auto place = [&](int i) {
+    const bool second = i >= p0.parts;
+    const int k = second ? i - p0.parts : i;
+    if (k == 0) return second ? (size_t)row : own / 2 + (size_t)row;
+    return (second ? behind1 : behind0) + (size_t)(k * (second || !big ? cols : 128));
+  };
+  // each lane's maximum and sum in one pass, then the warp's
   float top = kLowest, total = 0.f;
-  float2 acc[E / 2];
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) acc[e] = make_float2(0.f, 0.f);
-  if (!ended) {
-    const RowParts parts(A, seg, ws, warps, cols, b, h);
-    for (int i = lane; i < parts.n; i += 32) top = fmaxf(top, ws.ml[parts.place(i)].x);
-    top = warp_max(top);
-    for (int i = lane; i < parts.n; i += 32) {
-      const float2 ml = ws.ml[parts.place(i)];
-      total = fmaf(ml.y, ex2_approx(ml.x - top), total);
-    }
-    total = warp_sum(total);
 #pragma unroll 4
-    for (int i = part; i < parts.n; i += share) {
-      const size_t at = parts.place(i);
-      const float f = ex2_approx(ws.ml[at].x - top);
-      const float2* v = reinterpret_cast<const float2*>(ws.o + at * D);
+  for (int i = lane; i < n; i += 32) {
+    const Partial x = ws.partial[place(i)];
+    const float m = fmaxf(top, x.m);
+    total = fmaf(total, ex2_approx(top - m), x.l * ex2_approx(x.m - m));
+    top = m;
+  }
+  const float most = warp_max(top);
+  total = warp_sum(total * ex2_approx(top - most));
+  float2 acc[E];
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) acc[e] = ffma2(v[lane + 32 * e], make_float2(f, f), acc[e]);
+  for (int e = 0; e < E; ++e) acc[e] = make_float2(0.f, 0.f);
+  for (int i0 = part; i0 < n; i0 += BATCH * share) {
+    float f[BATCH];
+    float2 v[BATCH][E];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * share;
+      const size_t at = place(i < n ? i : i0);
+      f[k] = i < n ? ws.partial[at].m : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = reinterpret_cast<const float2*>(ws.o + at * D)[lane + 32 * e];
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float w = ex2_approx(f[k] - most);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = ffma2(v[k][e], make_float2(w, w), acc[e]);
     }
   }
   if (share > 1) {
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) sums[warp][lane + 32 * e] = acc[e];
+    for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = acc[e];
     __syncthreads();
     if (part) return;
+#pragma unroll 4
     for (int w = 1; w < share; ++w)
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) acc[e] = fadd2(acc[e], sums[warp + w][lane + 32 * e]);
+      for (int e = 0; e < E; ++e) acc[e] = fadd2(acc[e], sums[warp + w][lane + 32 * e]);
   }
   if (!live) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) out[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
+  for (int e = 0; e < E; ++e) out[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
   if (lane == 0 && A.lse)
-    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (most + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 template <int D, int BITS, int NT, int CAP>
@@ -654,9 +639,9 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   // as many warps to a row as it can have partial results to spare, on average
   const int64_t rows = (int64_t)a.B * a.Hq;
   const int64_t most = 2 + ((int64_t)kBlocks * warps * (a.Hq / a.kv.Hkv) + (a.big ? kBlocks * 128 : 0)) / rows;
-  const int share = most > 24 ? 8 : most > 12 ? 4 : most > 6 ? 2 : 1, per = kJoinWarps / share;
+  const int share = most > 48 ? 16 : most > 24 ? 8 : most > 12 ? 4 : most > 6 ? 2 : 1, per = kJoinWarps / share;
   return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), st, a, share,
-                       (int)C::COLS, kBlocks * warps, seg);
+                       (int)C::COLS, seg);
 }
 
 template <int D, int BITS>

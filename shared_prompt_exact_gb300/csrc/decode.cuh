@@ -60,28 +60,28 @@ __device__ __forceinline__ int tiles_of(int lo, int end) {
   return lo < end ? (end + TILE - 1) / TILE - lo / TILE : 0;
 }
 
+// A partial result of one row: its maximum (base 2) and sum, and at a source's first tile who goes on with
+// the source: `parts` partial results, of this worker and of those behind it.
+struct alignas(16) Partial {
+  float m, l;
+  uint32_t worker;
+  int parts;
+};
 struct Workspace {
-  uint32_t* cum;      // [G + B + 1] tiles before each source, of one kv-head
-  uint32_t* big_cum;  // [G + 1] the same of prompt.cu's prompts
-  float2* ml;         // [slots] maximum (base 2) and sum
-  float* o;           // [slots][D]
+  Partial* partial;  // [slots]
+  float* o;          // [slots][D] weighted values
 };
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-// Slots of partial results: the rows' own ones of the responses and of the prompts; then those for what a worker
-// goes on with that another one began: 16 for a warp, 128 for a block of prompt.cu.
+// Slots: the rows' own ones of the responses and of the prompts, for a source's first tiles; then those for what a
+// worker goes on with that another one began: 16 for a warp, 128 for a block of prompt.cu.
 constexpr size_t kWarpSlots = (size_t)kBlocks * 16 * 16, kBlockSlots = (size_t)kBlocks * 128;
 __host__ __device__ inline size_t own_slots(int B, int Hq) { return 2 * (size_t)B * Hq; }
 __host__ __device__ inline size_t slots_of(int B, int Hq) { return own_slots(B, Hq) + kWarpSlots + kBlockSlots; }
 __host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
   uint8_t* at = static_cast<uint8_t*>(p);
   Workspace w;
-  w.cum = reinterpret_cast<uint32_t*>(at);
-  at += align256(sizeof(uint32_t) * (kMaxSegs + kMaxResponses + 1));
-  w.big_cum = reinterpret_cast<uint32_t*>(at);
-  at += align256(sizeof(uint32_t) * (kBigGroups + 1));
-  w.ml = reinterpret_cast<float2*>(at);
-  at += align256(sizeof(float2) * slots_of(B, Hq));
-  w.o = reinterpret_cast<float*>(at);
+  w.partial = reinterpret_cast<Partial*>(at);
+  w.o = reinterpret_cast<float*>(at + align256(sizeof(Partial) * slots_of(B, Hq)));
   return w;
 }
 
@@ -107,14 +107,14 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
                                              uint32_t* scratch) {
   const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
   uint32_t* cum = src.cum;
+  for (int b = tid; b < A.B; b += THREADS) src.len[G + b] = response_len(A, b, A.status);
   for (int g = tid; g < G; g += THREADS) {
     cum[1 + g] = 0x7fffffffu;
     src.len[g] = prompt_len(A, g, A.status);
   }
   __syncthreads();
   for (int b = tid; b < A.B; b += THREADS) {
-    const int len = response_len(A, b, A.status);
-    src.len[G + b] = len;
+    const int len = src.len[G + b];
     if (len >= 0) atomicMin(&cum[1 + seg_of(seg, b)], (uint32_t)len);
     if (!BIG) cum[1 + G + b] = (uint32_t)tiles_of<TILE>(first_own(A, len), len) * (uint32_t)((GQ + COLS - 1) / COLS);
   }

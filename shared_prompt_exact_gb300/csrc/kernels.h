@@ -253,6 +253,21 @@ cudaError_t launch_read(int D, const ReadArgs& a, int S, const int32_t* off, cud
 
 // ---- attention of one token per response over the cache (decode.cu)
 constexpr int kMaxResponses = 8192;
+
+// Quotients of 0 <= x < 2^31 by a d that the host knows: with 2^s the first power of two from d on,
+// x / d = (x + floor(x m / 2^32)) / 2^s for m = floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv(int by = 1) : d((uint32_t)by), mul(0), shift(0) {
+    while ((1u << shift) < d) ++shift;
+    mul = (uint32_t)((((uint64_t)1 << 32) * ((((uint64_t)1) << shift) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int x) const {
+    return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+  }
+#endif
+};
 struct DecodeArgs {
   const __nv_bfloat16* q;  // head h of response b at b * q_stride + h * D
   int64_t q_stride;        // elements
@@ -266,6 +281,7 @@ struct DecodeArgs {
   float* lse;        // may be null
   void* workspace;
   uint32_t* status;
+  FastDiv by_ps, by_heads;  // by the page size and by Hq / Hkv
   bool big;          // some prompts go to launch_prompt: of groups with kBigRows rows (responses x Hq / Hkv) or more
 };
 // A group's prompt is worth the tensor cores' large tiles from here on.

@@ -8,8 +8,8 @@
 //
 // Warps:
 //   loaders of keys, loaders of values, each with a ring of their own.  bf16: one warp each, 8 lanes of which load a
-//     tile's 16-token pieces by TMA, each from its page.  4 bits: two warps each; a thread decodes two
-//     rows (codes loaded a tile ahead) and writes them as bf16 in the swizzled layout that TMA would leave.  The decoded
+//     tile's 16-token pieces by TMA, each from its page.  4 bits: four warps each; a thread decodes
+//     a row (its codes loaded a tile ahead) and writes them as bf16 in the swizzled layout that TMA would leave.  The decoded
 //     order within 8 values is 0, 4, 1, 5, ... (decode2); the queries are written in the same order, and the
 //     output's columns are put right at the end.
 //   an issuer of S = Q K^T, an issuer of O += P V, eight softmax warps: as in fwd.cu.
@@ -34,10 +34,10 @@ struct PromptCfg {
   static constexpr int QCH = D / 64;                    // 64-column chunks of a row
   static constexpr int TILE_BYTES = QCH * BN * 128;
   static constexpr int NK = 3, NV = 2;                  // tiles in the rings of keys and of values
-  static constexpr int LW = BITS == 16 ? 1 : 2;         // loader warps of each
-  static constexpr int V_WARP = LW, SOFTMAX = 4;        // warps 4 .. 11: softmax
-  static constexpr int S_WARP = BITS == 16 ? 2 : 12, PV_WARP = S_WARP + 1;
-  static constexpr int THREADS = BITS == 16 ? 384 : 448;
+  static constexpr int LW = BITS == 16 ? 1 : 4;         // loader warps of each
+  static constexpr int V_WARP = LW, SOFTMAX = BITS == 16 ? 4 : 8;  // the first of eight softmax warps
+  static constexpr int S_WARP = BITS == 16 ? 2 : 16, PV_WARP = S_WARP + 1;
+  static constexpr int THREADS = BITS == 16 ? 384 : 640;
   static constexpr int OFF_K = TILE_BYTES, OFF_V = OFF_K + NK * TILE_BYTES, RINGS = OFF_V + NV * TILE_BYTES;
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
@@ -45,14 +45,23 @@ struct PromptCfg {
 
 struct PromptCtl {
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t q_full, s_full[2], p_full[2], pv_done[2], pv_issued[2], pair_done[4], drain, drain2;
+  uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], pv_issued[2], pair_done[4], drain, drain2;
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t scratch[16];
+  uint32_t scratch[20];
   float half_m[256], half_l[256];
 };
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // A warp's wait; its lanes go on, or give up, together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const FailState& fs) {
@@ -62,7 +71,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 // One prompt, kv-head and block of 128 rows: the tiles of it that are this block's.
 struct Segment {
   int g, kvh, r0, row_end, P, lo, first, last;
-  bool opens;  // its first tile is here
+  int parts;   // blocks that have a part of it, this one and those behind, if its first tile is here; else 0
 };
 
 template <int D, int BITS, int CAP>
@@ -77,7 +86,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   const Sources src{reinterpret_cast<uint32_t*>(smem + C::RINGS), reinterpret_cast<int*>(smem + C::RINGS) + 2 * A.G + 1,
                     reinterpret_cast<int*>(smem + C::RINGS) + A.G + 1};
   const uint32_t* cum = src.cum;
-  const uint32_t warp = warp_id(), lane = lane_id();
+  const uint32_t warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int GQ = A.Hq / A.kv.Hkv, ps = A.kv.ps;
   FailState fs{&ctl.abort_flag, A.status, kLaunchWaitLimitNs};
 
@@ -92,6 +101,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       mbar_init(&ctl.v_empty[i], 1);
     }
     mbar_init(&ctl.q_full, 256);
+    mbar_init(&ctl.q_free, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i], 8);
@@ -113,8 +123,6 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
   const uint32_t tmem = ctl.tmem_base;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= A.G; i += C::THREADS) ws.big_cum[i] = cum[i];
   const Deal deal = make_deal(cum[A.G], A.kv.Hkv, kBlocks);
   const uint64_t begin = first_tile(deal, blockIdx.x), stop = first_tile(deal, blockIdx.x + 1);
   auto next_segment = [&](uint64_t& at) {
@@ -128,6 +136,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     const int tiles = (int)((cum[s.g + 1] - cum[s.g]) / (uint32_t)blocks);
     const int block = (int)(local - cum[s.g]) / tiles, t0 = (int)(local - cum[s.g]) - block * tiles;
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
+    s.parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - blockIdx.x) + 1;
     at += (uint64_t)(t1 - t0);
     s.r0 = begin_row + block * C::BM;
     s.P = src.len[s.g];
@@ -135,17 +144,19 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     const int tile0 = (s.P + C::BN - 1) / C::BN - tiles;
     s.first = tile0 + t0;
     s.last = tile0 + t1;
-    s.opens = t0 == 0;
     return s;
   };
   // page of a token of the prompt, or -1
   auto page_of = [&](const Segment& s, int token) {
-    const int page = token < s.P ? A.prompt_table[(int64_t)s.g * A.max_prompt_pages + token / ps] : -1;
+    const int page = token < s.P ? A.prompt_table[(int64_t)s.g * A.max_prompt_pages + A.by_ps(token)] : -1;
     return (uint32_t)page < (uint32_t)A.kv.pages ? page : -1;
   };
 
+  // 4 bits: 20 warps start with 96 registers a thread; the softmax warps take over what the others leave:
+  // 2 x 72 + 2 x 144 + 48 for the five warpgroups, 5 x 96 in all
   if (warp < 2 * C::LW) {
     // ------------------------------------------------------------ loaders
+    if (BITS == 4) registers_down<72>();
     const bool values = warp >= C::V_WARP;
     const int slots = values ? C::NV : C::NK;
     uint64_t* full = values ? ctl.v_full : ctl.k_full;
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         for (int tile = s.first; tile < s.last; ++tile) {
           const bool have = lane < 8 && page >= 0;
           const bool whole = have && (!values || (token >= s.lo && token + 16 <= s.P));
-          const int row = have ? (int)cache_row(A.kv, page, s.kvh, token % ps) : 0;
+          const int row = have ? (int)cache_row(A.kv, page, s.kvh, token - A.by_ps(token) * ps) : 0;
           token += C::BN;
           const int next = tile + 1 < s.last ? page_of(s, token) : -1;
           if (!(ok = warp_wait(&empty[slot], phase, fs))) break;
@@ -205,61 +216,63 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
           mbar_wait_drain(&full[(filled - back) % slots], ((filled - back) / slots) & 1, kWaitLimitNs);
     } else {
       constexpr int U = D / 32;  // 16-byte vectors of a row's codes: one for each group of 32 values
-      const int mine = (int)(warp - (values ? C::V_WARP : 0)) * 32 + (int)lane;  // rows mine and mine + 64 of a tile
+      const int mine = (int)(warp - (values ? C::V_WARP : 0)) * 32 + (int)lane;  // this thread's row of a tile
       const uint8_t* pool = static_cast<const uint8_t*>(values ? A.kv.v : A.kv.k);
       const __nv_bfloat16* scales = values ? A.kv.vs : A.kv.ks;
-      uint4 codes[2][U];
-      __nv_bfloat162 sc[2][U / 2];
+      uint4 codes[U];
+      __nv_bfloat162 sc[U / 2];
+      int page = -1;  // of the row in the tile after the one in `codes`
+      auto find = [&](const Segment& s, int tile) {
+        const int token = tile * C::BN + mine;
+        page = tile < s.last && token >= s.lo ? page_of(s, token) : -1;
+      };
       auto load = [&](const Segment& s, int tile) {
+        const int token = tile * C::BN + mine;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int token = tile * C::BN + mine + 64 * h;
-          const int page = token >= s.lo ? page_of(s, token) : -1;
+        for (int u = 0; u < U; ++u) codes[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int u = 0; u < U; ++u) codes[h][u] = make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U / 2; ++u) sc[u] = __float2bfloat162_rn(0.f);
+        if (page >= 0) {
+          const int64_t row = cache_row(A.kv, page, s.kvh, token - A.by_ps(token) * ps);
+          const uint4* from = reinterpret_cast<const uint4*>(pool + row * (D / 2));
+          const __nv_bfloat162* sf = reinterpret_cast<const __nv_bfloat162*>(scales + row * U);
 #pragma unroll
-          for (int u = 0; u < U / 2; ++u) sc[h][u] = __float2bfloat162_rn(0.f);
-          if (page >= 0) {
-            const int64_t row = cache_row(A.kv, page, s.kvh, token % ps);
-            const uint4* from = reinterpret_cast<const uint4*>(pool + row * (D / 2));
-            const __nv_bfloat162* sf = reinterpret_cast<const __nv_bfloat162*>(scales + row * U);
+          for (int u = 0; u < U; ++u) codes[u] = from[u];
 #pragma unroll
-            for (int u = 0; u < U; ++u) codes[h][u] = from[u];
-#pragma unroll
-            for (int u = 0; u < U / 2; ++u) sc[h][u] = sf[u];
-          }
+          for (int u = 0; u < U / 2; ++u) sc[u] = sf[u];
         }
       };
       for (uint64_t at = begin; at < stop && ok;) {
         const Segment s = next_segment(at);
+        find(s, s.first);
         load(s, s.first);
+        find(s, s.first + 1);
         for (int tile = s.first; tile < s.last; ++tile) {
           if (!(ok = warp_wait(&empty[slot], phase, fs))) break;
           uint8_t* dst = ring + slot * C::TILE_BYTES;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int u = 0; u < U; ++u) {
+            const __nv_bfloat162 s2 = u & 1 ? __high2bfloat162(sc[u / 2]) : __low2bfloat162(sc[u / 2]);
+            const __nv_bfloat162 o2 = __hmul2(s2, __float2bfloat162_rn(-24.f));
+            const uint32_t w[4] = {codes[u].x, codes[u].y, codes[u].z, codes[u].w};
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const __nv_bfloat162 s2 = u & 1 ? __high2bfloat162(sc[h][u / 2]) : __low2bfloat162(sc[h][u / 2]);
-              const __nv_bfloat162 o2 = __hmul2(s2, __float2bfloat162_rn(-24.f));
-              const uint32_t w[4] = {codes[h][u].x, codes[h][u].y, codes[h][u].z, codes[h][u].w};
+            for (int i = 0; i < 4; ++i) {
+              uint32_t p[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 x;
-                uint32_t* p = &x.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 d = decode2(w[i] >> (4 * e), s2, o2);
-                  p[e] = *reinterpret_cast<const uint32_t*>(&d);
-                }
-                const int c = 4 * u + i;  // 16-byte chunk of the row
-                *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine + 64 * h, c & 7)) = x;
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 d = decode2(w[i] >> (4 * e), s2, o2);
+                p[e] = *reinterpret_cast<const uint32_t*>(&d);
               }
+              const int c = 4 * u + i;  // 16-byte chunk of the row
+              *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine, c & 7)) =
+                  make_uint4(p[0], p[1], p[2], p[3]);
             }
+          }
           fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]);
-          if (tile + 1 < s.last) load(s, tile + 1);
+          load(s, tile + 1);  // nothing behind the last one
+          find(s, tile + 2);
           if (++slot == slots) {
             slot = 0;
             phase ^= 1;
@@ -267,79 +280,9 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         }
       }
     }
-  } else if (warp == C::S_WARP) {
-    // ------------------------------------------------------------ S issuer
-    constexpr uint32_t idS = idesc_bf16(128, C::BN, 0, 0);
-    const uint64_t qdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint32_t ring = smem_u32(smem + C::OFF_K);
-    bool ok = true;
-    int jj = 0, n_seg = 0;
-    for (uint64_t at = begin; at < stop && ok; ++n_seg) {
-      const Segment s = next_segment(at);
-      if (!(ok = warp_wait(&ctl.q_full, n_seg & 1, fs))) break;
-      for (int tile = s.first; tile < s.last; ++tile, ++jj) {
-        const uint32_t b = jj & 1, tS = tmem + C::TM_S + b * C::BN;
-        const int slot = jj % C::NK;
-        if (jj >= 2 && !(ok = warp_wait(&ctl.pv_issued[b], ((jj >> 1) - 1) & 1, fs))) break;
-        if (!(ok = warp_wait(&ctl.k_full[slot], (jj / C::NK) & 1, fs))) break;
-        tc_fence_after();
-        const uint64_t kdesc = sdesc_sw128(ring + slot * C::TILE_BYTES, 16, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int c = 0; c < QCH; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ss(tS, sdesc_add(qdesc, c * C::BM * 128 + k * 32), sdesc_add(kdesc, c * C::BN * 128 + k * 32), idS,
-                          (c | k) != 0);
-          mma_commit(&ctl.k_empty[slot]);
-          mma_commit(&ctl.s_full[b]);
-        }
-        __syncwarp();
-      }
-    }
-    if (begin < stop) {  // every MMA issued above ends before TMEM is released
-      if (elect_one()) mma_commit(&ctl.drain);
-      __syncwarp();
-      mbar_wait_drain(&ctl.drain, 0, kWaitLimitNs);
-    }
-  } else if (warp == C::PV_WARP) {
-    // ------------------------------------------------------------ PV issuer
-    constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
-    const uint32_t ring = smem_u32(smem + C::OFF_V);
-    bool ok = true;
-    int jj = 0;
-    for (uint64_t at = begin; at < stop && ok;) {
-      const Segment s = next_segment(at);
-      for (int tile = s.first; tile < s.last; ++tile, ++jj) {
-        const uint32_t b = jj & 1, tP = tmem + C::TM_S + b * C::BN, acc0 = tile > s.first ? 1u : 0u;
-        const int slot = jj % C::NV;
-        if (!(ok = warp_wait(&ctl.p_full[b], (jj >> 1) & 1, fs))) break;
-        if (!(ok = warp_wait(&ctl.v_full[slot], (jj / C::NV) & 1, fs))) break;
-        tc_fence_after();
-        const uint64_t vdesc = sdesc_sw128(ring + slot * C::TILE_BYTES, C::BN * 128, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < C::HC / 16; ++k)
-              mma_bf16_ts(tmem + C::TM_O + h * D, tP + h * C::HC + k * 8, sdesc_add(vdesc, (h * C::HC + k * 16) * 128), idO,
-                          k > 0 ? 1u : acc0);
-          mma_commit(&ctl.v_empty[slot]);
-          mma_commit(&ctl.pv_done[b]);
-        }
-        __syncwarp();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.pv_issued[b]);
-      }
-    }
-    if (begin < stop) {
-      if (elect_one()) mma_commit(&ctl.drain2);
-      __syncwarp();
-      mbar_wait_drain(&ctl.drain2, 0, kWaitLimitNs);
-    }
   } else if (warp >= C::SOFTMAX && warp < C::SOFTMAX + 8) {
     // ------------------------------------------------------------ softmax
+    if (BITS == 4) registers_up<144>();
     const uint32_t wq = warp & 3;
     const int half = (int)(warp - C::SOFTMAX) >> 2, row = (int)(wq * 32 + lane);
     const uint32_t tl = tmem + ((wq * 32) << 16), tO = tl + C::TM_O + half * D;
@@ -349,8 +292,10 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     for (uint64_t at = begin; at < stop && ok; ++n_seg) {
       const Segment s = next_segment(at);
       // ---- this thread's half of its query; every product with the previous ones has been waited for
-      const int r = s.r0 + row, b_of = r / GQ, head = s.kvh * GQ + (r - b_of * GQ);
+      const int r = s.r0 + row, b_of = A.by_heads(r), head = s.kvh * GQ + (r - b_of * GQ);
       int lo = 0x7fffffff;  // first token that the row sees
+      // the queries go where other warps may still pass on their partial results
+      if (n_seg > 0 && !(ok = warp_wait(&ctl.q_free, (n_seg - 1) & 1, fs))) break;
       {
         const uint4* q = reinterpret_cast<const uint4*>(A.q + b_of * A.q_stride + (int64_t)head * D) + half * (D / 16);
 #pragma unroll
@@ -453,28 +398,119 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       const float mtot = fmaxf(m0, m1), mref = mtot == -INFINITY ? kLowest : mtot;
       const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mref), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mref);
       const size_t own = own_slots(A.B, A.Hq);
-      const size_t to = s.opens ? own / 2 + (size_t)b_of * A.Hq + head : own + kWarpSlots + (size_t)blockIdx.x * 128 + row;
+      const size_t to = s.parts ? own / 2 + (size_t)b_of * A.Hq + head : own + kWarpSlots + (size_t)blockIdx.x * 128 + row;
       constexpr int OC = D / 2;  // output columns of this thread
-      float* out = ws.o + to * D + half * OC;
+      // 16 columns at a time through 2 KB of the queries' place (their products are done), so that 4 lanes write
+      // 64 bytes of one row; the rows' slots are consecutive but where a response's other heads lie between
+      float* stage = reinterpret_cast<float*>(smem) + (warp - C::SOFTMAX) * 512;
+      const uint32_t slot_lo = (uint32_t)to, slot_hi = (uint32_t)(to >> 32), live = __ballot_sync(0xffffffffu, r < s.row_end);
 #pragma unroll
       for (int c4 = 0; c4 < OC / 32; ++c4) {
         uint32_t u0[32], u1[32];
         tmem_ld32(tl + C::TM_O + half * OC + c4 * 32, u0);
         tmem_ld32(tl + C::TM_O + D + half * OC + c4 * 32, u1);
         tmem_ld_wait();
-        if (r < s.row_end) {
-          float y[32];
+        float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = BITS == 4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;  // column i is value d
-            y[d] = fmaf(__uint_as_float(u1[i]), f1, __uint_as_float(u0[i]) * f0);
+        for (int i = 0; i < 32; ++i) {
+          const int d = BITS == 4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;  // column i is value d
+          y[d] = fmaf(__uint_as_float(u1[i]), f1, __uint_as_float(u0[i]) * f0);
+        }
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // four 16-byte vectors a row, at places that differ from row to row
+            *reinterpret_cast<float4*>(stage + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4) =
+                make_float4(y[16 * c2 + 4 * i], y[16 * c2 + 4 * i + 1], y[16 * c2 + 4 * i + 2], y[16 * c2 + 4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int from = 8 * k + (int)(lane >> 2), i = lane & 3;
+            const float4 x = *reinterpret_cast<const float4*>(stage + from * 16 + ((i ^ (from >> 1)) & 3) * 4);
+            const size_t at_slot = (size_t)__shfl_sync(0xffffffffu, slot_lo, from) |
+                                   (size_t)__shfl_sync(0xffffffffu, slot_hi, from) << 32;
+            if (live >> from & 1)
+              *reinterpret_cast<float4*>(ws.o + at_slot * D + half * OC + c4 * 32 + c2 * 16 + i * 4) = x;
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(out + c4 * 32 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          __syncwarp();
         }
       }
-      if (r < s.row_end && half == 0) ws.ml[to] = make_float2(mref, l0 * f0 + l1 * f1);
+      if (lane == 0) mbar_arrive(&ctl.q_free);
+      if (r < s.row_end && half == 0) ws.partial[to] = Partial{mref, l0 * f0 + l1 * f1, blockIdx.x, s.parts};
+    }
+  } else {
+    if (BITS == 4) registers_down<48>();  // the whole warpgroup, idle warps too
+    if (warp == C::S_WARP) {
+      // ------------------------------------------------------------ S issuer
+      constexpr uint32_t idS = idesc_bf16(128, C::BN, 0, 0);
+      const uint64_t qdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint32_t ring = smem_u32(smem + C::OFF_K);
+      bool ok = true;
+      int jj = 0, n_seg = 0;
+      for (uint64_t at = begin; at < stop && ok; ++n_seg) {
+        const Segment s = next_segment(at);
+        if (!(ok = warp_wait(&ctl.q_full, n_seg & 1, fs))) break;
+        for (int tile = s.first; tile < s.last; ++tile, ++jj) {
+          const uint32_t b = jj & 1, tS = tmem + C::TM_S + b * C::BN;
+          const int slot = jj % C::NK;
+          if (jj >= 2 && !(ok = warp_wait(&ctl.pv_issued[b], ((jj >> 1) - 1) & 1, fs))) break;
+          if (!(ok = warp_wait(&ctl.k_full[slot], (jj / C::NK) & 1, fs))) break;
+          tc_fence_after();
+          const uint64_t kdesc = sdesc_sw128(ring + slot * C::TILE_BYTES, 16, 1024);
+          if (elect_one()) {
+  #pragma unroll
+            for (int c = 0; c < QCH; ++c)
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(tS, sdesc_add(qdesc, c * C::BM * 128 + k * 32), sdesc_add(kdesc, c * C::BN * 128 + k * 32), idS,
+                            (c | k) != 0);
+            mma_commit(&ctl.k_empty[slot]);
+            mma_commit(&ctl.s_full[b]);
+          }
+          __syncwarp();
+        }
+      }
+      if (begin < stop) {  // every MMA issued above ends before TMEM is released
+        if (elect_one()) mma_commit(&ctl.drain);
+        __syncwarp();
+        mbar_wait_drain(&ctl.drain, 0, kWaitLimitNs);
+      }
+    } else if (warp == C::PV_WARP) {
+      // ------------------------------------------------------------ PV issuer
+      constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+      const uint32_t ring = smem_u32(smem + C::OFF_V);
+      bool ok = true;
+      int jj = 0;
+      for (uint64_t at = begin; at < stop && ok;) {
+        const Segment s = next_segment(at);
+        for (int tile = s.first; tile < s.last; ++tile, ++jj) {
+          const uint32_t b = jj & 1, tP = tmem + C::TM_S + b * C::BN, acc0 = tile > s.first ? 1u : 0u;
+          const int slot = jj % C::NV;
+          if (!(ok = warp_wait(&ctl.p_full[b], (jj >> 1) & 1, fs))) break;
+          if (!(ok = warp_wait(&ctl.v_full[slot], (jj / C::NV) & 1, fs))) break;
+          tc_fence_after();
+          const uint64_t vdesc = sdesc_sw128(ring + slot * C::TILE_BYTES, C::BN * 128, 1024);
+          if (elect_one()) {
+  #pragma unroll
+            for (int h = 0; h < 2; ++h)
+  #pragma unroll
+              for (int k = 0; k < C::HC / 16; ++k)
+                mma_bf16_ts(tmem + C::TM_O + h * D, tP + h * C::HC + k * 8, sdesc_add(vdesc, (h * C::HC + k * 16) * 128), idO,
+                            k > 0 ? 1u : acc0);
+            mma_commit(&ctl.v_empty[slot]);
+            mma_commit(&ctl.pv_done[b]);
+          }
+          __syncwarp();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.pv_issued[b]);
+        }
+      }
+      if (begin < stop) {
+        if (elect_one()) mma_commit(&ctl.drain2);
+        __syncwarp();
+        mbar_wait_drain(&ctl.drain2, 0, kWaitLimitNs);
+      }
     }
   }
 
