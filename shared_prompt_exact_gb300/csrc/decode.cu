@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const Sources src{reinterpret_cast<uint32_t*>(smem + warps * C::RING),
                     reinterpret_cast<int*>(smem + warps * C::RING) + A.G + A.B + 1, nullptr};
   const uint32_t* cum = src.cum;
-  __shared__ uint32_t scratch[C::WARPS];
+  __shared__ uint32_t scratch[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     const int b0 = prompt ? seg.off[s] : s - A.G;
     const int row_begin = b0 * GQ, row_end = (prompt ? seg.off[s + 1] : b0 + 1) * GQ;
     const int blocks = (row_end - row_begin + C::COLS - 1) / C::COLS;
-    const int tiles = (int)((cum[s + 1] - cum[s]) / (uint32_t)blocks);
-    const int block = (int)(local - cum[s]) / tiles, t0 = (int)(local - cum[s]) - block * tiles;
+    const int tiles = (int)divide(cum[s + 1] - cum[s], (uint32_t)blocks);
+    const int block = (int)divide(local - cum[s], (uint32_t)tiles), t0 = (int)(local - cum[s]) - block * tiles;
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
     const int parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - worker) + 1;
     at += (uint64_t)(t1 - t0);
@@ -579,10 +579,15 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int i = i0 + k * share;
-      const size_t at = place(i < n ? i : i0);
-      f[k] = i < n ? ws.partial[at].m : -INFINITY;
+      f[k] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = reinterpret_cast<const float2*>(ws.o + at * D)[lane + 32 * e];
+      for (int e = 0; e < E; ++e) v[k][e] = make_float2(0.f, 0.f);
+      if (i < n) {
+        const size_t at = place(i);
+        f[k] = ws.partial[at].m;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = reinterpret_cast<const float2*>(ws.o + at * D)[lane + 32 * e];
+      }
     }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
@@ -636,10 +641,9 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   cfg.attrs = &behind;
   cfg.numAttrs = a.big ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, BITS, NT, CAP>, a, seg)) != cudaSuccess) return e;
-  // as many warps to a row as it can have partial results to spare, on average
-  const int64_t rows = (int64_t)a.B * a.Hq;
-  const int64_t most = 2 + ((int64_t)kBlocks * warps * (a.Hq / a.kv.Hkv) + (a.big ? kBlocks * 128 : 0)) / rows;
-  const int share = most > 48 ? 16 : most > 24 ? 8 : most > 12 ? 4 : most > 6 ? 2 : 1, per = kJoinWarps / share;
+  // few rows can have many partial results each: as many warps to a row as there are warps for
+  const int64_t rows = (int64_t)a.B * a.Hq, spare = kBlocks * kJoinWarps / rows;
+  const int share = spare >= 16 ? 16 : spare >= 8 ? 8 : spare >= 4 ? 4 : spare >= 2 ? 2 : 1, per = kJoinWarps / share;
   return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), st, a, share,
                        (int)C::COLS, seg);
 }

@@ -22,7 +22,16 @@ struct Deal {
   uint64_t total, chunk;  // tiles of all kv-heads, and those of one worker: worker w has w chunk .. (w + 1) chunk - 1
   uint32_t per_head;
 };
-__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {  // in 32 bits where that does
+// a / b.  Small operands go through fp32: the quotient is off by one at most (an integer division is
+// a call of some 250 cycles, and a warp needs five before its first tile).
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+  if ((a | b) >> 24 == 0) {
+    uint32_t q = (uint32_t)__fdividef((float)(uint32_t)a, (float)(uint32_t)b);
+    const int r = (int)(uint32_t)a - (int)(q * (uint32_t)b);
+    if (r < 0) --q;
+    if (r >= (int)(uint32_t)b) ++q;
+    return q;
+  }
   return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
 }
 __device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int workers) {
@@ -106,36 +115,43 @@ template <int COLS, int TILE, bool BIG, int CAP>
 __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
                                              uint32_t* scratch) {
   const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
+  const int lane = tid & 31, warp = tid >> 5;
   uint32_t* cum = src.cum;
-  for (int b = tid; b < A.B; b += THREADS) src.len[G + b] = response_len(A, b, A.status);
-  for (int g = tid; g < G; g += THREADS) {
-    cum[1 + g] = 0x7fffffffu;
-    src.len[g] = prompt_len(A, g, A.status);
-  }
+#pragma unroll 2
+  for (int i = tid; i < G + A.B; i += THREADS)
+    src.len[i] = i < G ? prompt_len(A, i, A.status) : response_len(A, i - G, A.status);
   __syncthreads();
-  for (int b = tid; b < A.B; b += THREADS) {
-    const int len = src.len[G + b];
-    if (len >= 0) atomicMin(&cum[1 + seg_of(seg, b)], (uint32_t)len);
-    if (!BIG) cum[1 + G + b] = (uint32_t)tiles_of<TILE>(first_own(A, len), len) * (uint32_t)((GQ + COLS - 1) / COLS);
-  }
-  __syncthreads();
-  for (int g = tid; g < G; g += THREADS) {
-    const uint32_t least = cum[1 + g];
-    uint32_t tiles = 0;
-    if (BIG) src.least[g] = (int)least;
-    if (least != 0x7fffffffu && big_group(A, seg.off[g + 1] - seg.off[g]) == BIG) {
-      const int P = src.len[g], rows = (seg.off[g + 1] - seg.off[g]) * GQ;
-      tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)((rows + COLS - 1) / COLS);
+  if (!BIG) {
+    const int blocks = (GQ + COLS - 1) / COLS;
+    for (int b = tid; b < A.B; b += THREADS) {
+      const int len = src.len[G + b];
+      cum[1 + G + b] = (uint32_t)tiles_of<TILE>(first_own(A, len), len) * (uint32_t)blocks;
     }
-    cum[1 + g] = tiles;
+  }
+  for (int g = warp; g < G; g += THREADS >> 5) {
+    const int from = seg.off[g], to = seg.off[g + 1];
+    uint32_t least = 0x7fffffffu;
+    for (int b = from + lane; b < to; b += 32) {
+      const int len = src.len[G + b];
+      if (len >= 0) least = min(least, (uint32_t)len);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+      uint32_t tiles = 0;
+      if (BIG) src.least[g] = (int)least;
+      if (least != 0x7fffffffu && big_group(A, to - from) == BIG) {
+        const int P = src.len[g];
+        tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)(((to - from) * GQ + COLS - 1) / COLS);
+      }
+      cum[1 + g] = tiles;
+    }
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
   // inclusive scan of cum[1 .. n]: every thread takes a run
-  const int per = (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);
+  const int per = n <= THREADS ? 1 : (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);
   uint32_t sum = 0;
   for (int i = from; i < to; ++i) sum += cum[i];
-  const int lane = tid & 31, warp = tid >> 5;
   uint32_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -144,8 +160,7 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
   }
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  uint32_t before = incl - sum;
-  for (int w = 0; w < warp; ++w) before += scratch[w];
+  uint32_t before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? scratch[lane] : 0u);
   for (int i = from; i < to; ++i) {
     before += cum[i];
     cum[i] = before;

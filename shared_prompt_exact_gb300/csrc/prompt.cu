@@ -48,7 +48,7 @@ struct PromptCtl {
   uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], pv_issued[2], pair_done[4], drain, drain2;
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t scratch[20];
+  uint32_t scratch[32];
   float half_m[256], half_l[256];
 };
 
@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     const int begin_row = seg.off[s.g] * GQ;
     s.row_end = seg.off[s.g + 1] * GQ;
     const int blocks = (s.row_end - begin_row + C::BM - 1) / C::BM;
-    const int tiles = (int)((cum[s.g + 1] - cum[s.g]) / (uint32_t)blocks);
-    const int block = (int)(local - cum[s.g]) / tiles, t0 = (int)(local - cum[s.g]) - block * tiles;
+    const int tiles = (int)divide(cum[s.g + 1] - cum[s.g], (uint32_t)blocks);
+    const int block = (int)divide(local - cum[s.g], (uint32_t)tiles), t0 = (int)(local - cum[s.g]) - block * tiles;
     const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
     s.parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - blockIdx.x) + 1;
     at += (uint64_t)(t1 - t0);
@@ -219,64 +219,72 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       const int mine = (int)(warp - (values ? C::V_WARP : 0)) * 32 + (int)lane;  // this thread's row of a tile
       const uint8_t* pool = static_cast<const uint8_t*>(values ? A.kv.v : A.kv.k);
       const __nv_bfloat16* scales = values ? A.kv.vs : A.kv.ks;
-      uint4 codes[U];
-      __nv_bfloat162 sc[U / 2];
-      int page = -1;  // of the row in the tile after the one in `codes`
+      struct Row {
+        uint4 codes[U];
+        __nv_bfloat162 sc[U / 2];
+      };
+      int page = -1;  // of this row in the tile that `load` takes next
       auto find = [&](const Segment& s, int tile) {
         const int token = tile * C::BN + mine;
         page = tile < s.last && token >= s.lo ? page_of(s, token) : -1;
       };
-      auto load = [&](const Segment& s, int tile) {
+      auto load = [&](Row& x, const Segment& s, int tile) {  // then finds the page for the next one
         const int token = tile * C::BN + mine;
 #pragma unroll
-        for (int u = 0; u < U; ++u) codes[u] = make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < U; ++u) x.codes[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < U / 2; ++u) sc[u] = __float2bfloat162_rn(0.f);
+        for (int u = 0; u < U / 2; ++u) x.sc[u] = __float2bfloat162_rn(0.f);
         if (page >= 0) {
           const int64_t row = cache_row(A.kv, page, s.kvh, token - A.by_ps(token) * ps);
           const uint4* from = reinterpret_cast<const uint4*>(pool + row * (D / 2));
           const __nv_bfloat162* sf = reinterpret_cast<const __nv_bfloat162*>(scales + row * U);
 #pragma unroll
-          for (int u = 0; u < U; ++u) codes[u] = from[u];
+          for (int u = 0; u < U; ++u) x.codes[u] = from[u];
 #pragma unroll
-          for (int u = 0; u < U / 2; ++u) sc[u] = sf[u];
+          for (int u = 0; u < U / 2; ++u) x.sc[u] = sf[u];
+        }
+        find(s, tile + 1);
+      };
+      auto decode = [&](const Row& x) {
+        if (!(ok = warp_wait(&empty[slot], phase, fs))) return;
+        uint8_t* dst = ring + slot * C::TILE_BYTES;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const __nv_bfloat162 s2 = u & 1 ? __high2bfloat162(x.sc[u / 2]) : __low2bfloat162(x.sc[u / 2]);
+          const __nv_bfloat162 o2 = __hmul2(s2, __float2bfloat162_rn(-24.f));
+          const uint32_t w[4] = {x.codes[u].x, x.codes[u].y, x.codes[u].z, x.codes[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 d = decode2(w[i] >> (4 * e), s2, o2);
+              p[e] = *reinterpret_cast<const uint32_t*>(&d);
+            }
+            const int c = 4 * u + i;  // 16-byte chunk of the row
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine, c & 7)) =
+                make_uint4(p[0], p[1], p[2], p[3]);
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1;
         }
       };
+      Row x, y;  // codes of two tiles, on their way while the ones before are decoded
       for (uint64_t at = begin; at < stop && ok;) {
         const Segment s = next_segment(at);
         find(s, s.first);
-        load(s, s.first);
-        find(s, s.first + 1);
-        for (int tile = s.first; tile < s.last; ++tile) {
-          if (!(ok = warp_wait(&empty[slot], phase, fs))) break;
-          uint8_t* dst = ring + slot * C::TILE_BYTES;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const __nv_bfloat162 s2 = u & 1 ? __high2bfloat162(sc[u / 2]) : __low2bfloat162(sc[u / 2]);
-            const __nv_bfloat162 o2 = __hmul2(s2, __float2bfloat162_rn(-24.f));
-            const uint32_t w[4] = {codes[u].x, codes[u].y, codes[u].z, codes[u].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t p[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 d = decode2(w[i] >> (4 * e), s2, o2);
-                p[e] = *reinterpret_cast<const uint32_t*>(&d);
-              }
-              const int c = 4 * u + i;  // 16-byte chunk of the row
-              *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine, c & 7)) =
-                  make_uint4(p[0], p[1], p[2], p[3]);
-            }
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
-          load(s, tile + 1);  // nothing behind the last one
-          find(s, tile + 2);
-          if (++slot == slots) {
-            slot = 0;
-            phase ^= 1;
-          }
+        load(x, s, s.first);
+        for (int tile = s.first; tile < s.last && ok; tile += 2) {
+          load(y, s, tile + 1);
+          decode(x);
+          if (tile + 1 >= s.last || !ok) break;
+          load(x, s, tile + 2);
+          decode(y);
         }
       }
     }
@@ -297,16 +305,24 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       // the queries go where other warps may still pass on their partial results
       if (n_seg > 0 && !(ok = warp_wait(&ctl.q_free, (n_seg - 1) & 1, fs))) break;
       {
-        const uint4* q = reinterpret_cast<const uint4*>(A.q + b_of * A.q_stride + (int64_t)head * D) + half * (D / 16);
+        // the warp's 16 rows, D / 8 lanes to a row
+        constexpr int LR = D / 8, AT_ONCE = 32 / LR;
+        const int first_row = (int)(warp - C::SOFTMAX) * 16 + (int)lane / LR, c = (int)lane % LR;
+        uint4 x[16 / AT_ONCE];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < s.row_end) x = q[i];
+        for (int i = 0; i < 16 / AT_ONCE; ++i) {
+          const int rr = s.r0 + first_row + i * AT_ONCE, bb = A.by_heads(rr);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (rr < s.row_end)
+            x[i] = reinterpret_cast<const uint4*>(A.q + bb * A.q_stride + (int64_t)(s.kvh * GQ + rr - bb * GQ) * D)[c];
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / AT_ONCE; ++i) {
+          uint4 y = x[i];
           if (BITS == 4)  // values e and e + 4 together, as decode2 leaves them
-            x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
-                           __byte_perm(x.y, x.w, 0x7632));
-          const int c = half * (D / 16) + i;
-          *reinterpret_cast<uint4*>(smem + (c >> 3) * C::BM * 128 + sw128_offset(row, c & 7)) = x;
+            y = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410),
+                           __byte_perm(y.y, y.w, 0x7632));
+          *reinterpret_cast<uint4*>(smem + (c >> 3) * C::BM * 128 + sw128_offset(first_row + i * AT_ONCE, c & 7)) = y;
         }
         if (r < s.row_end) {
           const int len = src.len[A.G + b_of];
