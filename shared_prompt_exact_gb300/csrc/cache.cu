@@ -73,13 +73,19 @@ __device__ __forceinline__ uint2 quantise16(const float (&x)[16], __nv_bfloat16&
   const uint32_t bits = (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0x7ffffu) & ~0x7ffffu;
   scale = top < 0x7f800000u ? __ushort_as_bfloat16((unsigned short)(bits >> 16))
                             : __ushort_as_bfloat16((unsigned short)0x7fc0u);
-  const float step = top != 0u && top < 0x7f800000u ? __uint_as_float(bits) : 1.f;
+  if (top >= 0x7f800000u || bits == 0u) return make_uint2(0x88888888u, 0x88888888u);  // not finite, or zeros
+  // n = |x| / step by the reciprocal, off by one at most; what is left of |x| says which way, exactly.  Steps whose
+  // reciprocal would overflow are taken with their values to where it does not.
+  const float up = __uint_as_float(bits) < 1e-30f ? 0x1p64f : 1.f;
+  const float step = __uint_as_float(bits) * up, inv = __fdiv_rn(1.f, step), half = 0.5f * step;
   uint32_t out[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const float n = floorf(__fdiv_rn(fabsf(x[e]), step) + 0.5f);
-    const int code = 8 + (top < 0x7f800000u ? (int)copysignf(n, x[e]) : 0);
-    out[e >> 3] |= (uint32_t)(code & 15) << (4 * (e & 7));
+    const float a = fabsf(x[e]) * up, t = fmaf(a, inv, 12582912.f);  // 1.5 x 2^23: the sum is rounded to a whole number
+    const float left = fmaf(-(t - 12582912.f), step, a);
+    int n = (int)(__float_as_uint(t) & 15u) + (left >= half ? 1 : 0) - (left < -half ? 1 : 0);
+    if (x[e] < 0.f) n = -n;
+    out[e >> 3] |= (uint32_t)(8 + n) << (4 * (e & 7));
   }
   return make_uint2(out[0], out[1]);
 }
@@ -261,15 +267,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const 
           const uint32_t w = static_cast<const uint32_t*>(pool)[row * V + u % V];
           const __nv_bfloat162 sc = __bfloat162bfloat162(scales[row * (D / kGroup) + u % V / 4]);
           const __nv_bfloat162 off = __hmul2(sc, __float2bfloat162_rn(-24.f));
-          // codes 0 and 4, 1 and 5, ...
-          uint32_t p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 d = decode2(w >> (4 * e), sc, off);
-            p[e] = *reinterpret_cast<const uint32_t*>(&d);
-          }
-          y = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
-                         __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+          const uint4 p = decode8(w, sc, off);
+          y = make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410), __byte_perm(p.x, p.y, 0x7632),
+                         __byte_perm(p.z, p.w, 0x7632));
         }
       }
       out[which][u] = y;

@@ -32,12 +32,26 @@ __device__ __forceinline__ int64_t cache_row(const PagedKV& kv, int page, int he
   return ((int64_t)page * kv.Hkv + head) * kv.ps + slot;
 }
 
-// Two codes at bits 0-3 and 16-19 of w as their values: 16 + code has the code in the mantissa's top
-// four bits, and (16 + code) s - 24 s = (code - 8) s is exact in bf16, since scales have 5 significant
-// bits (24 s has 7 at most, the result 8).
-__device__ __forceinline__ __nv_bfloat162 decode2(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 minus24s) {
-  const uint32_t u = (w << 3 & 0x00780078u) | 0x41804180u;
-  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, minus24s);
+// (x & mask) | bits in one instruction (with both constants as immediates it becomes two).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+  return r;
+}
+
+// Codes E and E + 4 of the 8 in w as their values: 16 + code has the code in the mantissa's top four bits, and
+// (16 + code) s - 24 s = (code - 8) s is exact in bf16, since scales have 5 significant bits (24 s has 7 at most,
+// the result 8).
+template <int E>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 minus24s) {
+  const uint32_t u = and_or(E == 0 ? w << 3 : w >> (E == 0 ? 0 : 4 * E - 3), 0x00780078u, 0x41804180u);
+  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, minus24s);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// All 8 codes of w: 0 and 4, 1 and 5, 2 and 6, 3 and 7.
+__device__ __forceinline__ uint4 decode8(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 minus24s) {
+  return make_uint4(decode_pair<0>(w, s, minus24s), decode_pair<1>(w, s, minus24s), decode_pair<2>(w, s, minus24s),
+                    decode_pair<3>(w, s, minus24s));
 }
 
 }  // namespace dkv

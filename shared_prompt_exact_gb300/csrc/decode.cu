@@ -91,14 +91,6 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* 
   }
 }
 
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-// Codes e and e + 4 of word w (cache.cuh's decode2 with the shifts folded).
-template <int E>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 minus24s) {
-  const uint32_t u = ((E == 0 ? w << 3 : w >> (E == 0 ? 0 : 4 * E - 3)) & 0x00780078u) | 0x41804180u;
-  return bits(__hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s, minus24s));
-}
-
 // ---------------------------------------------------------------- a warp's walk
 template <int D, int BITS, int NT, int CAP>
 __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)

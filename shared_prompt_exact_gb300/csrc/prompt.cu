@@ -10,7 +10,7 @@
 //   loaders of keys, loaders of values, each with a ring of their own.  bf16: one warp each, 8 lanes of which load a
 //     tile's 16-token pieces by TMA, each from its page.  4 bits: four warps each; a thread decodes
 //     a row (its codes loaded a tile ahead) and writes them as bf16 in the swizzled layout that TMA would leave.  The decoded
-//     order within 8 values is 0, 4, 1, 5, ... (decode2); the queries are written in the same order, and the
+//     order within 8 values is 0, 4, 1, 5, ... (decode8); the queries are written in the same order, and the
 //     output's columns are put right at the end.
 //   an issuer of S = Q K^T, an issuer of O += P V, eight softmax warps: as in fwd.cu.
 // Values that no row sees may hold anything: rows of a tile outside the prompt or before its first seen token are
@@ -255,15 +255,8 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
           const uint32_t w[4] = {x.codes[u].x, x.codes[u].y, x.codes[u].z, x.codes[u].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 d = decode2(w[i] >> (4 * e), s2, o2);
-              p[e] = *reinterpret_cast<const uint32_t*>(&d);
-            }
             const int c = 4 * u + i;  // 16-byte chunk of the row
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine, c & 7)) =
-                make_uint4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * C::BN * 128 + sw128_offset(mine, c & 7)) = decode8(w[i], s2, o2);
           }
         }
         fence_async();
@@ -319,7 +312,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 16 / AT_ONCE; ++i) {
           uint4 y = x[i];
-          if (BITS == 4)  // values e and e + 4 together, as decode2 leaves them
+          if (BITS == 4)  // values e and e + 4 together, as decode8 leaves them
             y = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410),
                            __byte_perm(y.y, y.w, 0x7632));
           *reinterpret_cast<uint4*>(smem + (c >> 3) * C::BM * 128 + sw128_offset(first_row + i * AT_ONCE, c & 7)) = y;
