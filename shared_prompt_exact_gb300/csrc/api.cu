@@ -663,10 +663,9 @@ bool table_fits(int max_pages, int page_size) {
   return max_pages >= 1 && (int64_t)max_pages * page_size <= INT32_MAX;
 }
 
-int status_of_device(uint32_t** status) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DUALKV_ERR_CUDA;
-  return status_word(dev, status);
+int status_of_device(uint32_t** status, int* device) {
+  if (cudaGetDevice(device) != cudaSuccess) return DUALKV_ERR_CUDA;
+  return status_word(*device, status);
 }
 
 int append_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -729,7 +728,7 @@ int append_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride
   a.inter = interleaved != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
-  if ((rc = status_of_device(&a.status))) return rc;
+  if ((rc = status_of_device(&a.status, &a.device))) return rc;
   return timed(DUALKV_KERNEL_CACHE, st, [&] { return launch_append(D, a, S, off, st); }) == cudaSuccess ? DUALKV_OK
                                                                                                       : DUALKV_ERR_CUDA;
 }
@@ -737,6 +736,7 @@ int append_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride
 int read_impl(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages, const int32_t* lens, int S,
               const int32_t* off, int Hkv, int D, void* k_out, void* v_out, void* stream) {
   ReadArgs a{};
+  int device = 0;
   uint64_t head_rows = 0;
   int rc = check_offsets(S, off);
   if (rc) return rc;
@@ -759,7 +759,7 @@ int read_impl(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages,
   a.v_out = static_cast<__nv_bfloat16*>(v_out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
-  if ((rc = status_of_device(&a.status))) return rc;
+  if ((rc = status_of_device(&a.status, &device))) return rc;
   return timed(DUALKV_KERNEL_CACHE, st, [&] { return launch_read(D, a, S, off, st); }) == cudaSuccess ? DUALKV_OK
                                                                                                     : DUALKV_ERR_CUDA;
 }
@@ -830,7 +830,7 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   a.workspace = workspace;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
-  if ((rc = status_of_device(&a.status))) return rc;
+  if ((rc = status_of_device(&a.status, &a.device))) return rc;
   CUtensorMap tk = {}, tv = {};
   if (D != 512 && prompts && G <= kBigGroups && B <= kBigResponses && head_rows <= INT32_MAX) {
     for (int g = 0; g < G; ++g) a.big |= (uint64_t)(groups[g + 1] - groups[g]) * GQ >= kBigRows;

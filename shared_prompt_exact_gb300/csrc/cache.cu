@@ -17,6 +17,7 @@
 
 #include "cache.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
 #include "segs.cuh"
@@ -281,8 +282,7 @@ template <int D, int BITS, int CAP>
 cudaError_t append_c(const AppendArgs& a, int S, const int32_t* off, cudaStream_t st) {
   const SegTable<CAP> seg = make_segs<CAP>(0, S, off);
   constexpr int smem = (int)sizeof(AppendShared<D, BITS>);
-  const cudaError_t e =
-      cudaFuncSetAttribute(append_kernel<D, BITS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared<&append_kernel<D, BITS, CAP>>(a.device, smem);
   if (e != cudaSuccess) return e;
   const int heads = 512 / D, steps = (a.Hq + heads - 1) / heads + 2 * ((a.kv.Hkv + heads - 1) / heads);
   const int64_t need = (a.T + kWarps - 1) / kWarps;

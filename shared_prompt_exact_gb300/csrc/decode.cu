@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const uint32_t* cum = src.cum;
   __shared__ uint32_t scratch[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int GQ = A.Hq / A.kv.Hkv, sources = A.G + A.B;
+  const int GQ = (int)A.by_heads.d, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   deal_sources<C::COLS, C::TILE, false>(A, seg, src, scratch);
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
   const bool live = row < (int64_t)A.B * A.Hq;
   const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
-  const int GQ = A.Hq / A.kv.Hkv, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
+  const int GQ = (int)A.by_heads.d, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
   // which sources the row sees, as the kernels that left the partial results decided
   const int len = response_len(A, b, nullptr), P = prompt_len(A, g, nullptr);
@@ -615,7 +615,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   // many sources take the place of some warps' rings
   const int cum = (2 * (a.G + a.B) + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
   const int warps = room < C::WARPS ? room : C::WARPS, smem = warps * C::RING + cum;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, BITS, NT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared<&decode_kernel<D, BITS, NT, CAP>>(a.device, kMostShared);
   if (e != cudaSuccess) return e;
   if (a.big) {
     if constexpr (D != 512) {

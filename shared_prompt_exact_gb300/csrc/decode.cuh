@@ -96,7 +96,7 @@ __host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
 
 // Whether a prompt is left to prompt.cu's kernel, which takes 128 of its rows at once.
 __device__ __forceinline__ bool big_group(const DecodeArgs& A, int responses) {
-  return A.big && responses * (A.Hq / A.kv.Hkv) >= kBigRows;
+  return A.big && responses * (int)A.by_heads.d >= kBigRows;
 }
 
 // What a block knows of the sources, in shared memory.
@@ -114,7 +114,7 @@ __device__ __forceinline__ int first_own(const DecodeArgs& A, int n) { return A.
 template <int COLS, int TILE, bool BIG, int CAP>
 __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
                                              uint32_t* scratch) {
-  const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = A.Hq / A.kv.Hkv, tid = threadIdx.x, THREADS = blockDim.x;
+  const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = (int)A.by_heads.d, tid = threadIdx.x, THREADS = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5;
   uint32_t* cum = src.cum;
 #pragma unroll 2

@@ -238,6 +238,7 @@ struct AppendArgs {
   float w0, eps;
   bool weight_f32, inter;
   uint32_t* status;
+  int device;
 };
 cudaError_t launch_append(int D, const AppendArgs& a, int S, const int32_t* off, cudaStream_t st);
 
@@ -282,6 +283,7 @@ struct DecodeArgs {
   void* workspace;
   uint32_t* status;
   FastDiv by_ps, by_heads;  // by the page size and by Hq / Hkv
+  int device;
   bool big;          // some prompts go to launch_prompt: of groups with kBigRows rows (responses x Hq / Hkv) or more
 };
 // A group's prompt is worth the tensor cores' large tiles from here on.

@@ -21,6 +21,7 @@
 #include "cache.cuh"
 #include "decode.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "segs.cuh"
 
@@ -39,6 +40,7 @@ struct PromptCfg {
   static constexpr int S_WARP = BITS == 16 ? 2 : 16, PV_WARP = S_WARP + 1;
   static constexpr int THREADS = BITS == 16 ? 384 : 640;
   static constexpr int OFF_K = TILE_BYTES, OFF_V = OFF_K + NK * TILE_BYTES, RINGS = OFF_V + NV * TILE_BYTES;
+  static constexpr int MOST_SHARED = RINGS + 1024 + (3 * kBigGroups + kBigResponses + 1) * (int)sizeof(uint32_t);
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 };
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
                     reinterpret_cast<int*>(smem + C::RINGS) + A.G + 1};
   const uint32_t* cum = src.cum;
   const uint32_t warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
-  const int GQ = A.Hq / A.kv.Hkv, ps = A.kv.ps;
+  const int GQ = (int)A.by_heads.d, ps = A.kv.ps;
   FailState fs{&ctl.abort_flag, A.status, kLaunchWaitLimitNs};
 
   if (threadIdx.x == 0) {
@@ -146,11 +148,12 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     s.last = tile0 + t1;
     return s;
   };
-  // page of a token of the prompt, or -1
-  auto page_of = [&](const Segment& s, int token) {
-    const int page = token < s.P ? A.prompt_table[(int64_t)s.g * A.max_prompt_pages + A.by_ps(token)] : -1;
-    return (uint32_t)page < (uint32_t)A.kv.pages ? page : -1;
+  // the table's entry for a token, -1 behind the prompt: to be held against the pool's pages where it is used, a tile
+  // later, so that nothing waits for its load
+  auto entry_of = [&](const Segment& s, int token) {
+    return token < s.P ? A.prompt_table[(int64_t)s.g * A.max_prompt_pages + A.by_ps(token)] : -1;
   };
+  auto is_page = [&](int entry) { return (uint32_t)entry < (uint32_t)A.kv.pages; };
 
   // 4 bits: 20 warps start with 96 registers a thread; the softmax warps take over what the others leave:
   // 2 x 72 + 2 x 144 + 48 for the five warpgroups, 5 x 96 in all
@@ -171,13 +174,13 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       if (lane == 0) tma_prefetch_desc(tm);
       for (uint64_t at = begin; at < stop && ok;) {
         const Segment s = next_segment(at);
-        int token = s.first * C::BN + 16 * (int)(lane & 7), page = page_of(s, token);
+        int token = s.first * C::BN + 16 * (int)(lane & 7), page = entry_of(s, token);
         for (int tile = s.first; tile < s.last; ++tile) {
-          const bool have = lane < 8 && page >= 0;
+          const bool have = lane < 8 && is_page(page);
           const bool whole = have && (!values || (token >= s.lo && token + 16 <= s.P));
           const int row = have ? (int)cache_row(A.kv, page, s.kvh, token - A.by_ps(token) * ps) : 0;
           token += C::BN;
-          const int next = tile + 1 < s.last ? page_of(s, token) : -1;
+          const int next = tile + 1 < s.last ? entry_of(s, token) : -1;
           if (!(ok = warp_wait(&empty[slot], phase, fs))) break;
           uint8_t* dst = ring + slot * C::TILE_BYTES;
           const uint32_t boxes = __ballot_sync(0xffffffffu, whole), have_mask = __ballot_sync(0xffffffffu, have);
@@ -223,10 +226,10 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         uint4 codes[U];
         __nv_bfloat162 sc[U / 2];
       };
-      int page = -1;  // of this row in the tile that `load` takes next
+      int page = -1;  // table's entry for this row in the tile that `load` takes next
       auto find = [&](const Segment& s, int tile) {
         const int token = tile * C::BN + mine;
-        page = tile < s.last && token >= s.lo ? page_of(s, token) : -1;
+        page = tile < s.last && token >= s.lo ? entry_of(s, token) : -1;
       };
       auto load = [&](Row& x, const Segment& s, int tile) {  // then finds the page for the next one
         const int token = tile * C::BN + mine;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         for (int u = 0; u < U; ++u) x.codes[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int u = 0; u < U / 2; ++u) x.sc[u] = __float2bfloat162_rn(0.f);
-        if (page >= 0) {
+        if (is_page(page)) {
           const int64_t row = cache_row(A.kv, page, s.kvh, token - A.by_ps(token) * ps);
           const uint4* from = reinterpret_cast<const uint4*>(pool + row * (D / 2));
           const __nv_bfloat162* sf = reinterpret_cast<const __nv_bfloat162*>(scales + row * U);
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         const int clo = lo - kl0, chi = s.P - 1 - kl0;  // allowed columns [clo, chi] of this half
         // 16-token pieces of the half without a page: their keys do not count
         const int piece = kl0 + 16 * (int)(lane & 3);
-        const uint32_t gone = __ballot_sync(0xffffffffu, lane < 4 && piece < s.P && piece + 15 >= s.lo && page_of(s, piece) < 0);
+        const uint32_t gone = __ballot_sync(0xffffffffu, lane < 4 && piece < s.P && piece + 15 >= s.lo && !is_page(entry_of(s, piece)));
         if (gone && lane == 0 && A.status) atomicOr(A.status, kDevErrBounds);
         const bool full = clo <= 0 && chi >= C::HC - 1 && !gone;
         if (!(ok = warp_wait(&ctl.s_full[b], (jj >> 1) & 1, fs))) break;
@@ -535,8 +538,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   using C = PromptCfg<D, BITS>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
   const int smem = C::RINGS + 1024 + (3 * a.G + a.B + 1) * (int)sizeof(uint32_t);
-  const cudaError_t e =
-      cudaFuncSetAttribute(prompt_kernel<D, BITS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared<&prompt_kernel<D, BITS, CAP>>(a.device, C::MOST_SHARED);
   if (e != cudaSuccess) return e;
   prompt_kernel<D, BITS, CAP><<<kBlocks, C::THREADS, smem, st>>>(tk, tv, a, seg);
   return cudaGetLastError();
