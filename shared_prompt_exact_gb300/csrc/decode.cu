@@ -502,32 +502,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
 }
 
 // ---------------------------------------------------------------- the join
-constexpr int kJoinWarps = 16;
-constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinWarps = 16;  // most warps of a block
 
-__device__ __forceinline__ float lse_of(float top, float total) {
-  return total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
-}
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-  return x;
-}
-
-// `share` warps of a block take a row's partial results by turns, and the first of them adds up what they have.  The
-// kernel may start before the partial results are complete, so nothing that reads them is __restrict__.
+// `share` warps take a row's partial results by turns, some at once with their loads together; each keeps a running
+// maximum, and the first of them joins what they have.  The kernel may start before the partial results are
+// complete, so nothing that reads them is __restrict__.
 template <int D, int CAP>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     join_kernel(const DecodeArgs A, int share, int cols, const __grid_constant__ SegTable<CAP> seg) {
   constexpr int E = D / 64, BATCH = D == 512 ? 2 : 8;  // float2s of a lane; partial results on their way at once
   __shared__ float2 sums[kJoinWarps][D / 2];
+  __shared__ float2 ml[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & (share - 1);
-  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / share) + warp / share;
+  const int64_t row = (int64_t)blockIdx.x * ((blockDim.x >> 5) / share) + warp / share;
   const bool live = row < (int64_t)A.B * A.Hq;
   const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
   const int GQ = (int)A.by_heads.d, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
@@ -537,10 +524,11 @@ __global__ void __launch_bounds__(kJoinThreads)
   const bool sees_own = live && len > 0, sees_prompt = live && len >= 0 && first_position(A, P, len) < P;
   const bool big = big_group(A, seg.off[g + 1] - seg.off[g]);
   const size_t own = own_slots(A.B, A.Hq);
+  const int in_group = (b - seg.off[g]) * GQ + j;
   cudaGridDependencySynchronize();
   const Partial none{kLowest, 0.f, 0, 0};
   const Partial p0 = sees_prompt ? ws.partial[own / 2 + row] : none, p1 = sees_own ? ws.partial[row] : none;
-  const int n = p0.parts + p1.parts, in_group = (b - seg.off[g]) * GQ + j;
+  const int n = p0.parts + p1.parts;
   // slots of the workers behind a source's first one
   const size_t behind0 = big ? own + kWarpSlots + (size_t)p0.worker * 128 + (in_group & 127)
                              : own + (size_t)p0.worker * cols + (in_group & (cols - 1));
@@ -551,39 +539,37 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (k == 0) return second ? (size_t)row : own / 2 + (size_t)row;
     return (second ? behind1 : behind0) + (size_t)(k * (second || !big ? cols : 128));
   };
-  // each lane's maximum and sum in one pass, then the warp's
   float top = kLowest, total = 0.f;
-#pragma unroll 4
-  for (int i = lane; i < n; i += 32) {
-    const Partial x = ws.partial[place(i)];
-    const float m = fmaxf(top, x.m);
-    total = fmaf(total, ex2_approx(top - m), x.l * ex2_approx(x.m - m));
-    top = m;
-  }
-  const float most = warp_max(top);
-  total = warp_sum(total * ex2_approx(top - most));
   float2 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float2(0.f, 0.f);
   for (int i0 = part; i0 < n; i0 += BATCH * share) {
-    float f[BATCH];
-    float2 v[BATCH][E];
+    float2 f[BATCH], v[BATCH][E];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int i = i0 + k * share;
-      f[k] = -INFINITY;
+      f[k] = make_float2(kLowest, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[k][e] = make_float2(0.f, 0.f);
       if (i < n) {
         const size_t at = place(i);
-        f[k] = ws.partial[at].m;
+        f[k] = *reinterpret_cast<const float2*>(&ws.partial[at]);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[k][e] = reinterpret_cast<const float2*>(ws.o + at * D)[lane + 32 * e];
       }
     }
+    float most = top;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) most = fmaxf(most, f[k].x);
+    const float old = ex2_approx(top - most);
+    top = most;
+    total *= old;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmul2(acc[e], make_float2(old, old));
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const float w = ex2_approx(f[k] - most);
+      const float w = ex2_approx(f[k].x - most);
+      total = fmaf(f[k].y, w, total);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = ffma2(v[k][e], make_float2(w, w), acc[e]);
     }
@@ -591,12 +577,24 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (share > 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) ml[warp] = make_float2(top, total);
     __syncthreads();
     if (part) return;
-#pragma unroll 4
-    for (int w = 1; w < share; ++w)
+    float most = top;
+    for (int w = 1; w < share; ++w) most = fmaxf(most, ml[warp + w].x);
+    const float mine = ex2_approx(top - most);
+    top = most;
+    total *= mine;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fadd2(acc[e], sums[warp + w][lane + 32 * e]);
+    for (int e = 0; e < E; ++e) acc[e] = fmul2(acc[e], make_float2(mine, mine));
+#pragma unroll 4
+    for (int w = 1; w < share; ++w) {
+      const float2 x = ml[warp + w];
+      const float f = ex2_approx(x.x - most);
+      total = fmaf(x.y, f, total);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = ffma2(sums[warp + w][lane + 32 * e], make_float2(f, f), acc[e]);
+    }
   }
   if (!live) return;
   const float inv = total > 0.f ? 1.f / total : 0.f;
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
   for (int e = 0; e < E; ++e) out[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
   if (lane == 0 && A.lse)
-    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (most + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 template <int D, int BITS, int NT, int CAP>
@@ -633,10 +631,10 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   cfg.attrs = &behind;
   cfg.numAttrs = a.big ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, BITS, NT, CAP>, a, seg)) != cudaSuccess) return e;
-  // few rows can have many partial results each: as many warps to a row as there are warps for
+  // few rows can have many partial results each: as many warps to a row as there are warps for, in blocks of 4 or more
   const int64_t rows = (int64_t)a.B * a.Hq, spare = kBlocks * kJoinWarps / rows;
-  const int share = spare >= 16 ? 16 : spare >= 8 ? 8 : spare >= 4 ? 4 : spare >= 2 ? 2 : 1, per = kJoinWarps / share;
-  return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), st, a, share,
+  const int share = spare >= 16 ? 16 : spare >= 8 ? 8 : spare >= 4 ? 4 : spare >= 2 ? 2 : 1, per = share < 4 ? 4 / share : 1;
+  return launch_behind(join_kernel<D, CAP>, dim3((unsigned)((rows + per - 1) / per)), dim3(per * share * 32), st, a, share,
                        (int)C::COLS, seg);
 }
 

@@ -158,9 +158,12 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
     const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  uint32_t before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? scratch[lane] : 0u);
+  uint32_t before = incl - sum;
+  if (n > 32) {  // else the first warp has them all
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    before += __reduce_add_sync(0xffffffffu, lane < warp ? scratch[lane] : 0u);
+  }
   for (int i = from; i < to; ++i) {
     before += cum[i];
     cum[i] = before;
