@@ -65,28 +65,49 @@ struct AppendShared {
   uint4 ring[kDepth][2][kThreads];
 };
 
+// Largest and smallest of three, NaN if one of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.
 __device__ __forceinline__ uint2 quantise16(const float (&x)[16], __nv_bfloat16& scale) {
-  uint32_t top = 0;
+  float hi = max3(x[0], x[1], x[2]), lo = min3(x[0], x[1], x[2]);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);  // NaN above infinity above all
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  const uint32_t bits = (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0x7ffffu) & ~0x7ffffu;
-  scale = top < 0x7f800000u ? __ushort_as_bfloat16((unsigned short)(bits >> 16))
-                            : __ushort_as_bfloat16((unsigned short)0x7fc0u);
-  if (top >= 0x7f800000u || bits == 0u) return make_uint2(0x88888888u, 0x88888888u);  // not finite, or zeros
-  // n = |x| / step by the reciprocal, off by one at most; what is left of |x| says which way, exactly.  Steps whose
-  // reciprocal would overflow are taken with their values to where it does not.
-  const float up = __uint_as_float(bits) < 1e-30f ? 0x1p64f : 1.f;
-  const float step = __uint_as_float(bits) * up, inv = __fdiv_rn(1.f, step), half = 0.5f * step;
-  uint32_t out[2] = {0, 0};
+  for (int e = 3; e < 15; e += 2) {
+    hi = max3(hi, x[e], x[e + 1]);
+    lo = min3(lo, x[e], x[e + 1]);
+  }
+  hi = max3(hi, x[15], -min3(lo, x[15], x[15]));
+  const float top = max3(hi, __shfl_xor_sync(0xffffffffu, hi, 1), hi);
+  const uint32_t bits = (__float_as_uint(__fdiv_rn(top, 7.f)) + 0x7ffffu) & ~0x7ffffu;
+  const bool finite = top < __uint_as_float(0x7f800000u);  // false for NaN
+  scale = __ushort_as_bfloat16((unsigned short)(finite ? bits >> 16 : 0x7fc0u));
+  if (!finite || bits == 0u) return make_uint2(0x88888888u, 0x88888888u);  // not finite, or zeros
+  // x / step by the smallest float above 1 / step: a value half way between two multiples comes out above it (away from
+  // zero) and goes to the farther one, any other value is moved by 2^-23 of it at most.  The sum with 1.5 x 2^23 + 8
+  // is rounded to a whole number, whose low bits are n + 8; the eight codes are shifted together with the
+  // upper bits in place, which are subtracted at once.
+  float up = 1.f, step = __uint_as_float(bits);
+  if (step < 1e-36f) {  // its reciprocal could overflow: the same with both 2^64 times as large
+    up = 0x1p64f;
+    step *= up;
+  }
+  const float inv = __uint_as_float(__float_as_uint(__frcp_rd(step)) + 1u);
+  uint32_t out[2];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float a = fabsf(x[e]) * up, t = fmaf(a, inv, 12582912.f);  // 1.5 x 2^23: the sum is rounded to a whole number
-    const float left = fmaf(-(t - 12582912.f), step, a);
-    int n = (int)(__float_as_uint(t) & 15u) + (left >= half ? 1 : 0) - (left < -half ? 1 : 0);
-    if (x[e] < 0.f) n = -n;
-    out[e >> 3] |= (uint32_t)(8 + n) << (4 * (e & 7));
+  for (int w = 0; w < 2; ++w) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) sum = (sum << 4) + __float_as_uint(fmaf(x[8 * w + e] * up, inv, 12582920.f));
+    out[w] = sum - 0x4b400000u * 0x11111111u;
   }
   return make_uint2(out[0], out[1]);
 }
@@ -107,9 +128,18 @@ __device__ __forceinline__ void turn(Vec8& a, Vec8& b, const Angles& g, const La
   }
 }
 
+// A lane's eight values in their order.
 __device__ __forceinline__ void natural8(const Vec8& v, float* to) {
   *reinterpret_cast<float4*>(to) = make_float4(v.v[0].x, v.v[2].x, v.v[0].y, v.v[2].y);
   *reinterpret_cast<float4*>(to + 4) = make_float4(v.v[1].x, v.v[3].x, v.v[1].y, v.v[3].y);
+}
+
+// Place of value p (a multiple of 4) of a step's 512 in shared memory: vectors of 16 bytes, so that neither the lanes that
+// write neighbouring ones nor those that read every fourth meet in a bank.
+__device__ __forceinline__ int spread(int p) { return p ^ ((p >> 5 & 3) << 2); }
+__device__ __forceinline__ void store8(const Vec8& v, float* base, int p) {
+  *reinterpret_cast<float4*>(base + spread(p)) = make_float4(v.v[0].x, v.v[2].x, v.v[0].y, v.v[2].y);
+  *reinterpret_cast<float4*>(base + spread(p + 4)) = make_float4(v.v[1].x, v.v[3].x, v.v[1].y, v.v[3].y);
 }
 
 // 16 values from natural order into a row of the 4-bit pools.
@@ -139,20 +169,34 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
   const int begin = steps * (int)blockIdx.y / (int)gridDim.y, end = steps * ((int)blockIdx.y + 1) / (int)gridDim.y;
   const int64_t first = (int64_t)blockIdx.x * kWarps + warp, stride = (int64_t)gridDim.x * kWarps;
 
+  // the copies' place in the walk: x is the lane's first vector of the head, the second lies dx behind
   int64_t at = first;
-  int s_at = begin;
+  int s_at = begin, h_at = 0, heads_at = 0, dx = 0;
+  const __nv_bfloat16* x = nullptr;
+  auto place_copies = [&]() {
+    const int part = s_at < nq ? 0 : s_at < nq + nk ? 1 : 2;
+    h_at = slot + (s_at - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * S;
+    heads_at = part == 0 ? A.Hq : Hkv;
+    dx = part == 2 ? vb - va : m.b - m.a;
+    x = (part == 0 ? A.q + at * A.q_stride : part == 1 ? A.k + at * A.k_stride : A.v + at * A.v_stride) + h_at * D +
+        (part == 2 ? va : m.a);
+  };
+  place_copies();
   auto fetch = [&](int stage) {
     if (at < A.T) {
-      const int part = s_at < nq ? 0 : s_at < nq + nk ? 1 : 2;
-      const int h = slot + (s_at - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * S;
-      const __nv_bfloat16* x = (part == 0 ? A.q + at * A.q_stride : part == 1 ? A.k + at * A.k_stride : A.v + at * A.v_stride) + h * D;
-      if (h < (part == 0 ? A.Hq : Hkv)) {
-        copy16(&sh.ring[stage][0][threadIdx.x], x + (part == 2 ? va : m.a));
-        copy16(&sh.ring[stage][1][threadIdx.x], x + (part == 2 ? vb : m.b));
+      if (h_at < heads_at) {
+        copy16(&sh.ring[stage][0][threadIdx.x], x);
+        copy16(&sh.ring[stage][1][threadIdx.x], x + dx);
       }
-      if (++s_at == end) {
+      h_at += S;
+      x += S * D;
+      ++s_at;
+      if (s_at == end) {
         s_at = begin;
         at += stride;
+        if (at < A.T) place_copies();
+      } else if (s_at == nq || s_at == nq + nk) {
+        place_copies();
       }
     }
     copies_commit();
@@ -178,33 +222,20 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
     at_row.pos = (uint32_t)A.starts[s] + (uint32_t)index;
     find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at_row);
     const Angles ang = row_angles((int)at_row.pos, sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
-    for (int step = begin; step < end; ++step) {
-      const int part = step < nq ? 0 : step < nq + nk ? 1 : 2;
-      const int h = slot + (step - (part == 0 ? 0 : part == 1 ? nq : nq + nk)) * S;
+    auto next = [&](uint4& ra, uint4& rb) {
       fetch(stage == 0 ? kDepth - 1 : stage - 1);
       copies_wait<kDepth - 1>();
-      const uint4 ra = sh.ring[stage][0][threadIdx.x], rb = sh.ring[stage][1][threadIdx.x];
+      ra = sh.ring[stage][0][threadIdx.x];
+      rb = sh.ring[stage][1][threadIdx.x];
       stage = stage == kDepth - 1 ? 0 : stage + 1;
-      const bool live = part == 0 ? h < A.Hq : h < Hkv && at_row.page >= 0;
-      const int64_t row = part == 0 ? t * A.Hq + h : cache_row(A.kv, at_row.page, h, at_row.slot);
-      if (part == 2) {
-        if (BITS == 16) {
-          if (live) {
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.v) + row * D;
-            *reinterpret_cast<uint4*>(y + va) = ra;
-            *reinterpret_cast<uint4*>(y + vb) = rb;
-          }
-        } else {
-          float x[16];
-          natural8(unpack8(ra), x);
-          natural8(unpack8(rb), x + 8);
-          store_codes<D>(x, A.kv.v, A.kv.vs, row, i, live);
-        }
-        continue;
-      }
-      Vec8 a = unpack8(ra), b = unpack8(rb);
+    };
+    // norm and rotation of the head in the next step
+    auto turned = [&](const float* w, Vec8& a, Vec8& b) {
+      uint4 ra, rb;
+      next(ra, rb);
+      a = unpack8(ra);
+      b = unpack8(rb);
       if (norm) {
-        const float* w = sh.w[part];
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
@@ -218,23 +249,61 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         }
       }
       turn(a, b, ang, m, A.inter);
-      if (part == 0 || BITS == 16) {
+    };
+    Vec8 a, b;
+    {
+      int h = slot + begin * S;
+      __nv_bfloat16* y = A.q_out + (t * A.Hq + h) * D + m.a;
+      for (int step = begin; step < min(end, nq); ++step, h += S, y += S * D) {
+        turned(sh.w[0], a, b);
+        if (h < A.Hq) {
+          *reinterpret_cast<uint4*>(y) = pack8(a);
+          *reinterpret_cast<uint4*>(y + m.b - m.a) = pack8(b);
+        }
+      }
+    }
+    const int64_t page_row = cache_row(A.kv, at_row.page, 0, at_row.slot);
+    for (int step = max(begin, nq); step < min(end, nq + nk); ++step) {
+      const int h = slot + (step - nq) * S;
+      const bool live = h < Hkv && at_row.page >= 0;
+      const int64_t row = page_row + (int64_t)h * A.kv.ps;
+      turned(sh.w[1], a, b);
+      if constexpr (BITS == 16) {
         if (live) {
-          __nv_bfloat16* y = (part == 0 ? A.q_out : static_cast<__nv_bfloat16*>(A.kv.k)) + row * D;
-          *reinterpret_cast<uint4*>(y + m.a) = pack8(a);
-          *reinterpret_cast<uint4*>(y + m.b) = pack8(b);
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.k) + row * D + m.a;
+          *reinterpret_cast<uint4*>(y) = pack8(a);
+          *reinterpret_cast<uint4*>(y + m.b - m.a) = pack8(b);
         }
       } else {  // groups of 32 lie across lanes: through shared memory into the values' order
-        float* keys = sh.k[BITS == 4 ? warp : 0];
-        natural8(a, keys + slot * D + m.a);
-        natural8(b, keys + slot * D + m.b);
+        float* keys = sh.k[warp];
+        store8(a, keys, slot * D + m.a);
+        store8(b, keys, slot * D + m.b);
         __syncwarp();
-        float x[16];
+        float v[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(keys + 16 * lane + e);
+          *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(keys + spread(16 * lane + e));
         __syncwarp();
-        store_codes<D>(x, A.kv.k, A.kv.ks, row, i, live);
+        store_codes<D>(v, A.kv.k, A.kv.ks, row, i, live);
+      }
+    }
+    for (int step = max(begin, nq + nk); step < end; ++step) {
+      const int h = slot + (step - nq - nk) * S;
+      const bool live = h < Hkv && at_row.page >= 0;
+      const int64_t row = page_row + (int64_t)h * A.kv.ps;
+      uint4 ra, rb;
+      next(ra, rb);
+      if constexpr (BITS == 16) {
+        if (live) {
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.v) + row * D;
+          *reinterpret_cast<uint4*>(y + va) = ra;
+          *reinterpret_cast<uint4*>(y + vb) = rb;
+        }
+      } else {
+        float v[16];
+        natural8(unpack8(ra), v);
+        natural8(unpack8(rb), v + 8);
+        store_codes<D>(v, A.kv.v, A.kv.vs, row, i, live);
       }
     }
   }
@@ -253,28 +322,45 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const 
   find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at);
   const int n = A.kv.Hkv * V;
   uint4* out[2] = {reinterpret_cast<uint4*>(A.k_out) + t * n, reinterpret_cast<uint4*>(A.v_out) + t * n};
+  // keys and values, two vectors of each at once on their way
+  const int64_t row0 = cache_row(A.kv, at.page, 0, at.slot);
+  constexpr int BATCH = 2;
+  for (int u0 = lane; u0 < n; u0 += 32 * BATCH) {
+    uint4 y[BATCH][2];
+    uint32_t w[BATCH][2];
+    __nv_bfloat16 sc[BATCH][2];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const void* pool = which ? A.kv.v : A.kv.k;
-    const __nv_bfloat16* scales = which ? A.kv.vs : A.kv.ks;
-#pragma unroll 4
-    for (int u = lane; u < n; u += 32) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (at.page >= 0) {
-        const int64_t row = cache_row(A.kv, at.page, u / V, at.slot);
-        if (BITS == 16) {
-          y = static_cast<const uint4*>(pool)[row * V + u % V];
-        } else {
-          const uint32_t w = static_cast<const uint32_t*>(pool)[row * V + u % V];
-          const __nv_bfloat162 sc = __bfloat162bfloat162(scales[row * (D / kGroup) + u % V / 4]);
-          const __nv_bfloat162 off = __hmul2(sc, __float2bfloat162_rn(-24.f));
-          const uint4 p = decode8(w, sc, off);
-          y = make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410), __byte_perm(p.x, p.y, 0x7632),
-                         __byte_perm(p.z, p.w, 0x7632));
+    for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const int u = u0 + 32 * k;
+        const void* pool = which ? A.kv.v : A.kv.k;
+        const int64_t row = row0 + (int64_t)(u / V) * A.kv.ps;
+        y[k][which] = make_uint4(0, 0, 0, 0);
+        w[k][which] = 0;
+        sc[k][which] = __ushort_as_bfloat16(0);
+        if (at.page >= 0 && u < n) {
+          if (BITS == 16) {
+            y[k][which] = static_cast<const uint4*>(pool)[row * V + u % V];
+          } else {
+            w[k][which] = static_cast<const uint32_t*>(pool)[row * V + u % V];
+            sc[k][which] = (which ? A.kv.vs : A.kv.ks)[row * (D / kGroup) + u % V / 4];
+          }
         }
       }
-      out[which][u] = y;
-    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const int u = u0 + 32 * k;
+        if (BITS == 4) {
+          const __nv_bfloat162 s2 = __bfloat162bfloat162(sc[k][which]);
+          const uint4 p = decode8(w[k][which], s2, __hmul2(s2, __float2bfloat162_rn(-24.f)));
+          y[k][which] = make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410),
+                                   __byte_perm(p.x, p.y, 0x7632), __byte_perm(p.z, p.w, 0x7632));
+        }
+        if (u < n) out[which][u] = y[k][which];
+      }
   }
 }
 
