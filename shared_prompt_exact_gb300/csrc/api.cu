@@ -722,6 +722,7 @@ int append_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride
   a.T = T;
   a.Hq = Hq;
   a.half = rope_dim / 2;
+  a.by_ps = FastDiv(cache->page_size);
   a.w0 = weight_offset;
   a.eps = eps;
   a.weight_f32 = weight_dtype == DUALKV_F32;
@@ -755,6 +756,7 @@ int read_impl(const dualkv_kv_cache* cache, const int32_t* pages, int max_pages,
   a.lens = lens;
   a.max_pages = max_pages;
   a.T = off[S];
+  a.by_ps = FastDiv(cache->page_size);
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
   a.v_out = static_cast<__nv_bfloat16*>(v_out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

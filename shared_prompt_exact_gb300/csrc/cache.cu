@@ -29,29 +29,46 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kDepth = 3;  // steps in a lane's ring, as in rope.cu
+constexpr int kResident = 152 * 2;  // blocks of the append that the GPU holds
 
-// Where row t of the call goes: its position, and its page and slot (page < 0: nowhere).
+// Where a row of the call goes: its position, its slot in a page, and the table's entry for that page, which is
+// held against the pool where it is used (-1: there is none).
 struct Place {
   uint32_t pos;
-  int page, slot;
+  int slot, entry;
+};
+// The stream's numbers for row t, and from them the row's place: two loads behind one another, so a warp that has
+// several rows asks for each a row ahead.
+struct StreamOf {
+  int s, len, start;
 };
 template <int CAP>
-__device__ __forceinline__ int index_of(const SegTable<CAP>& seg, const int32_t* lens, int t, int& s) {
-  s = seg_of(seg, t);
-  return lens[s] - (seg.off[s + 1] - t);
+__device__ __forceinline__ StreamOf stream_of(const SegTable<CAP>& seg, const int32_t* lens, const int32_t* starts, int64_t t,
+                                              int64_t T) {
+  StreamOf x{0, 0, 0};
+  if (t >= T) return x;
+  x.s = seg_of(seg, (int)t);
+  x.len = lens[x.s];
+  if (starts) x.start = starts[x.s];
+  return x;
 }
 template <int CAP>
-__device__ __forceinline__ void find_page(const PagedKV& kv, const SegTable<CAP>& seg, const int32_t* table,
-                                          int max_pages, int t, int s, int index, uint32_t* status, Place& at) {
-  at.page = -1;
-  at.slot = 0;
-  if (index < t - seg.off[s]) {  // the stream is said to hold fewer tokens than this call has of it
-    if (status) atomicOr(status, kDevErrBounds);
-    return;
-  }
-  const int place = index / kv.ps;
-  at.slot = index - place * kv.ps;
-  at.page = page_at(kv, table + (int64_t)s * max_pages, max_pages, place, status);
+__device__ __forceinline__ Place place_of(const StreamOf& x, const FastDiv& by_ps, const SegTable<CAP>& seg,
+                                          const int32_t* table, int max_pages, int64_t t, int64_t T) {
+  Place p{0, 0, -1};
+  if (t >= T) return p;
+  const int index = x.len - (seg.off[x.s + 1] - (int)t);
+  p.pos = (uint32_t)x.start + (uint32_t)index;
+  if (index < (int)t - seg.off[x.s]) return p;  // the stream is said to hold fewer tokens than this call has of it
+  const int page = by_ps(index);
+  p.slot = index - page * (int)by_ps.d;
+  if (page < max_pages) p.entry = table[(int64_t)x.s * max_pages + page];
+  return p;
+}
+__device__ __forceinline__ bool has_page(const PagedKV& kv, const Place& p, uint32_t* status) {
+  if ((uint32_t)p.entry < (uint32_t)kv.pages) return true;
+  if (status) atomicOr(status, kDevErrBounds);
+  return false;
 }
 
 // What a block of the append keeps in shared memory.
@@ -215,12 +232,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
   __syncthreads();
 
   int stage = 0;
+  Place coming = place_of(stream_of(seg, A.lens, A.starts, first, A.T), A.by_ps, seg, A.table, A.max_pages, first, A.T);
+  StreamOf after = stream_of(seg, A.lens, A.starts, first + stride, A.T);
   for (int64_t t = first; t < A.T; t += stride) {
-    int s;
-    const int index = index_of(seg, A.lens, (int)t, s);
-    Place at_row;
-    at_row.pos = (uint32_t)A.starts[s] + (uint32_t)index;
-    find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at_row);
+    const Place at_row = coming;
+    coming = place_of(after, A.by_ps, seg, A.table, A.max_pages, t + stride, A.T);
+    after = stream_of(seg, A.lens, A.starts, t + 2 * stride, A.T);
+    const bool stored = has_page(A.kv, at_row, A.status);
     const Angles ang = row_angles((int)at_row.pos, sh.freq, A.half, sh.cs[warp], sh.sn[warp], lane, m, A.inter);
     auto next = [&](uint4& ra, uint4& rb) {
       fetch(stage == 0 ? kDepth - 1 : stage - 1);
@@ -262,10 +280,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         }
       }
     }
-    const int64_t page_row = cache_row(A.kv, at_row.page, 0, at_row.slot);
+    const int64_t page_row = cache_row(A.kv, at_row.entry, 0, at_row.slot);
     for (int step = max(begin, nq); step < min(end, nq + nk); ++step) {
       const int h = slot + (step - nq) * S;
-      const bool live = h < Hkv && at_row.page >= 0;
+      const bool live = h < Hkv && stored;
       const int64_t row = page_row + (int64_t)h * A.kv.ps;
       turned(sh.w[1], a, b);
       if constexpr (BITS == 16) {
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
     }
     for (int step = max(begin, nq + nk); step < end; ++step) {
       const int h = slot + (step - nq - nk) * S;
-      const bool live = h < Hkv && at_row.page >= 0;
+      const bool live = h < Hkv && stored;
       const int64_t row = page_row + (int64_t)h * A.kv.ps;
       uint4 ra, rb;
       next(ra, rb);
@@ -316,14 +334,12 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   if (t >= A.T) return;
-  int s;
-  const int index = index_of(seg, A.lens, (int)t, s);
-  Place at;
-  find_page(A.kv, seg, A.table, A.max_pages, (int)t, s, index, A.status, at);
+  const Place at = place_of(stream_of(seg, A.lens, nullptr, t, A.T), A.by_ps, seg, A.table, A.max_pages, t, A.T);
+  const bool stored = has_page(A.kv, at, A.status);
   const int n = A.kv.Hkv * V;
   uint4* out[2] = {reinterpret_cast<uint4*>(A.k_out) + t * n, reinterpret_cast<uint4*>(A.v_out) + t * n};
   // keys and values, two vectors of each at once on their way
-  const int64_t row0 = cache_row(A.kv, at.page, 0, at.slot);
+  const int64_t row0 = cache_row(A.kv, at.entry, 0, at.slot);
   constexpr int BATCH = 2;
   for (int u0 = lane; u0 < n; u0 += 32 * BATCH) {
     uint4 y[BATCH][2];
@@ -339,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const 
         y[k][which] = make_uint4(0, 0, 0, 0);
         w[k][which] = 0;
         sc[k][which] = __ushort_as_bfloat16(0);
-        if (at.page >= 0 && u < n) {
+        if (stored && u < n) {
           if (BITS == 16) {
             y[k][which] = static_cast<const uint4*>(pool)[row * V + u % V];
           } else {
@@ -371,10 +387,13 @@ cudaError_t append_c(const AppendArgs& a, int S, const int32_t* off, cudaStream_
   const cudaError_t e = allow_shared<&append_kernel<D, BITS, CAP>>(a.device, smem);
   if (e != cudaSuccess) return e;
   const int heads = 512 / D, steps = (a.Hq + heads - 1) / heads + 2 * ((a.kv.Hkv + heads - 1) / heads);
-  const int64_t need = (a.T + kWarps - 1) / kWarps;
-  int64_t spare = 304 / need;
-  if (spare < 1) spare = 1;
-  const dim3 grid((unsigned)(need < 1824 ? need : 1824), (unsigned)(spare < steps ? spare : steps));
+  // few rows share their steps among block rows; from two resident blocks per SM on a warp takes several rows (a block
+  // needs some 2.5 us before its first), up to six rounds of blocks where there are more than 8 rows for each warp
+  const int64_t need = (a.T + kWarps - 1) / kWarps, spare = kResident / need;
+  int64_t rounds = need / (8 * kResident);
+  rounds = rounds < 1 ? 1 : rounds > 6 ? 6 : rounds;
+  const int64_t blocks = need <= kResident ? need : rounds * kResident;
+  const dim3 grid((unsigned)blocks, (unsigned)(spare < 1 ? 1 : spare < steps ? spare : steps));
   append_kernel<D, BITS, CAP><<<grid, kThreads, smem, st>>>(a, seg);
   return cudaGetLastError();
 }

@@ -218,6 +218,20 @@ struct PolicyArgs {
 cudaError_t launch_policy(bool backward, const PolicyArgs& a, int N, const int32_t* off, cudaStream_t st);
 size_t policy_workspace_bytes(int N, const int32_t* off);
 
+// Quotients of 0 <= x < 2^31 by a d that the host knows: with 2^s the first power of two from d on,
+// x / d = (x + floor(x m / 2^32)) / 2^s for m = floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv(int by = 1) : d((uint32_t)by), mul(0), shift(0) {
+    while ((1u << shift) < d) ++shift;
+    mul = (uint32_t)((((uint64_t)1 << 32) * ((((uint64_t)1) << shift) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int x) const {
+    return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+  }
+#endif
+};
 // ---- paged key/value cache (cache.cu)
 struct PagedKV {
   void *k, *v;              // [pages, Hkv, ps, D] bf16, or codes [pages, Hkv, ps, D / 2]
@@ -237,6 +251,7 @@ struct AppendArgs {
   int Hq, half;
   float w0, eps;
   bool weight_f32, inter;
+  FastDiv by_ps;
   uint32_t* status;
   int device;
 };
@@ -248,6 +263,7 @@ struct ReadArgs {
   int max_pages;
   int64_t T;
   __nv_bfloat16 *k_out, *v_out;  // contiguous
+  FastDiv by_ps;
   uint32_t* status;
 };
 cudaError_t launch_read(int D, const ReadArgs& a, int S, const int32_t* off, cudaStream_t st);
@@ -255,20 +271,6 @@ cudaError_t launch_read(int D, const ReadArgs& a, int S, const int32_t* off, cud
 // ---- attention of one token per response over the cache (decode.cu)
 constexpr int kMaxResponses = 8192;
 
-// Quotients of 0 <= x < 2^31 by a d that the host knows: with 2^s the first power of two from d on,
-// x / d = (x + floor(x m / 2^32)) / 2^s for m = floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery).
-struct FastDiv {
-  uint32_t d, mul, shift;
-  FastDiv(int by = 1) : d((uint32_t)by), mul(0), shift(0) {
-    while ((1u << shift) < d) ++shift;
-    mul = (uint32_t)((((uint64_t)1 << 32) * ((((uint64_t)1) << shift) - d)) / d + 1);
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ int operator()(int x) const {
-    return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
-  }
-#endif
-};
 struct DecodeArgs {
   const __nv_bfloat16* q;  // head h of response b at b * q_stride + h * D
   int64_t q_stride;        // elements
