@@ -835,7 +835,14 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   if ((rc = status_of_device(&a.status, &a.device))) return rc;
   CUtensorMap tk = {}, tv = {};
   if (D != 512 && prompts && G <= kBigGroups && B <= kBigResponses && head_rows <= INT32_MAX) {
-    for (int g = 0; g < G; ++g) a.big |= (uint64_t)(groups[g + 1] - groups[g]) * GQ >= kBigRows;
+    // by the tables' sizes; the kernels decide by the lengths
+    uint64_t work = 0;
+    const uint64_t most = (uint64_t)max_prompt_pages * (uint64_t)cache->page_size;
+    for (int g = 0; g < G; ++g) {
+      const uint64_t rows = (uint64_t)(groups[g + 1] - groups[g]) * GQ;
+      if (rows >= kBigRows) work += rows * most;
+    }
+    a.big = work * (uint64_t)Hkv >= kBigWork;
     if (a.big && cache->bits == 16) {
       if ((rc = ensure_encode())) return rc;
       if (make_tmap(&tk, cache->k, (int64_t)head_rows, 1, D, 16) || make_tmap(&tv, cache->v, (int64_t)head_rows, 1, D, 16))

@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const int warps = blockDim.x >> 5;
   extern __shared__ __align__(16) uint8_t smem[];
   const Sources src{reinterpret_cast<uint32_t*>(smem + warps * C::RING),
-                    reinterpret_cast<int*>(smem + warps * C::RING) + A.G + A.B + 1, nullptr};
+                    reinterpret_cast<int*>(smem + warps * C::RING) + A.G + A.B + 1,
+                    reinterpret_cast<int*>(smem + warps * C::RING) + 2 * (A.G + A.B) + 1};
   const uint32_t* cum = src.cum;
   __shared__ uint32_t scratch[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -522,15 +523,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   // which sources the row sees, as the kernels that left the partial results decided
   const int len = response_len(A, b, nullptr), P = prompt_len(A, g, nullptr);
   const bool sees_own = live && len > 0, sees_prompt = live && len >= 0 && first_position(A, P, len) < P;
-  const bool big = big_group(A, seg.off[g + 1] - seg.off[g]);
   const size_t own = own_slots(A.B, A.Hq);
   const int in_group = (b - seg.off[g]) * GQ + j;
   cudaGridDependencySynchronize();
   const Partial none{kLowest, 0.f, 0, 0};
   const Partial p0 = sees_prompt ? ws.partial[own / 2 + row] : none, p1 = sees_own ? ws.partial[row] : none;
+  const bool big = p0.worker & kBlockWorker;
   const int n = p0.parts + p1.parts;
   // slots of the workers behind a source's first one
-  const size_t behind0 = big ? own + kWarpSlots + (size_t)p0.worker * 128 + (in_group & 127)
+  const size_t behind0 = big ? own + kWarpSlots + (size_t)(p0.worker & ~kBlockWorker) * 128 + (in_group & 127)
                              : own + (size_t)p0.worker * cols + (in_group & (cols - 1));
   const size_t behind1 = own + (size_t)p1.worker * cols + (j & (cols - 1));
   auto place = [&](int i) {
@@ -611,7 +612,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   using C = Cfg<D, BITS, NT>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
   // many sources take the place of some warps' rings
-  const int cum = (2 * (a.G + a.B) + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
+  const int cum = (3 * a.G + 2 * a.B + 1) * (int)sizeof(uint32_t), room = (kMostShared - cum) / C::RING;
   const int warps = room < C::WARPS ? room : C::WARPS, smem = warps * C::RING + cum;
   cudaError_t e = allow_shared<&decode_kernel<D, BITS, NT, CAP>>(a.device, kMostShared);
   if (e != cudaSuccess) return e;

@@ -70,7 +70,8 @@ __device__ __forceinline__ int tiles_of(int lo, int end) {
 }
 
 // A partial result of one row: its maximum (base 2) and sum, and at a source's first tile who goes on with
-// the source: `parts` partial results, of this worker and of those behind it.
+// the source: `parts` partial results, of this worker (kBlockWorker: a block of prompt.cu) and of those behind it.
+constexpr uint32_t kBlockWorker = 0x80000000u;
 struct alignas(16) Partial {
   float m, l;
   uint32_t worker;
@@ -94,29 +95,30 @@ __host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
   return w;
 }
 
-// Whether a prompt is left to prompt.cu's kernel, which takes 128 of its rows at once.
-__device__ __forceinline__ bool big_group(const DecodeArgs& A, int responses) {
-  return A.big && responses * (int)A.by_heads.d >= kBigRows;
-}
-
 // What a block knows of the sources, in shared memory.
 struct Sources {
   uint32_t* cum;  // [n + 1] tiles before each source, of one kv-head
   int* len;       // [n] tokens of the prompts (0 .. G - 1) and of the responses (negative: ended)
-  int* least;     // BIG: [G] fewest tokens of a group's response that has not ended, or INT_MAX
+  int* first;     // [G] first token of the prompt that a response of the group sees; the prompt's length if none does
 };
 
 // First token of its own that a response of n tokens sees.
 __device__ __forceinline__ int first_own(const DecodeArgs& A, int n) { return A.window > 0 ? max(0, n - A.window) : 0; }
 
-// Fills in the above, by the whole block.  BIG: tiles of the prompts that big_group names alone, n = G; else of the
-// other prompts and of all responses, n = G + B.  Lengths are kept of all sources either way.
+// Fills in the above, by the whole block.  BIG: the tiles that prompt.cu's kernel takes, of prompts of groups with kBigRows
+// rows and more, n = G; else those of the other prompts and of all responses, n = G + B.  Lengths are kept of all
+// sources either way.  Both kernels come to the same decision, from the same numbers.
 template <int COLS, int TILE, bool BIG, int CAP>
 __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
                                              uint32_t* scratch) {
+  __shared__ unsigned long long work;  // tokens times rows of large groups
   const int G = A.G, n = BIG ? A.G : A.G + A.B, GQ = (int)A.by_heads.d, tid = threadIdx.x, THREADS = blockDim.x;
   const int lane = tid & 31, warp = tid >> 5;
   uint32_t* cum = src.cum;
+  if (tid == 0) {
+    work = 0;
+    cum[0] = 0;
+  }
 #pragma unroll 2
   for (int i = tid; i < G + A.B; i += THREADS)
     src.len[i] = i < G ? prompt_len(A, i, A.status) : response_len(A, i - G, A.status);
@@ -137,16 +139,20 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
     }
     least = __reduce_min_sync(0xffffffffu, least);
     if (lane == 0) {
-      uint32_t tiles = 0;
-      if (BIG) src.least[g] = (int)least;
-      if (least != 0x7fffffffu && big_group(A, to - from) == BIG) {
-        const int P = src.len[g];
-        tiles = (uint32_t)tiles_of<TILE>(first_position(A, P, (int)least), P) * (uint32_t)(((to - from) * GQ + COLS - 1) / COLS);
-      }
-      cum[1 + g] = tiles;
+      const int P = src.len[g], rows = (to - from) * GQ;
+      const int first = least == 0x7fffffffu ? P : min(P, first_position(A, P, (int)least));
+      src.first[g] = first;
+      if (A.big && rows >= kBigRows && first < P)
+        atomicAdd(&work, (unsigned long long)(P - first) * (unsigned long long)rows);
     }
   }
-  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+  const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= kBigWork;
+  for (int g = tid; g < G; g += THREADS) {
+    const int rows = (seg.off[g + 1] - seg.off[g]) * GQ;
+    const bool mine = (big && rows >= kBigRows) == BIG;
+    cum[1 + g] = mine ? (uint32_t)tiles_of<TILE>(src.first[g], src.len[g]) * (uint32_t)((rows + COLS - 1) / COLS) : 0u;
+  }
   __syncthreads();
   // inclusive scan of cum[1 .. n]: every thread takes a run
   const int per = n <= THREADS ? 1 : (n + THREADS - 1) / THREADS, from = 1 + tid * per, to = min(n + 1, from + per);

@@ -286,11 +286,16 @@ struct DecodeArgs {
   uint32_t* status;
   FastDiv by_ps, by_heads;  // by the page size and by Hq / Hkv
   int device;
-  bool big;          // some prompts go to launch_prompt: of groups with kBigRows rows (responses x Hq / Hkv) or more
+  bool big;          // launch_prompt's kernel runs before and takes the prompts that are worth it
 };
-// A group's prompt is worth the tensor cores' large tiles from here on.
+// Prompts of groups with this many rows and more go to launch_prompt's kernel ...
 constexpr int kBigRows = 32;
-constexpr int kBigGroups = 512;    // most groups of a call whose prompts may go there: their lengths are in shared memory
+// ... where the tokens that the groups see times their rows and the kv-heads come to this much.  Two groups of 32 responses
+// with 8 kv-heads of 128, 4 rows each, over 400 / 1,600 / 6,400 tokens of prompt (0.8, 3.3, 13 M): 26 / 34 / 43 us
+// there, 21 / 36 / 95 us by decode.cu's warps alone in bf16; 26 / 34 / 38 and 19 / 29 / 60 in 4 bits; 4 kv-heads of 64:
+// 18 / 20 / 24 and 13 / 17 / 31 (0.4, 1.6, 6.6 M).
+constexpr unsigned long long kBigWork = 4000000;
+constexpr int kBigGroups = 512;      // most groups of a call with that kernel: their lengths are in shared memory
 constexpr int kBigResponses = 4096;  // and most responses
 // tk, tv: views (make_tmap, boxes of 16 rows) of the bf16 pools, used where a.big and the cache holds bf16
 cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,

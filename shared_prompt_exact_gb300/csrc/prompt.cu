@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     at += (uint64_t)(t1 - t0);
     s.r0 = begin_row + block * C::BM;
     s.P = src.len[s.g];
-    s.lo = first_position(A, s.P, src.least[s.g]);
+    s.lo = src.first[s.g];
     const int tile0 = (s.P + C::BN - 1) / C::BN - tiles;
     s.first = tile0 + t0;
     s.last = tile0 + t1;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         }
       }
       if (lane == 0) mbar_arrive(&ctl.q_free);
-      if (r < s.row_end && half == 0) ws.partial[to] = Partial{mref, l0 * f0 + l1 * f1, blockIdx.x, s.parts};
+      if (r < s.row_end && half == 0) ws.partial[to] = Partial{mref, l0 * f0 + l1 * f1, kBlockWorker | blockIdx.x, s.parts};
     }
   } else {
     if (BITS == 4) registers_down<48>();  // the whole warpgroup, idle warps too
