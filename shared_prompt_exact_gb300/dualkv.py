@@ -664,25 +664,30 @@ class KVCache:
     (uint8 [pages, Hkv, page_size, D / 2]), with bf16 scales [pages, Hkv, page_size, D / 32].  It wraps tensors
     that the caller owns; ``KVCache.empty`` allocates them."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "bits", "pages", "Hkv", "page_size", "D", "device", "_c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "Hkv", "page_size", "D", "device", "_c")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if not isinstance(k, _Tensor) or not k.is_cuda or k.dim() != 4:
             raise ValueError("KVCache: k must be a CUDA tensor [pages, heads, page size, values]")
-        if (k_scale is None) != (v_scale is None):
-            raise ValueError("KVCache: k_scale and v_scale go together")
-        dev, shape = k.get_device(), k.shape
+        shape, dev = k.shape, k.get_device()
         pages, Hkv, ps, width = shape
-        dtypes = _BF16 if k_scale is None else _U8
-        struct = _CacheStruct(_arg("KVCache", "k", k, shape, dtypes, dev), _arg("KVCache", "v", v, shape, dtypes, dev),
-                              None, None, pages, ps, 16)
-        if k_scale is not None:
-            groups = (pages, Hkv, ps, 2 * width // CACHE_GROUP)
-            struct.k_scale = _arg("KVCache", "k_scale", k_scale, groups, _BF16, dev)
-            struct.v_scale = _arg("KVCache", "v_scale", v_scale, groups, _BF16, dev)
-            struct.bits, width = 4, 2 * width
+        if k_scale is None and v_scale is None:
+            struct = _CacheStruct(_arg("KVCache", "k", k, shape, _BF16, dev), _arg("KVCache", "v", v, shape, _BF16, dev),
+                                  None, None, pages, ps, 16)
+        elif k_scale is None or v_scale is None:
+            raise ValueError("KVCache: k_scale and v_scale go together")
+        else:
+            width *= 2
+            groups = (pages, Hkv, ps, width // CACHE_GROUP)
+            struct = _CacheStruct(_arg("KVCache", "k", k, shape, _U8, dev), _arg("KVCache", "v", v, shape, _U8, dev),
+                                  _arg("KVCache", "k_scale", k_scale, groups, _BF16, dev),
+                                  _arg("KVCache", "v_scale", v_scale, groups, _BF16, dev), pages, ps, 4)
         self.k, self.v, self.k_scale, self.v_scale, self.device, self._c = k, v, k_scale, v_scale, dev, struct
-        self.bits, self.pages, self.Hkv, self.page_size, self.D = struct.bits, pages, Hkv, ps, width
+        self.pages, self.Hkv, self.page_size, self.D = pages, Hkv, ps, width
+
+    @property
+    def bits(self):
+        return self._c.bits
 
     @classmethod
     def empty(cls, pages, Hkv, page_size, D, bits=16, device="cuda"):
@@ -710,10 +715,13 @@ def _cache_arg(where, cache, Hkv, D, device):
 
 def _table(where, name, pages, streams, device):
     """Address and width of a page table."""
+    if isinstance(pages, _Tensor) and pages.dtype == torch.int32 and pages.is_contiguous() and pages.get_device() == device:
+        shape = pages.shape
+        if len(shape) == 2 and shape[0] == streams and shape[1] < _TOO_FAR:
+            return pages.data_ptr(), shape[1]
     if not isinstance(pages, _Tensor) or pages.dim() != 2 or pages.shape[1] >= _TOO_FAR:
         raise ValueError(f"{where}: {name} must be a tensor [streams, most pages]")
-    width = pages.shape[1]
-    return _arg(where, name, pages, (streams, width), _I32, device), width
+    _refuse(where, name, pages, torch.Size((streams, pages.shape[1])), _I32, device, "must be contiguous")
 
 
 def _last_offset(where, name, n, offsets):
@@ -735,7 +743,7 @@ def dualkv_cache_append(q, k, v, q_weight, k_weight, weight_offset, eps, inv_fre
     S, rope_dim = int(S), int(rope_dim)
     T = _last_offset(where, "row_offsets", S, row_offsets)
     dev = torch.cuda.current_device()
-    if max(Hq, Hkv, D, rope_dim) >= _TOO_FAR:
+    if Hq >= _TOO_FAR or Hkv >= _TOO_FAR or D >= _TOO_FAR or rope_dim >= _TOO_FAR:
         _counts(where, Hq=Hq, Hkv=Hkv, D=D, rope_dim=rope_dim)
     inner = (D, 1)
     qkv = (_rows(where, "q", q, (T, Hq, D), inner, _BF16, dev) + _rows(where, "k", k, (T, Hkv, D), inner, _BF16, dev)
@@ -789,7 +797,7 @@ def dualkv_decode(q, cache, prompt_pages, prompt_lens, pages, lens, G, groups, H
     G = int(G)
     B = _last_offset(where, "groups", G, groups)
     dev = torch.cuda.current_device()
-    if max(Hq, Hkv, D, abs(window)) >= _TOO_FAR:
+    if Hq >= _TOO_FAR or Hkv >= _TOO_FAR or D >= _TOO_FAR or not -_TOO_FAR <= window < _TOO_FAR:
         _counts(where, Hq=Hq, Hkv=Hkv, D=D, window=window)
     if (prompt_pages is None) != (prompt_lens is None):
         raise ValueError(f"{where}: prompt_pages and prompt_lens go together")
