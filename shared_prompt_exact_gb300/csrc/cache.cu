@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         (part == 2 ? va : m.a);
   };
   place_copies();
+  cudaGridDependencySynchronize();
   auto fetch = [&](int stage) {
     if (at < A.T) {
       if (h_at < heads_at) {
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs A, const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
   if (t >= A.T) return;
+  cudaGridDependencySynchronize();
   const Place at = place_of(stream_of(seg, A.lens, nullptr, t, A.T), A.by_ps, seg, A.table, A.max_pages, t, A.T);
   const bool stored = has_page(A.kv, at, A.status);
   const int n = A.kv.Hkv * V;
@@ -394,15 +396,13 @@ cudaError_t append_c(const AppendArgs& a, int S, const int32_t* off, cudaStream_
   rounds = rounds < 1 ? 1 : rounds > 6 ? 6 : rounds;
   const int64_t blocks = need <= kResident ? need : rounds * kResident;
   const dim3 grid((unsigned)blocks, (unsigned)(spare < 1 ? 1 : spare < steps ? spare : steps));
-  append_kernel<D, BITS, CAP><<<grid, kThreads, smem, st>>>(a, seg);
-  return cudaGetLastError();
+  return launch_behind_shared(append_kernel<D, BITS, CAP>, grid, dim3(kThreads), smem, st, a, seg);
 }
 
 template <int D, int BITS, int CAP>
 cudaError_t read_c(const ReadArgs& a, int S, const int32_t* off, cudaStream_t st) {
   const SegTable<CAP> seg = make_segs<CAP>(0, S, off);
-  read_kernel<D, BITS, CAP><<<(unsigned)((a.T + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, seg);
-  return cudaGetLastError();
+  return launch_behind(read_kernel<D, BITS, CAP>, dim3((unsigned)((a.T + kWarps - 1) / kWarps)), dim3(kThreads), st, a, seg);
 }
 
 template <int D, int CAP>

@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = (int)A.by_heads.d, sources = A.G + A.B;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  if (!A.big) cudaGridDependencySynchronize();  // else prompt.cu's kernel has seen to it before this one could start
   deal_sources<C::COLS, C::TILE, false>(A, seg, src, scratch);
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);
   // neighbouring shares go to different SMs, so that a short batch spreads over all of them
@@ -621,17 +622,9 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
       if ((e = launch_prompt(D, a, tk, tv, groups, st)) != cudaSuccess) return e;
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kBlocks);
-  cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute behind;
-  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  behind.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &behind;
-  cfg.numAttrs = a.big ? 1 : 0;
-  if ((e = cudaLaunchKernelEx(&cfg, decode_kernel<D, BITS, NT, CAP>, a, seg)) != cudaSuccess) return e;
+  if ((e = launch_behind_shared(decode_kernel<D, BITS, NT, CAP>, dim3(kBlocks), dim3(warps * 32), smem, st, a, seg)) !=
+      cudaSuccess)
+    return e;
   // few rows can have many partial results each: as many warps to a row as there are warps for, in blocks of 4 or more
   const int64_t rows = (int64_t)a.B * a.Hq, spare = kBlocks * kJoinWarps / rows;
   const int share = spare >= 16 ? 16 : spare >= 8 ? 8 : spare >= 4 ? 4 : spare >= 2 ? 2 : 1, per = share < 4 ? 4 / share : 1;

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  cudaGridDependencySynchronize();
   deal_sources<128, 128, true>(A, seg, src, ctl.scratch);  // ends with a barrier
   tc_fence_after();
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
@@ -540,8 +541,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
   const int smem = C::RINGS + 1024 + (3 * a.G + a.B + 1) * (int)sizeof(uint32_t);
   const cudaError_t e = allow_shared<&prompt_kernel<D, BITS, CAP>>(a.device, C::MOST_SHARED);
   if (e != cudaSuccess) return e;
-  prompt_kernel<D, BITS, CAP><<<kBlocks, C::THREADS, smem, st>>>(tk, tv, a, seg);
-  return cudaGetLastError();
+  return launch_behind_shared(prompt_kernel<D, BITS, CAP>, dim3(kBlocks), dim3(C::THREADS), smem, st, tk, tv, a, seg);
 }
 
 template <int D, int BITS>

@@ -167,6 +167,12 @@ LONG = [
                                             ps=128)),
     ("many short responses", dict(groups=list(range(0, 1201, 2)), prompts=_ragged(600, 0, 30, 7), lens=_ragged(1200, -1, 40, 8),
                                   Hq=2, Hkv=1, D=64, ps=16)),
+    ("prompt by the block kernel", dict(groups=[0, 40, 41], prompts=[7_001, 130], lens=_ragged(41, -1, 300, 13), Hq=32, Hkv=8,
+                                        D=128, ps=64)),
+    ("its rows in several blocks", dict(groups=[0, 60, 75, 80], prompts=[3_003, 2_050, 4_000], lens=_ragged(80, 0, 200, 14), Hq=21,
+                                        Hkv=3, D=64, ps=48)),
+    ("block kernel under a window", dict(groups=[0, 50, 90], prompts=[6_000, 5_555], lens=_ragged(90, 0, 1400, 15), Hq=32, Hkv=8,
+                                         D=64, ps=16, window=1300)),
     ("wide and long", dict(groups=[0, 8], prompts=[3_000], lens=_ragged(8, 0, 900, 9), Hq=8, Hkv=2, D=512, ps=64)),
 ]
 
@@ -231,6 +237,41 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_graphs():
     c.check(out, lse)
 
 
+def test_in_graphs_behind_copies_and_other_kernels():
+    # the calls' kernels may start before what is in front of them is done: copies, fills and other kernels whose results
+    # they need, in a captured graph and out of it
+    c = Case([0, 16], [900], _ragged(16, 1, 300, 42), 8, 2, 128, 32, 16, seed=43)
+    big = Case([0, 32], [3000], _ragged(32, 1, 300, 44), 32, 8, 128, 64, 16, seed=45)
+    for x in (c, big):
+        want, want_lse = x.run()
+        lens, q = x.d_lens.clone(), x.q.clone()
+        ws = torch.empty(dk.dualkv_decode_workspace_bytes(x.G, x.groups, x.Hq, x.Hkv, x.D), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+        big_fill = torch.empty(1 << 26, device="cuda")
+
+        def step():
+            big_fill.fill_(1.0)      # takes long enough that a kernel that did not wait would be caught
+            x.d_lens.copy_(lens)
+            x.q.copy_(q)
+            dk.dualkv_decode(x.q, x.cache, x.d_tables[0], x.d_prompts, x.d_tables[1], x.d_lens, x.G, x.groups, x.Hq, x.Hkv, x.D,
+                             x.scale, 0, out, lse, ws)
+            x.q.zero_()              # and what comes behind waits for them
+            x.d_lens.fill_(-1)
+
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(want, out) and torch.equal(want_lse, lse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(want, out) and torch.equal(want_lse, lse)
+    dk.dualkv_check_status()
+
+
 def test_lengths_beyond_the_tables_and_pages_that_do_not_exist():
     c = Case([0, 4], [40], [30, 20, 10, 50], 4, 2, 64, 16, 16, seed=50)
     out, lse = c.run()
@@ -245,6 +286,28 @@ def test_lengths_beyond_the_tables_and_pages_that_do_not_exist():
         assert torch.equal(bad_out[b], out[b]) and torch.equal(bad_lse[:, b], lse[:, b])
     # response 1 as if its tokens 16 .. 19 were not there, in place of counting what lies elsewhere
     assert bool(torch.isfinite(bad_out[1]).all()) and bool((bad_lse[:, 1] <= lse[:, 1]).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pools_past_32_bit_offsets(bits):
+    # pages at both ends of a pool of 2.4 G values, the last ones beyond 2^31 values (4 bits: 2^30 bytes of codes); the
+    # same tokens in a small pool give the same bits
+    ps, Hkv, Hq, D = 64, 8, 32, 128
+    c = Case([0, 2, 40], [300, 4000], _ragged(40, 0, 200, 60), Hq, Hkv, D, ps, bits, seed=61)
+    want, want_lse = c.run()
+    pool = 37_000
+    far = dk.KVCache.empty(pool, Hkv, ps, D, bits)
+    move = torch.arange(c.cache.pages, device="cuda") * 3
+    move[::2] = pool - 1 - move[::2]
+    pairs = [(far.k, c.cache.k), (far.v, c.cache.v)]
+    if bits == 4:
+        pairs += [(far.k_scale, c.cache.k_scale), (far.v_scale, c.cache.v_scale)]
+    for a, b in pairs:
+        a[move] = b
+    tables = [torch.where(t >= 0, move[t.long().clamp(min=0)], -1).to(torch.int32) for t in c.d_tables]
+    out, lse = dk.decode(c.q, far, tables[0], c.d_prompts, tables[1], c.d_lens, c.groups)
+    dk.dualkv_check_status()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
 def test_without_prompts_and_without_lse():
