@@ -94,8 +94,9 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return r;
 }
 
-// Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.
-__device__ __forceinline__ uint2 quantise16(const float (&x)[16], __nv_bfloat16& scale) {
+// Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.  `ties`: the values are bf16, so
+// they can lie half way between two multiples of the step.
+__device__ __forceinline__ uint2 quantise16(const float (&x)[16], bool ties, __nv_bfloat16& scale) {
   float hi = max3(x[0], x[1], x[2]), lo = min3(x[0], x[1], x[2]);
 #pragma unroll
   for (int e = 3; e < 15; e += 2) {
@@ -108,16 +109,17 @@ __device__ __forceinline__ uint2 quantise16(const float (&x)[16], __nv_bfloat16&
   const bool finite = top < __uint_as_float(0x7f800000u);  // false for NaN
   scale = __ushort_as_bfloat16((unsigned short)(finite ? bits >> 16 : 0x7fc0u));
   if (!finite || bits == 0u) return make_uint2(0x88888888u, 0x88888888u);  // not finite, or zeros
-  // x / step by the smallest float above 1 / step: a value half way between two multiples comes out above it (away from
-  // zero) and goes to the farther one, any other value is moved by 2^-23 of it at most.  The sum with 1.5 x 2^23 + 8
-  // is rounded to a whole number, whose low bits are n + 8; the eight codes are shifted together with the
-  // upper bits in place, which are subtracted at once.
+  // x / step by the reciprocal.  bf16 values take the smallest float above it: one half way comes out above (away
+  // from zero) and goes to the farther multiple, any other is moved by 2^-23 of it at most, less than it is away from half
+  // way.  Values of fp32 take the nearest float, which moves them by 2^-24.  The sum with 1.5 x 2^23 + 8 is rounded to
+  // a whole number, whose low bits are n + 8; the eight codes are shifted together with the upper bits in place,
+  // which are subtracted at once.
   float up = 1.f, step = __uint_as_float(bits);
   if (step < 1e-36f) {  // its reciprocal could overflow: the same with both 2^64 times as large
     up = 0x1p64f;
     step *= up;
   }
-  const float inv = __uint_as_float(__float_as_uint(__frcp_rd(step)) + 1u);
+  const float inv = ties ? __uint_as_float(__float_as_uint(__frcp_rd(step)) + 1u) : __frcp_rn(step);
   uint32_t out[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -161,10 +163,10 @@ __device__ __forceinline__ void store8(const Vec8& v, float* base, int p) {
 
 // 16 values from natural order into a row of the 4-bit pools.
 template <int D>
-__device__ __forceinline__ void store_codes(const float (&x)[16], void* codes, __nv_bfloat16* scales, int64_t row, int i,
+__device__ __forceinline__ void store_codes(const float (&x)[16], bool ties, void* codes, __nv_bfloat16* scales, int64_t row, int i,
                                             bool live) {
   __nv_bfloat16 scale;
-  const uint2 c = quantise16(x, scale);
+  const uint2 c = quantise16(x, ties, scale);
   if (!live) return;
   *reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + row * (D / 2) + 8 * i) = c;
   if ((i & 1) == 0) scales[row * (D / kGroup) + i / 2] = scale;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
     for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
       const void* w = d < D ? A.q_weight : A.k_weight;
       const int e = d % D;
-      sh.w[d / D][split_at(e, D)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
+      sh.w[d / D][split_at(e, D)] = (BITS == 4 && d >= D ? 0.f : A.w0) + (A.weight_f32 ? static_cast<const float*>(w)[e]
                                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]));
     }
   }
@@ -248,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       rb = sh.ring[stage][1][threadIdx.x];
       stage = stage == kDepth - 1 ? 0 : stage + 1;
     };
-    // norm and rotation of the head in the next step
-    auto turned = [&](const float* w, Vec8& a, Vec8& b) {
+    // norm and rotation of the head in the next step; `codes`: for 4 bits
+    auto turned = [&](const float* w, bool codes, Vec8& a, Vec8& b) {
       uint4 ra, rb;
       next(ra, rb);
       a = unpack8(ra);
@@ -258,13 +260,26 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
-        const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
-        const float2 rr = make_float2(r, r);
+        const float mean = group_sum<G>(ss) * (1.f / D) + A.eps;
+        float r = rsqrtf(mean);
+        if (codes) {
+          // one step of Newton's method with the product's rounding error: the root's last bits decide which values pass
+          // half way between two multiples (an error of 2^-23 moves one value in 5 million to the other one)
+          const float h = mean * r, low = fmaf(mean, r, -h);
+          r = fmaf(0.5f * r, fmaf(-h, r, 1.f) - low * r, r);
+        }
+        const float2 rr = make_float2(r, r), w0 = make_float2(A.w0, A.w0);
         const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
-          b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
+          if (codes) {  // x r w + x r w0: the weights are not rounded with their offset
+            const float2 x = fmul2(a.v[e], rr), z = fmul2(b.v[e], rr);
+            a.v[e] = ffma2(x, wa.v[e], fmul2(x, w0));
+            b.v[e] = ffma2(z, wb.v[e], fmul2(z, w0));
+          } else {
+            a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
+            b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
+          }
         }
       }
       turn(a, b, ang, m, A.inter);
@@ -274,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       int h = slot + begin * S;
       __nv_bfloat16* y = A.q_out + (t * A.Hq + h) * D + m.a;
       for (int step = begin; step < min(end, nq); ++step, h += S, y += S * D) {
-        turned(sh.w[0], a, b);
+        turned(sh.w[0], false, a, b);
         if (h < A.Hq) {
           *reinterpret_cast<uint4*>(y) = pack8(a);
           *reinterpret_cast<uint4*>(y + m.b - m.a) = pack8(b);
@@ -286,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       const int h = slot + (step - nq) * S;
       const bool live = h < Hkv && stored;
       const int64_t row = page_row + (int64_t)h * A.kv.ps;
-      turned(sh.w[1], a, b);
+      turned(sh.w[1], BITS == 4, a, b);
       if constexpr (BITS == 16) {
         if (live) {
           __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.k) + row * D + m.a;
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         for (int e = 0; e < 16; e += 4)
           *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(keys + spread(16 * lane + e));
         __syncwarp();
-        store_codes<D>(v, A.kv.k, A.kv.ks, row, i, live);
+        store_codes<D>(v, !norm, A.kv.k, A.kv.ks, row, i, live);
       }
     }
     for (int step = max(begin, nq + nk); step < end; ++step) {
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         float v[16];
         natural8(unpack8(ra), v);
         natural8(unpack8(rb), v + 8);
-        store_codes<D>(v, A.kv.v, A.kv.vs, row, i, live);
+        store_codes<D>(v, true, A.kv.v, A.kv.vs, row, i, live);
       }
     }
   }
