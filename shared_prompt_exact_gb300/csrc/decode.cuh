@@ -22,10 +22,10 @@ struct Deal {
   uint64_t total, chunk;  // tiles of all kv-heads, and those of one worker: worker w has w chunk .. (w + 1) chunk - 1
   uint32_t per_head;
 };
-// a / b.  Small operands go through fp32: the quotient is off by one at most (an integer division is
-// a call of some 250 cycles, and a warp needs five before its first tile).
+// a / b.  Operands below 2^21 go through fp32, whose quotient is off by 2 units in the last place, so by half at most,
+// and its whole part by one (an integer division takes some 250 cycles, and a warp needs five before its first tile).
 __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
-  if ((a | b) >> 24 == 0) {
+  if ((a | b) >> 21 == 0) {
     uint32_t q = (uint32_t)__fdividef((float)(uint32_t)a, (float)(uint32_t)b);
     const int r = (int)(uint32_t)a - (int)(q * (uint32_t)b);
     if (r < 0) --q;

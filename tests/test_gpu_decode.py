@@ -63,6 +63,9 @@ class Case:
         self._spoil()
         q = rn(self.B, Hq * D + (64 if strided else 0)).to(BF)
         self.q = q[:, :Hq * D].view(self.B, Hq, D) if strided else q.view(self.B, Hq, D)
+        for b, n in enumerate(lens):  # nothing of a response that has ended is used
+            if n < 0:
+                self.q[b] = float("nan")
         i32 = lambda t: torch.tensor(t, dtype=torch.int32, device="cuda")  # noqa: E731
         self.d_tables = [torch.from_numpy(t).cuda() for t in self.tables]
         self.d_prompts, self.d_lens = i32(prompts), i32(lens)
@@ -113,7 +116,7 @@ class Case:
             assert np.all(np.abs(out[b] - want) <= tol), (b, float(np.max(np.abs(out[b] - want) - tol)))
             empty = np.isneginf(want_lse)
             assert np.array_equal(np.isneginf(lse[:, b]), empty)
-            e = np.abs(lse[:, b] - want_lse)[~empty]
+            e = np.abs(lse[~empty, b] - want_lse[~empty])
             assert np.all(e <= (d + 2.0 ** -20 + 4 * U * np.abs(np.where(empty, 0, want_lse)))[~empty]), (b, e.max())
 
 
