@@ -105,10 +105,25 @@ struct Sources {
 // First token of its own that a response of n tokens sees.
 __device__ __forceinline__ int first_own(const DecodeArgs& A, int n) { return A.window > 0 ? max(0, n - A.window) : 0; }
 
+// Tiles that a block of COLS rows of a prompt sees under a window: from the first token that one of its responses does on.
+template <int COLS, int TILE, int CAP>
+__device__ __forceinline__ int block_tiles(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src, int g,
+                                           int block) {
+  const int GQ = (int)A.by_heads.d, P = src.len[g], row = seg.off[g] * GQ + block * COLS;
+  const int last = min(row + COLS, seg.off[g + 1] * GQ) - 1;
+  int first = P;
+  for (int b = A.by_heads(row); b <= A.by_heads(last); ++b) {
+    const int len = src.len[A.G + b];
+    if (len >= 0) first = min(first, first_position(A, P, len));
+  }
+  return tiles_of<TILE>(first, P);
+}
+
 // Fills in the above, by the whole block.  BIG: the tiles that prompt.cu's kernel takes, of prompts of groups with kBigRows
 // rows and more, n = G; else those of the other prompts and of all responses, n = G + B.  Lengths are kept of all
-// sources either way.  Both kernels come to the same decision, from the same numbers.
-template <int COLS, int TILE, bool BIG, int CAP>
+// sources either way.  Both kernels come to the same decision, from the same numbers.  BLOCKS: under a window, each
+// block of a prompt's rows counts its own tiles.
+template <int COLS, int TILE, bool BIG, bool BLOCKS, int CAP>
 __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
                                              uint32_t* scratch) {
   __shared__ unsigned long long work;  // tokens times rows of large groups
@@ -148,7 +163,17 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
   }
   __syncthreads();
   const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= kBigWork;
-  for (int g = tid; g < G; g += THREADS) {
+  if (BLOCKS) {
+    for (int g = warp; g < G; g += THREADS >> 5) {
+      const int rows = (seg.off[g + 1] - seg.off[g]) * GQ, blocks = (rows + COLS - 1) / COLS;
+      uint32_t tiles = 0;
+      if (!(big && rows >= kBigRows) && src.first[g] < src.len[g])
+        for (int i = lane; i < blocks; i += 32) tiles += (uint32_t)block_tiles<COLS, TILE>(A, seg, src, g, i);
+      tiles = __reduce_add_sync(0xffffffffu, tiles);
+      if (lane == 0) cum[1 + g] = tiles;
+    }
+  }
+  for (int g = tid; g < G && !BLOCKS; g += THREADS) {
     const int rows = (seg.off[g + 1] - seg.off[g]) * GQ;
     const bool mine = (big && rows >= kBigRows) == BIG;
     cum[1 + g] = mine ? (uint32_t)tiles_of<TILE>(src.first[g], src.len[g]) * (uint32_t)((rows + COLS - 1) / COLS) : 0u;

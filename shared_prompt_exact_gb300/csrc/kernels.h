@@ -300,6 +300,7 @@ constexpr int kBigResponses = 4096;  // and most responses
 // tk, tv: views (make_tmap, boxes of 16 rows) of the bf16 pools, used where a.big and the cache holds bf16
 cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
                           cudaStream_t st);
+cudaError_t launch_walk_window(int D, const DecodeArgs& a, const int32_t* groups, cudaStream_t st);
 cudaError_t launch_prompt(int D, const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const int32_t* groups,
                           cudaStream_t st);
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D);
