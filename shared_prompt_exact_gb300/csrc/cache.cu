@@ -13,6 +13,10 @@
 // Both touch each value once and are bound by HBM bandwidth (few rows: by latency).  The walk over
 // rows and heads, the loads ahead through shared memory and the arithmetic are rope.cu's: one warp per
 // row, q's heads first, then k's, then v's.  Keys are quantised from fp32, before any rounding to bf16.
+// Measured: append of 71,680 rows of 32 + 2 x 8 heads of 128 in bf16 267 us (6.6 TB/s), of 23,200 rows of 8 + 2 x 2 heads of
+// 512 in 4 bits 90 us (5.6 TB/s: bound by issue, 2,650 instructions a row; 122 us with a division and a comparison
+// for every code, 99 with a row's place found when it is needed); read of 131,072 rows of 8 heads of 128 156 us (6.9 TB/s; 177
+// with the values asked for behind the keys).
 #include <cuda_bf16.h>
 
 #include "cache.cuh"

@@ -10,6 +10,9 @@ namespace {
 // ---------------------------------------------------------------- the join
 constexpr int kJoinWarps = 16;  // most warps of a block
 
+// Bound by latency: the row's own two partial results say how many others there are and where; then those, 8 to a warp
+// at once.  300 of them a row (32 rows) in 7.6 us, 7 (6,144 rows) in 9; with every warp working its row's places out from the
+// deal it was 20 and 14.
 // `share` warps take a row's partial results by turns, some at once with their loads together; each keeps a running
 // maximum, and the first of them joins what they have.  The kernel may start before the partial results are
 // complete, so nothing that reads them is __restrict__.
