@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   }
   tc_fence_before();
   cudaGridDependencySynchronize();
-  deal_sources<128, 128, true, false>(A, seg, src, ctl.scratch);  // ends with a barrier
+  deal_sources<128, 128, true, false>(A, seg, src, ctl.scratch);
+  __syncthreads();
   tc_fence_after();
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
   const uint32_t tmem = ctl.tmem_base;
