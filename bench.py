@@ -425,7 +425,9 @@ def measure_fresh_layouts(base, dev, stream, steps):
     from shared_prompt_exact_gb300 import dualkv
     lists = fresh_r_lists(steps, N=base.N)
     ws_ = [wl.custom(base.P, R, base.Hq, base.Hkv, base.D, base.window, seed=base.seed) for R in lists]
-    Tmax = max(x.T for x in ws_)
+    warm = [wl.custom(base.P, R, base.Hq, base.Hkv, base.D, base.window, seed=base.seed)
+            for R in fresh_r_lists(3, N=base.N, seed=base.seed + 777)]
+    Tmax = max(x.T for x in ws_ + warm)
     gen = torch.Generator(device=dev).manual_seed(base.seed)
     rnd = lambda *shape: torch.randn(*shape, generator=gen, device=dev).to(torch.bfloat16)  # noqa: E731
     q, k, v, do = rnd(Tmax, base.Hq, base.D), rnd(Tmax, base.Hkv, base.D), rnd(Tmax, base.Hkv, base.D), \
@@ -433,7 +435,7 @@ def measure_fresh_layouts(base, dev, stream, steps):
     out = torch.empty_like(q)
     lse_all = torch.empty(base.Hq * Tmax, dtype=torch.float32, device=dev)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws_bytes = max(dualkv.dualkv_bwd_workspace_bytes(x.P, x.N, x.offsets, x.Hq, x.Hkv, x.D, x.window) for x in ws_)
+    ws_bytes = max(dualkv.dualkv_bwd_workspace_bytes(x.P, x.N, x.offsets, x.Hq, x.Hkv, x.D, x.window) for x in ws_ + warm)
     wsb = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
 
     def step(x):
@@ -447,8 +449,6 @@ def measure_fresh_layouts(base, dev, stream, steps):
     flops = sum(sum(useful_flops(layout_pairs(x), x.D, x.Hq)) for x in ws_)
     # fresh: drop every plan, warm up on three other layouts, then a layout not seen
     # before on each timed step
-    warm = [wl.custom(base.P, R, base.Hq, base.Hkv, base.D, base.window, seed=base.seed)
-            for R in fresh_r_lists(3, N=base.N, seed=base.seed + 777)]
     torch.cuda.synchronize(dev)
     dualkv.dualkv_release()
     for x in warm:
