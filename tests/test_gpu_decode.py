@@ -240,6 +240,35 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_graphs():
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("bits,D", [(16, 128), (4, 64), (16, 512)])
+def test_the_most_sources(bits, D):
+    # as many groups and responses as a call takes: their lengths leave room for fewer warps
+    sizes = np.array([2] * 4094 + [4])
+    r = np.random.default_rng(70)
+    c = Case([0] + np.cumsum(sizes).tolist(), r.integers(0, 4, 4095).tolist(), r.integers(-1, 6, 8192).tolist(), 2, 1, D, 16, bits,
+             seed=71)
+    out, lse = c.run()
+    dk.dualkv_check_status()
+    c.check(out, lse, only=list(range(0, 8192, 97)) + [8191])
+
+
+def test_two_streams_at_once():
+    # two batches with prompts for the block kernel, each with its own workspace, on two streams in turn: their kernels share
+    # the GPU in any order
+    cases = [Case([0, 40], [6000], _ragged(40, 0, 200, 80 + i), 32, 8, 128, 64, bits, seed=80 + i) for i, bits in enumerate((16, 4))]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(12):
+        for c, s in zip(cases, streams):
+            got.append(c.run(stream=s))
+    torch.cuda.synchronize()
+    dk.dualkv_check_status()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
 def test_in_graphs_behind_copies_and_other_kernels():
     # the calls' kernels may start before what is in front of them is done: copies, fills and other kernels whose results
     # they need, in a captured graph and out of it
