@@ -24,14 +24,15 @@ struct Deal {
 };
 // a / b.  Operands below 2^21 go through fp32, whose quotient is off by 2 units in the last place, so by half at most,
 // and its whole part by one (an integer division takes some 250 cycles, and a warp needs five before its first tile).
+__device__ __forceinline__ uint32_t divide_small(uint32_t a, uint32_t b) {
+  uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
+  const int r = (int)a - (int)(q * b);
+  if (r < 0) --q;
+  if (r >= (int)b) ++q;
+  return q;
+}
 __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
-  if ((a | b) >> 21 == 0) {
-    uint32_t q = (uint32_t)__fdividef((float)(uint32_t)a, (float)(uint32_t)b);
-    const int r = (int)(uint32_t)a - (int)(q * (uint32_t)b);
-    if (r < 0) --q;
-    if (r >= (int)(uint32_t)b) ++q;
-    return q;
-  }
+  if ((a | b) >> 21 == 0) return divide_small((uint32_t)a, (uint32_t)b);
   return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
 }
 __device__ __forceinline__ Deal make_deal(uint32_t per_head, int Hkv, int workers) {
@@ -124,6 +125,9 @@ __device__ __forceinline__ int block_tiles(const DecodeArgs& A, const SegTable<C
 // sources either way.  Both kernels come to the same decision, from the same numbers.  BLOCKS: under a window, each
 // block of a prompt's rows counts its own tiles.
 //
+// Loops that run a few times, once a launch, are not unrolled here: their instructions come from L2, and a kernel's start waits
+// for them (0.3 to 1 us a call).
+//
 // Few sources: every warp for itself, with two sources to a lane, all of them writing the same, so that no barrier lies
 // between a warp and its first tile (32 responses behind one prompt, two such kernels: 52.8 -> 52.0 us).
 constexpr int kFewSources = 64, kFewGroups = 8;
@@ -141,8 +145,10 @@ __device__ __forceinline__ void deal_few(const DecodeArgs& A, const SegTable<CAP
     if (lane + 32 * k < all) src.len[lane + 32 * k] = len[k];
   __syncwarp();
   unsigned long long work = 0;
+#pragma unroll 1
   for (int g = 0; g < G; ++g) {
     uint32_t least = 0x7fffffffu;
+#pragma unroll 1
     for (int b = seg.off[g] + lane; b < seg.off[g + 1]; b += 32)
       if (src.len[G + b] >= 0) least = min(least, (uint32_t)src.len[G + b]);
     least = __reduce_min_sync(0xffffffffu, least);
@@ -167,6 +173,7 @@ __device__ __forceinline__ void deal_few(const DecodeArgs& A, const SegTable<CAP
     }
   }
   if (BLOCKS) {
+#pragma unroll 1
     for (int g = 0; g < G; ++g) {
       const int rows = (seg.off[g + 1] - seg.off[g]) * GQ, blocks = (rows + COLS - 1) / COLS;
       uint32_t n = 0;
@@ -275,6 +282,7 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
 // Source holding tile `t` of a kv-head: the largest s with cum[s] <= t.
 __device__ __forceinline__ int source_of(const uint32_t* cum, int n, uint32_t t) {
   int lo = 0, hi = n - 1;
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (cum[mid] <= t) lo = mid;

@@ -3,7 +3,7 @@
 // A group's rows for one kv-head (its responses' heads: 32 responses of 4 heads are 128) see the same prompt, so
 // this is a product of matrices: 128 rows meet tiles of 128 keys on the tensor cores (tcgen05), as
 // in fwd.cu's forward of head dimensions 64 and 128.  What differs: keys and values come from pages, a block
-// takes an equal share of all prompts' tiles whatever their lengths (decode.cuh's deal), and it leaves partial results,
+// takes an equal share of all prompts' tiles (decode.cuh's deal; whole_chunk), and it leaves partial results,
 // fp32 values with a row's maximum and sum, which decode.cu's join puts together with the responses'.
 //
 // Warps:
@@ -46,7 +46,7 @@ struct PromptCfg {
   static constexpr int S_WARP = BITS == 16 ? 2 : 16, PV_WARP = S_WARP + 1;
   static constexpr int THREADS = BITS == 16 ? 384 : 640;
   static constexpr int OFF_K = TILE_BYTES, OFF_V = OFF_K + NK * TILE_BYTES, RINGS = OFF_V + NV * TILE_BYTES;
-  static constexpr int MOST_SHARED = RINGS + 1024 + (3 * kBigGroups + kBigResponses + 1) * (int)sizeof(uint32_t);
+  static constexpr int MOST_SHARED = RINGS + 1024 + (4 * kBigGroups + kBigResponses + 2) * (int)sizeof(uint32_t);
   static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
   static constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 };
@@ -56,6 +56,7 @@ struct PromptCtl {
   uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2], pv_issued[2], pair_done[4], drain, drain2;
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t chunk;
   uint32_t scratch[32];
   float half_m[256], half_l[256];
 };
@@ -76,6 +77,41 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, fs));
 }
 
+// Tiles of a chunk so that no block has parts of two pieces (a piece: a prompt, kv-head and block of rows), each piece
+// filled up to a multiple of the chunk with tiles that nobody forms.  A block that goes on to another piece waits for its
+// partial results and its new queries, as long as for MORE tiles; 0 if no chunk up to so much larger than the mean, d.chunk,
+// leaves enough blocks for it.  One warp; lane i tries d.chunk + i.
+// Whole calls, 32/8 heads of 128: one prompt of 5,000 tokens for 32 responses 33 -> 27 us, two of 8,000 in 4 bits for
+// 64/8 heads 88 -> 74.  The search costs 1 us where nothing is to be filled up (6,144 tokens: 52.3 -> 52.9).  MORE = 6 is slower
+// (twelve prompts of 1,000 to 3,000: 96 us, not 93), and without a bound eight prompts of 300 to 9,000 take 179, not 120.
+template <int MORE, int CAP>
+__device__ __forceinline__ uint32_t whole_chunk(const DecodeArgs& A, const SegTable<CAP>& seg, const Sources& src,
+                                                const Deal& d, uint32_t* padded) {
+  const int G = A.G, Hkv = A.kv.Hkv, lane = threadIdx.x & 31;
+  if (G > kBlocks || d.chunk == 0 || (d.chunk | src.cum[G]) >> 20) return 0;
+  const uint32_t c = (uint32_t)d.chunk + lane;
+  uint32_t n = 0;
+#pragma unroll 1
+  for (int g = 0; g < G; ++g) {
+    if (src.cum[g + 1] == src.cum[g]) continue;
+    const uint32_t blocks = (uint32_t)((seg.off[g + 1] - seg.off[g]) * (int)A.by_heads.d + 127) / 128;
+    n += blocks * divide_small((uint32_t)tiles_of<128>(src.first[g], src.len[g]) + c - 1, c);
+  }
+  const uint32_t fits = __ballot_sync(0xffffffffu, lane <= MORE && n * (uint64_t)Hkv <= kBlocks);
+  if (!fits) return 0;
+  const uint32_t chunk = (uint32_t)d.chunk + __ffs(fits) - 1;
+  uint32_t before = 0;
+#pragma unroll 1
+  for (int g = 0; g < G; ++g) {
+    if (lane == 0) padded[g] = before;
+    if (src.cum[g + 1] == src.cum[g]) continue;
+    const uint32_t blocks = (uint32_t)((seg.off[g + 1] - seg.off[g]) * (int)A.by_heads.d + 127) / 128;
+    before += blocks * chunk * divide_small((uint32_t)tiles_of<128>(src.first[g], src.len[g]) + chunk - 1, chunk);
+  }
+  if (lane == 0) padded[G] = before;
+  return chunk;
+}
+
 // One prompt, kv-head and block of 128 rows: the tiles of it that are this block's.
 struct Segment {
   int g, kvh, r0, row_end, P, lo, first, last;
@@ -93,7 +129,6 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   __shared__ PromptCtl ctl;
   const Sources src{reinterpret_cast<uint32_t*>(smem + C::RINGS), reinterpret_cast<int*>(smem + C::RINGS) + 2 * A.G + 1,
                     reinterpret_cast<int*>(smem + C::RINGS) + A.G + 1};
-  const uint32_t* cum = src.cum;
   const uint32_t warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int GQ = (int)A.by_heads.d, ps = A.kv.ps;
   FailState fs{&ctl.abort_flag, A.status, kLaunchWaitLimitNs};
@@ -128,12 +163,24 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   tc_fence_before();
   cudaGridDependencySynchronize();
   deal_sources<128, 128, true, false>(A, seg, src, ctl.scratch);
+  uint32_t* padded = src.cum + 3 * A.G + A.B + 1;  // [G + 1] tiles before each prompt, with those that fill up its pieces
+  Deal deal = make_deal(src.cum[A.G], A.kv.Hkv, kBlocks);
+  if (warp == 0) {
+    const uint32_t chunk = whole_chunk<3>(A, seg, src, deal, padded);
+    if (lane == 0) ctl.chunk = chunk;
+  }
   __syncthreads();
   tc_fence_after();
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
   const uint32_t tmem = ctl.tmem_base;
   const Workspace ws = carve(A.workspace, A.B, A.Hq);
-  const Deal deal = make_deal(cum[A.G], A.kv.Hkv, kBlocks);
+  const uint32_t* cum = src.cum;
+  if (ctl.chunk) {
+    cum = padded;
+    deal.per_head = cum[A.G];
+    deal.total = (uint64_t)deal.per_head * (uint64_t)A.kv.Hkv;
+    deal.chunk = ctl.chunk;
+  }
   const uint64_t begin = first_tile(deal, blockIdx.x), stop = first_tile(deal, blockIdx.x + 1);
   auto next_segment = [&](uint64_t& at) {
     Segment s;
@@ -143,15 +190,16 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
     const int begin_row = seg.off[s.g] * GQ;
     s.row_end = seg.off[s.g + 1] * GQ;
     const int blocks = (s.row_end - begin_row + C::BM - 1) / C::BM;
-    const int tiles = (int)divide(cum[s.g + 1] - cum[s.g], (uint32_t)blocks);
-    const int block = (int)divide(local - cum[s.g], (uint32_t)tiles), t0 = (int)(local - cum[s.g]) - block * tiles;
-    const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
-    s.parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - blockIdx.x) + 1;
-    at += (uint64_t)(t1 - t0);
-    s.r0 = begin_row + block * C::BM;
     s.P = src.len[s.g];
     s.lo = src.first[s.g];
-    const int tile0 = (s.P + C::BN - 1) / C::BN - tiles;
+    const int tile0 = s.lo / C::BN, tiles = tiles_of<C::BN>(s.lo, s.P);
+    const uint32_t all = cum[s.g + 1] - cum[s.g], from = local - cum[s.g];
+    const int room = blocks == 1 ? (int)all : (int)divide(all, (uint32_t)blocks);
+    const int block = blocks == 1 ? 0 : (int)divide(from, (uint32_t)room), t0 = (int)from - block * room;
+    const int t1 = (int)min((uint64_t)tiles, (uint64_t)t0 + (stop - at));
+    s.parts = t0 ? 0 : (int)(worker_of(deal, at + (uint64_t)(tiles - 1)) - blockIdx.x) + 1;
+    at += (uint64_t)((t1 == tiles ? room : t1) - t0);
+    s.r0 = begin_row + block * C::BM;
     s.first = tile0 + t0;
     s.last = tile0 + t1;
     return s;
@@ -545,7 +593,7 @@ cudaError_t launch_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorM
                      cudaStream_t st) {
   using C = PromptCfg<D, BITS>;
   const SegTable<CAP> seg = make_segs<CAP>(0, a.G, groups);
-  const int smem = C::RINGS + 1024 + (3 * a.G + a.B + 1) * (int)sizeof(uint32_t);
+  const int smem = C::RINGS + 1024 + (4 * a.G + a.B + 2) * (int)sizeof(uint32_t);
   const cudaError_t e = allow_shared<&prompt_kernel<D, BITS, CAP>>(a.device, C::MOST_SHARED);
   if (e != cudaSuccess) return e;
   return launch_behind_shared(prompt_kernel<D, BITS, CAP>, dim3(kBlocks), dim3(C::THREADS), smem, st, tk, tv, a, seg);

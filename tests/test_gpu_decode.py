@@ -189,6 +189,29 @@ def test_long_streams(case, bits):
     c.check(out, lse, only=range(0, c.B, max(1, c.B // 40)))
 
 
+PIECES = [  # prompts of large groups, whose tiles are dealt by prompt, kv-head and block of 128 rows
+    ("a few, with a rest", dict(groups=[0, 32, 64, 96, 128, 160], prompts=[129, 4_097, 0, 7_000, 5_000],
+                                lens=_ragged(64, 0, 40, 16) + [-1] * 32 + _ragged(64, -1, 40, 17), Hq=8, Hkv=2, D=64, ps=16)),
+    ("nobody left of the longest", dict(groups=[0, 40, 80], prompts=[9_000, 8_321], lens=[-1] * 40 + _ragged(40, 0, 40, 18),
+                                        Hq=32, Hkv=8, D=128, ps=64)),
+    ("more of them than blocks", dict(groups=list(range(0, 2881, 32)), prompts=_ragged(90, 100, 700, 19),
+                                      lens=_ragged(2880, -1, 20, 20), Hq=8, Hkv=2, D=64, ps=16)),
+    ("more prompts than blocks", dict(groups=list(range(0, 4001, 20)), prompts=_ragged(200, 400, 800, 21),
+                                      lens=_ragged(4000, -1, 12, 22), Hq=2, Hkv=1, D=64, ps=16)),
+    ("one and a half to a block", dict(groups=[0, 64, 128], prompts=[4_000, 4_000], lens=_ragged(128, 0, 20, 23), Hq=64, Hkv=8,
+                                       D=64, ps=32)),
+]
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("case", PIECES, ids=[c[0] for c in PIECES])
+def test_prompts_dealt_in_pieces(case, bits):
+    c = Case(**case[1], bits=bits, seed=32)
+    out, lse = c.run()
+    dk.dualkv_check_status()
+    c.check(out, lse, only=range(0, c.B, max(1, c.B // 40)))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_layouts(seed):
     r = np.random.default_rng(1000 + seed)
