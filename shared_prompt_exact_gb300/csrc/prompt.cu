@@ -13,8 +13,8 @@
 //     order within 8 values is 0, 4, 1, 5, ... (decode8); the queries are written in the same order, and the
 //     output's columns are put right at the end.
 //   an issuer of S = Q K^T, an issuer of O += P V, eight softmax warps: as in fwd.cu.
-// Measured: 25 MB of one prompt of 6,144 tokens for 128 rows of 8 kv-heads in 14 us, six prompts of 3,000 tokens in 4 bits
-// in 23 to 30.  A block needs 15,000 cycles to its first scores (5,000 of them the deal; then its pages, its first keys, which
+// Measured, alone and from cold caches: 25 MB of one prompt of 6,144 tokens for 128 rows of 8 kv-heads in 18.7 us (14 behind
+// other calls), six prompts of 3,000 tokens in 4 bits in 28.8.  A block needs 15,000 cycles to its first scores (5,000 of them the deal; then its pages, its first keys, which
 // all blocks ask for at once), 1,000 a tile in bf16 and 2,200 in 4 bits (issue: the loaders' 250 instructions a row and
 // the softmax's 350 a tile share the schedulers; two loader warps an operand instead of four: 5,000), and 6,000 at its end,
 // where 64 KB of partial results go through 16 KB of shared memory so that rows are written in 64-byte runs (a row to
