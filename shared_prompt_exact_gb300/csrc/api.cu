@@ -842,7 +842,7 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
       const uint64_t rows = (uint64_t)(groups[g + 1] - groups[g]) * GQ;
       if (rows >= kBigRows) work += rows * most;
     }
-    a.big = work * (uint64_t)Hkv >= kBigWork;
+    a.big = work * (uint64_t)Hkv >= big_work(a.kv);
     if (a.big && cache->bits == 16) {
       if ((rc = ensure_encode())) return rc;
       if (make_tmap(&tk, cache->k, (int64_t)head_rows, 1, D, 16) || make_tmap(&tv, cache->v, (int64_t)head_rows, 1, D, 16))

@@ -158,7 +158,7 @@ __device__ __forceinline__ void deal_few(const DecodeArgs& A, const SegTable<CAP
     if (A.big && rows >= kBigRows) work += (unsigned long long)(P - first) * (unsigned long long)rows;
   }
   __syncwarp();
-  const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= kBigWork;
+  const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= big_work(A.kv);
   uint32_t tiles[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -239,7 +239,7 @@ __device__ __forceinline__ void deal_sources(const DecodeArgs& A, const SegTable
     }
   }
   __syncthreads();
-  const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= kBigWork;
+  const bool big = A.big && work * (unsigned long long)A.kv.Hkv >= big_work(A.kv);
   if (BLOCKS) {
     for (int g = warp; g < G; g += THREADS >> 5) {
       const int rows = (seg.off[g + 1] - seg.off[g]) * GQ, blocks = (rows + COLS - 1) / COLS;

@@ -290,11 +290,11 @@ struct DecodeArgs {
 };
 // Prompts of groups with this many rows and more go to launch_prompt's kernel ...
 constexpr int kBigRows = 32;
-// ... where the tokens that the groups see times their rows and the kv-heads come to this much.  Two groups of 32 responses
-// with 8 kv-heads of 128, 4 rows each, over 400 / 1,600 / 6,400 tokens of prompt (0.8, 3.3, 13 M): 26 / 34 / 43 us
-// there, 21 / 36 / 95 us by decode.cu's warps alone in bf16; 26 / 34 / 38 and 19 / 29 / 60 in 4 bits; 4 kv-heads of 64:
-// 18 / 20 / 24 and 13 / 17 / 31 (0.4, 1.6, 6.6 M).
-constexpr unsigned long long kBigWork = 4000000;
+// ... where the tokens that the groups see times their rows and the kv-heads come to this much.  32 responses, 8 kv-heads
+// of 128 with 4 rows each, behind 1,500 / 2,500 / 3,400 tokens (1.5, 2.6, 3.5 M): 24 / 24 / 26 us there, 23 / 29 / 35 by
+// decode_walk.cuh's warps alone in bf16; 22 / 23 / 23 and 17 / 22 / 26 in 4 bits.  Heads of 64, bf16: 19 and 17 at 2.3 M,
+// 20 and 23 at 3.8 M.
+__host__ __device__ inline unsigned long long big_work(const PagedKV& kv) { return kv.ks ? 3400000 : 2400000; }
 constexpr int kBigGroups = 512;      // most groups of a call with that kernel: their lengths are in shared memory
 constexpr int kBigResponses = 4096;  // and most responses
 // tk, tv: views (make_tmap, boxes of 16 rows) of the bf16 pools, used where a.big and the cache holds bf16
