@@ -356,9 +356,12 @@ int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float
  *   bits 4    k, v: device bytes [pages, Hkv, page_size, D / 2], value 2j of a token in the low half
  *             of byte j; k_scale, v_scale: device bf16 [pages, Hkv, page_size, D / 32].  A value is
  *             scale * (code - 8), codes 1 .. 15, with its group's scale (32 values of a head): a seventh of
- *             the group's largest magnitude (in fp32) rounded up to 5 significant bits, so the value
+ *             the group's largest magnitude rounded up to 5 significant bits, so the value
  *             is exact in bf16; a magnitude goes to the nearest code, from half way to the larger one.
- *             A group with a value that is not finite has the scale NaN.  |x| up to 9e37
+ *             Keys are quantised as their exact values behind norm and rotation, off by 2^-42 of
+ *             their pair's size and 2^-52 of their angle: only a border that near may be missed.
+ *             A group with a value that is not finite has the scale NaN.  |x| up to 9e37 (with a norm 1e18,
+ *             as in dualkv_qk_norm_rope: its mean of squares is in fp32)
  * page_size is a multiple of 16 up to 65,536; all pointers are 16-byte aligned.  A stream's tokens lie in
  * the pages that its row of a page table (device int32 [streams, max_pages]) names: token i in slot
  * i % page_size of page i / page_size of the row.  Entries behind a stream's last token are not used.

@@ -10,13 +10,17 @@
 //     a group with a value that is not finite gets the scale NaN
 // read: the same rows back in bf16.
 //
+// Codes and steps jump at borders, so those of the keys are decided by more than fp32: where its rounding errors could put a key
+// of a group on the other side (kKeyError), the group's keys are formed again in two floats each (exact_group).
+//
 // Both touch each value once and are bound by HBM bandwidth (few rows: by latency).  The walk over
 // rows and heads, the loads ahead through shared memory and the arithmetic are rope.cu's: one warp per
-// row, q's heads first, then k's, then v's.  Keys are quantised from fp32, before any rounding to bf16.
-// Measured: append of 71,680 rows of 32 + 2 x 8 heads of 128 in bf16 267 us (6.6 TB/s), of 23,200 rows of 8 + 2 x 2 heads of
-// 512 in 4 bits 90 us (5.6 TB/s: bound by issue, 2,650 instructions a row; 122 us with a division and a comparison
-// for every code, 99 with a row's place found when it is needed); read of 131,072 rows of 8 heads of 128 156 us (6.9 TB/s; 177
-// with the values asked for behind the keys).
+// row, q's heads first, then k's, then v's.  Keys are quantised before any rounding to bf16.
+// Measured: append of 71,680 rows of 32 + 2 x 8 heads of 128 in bf16 267 us (6.6 TB/s); of 23,200 rows of 8 + 2 x 2 heads of
+// 512 in 4 bits, with their read back, 118 us (bound by issue; 109 without the look at borders, which costs 4 % of the
+// instructions and, in 2 % of the steps, a group formed again: 2.7 us for a warp's first one; in fp64 it was 7 and the call 140 us;
+// 4 us less would remain of them if the bound were 8 times as small); read of 131,072 rows of 8 heads of 128 156 us (6.9 TB/s;
+// 177 with the values asked for behind the keys).
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
@@ -25,6 +29,7 @@
 #include "ptx.cuh"
 #include "rope.cuh"
 #include "segs.cuh"
+#include "twofloat.cuh"
 
 namespace dkv {
 
@@ -75,6 +80,13 @@ __device__ __forceinline__ bool has_page(const PagedKV& kv, const Place& p, uint
   return false;
 }
 
+// A group of keys that fp32 does not decide: group `group` of head `head` in row t at position pos, bound for row `row` of the pool.
+struct Undecided {
+  int64_t row;
+  int t, head, group;
+  uint32_t pos;
+};
+
 // What a block of the append keeps in shared memory.
 template <int D, int BITS>
 struct AppendShared {
@@ -82,56 +94,83 @@ struct AppendShared {
   alignas(16) float cs[kWarps][D / 2];
   alignas(16) float sn[kWarps][D / 2];
   uint64_t freq[D / 2];
-  alignas(16) float k[BITS == 4 ? kWarps : 1][BITS == 4 ? 512 : 4];  // a step's keys in their order
+  alignas(16) float k[BITS == 4 ? kWarps : 1][BITS == 4 ? 512 : 4];  // a step's keys, Vec8s in their order
+  alignas(8) float size[BITS == 4 ? kWarps : 1][BITS == 4 ? 64 : 2];  // of every 8: largest magnitude around, 0: exact
   uint4 ring[kDepth][2][kThreads];
 };
 
-// Largest and smallest of three, NaN if one of them is.
-__device__ __forceinline__ float max3(float a, float b, float c) {
+// Largest magnitude of three, NaN if one of them is.
+__device__ __forceinline__ float magnitude3(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
+__device__ __forceinline__ float magnitude8(const Vec8& x) {
+  return magnitude3(magnitude3(magnitude3(x.v[0].x, x.v[0].y, x.v[1].x), x.v[1].y, x.v[2].x),
+                    magnitude3(x.v[2].y, x.v[3].x, x.v[3].y), 0.f);
 }
 
-// Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.  `ties`: the values are bf16, so
-// they can lie half way between two multiples of the step.
-__device__ __forceinline__ uint2 quantise16(const float (&x)[16], bool ties, __nv_bfloat16& scale) {
-  float hi = max3(x[0], x[1], x[2]), lo = min3(x[0], x[1], x[2]);
-#pragma unroll
-  for (int e = 3; e < 15; e += 2) {
-    hi = max3(hi, x[e], x[e + 1]);
-    lo = min3(lo, x[e], x[e + 1]);
-  }
-  hi = max3(hi, x[15], -min3(lo, x[15], x[15]));
-  const float top = max3(hi, __shfl_xor_sync(0xffffffffu, hi, 1), hi);
-  const uint32_t bits = (__float_as_uint(__fdiv_rn(top, 7.f)) + 0x7ffffu) & ~0x7ffffu;
+// Error of a key in fp32, by the largest magnitude of the two vectors that its lane turned.  With u = 2^-24: sum of
+// squares 14 u, + eps u, root half of that and 4 u, product with the weight 3 u: 14.5 u of each value of a pair; cosine and
+// sine 1.6 u for the angle's float and 4 u; their products' roundings 2 u.  In all 16.5 u sqrt(2) + 5.6 u * 2 = 35 u.
+constexpr float kKeyError = 40.f * 0x1p-24f;
+
+// x rounded up to 5 significant bits.
+__device__ __forceinline__ uint32_t five_bits(float x) { return (__float_as_uint(x) + 0x7ffffu) & ~0x7ffffu; }
+// Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.  `size`: 0 where the values are bf16
+// as they came, else the magnitude that their errors go by (kKeyError); then `near` is set where an error could change a
+// code or the scale.
+template <bool KEYS>
+__device__ __forceinline__ uint2 quantise16(Vec8 (&x)[2], float size, __nv_bfloat16& scale, bool& near) {
+  const float most = magnitude3(magnitude8(x[0]), magnitude8(x[1]), 0.f);
+  const float top = magnitude3(most, __shfl_xor_sync(0xffffffffu, most, 1), most);
+  const float t = __fdiv_rn(top, 7.f);
+  const uint32_t bits = five_bits(t);
   const bool finite = top < __uint_as_float(0x7f800000u);  // false for NaN
   scale = __ushort_as_bfloat16((unsigned short)(finite ? bits >> 16 : 0x7fc0u));
+  near = false;
+  if (KEYS) {
+    const float around = magnitude3(size, __shfl_xor_sync(0xffffffffu, size, 1), size);
+    const float off = fmaf(around, kKeyError / 7.f, t * 0x1p-22f);
+    near = finite && around != 0.f && five_bits(fmaxf(t - off, 0.f)) != five_bits(t + off);  // a NaN around: true
+  }
   if (!finite || bits == 0u) return make_uint2(0x88888888u, 0x88888888u);  // not finite, or zeros
   // x / step by the reciprocal.  bf16 values take the smallest float above it: one half way comes out above (away
   // from zero) and goes to the farther multiple, any other is moved by 2^-23 of it at most, less than it is away from half
-  // way.  Values of fp32 take the nearest float, which moves them by 2^-24.  The sum with 1.5 x 2^23 + 8 is rounded to
+  // way.  Others take the nearest float, which moves them by 2^-24.  The sum with 1.5 x 2^23 + 8 is rounded to
   // a whole number, whose low bits are n + 8; the eight codes are shifted together with the upper bits in place,
   // which are subtracted at once.
-  float up = 1.f, step = __uint_as_float(bits);
-  if (step < 1e-36f) {  // its reciprocal could overflow: the same with both 2^64 times as large
-    up = 0x1p64f;
-    step *= up;
+  float step = __uint_as_float(bits);
+  if (step < 1e-36f) {  // its reciprocal could overflow: the same with everything 2^64 times as large
+    step *= 0x1p64f;
+    size *= 0x1p64f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e / 4].v[e % 4] = fmul2(x[e / 4].v[e % 4], make_float2(0x1p64f, 0x1p64f));
   }
-  const float inv = ties ? __uint_as_float(__float_as_uint(__frcp_rd(step)) + 1u) : __frcp_rn(step);
+  const bool exact = !KEYS || size == 0.f;
+  const float inv = exact ? __uint_as_float(__float_as_uint(__frcp_rd(step)) + 1u) : __frcp_rn(step);
+  const float2 inv2 = make_float2(inv, inv), minus = make_float2(-inv, -inv), magic = make_float2(12582920.f, 12582920.f);
   uint32_t out[2];
+  float far = 0.f;  // from the nearest multiple, in steps
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
+    float2 n[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      n[e] = ffma2(x[w].v[e], inv2, magic);
+      if (KEYS) {
+        const float2 d = ffma2(x[w].v[e], minus, fadd2(n[e], make_float2(-12582920.f, -12582920.f)));
+        far = magnitude3(far, d.x, d.y);
+      }
+    }
+    const float codes[8] = {n[0].x, n[2].x, n[0].y, n[2].y, n[1].x, n[3].x, n[1].y, n[3].y};
     uint32_t sum = 0;
 #pragma unroll
-    for (int e = 7; e >= 0; --e) sum = (sum << 4) + __float_as_uint(fmaf(x[8 * w + e] * up, inv, 12582920.f));
+    for (int e = 7; e >= 0; --e) sum = (sum << 4) + __float_as_uint(codes[e]);
     out[w] = sum - 0x4b400000u * 0x11111111u;
   }
+  // (2^-20: the reciprocal's error of 7 2^-24, and the differences')
+  if (KEYS) near |= !exact && !(far <= 0.5f - fmaf(size, kKeyError * inv, 0x1p-20f));
   return make_uint2(out[0], out[1]);
 }
 
@@ -151,33 +190,85 @@ __device__ __forceinline__ void turn(Vec8& a, Vec8& b, const Angles& g, const La
   }
 }
 
-// A lane's eight values in their order.
-__device__ __forceinline__ void natural8(const Vec8& v, float* to) {
-  *reinterpret_cast<float4*>(to) = make_float4(v.v[0].x, v.v[2].x, v.v[0].y, v.v[2].y);
-  *reinterpret_cast<float4*>(to + 4) = make_float4(v.v[1].x, v.v[3].x, v.v[1].y, v.v[3].y);
-}
-
 // Place of value p (a multiple of 4) of a step's 512 in shared memory: vectors of 16 bytes, so that neither the lanes that
 // write neighbouring ones nor those that read every fourth meet in a bank.
 __device__ __forceinline__ int spread(int p) { return p ^ ((p >> 5 & 3) << 2); }
 __device__ __forceinline__ void store8(const Vec8& v, float* base, int p) {
-  *reinterpret_cast<float4*>(base + spread(p)) = make_float4(v.v[0].x, v.v[2].x, v.v[0].y, v.v[2].y);
-  *reinterpret_cast<float4*>(base + spread(p + 4)) = make_float4(v.v[1].x, v.v[3].x, v.v[1].y, v.v[3].y);
+  *reinterpret_cast<float4*>(base + spread(p)) = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+  *reinterpret_cast<float4*>(base + spread(p + 4)) = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
 }
 
-// 16 values from natural order into a row of the 4-bit pools.
+// A lane's 16 codes into a row of the 4-bit pools.
 template <int D>
-__device__ __forceinline__ void store_codes(const float (&x)[16], bool ties, void* codes, __nv_bfloat16* scales, int64_t row, int i,
-                                            bool live) {
-  __nv_bfloat16 scale;
-  const uint2 c = quantise16(x, ties, scale);
-  if (!live) return;
+__device__ __forceinline__ void store_codes(const uint2& c, __nv_bfloat16 scale, void* codes, __nv_bfloat16* scales, int64_t row,
+                                            int i) {
   *reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + row * (D / 2) + 8 * i) = c;
   if ((i & 1) == 0) scales[row * (D / kGroup) + i / 2] = scale;
 }
 
+__device__ __forceinline__ Two shuffled(Two x, int o) {
+  return Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+}
+
+// One group of 32 keys from its row of k, a value to a lane: codes and scale into the pool.  Each key is off by 2^-42 of its
+// pair's size and 2^-52 of its angle; borders (7 step, an odd number of half steps) are exact in fp32.
+template <int D>
+__device__ __noinline__ void exact_group(const AppendArgs& A, const uint64_t* freq, const Undecided& u) {
+  const int lane = threadIdx.x & 31, d = kGroup * u.group + lane, half = A.half;
+  const __nv_bfloat16* x = A.k + u.t * A.k_stride + (int64_t)u.head * D;
+  // the value's partner in the rotation, if it is turned
+  const bool is_turned = d < 2 * half, second = A.inter ? (d & 1) != 0 : d >= half;
+  const int j = A.inter ? d >> 1 : second ? d - half : d, other = !is_turned ? d : A.inter ? d ^ 1 : second ? j : d + half;
+  Two y{__bfloat162float(x[d]), 0.f}, z{__bfloat162float(x[other]), 0.f};
+  if (A.k_weight) {
+    auto weight = [&](int e) {
+      return two_sum(A.weight_f32 ? static_cast<const float*>(A.k_weight)[e]
+                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(A.k_weight)[e]), A.w0);
+    };
+    const Two wy = weight(d), wz = weight(other);
+    float v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = __bfloat162float(x[lane + 32 * e]);
+    Two ss{0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {  // squares of 8 bits are exact
+      const Two s = two_sum(ss.hi, product(v[e], v[e]));
+      ss = Two{s.hi, ss.lo + s.lo};
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss = ss + shuffled(ss, o);
+    const Two mean = Two{ss.hi * (1.f / D), ss.lo * (1.f / D)} + Two{A.eps, 0.f}, r = refine_rsqrt(mean, rsqrtf(mean.hi));
+    y = y * r * wy;
+    z = z * r * wz;
+  }
+  if (is_turned) {
+    Two c, s;
+    cos_sin_turns((uint64_t)u.pos * freq[j], c, s);
+    y = y * c + (second ? z * s : -(z * s));
+  }
+  const bool negative = y.hi < 0.f;
+  if (negative) y = -y;
+  Two top = y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Two v = shuffled(top, o);
+    if (v > top) top = v;
+  }
+  // the smallest step of five bits with top <= 7 step: one that may be too small by one, then the comparison
+  uint32_t bits = five_bits(product(__fdiv_rn(top.hi, 7.f), 1.f - 0x1p-21f));
+  if (top > Two{product(7.f, __uint_as_float(bits)), 0.f}) bits += 0x80000u;
+  const float step = __uint_as_float(bits);
+  // the same for n with (n - 1/2) step <= y < (n + 1/2) step
+  int n = bits ? (int)rintf(__fdiv_rn(y.hi, step)) : 0;
+  auto reaches = [&](int k) { return !(Two{product((float)k - 0.5f, step), 0.f} > y); };
+  if (bits) n = n < 7 && reaches(n + 1) ? n + 1 : n > 0 && !reaches(n) ? n - 1 : n;
+  const int code = 8 + (negative ? -n : n), pair = code | __shfl_down_sync(0xffffffffu, code, 1) << 4;
+  if ((lane & 1) == 0) static_cast<uint8_t*>(A.kv.k)[u.row * (D / 2) + d / 2] = (uint8_t)pair;
+  if (lane == 0) A.kv.ks[u.row * (D / kGroup) + u.group] = __ushort_as_bfloat16((unsigned short)(bits >> 16));
+}
+
 template <int D, int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendArgs A,
                                                              const __grid_constant__ SegTable<CAP> seg) {
   constexpr int G = D / 16, S = 32 / G;
   extern __shared__ uint4 dynamic[];
@@ -232,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
     for (int d = threadIdx.x; d < 2 * D; d += kThreads) {
       const void* w = d < D ? A.q_weight : A.k_weight;
       const int e = d % D;
-      sh.w[d / D][split_at(e, D)] = (BITS == 4 && d >= D ? 0.f : A.w0) + (A.weight_f32 ? static_cast<const float*>(w)[e]
+      sh.w[d / D][split_at(e, D)] = A.w0 + (A.weight_f32 ? static_cast<const float*>(w)[e]
                                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[e]));
     }
   }
@@ -254,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       rb = sh.ring[stage][1][threadIdx.x];
       stage = stage == kDepth - 1 ? 0 : stage + 1;
     };
-    // norm and rotation of the head in the next step; `codes`: for 4 bits
-    auto turned = [&](const float* w, bool codes, Vec8& a, Vec8& b) {
+    // norm and rotation of the head in the next step
+    auto turned = [&](const float* w, Vec8& a, Vec8& b) {
       uint4 ra, rb;
       next(ra, rb);
       a = unpack8(ra);
@@ -264,26 +355,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = ffma2(b.v[e], b.v[e], ffma2(a.v[e], a.v[e], ss));
-        const float mean = group_sum<G>(ss) * (1.f / D) + A.eps;
-        float r = rsqrtf(mean);
-        if (codes) {
-          // one step of Newton's method with the product's rounding error: the root's last bits decide which values pass
-          // half way between two multiples (an error of 2^-23 moves one value in 5 million to the other one)
-          const float h = mean * r, low = fmaf(mean, r, -h);
-          r = fmaf(0.5f * r, fmaf(-h, r, 1.f) - low * r, r);
-        }
-        const float2 rr = make_float2(r, r), w0 = make_float2(A.w0, A.w0);
+        const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + A.eps);
+        const float2 rr = make_float2(r, r);
         const Vec8 wa = load8(w + m.a / 2, w + D / 2 + m.a / 2), wb = load8(w + m.b / 2, w + D / 2 + m.b / 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (codes) {  // x r w + x r w0: the weights are not rounded with their offset
-            const float2 x = fmul2(a.v[e], rr), z = fmul2(b.v[e], rr);
-            a.v[e] = ffma2(x, wa.v[e], fmul2(x, w0));
-            b.v[e] = ffma2(z, wb.v[e], fmul2(z, w0));
-          } else {
-            a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
-            b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
-          }
+          a.v[e] = fmul2(a.v[e], fmul2(rr, wa.v[e]));
+          b.v[e] = fmul2(b.v[e], fmul2(rr, wb.v[e]));
         }
       }
       turn(a, b, ang, m, A.inter);
@@ -293,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       int h = slot + begin * S;
       __nv_bfloat16* y = A.q_out + (t * A.Hq + h) * D + m.a;
       for (int step = begin; step < min(end, nq); ++step, h += S, y += S * D) {
-        turned(sh.w[0], false, a, b);
+        turned(sh.w[0], a, b);
         if (h < A.Hq) {
           *reinterpret_cast<uint4*>(y) = pack8(a);
           *reinterpret_cast<uint4*>(y + m.b - m.a) = pack8(b);
@@ -305,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
       const int h = slot + (step - nq) * S;
       const bool live = h < Hkv && stored;
       const int64_t row = page_row + (int64_t)h * A.kv.ps;
-      turned(sh.w[1], BITS == 4, a, b);
+      turned(sh.w[1], a, b);
       if constexpr (BITS == 16) {
         if (live) {
           __nv_bfloat16* y = static_cast<__nv_bfloat16*>(A.kv.k) + row * D + m.a;
@@ -316,13 +394,27 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
         float* keys = sh.k[warp];
         store8(a, keys, slot * D + m.a);
         store8(b, keys, slot * D + m.b);
+        const float around = magnitude3(magnitude8(a), magnitude8(b), 0.f);
+        sh.size[warp][(slot * D + m.a) / 8] = norm || (m.ta && at_row.pos) ? around : 0.f;
+        sh.size[warp][(slot * D + m.b) / 8] = norm || (m.tb && at_row.pos) ? around : 0.f;
         __syncwarp();
-        float v[16];
+        Vec8 v[2];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(keys + spread(16 * lane + e));
+        for (int e = 0; e < 2; ++e) {
+          v[e] = load8(keys + spread(16 * lane + 8 * e), keys + spread(16 * lane + 8 * e + 4));
+        }
+        const float2 sizes = *reinterpret_cast<const float2*>(&sh.size[warp][2 * lane]);
         __syncwarp();
-        store_codes<D>(v, !norm, A.kv.k, A.kv.ks, row, i, live);
+        __nv_bfloat16 scale;
+        bool near;
+        const uint2 c = quantise16<true>(v, magnitude3(sizes.x, sizes.y, sizes.x), scale, near);
+        uint32_t again = __ballot_sync(0xffffffffu, near && live);  // lanes; a group's first one stands for it
+        again = (again | again >> 1) & 0x55555555u;
+        if (live && !(again >> (lane & ~1) & 1)) store_codes<D>(c, scale, A.kv.k, A.kv.ks, row, i);
+        for (; again; again &= again - 1) {
+          const int from = __ffs(again) - 1, head = from / G + (step - nq) * S;
+          exact_group<D>(A, sh.freq, Undecided{page_row + (int64_t)head * A.kv.ps, (int)t, head, from % G / 2, at_row.pos});
+        }
       }
     }
     for (int step = max(begin, nq + nk); step < end; ++step) {
@@ -338,10 +430,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const AppendArgs A,
           *reinterpret_cast<uint4*>(y + vb) = rb;
         }
       } else {
-        float v[16];
-        natural8(unpack8(ra), v);
-        natural8(unpack8(rb), v + 8);
-        store_codes<D>(v, true, A.kv.v, A.kv.vs, row, i, live);
+        Vec8 v[2] = {unpack8(ra), unpack8(rb)};
+        __nv_bfloat16 scale;
+        bool near;
+        const uint2 c = quantise16<false>(v, 0.f, scale, near);
+        if (live) store_codes<D>(c, scale, A.kv.v, A.kv.vs, row, i);
       }
     }
   }
