@@ -553,7 +553,12 @@ int dualkv_selftest_timeout(uint64_t limit_ns, void* stream);
  *              first entry lies past the last row; the preprocess, which checks
  *              that list before the dQ kernel reads it, empties the entry;
  *   which = 4  the head-dimension-512 P / dS pass (same layout with D = 512);
- *              the first K/V tile of every CTA is never loaded.
+ *              the first K/V tile of every CTA is never loaded;
+ *   which = 6  dualkv_decode over a bf16 cache (32 responses behind a prompt of 4,096
+ *              tokens, 32 / 8 heads, D = 128): the first key tile of every CTA of the
+ *              kernel that takes the prompts is never loaded, so its partial results
+ *              are missing when the others' are put together;
+ *   which = 7  the same over a 4-bit cache.  (5 is not in use.)
  * The failure is recorded in the status word; a kernel whose wait ran out
  * drains its copies and tensor-core operations, frees its tensor memory and
  * returns;

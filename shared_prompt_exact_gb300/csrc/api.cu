@@ -1422,8 +1422,64 @@ static int selftest_pds512(uint64_t limit_ns, cudaStream_t st, uint32_t* status)
   return done(mark_use(&pl->last_use, st));
 }
 
+// A decode of 32 responses of one token behind a prompt of 4,096, 32 / 8 heads of 128, every token in the one page of a
+// cache of zeros; the first tile of keys of every block of the prompts' kernel is never loaded.  The
+// workspace holds what no kernel leaves there.
+static int selftest_decode(int bits, uint64_t limit_ns, cudaStream_t st, uint32_t* status, int device) {
+  constexpr int B = 32, P = 4096, Hq = 32, Hkv = 8, D = 128, ps = 16;
+  const int32_t groups[2] = {0, B};
+  const size_t pool = (size_t)Hkv * ps * D * 2, ws_bytes = decode_workspace_bytes(B, Hq, Hkv, D), rows = (size_t)B * Hq;
+  const size_t o_q = 2 * pool, o_out = o_q + rows * D * 2, o_lse = o_out + rows * D * 2, o_table = align256(o_lse + rows * 4),
+               o_lens = o_table + align256(4 * (P / ps)), o_plen = o_lens + align256(4 * B), o_ws = o_plen + 256;
+  uint8_t* mem = nullptr;
+  if (cudaMalloc(&mem, o_ws + ws_bytes) != cudaSuccess) return DUALKV_ERR_CUDA;
+  auto done = [&](int code) {
+    cudaStreamSynchronize(st);
+    cudaFree(mem);
+    return code;
+  };
+  const int32_t prompt_len = P;
+  std::vector<int32_t> ones(B, 1);
+  if (cudaMemsetAsync(mem, 0, o_ws, st) != cudaSuccess || cudaMemsetAsync(mem + o_ws, 0x7f, ws_bytes, st) != cudaSuccess ||
+      cudaMemcpyAsync(mem + o_lens, ones.data(), 4 * B, cudaMemcpyHostToDevice, st) != cudaSuccess ||
+      cudaMemcpyAsync(mem + o_plen, &prompt_len, 4, cudaMemcpyHostToDevice, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return done(DUALKV_ERR_CUDA);
+  DecodeArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(mem + o_q);
+  a.q_stride = Hq * D;
+  a.kv = PagedKV{mem, mem + pool, nullptr, nullptr, 1, ps, Hkv};
+  if (bits == 4) {
+    a.kv.ks = reinterpret_cast<__nv_bfloat16*>(mem + pool / 2);  // behind the codes, which take a quarter
+    a.kv.vs = reinterpret_cast<__nv_bfloat16*>(mem + pool + pool / 2);
+  }
+  a.prompt_table = a.table = reinterpret_cast<const int32_t*>(mem + o_table);  // a response needs one entry: 0
+  a.prompt_lens = reinterpret_cast<const int32_t*>(mem + o_plen);
+  a.lens = reinterpret_cast<const int32_t*>(mem + o_lens);
+  a.max_prompt_pages = P / ps;
+  a.max_pages = 1;
+  a.G = 1;
+  a.B = B;
+  a.Hq = Hq;
+  a.by_ps = FastDiv(ps);
+  a.by_heads = FastDiv(Hq / Hkv);
+  a.scale_log2 = 0.08838834764831845f * 1.4426950408889634f;
+  a.out = reinterpret_cast<__nv_bfloat16*>(mem + o_out);
+  a.lse = reinterpret_cast<float*>(mem + o_lse);
+  a.workspace = mem + o_ws;
+  a.status = status;
+  a.device = device;
+  a.wait_limit_ns = limit_ns;
+  a.test_skip_tile = 0;
+  a.big = (unsigned long long)P * B * Hq >= big_work(a.kv);
+  CUtensorMap tk = {}, tv = {};
+  if (bits == 16 && (make_tmap(&tk, a.kv.k, Hkv * ps, 1, D, 16) || make_tmap(&tv, a.kv.v, Hkv * ps, 1, D, 16)))
+    return done(DUALKV_ERR_CUDA);
+  return done(a.big && launch_decode(D, a, tk, tv, groups, st) == cudaSuccess ? DUALKV_OK : DUALKV_ERR_CUDA);
+}
+
 int dualkv_selftest_kernel(int which, uint64_t limit_ns, void* stream) {
-  if (which < 0 || which > 4) return DUALKV_ERR_INVALID;
+  if (which < 0 || which > 7 || which == 5) return DUALKV_ERR_INVALID;
   if (limit_ns < 1000000ull || limit_ns > 10000000000ull) return DUALKV_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(g_mu);
@@ -1434,6 +1490,7 @@ int dualkv_selftest_kernel(int which, uint64_t limit_ns, void* stream) {
   uint32_t* status = nullptr;
   if ((rc = status_word(dev, &status))) return rc;
   if (which == 4) return selftest_pds512(limit_ns, st, status);
+  if (which >= 6) return selftest_decode(which == 6 ? 16 : 4, limit_ns, st, status, dev);
   // a tiny layout with zero inputs: P = 128 and two responses of 128, one head, D = 128
   constexpr int P = 128, N = 2, Hq = 1, Hkv = 1, D = 128;
   const int32_t off[N + 1] = {0, 128, 256};

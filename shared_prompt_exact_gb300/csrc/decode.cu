@@ -35,7 +35,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int in_group = (b - seg.off[g]) * GQ + j;
   cudaGridDependencySynchronize();
   const Partial none{kLowest, 0.f, 0, 0};
-  const Partial p0 = sees_prompt ? ws.partial[own / 2 + row] : none, p1 = sees_own ? ws.partial[row] : none;
+  Partial p0 = sees_prompt ? ws.partial[own / 2 + row] : none, p1 = sees_own ? ws.partial[row] : none;
+  // A block of prompt.cu's whose wait ran out has left nothing, and what lies in its place may be anything: workers without
+  // places in the workspace are recorded and count as none.
+  auto hold = [&](Partial& p) {
+    const bool block = p.worker & kBlockWorker;
+    const size_t end = (size_t)(p.worker & ~kBlockWorker) + (size_t)max(p.parts, 0);
+    if (p.parts >= 1 && end * (size_t)(block ? 128 : cols) <= (block ? kBlockSlots : kWarpSlots)) return;
+    if (A.status) atomicOr(A.status, kDevErrBounds);
+    p = none;
+  };
+  if (sees_prompt) hold(p0);
+  if (sees_own) hold(p1);
   const bool big = p0.worker & kBlockWorker;
   const int n = p0.parts + p1.parts;
   // slots of the workers behind a source's first one

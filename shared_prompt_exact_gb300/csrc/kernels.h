@@ -287,6 +287,10 @@ struct DecodeArgs {
   FastDiv by_ps, by_heads;  // by the page size and by Hq / Hkv
   int device;
   bool big;          // launch_prompt's kernel runs before and takes the prompts that are worth it
+  uint64_t wait_limit_ns = kLaunchWaitLimitNs;
+  // failure-path self-test only (-1 otherwise): the tile of keys with this index in each block of launch_prompt's kernel
+  // is never loaded, so the wait for it runs out after wait_limit_ns
+  int test_skip_tile = -1;
 };
 // Prompts of groups with this many rows and more go to launch_prompt's kernel ...
 constexpr int kBigRows = 32;

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
                     reinterpret_cast<int*>(smem + C::RINGS) + A.G + 1};
   const uint32_t warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int GQ = (int)A.by_heads.d, ps = A.kv.ps;
-  FailState fs{&ctl.abort_flag, A.status, kLaunchWaitLimitNs};
+  FailState fs{&ctl.abort_flag, A.status, A.wait_limit_ns};
 
   if (threadIdx.x == 0) {
     ctl.abort_flag = 0;
@@ -256,9 +256,10 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
             fence_async();
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(boxes) * 16 * 128 * QCH);
+          const bool skip = !values && filled == A.test_skip_tile;  // failure-path self-test: never loaded
+          if (lane == 0 && !skip) mbar_arrive_expect_tx(&full[slot], __popc(boxes) * 16 * 128 * QCH);
           __syncwarp();
-          if (whole)
+          if (whole && !skip)
             for (int c = 0; c < QCH; ++c)
               tma_load_3d(dst + c * C::BN * 128 + lane * 16 * 128, tm, &full[slot], c * 64, 0, row);
           page = next;
@@ -271,8 +272,10 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       }
       // copies still in flight end before the block does
       if (!ok)
-        for (int back = 1; back <= slots && back <= filled; ++back)
+        for (int back = 1; back <= slots && back <= filled; ++back) {
+          if (!values && filled - back == A.test_skip_tile) continue;
           mbar_wait_drain(&full[(filled - back) % slots], ((filled - back) / slots) & 1, kWaitLimitNs);
+        }
     } else {
       constexpr int U = D / 32;  // 16-byte vectors of a row's codes: one for each group of 32 values
       const int mine = (int)(warp - (values ? C::V_WARP : 0)) * 32 + (int)lane;  // this thread's row of a tile
@@ -320,7 +323,8 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
+        if (lane == 0 && (values || filled != A.test_skip_tile)) mbar_arrive(&full[slot]);
+        ++filled;
         if (++slot == slots) {
           slot = 0;
           phase ^= 1;
