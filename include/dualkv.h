@@ -428,7 +428,8 @@ int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int ma
  *   pages, lens     device int32 [B, max_pages] and [B], B = groups[G].  lens[b] = 0: the prompt
  *                   alone; negative: the response has ended, and nothing is read for it
  *   groups          HOST int32 [G+1], groups[0] = 0, non-decreasing; G <= 4095, B <= 8192,
- *                   and the tables' tokens times the queries that see them below 2^38
+ *                   a table's tokens (max_pages * page_size) at most 2^31 - 256, and the
+ *                   tables' tokens times the queries that see them below 2^38
  *                   (DUALKV_ERR_UNSUPPORTED beyond).  B = 0: nothing is done
  *   scale           > 0; scale * log2(e) has to be finite
  *   window          <= 0: all tokens; else the last `window` ones

@@ -793,6 +793,9 @@ int decode_impl(const void* q, int64_t q_stride, const dualkv_kv_cache* cache, c
   if (prompts ? !table_fits(max_prompt_pages, cache->page_size) : max_prompt_pages != 0) return DUALKV_ERR_INVALID;
   const uint64_t B = (uint64_t)groups[G], uG = (uint64_t)G;
   if (B == 0) return DUALKV_OK;
+  // the kernels walk tiles of up to 128 tokens, two of them ahead, and count tokens in 32 bits
+  for (int n : {max_pages, max_prompt_pages})
+    if ((int64_t)n * cache->page_size > INT32_MAX - 255) return DUALKV_ERR_UNSUPPORTED;
   // the kernels count tiles of 16 tokens, once for every 8 queries that share them, in 32 bits
   const uint64_t GQ = (uint64_t)(Hq / Hkv), page_tiles = (uint64_t)cache->page_size / 16;
   uint64_t tiles = B * ((GQ + 7) / 8) * (uint64_t)max_pages * page_tiles;

@@ -1,0 +1,102 @@
+"""Decodes at the ends of 32 bits.  A stream of up to 2^31 - 256 tokens repeats one page, so its attention is that over the
+page's tokens, each as often as it occurs.
+
+Tolerances: as in test_gpu_decode, and for long sums: of n tokens a warp (912 of them at least) takes n / 912, and a lane
+or a matrix instruction adds up 16 of those at once, so that sums, which may be cut off at each of the `adds` = n / (16 * 912)
+additions, are off by `adds` 2^-23 of them.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from shared_prompt_exact_gb300 import build as pbuild
+from shared_prompt_exact_gb300 import dualkv as dk
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF = torch.bfloat16
+MOST = 2 ** 31 - 256
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    pbuild.build()
+    dk.load()
+
+
+def _cache(ps, Hkv, D, bits, pages=1, seed=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    if bits == 16:
+        return dk.KVCache(*(rn(pages, Hkv, ps, D).to(BF) for _ in range(2)))
+    scale = [((0.1 + 0.2 * torch.rand(pages, Hkv, ps, D // 32, generator=g, device="cuda")).to(BF).view(torch.int16) & ~7).view(BF)
+             for _ in range(2)]
+    return dk.KVCache(*(torch.randint(0, 256, (pages, Hkv, ps, D // 2), generator=g, device="cuda", dtype=torch.uint8)
+                        for _ in range(2)), *scale)
+
+
+def _values(cache, page=0):
+    """Keys and values of a page in 64 bits, [Hkv, ps, D]."""
+    k, v = (t[page].cpu() for t in (cache.k, cache.v))
+    if cache.bits == 16:
+        return k.double().numpy(), v.double().numpy()
+    return tuple(oc.values(oc.unpack_codes(x.numpy()), s[page].cpu().double().numpy())
+                 for x, s in ((k, cache.k_scale), (v, cache.v_scale)))
+
+
+def _counts(lo, hi, ps):
+    """How often tokens [lo, hi) of a stream that repeats a page hit each slot."""
+    full = lambda n: n // ps + (np.arange(ps) < n % ps)  # noqa: E731
+    return (full(hi) - full(lo)).astype(np.float64)
+
+
+def _check(out, lse, q, parts, scale, adds):
+    """out [Hq, D], lse [Hq] against attention over parts (keys, values, counts)."""
+    k, v = (np.concatenate([p[i] for p in parts], 1) for i in (0, 1))
+    n = np.concatenate([p[2] for p in parts])
+    Hkv, D = k.shape[0], k.shape[2]
+    qg = q.reshape(Hkv, -1, D)
+    x = scale * np.einsum("hgd,htd->hgt", qg, k)
+    x = np.where(n > 0, x, -np.inf)
+    m = x.max(-1, keepdims=True)
+    e = np.exp(x - m) * n
+    total = e.sum(-1, keepdims=True)
+    p = e / total
+    want, A = (np.einsum("hgt,htd->hgd", p, y).reshape(-1, D) for y in (v, np.abs(v)))
+    X = scale * np.einsum("hgd,htd->hgt", np.abs(qg), np.abs(k))[..., n > 0].max(-1).reshape(-1)
+    want_lse = (m + np.log(total)).reshape(-1)
+    d, long = (4 * D + 32) * U * X, 2 * U * adds
+    assert np.all(np.abs(out - want) <= 2.0 ** -8 * (np.abs(want) + A) + (2 * d[:, None] + 2.0 ** -20 + 2 * long) * A)
+    assert np.all(np.abs(lse - want_lse) <= d + 2.0 ** -20 + 4 * U * np.abs(want_lse) + 2 * long)
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _own(n, window, D, bits, Hq, Hkv, ps, table_tokens=MOST):
+    """One response of n tokens, all of them in one page."""
+    cache = _cache(ps, Hkv, D, bits)
+    pages = torch.zeros(1, table_tokens // ps, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q = torch.randn(1, Hq, D, generator=g, device="cuda").to(BF)
+    out, lse = dk.decode(q, cache, None, None, pages, _i32(n), [0, 1], window)
+    dk.dualkv_check_status()
+    lo = max(0, n - window) if window else 0
+    adds = -(-(n - lo) // (16 * 912)) + 8
+    _check(_np(out)[0], _np(lse)[:, 0], _np(q)[0], [(*_values(cache), _counts(lo, n, ps))], D ** -0.5, adds)
+
+
+@pytest.mark.parametrize("D,bits,ps", [(64, 4, 256), (64, 16, 16), (128, 16, 32), (128, 4, 64), (512, 16, 128), (512, 4, 256)])
+@pytest.mark.parametrize("n", [MOST, MOST - 1, MOST - 63, MOST - 64])
+def test_a_window_at_the_end_of_the_longest_table(D, bits, ps, n):
+    _own(n, 500, D, bits, 4, 1, ps)
+
+
+def test_every_token_of_the_longest_table():
+    _own(MOST, 0, 64, 4, 1, 1, 256)
