@@ -60,9 +60,9 @@ __device__ __forceinline__ int prompt_len(const DecodeArgs& A, int g, uint32_t* 
 __device__ __forceinline__ int response_len(const DecodeArgs& A, int b, uint32_t* status) {
   return clamp_len(A.lens[b], A.max_pages, A.kv.ps, status);
 }
-// First position that a response of n tokens behind a prompt of P sees.
+// First of the prompt's P tokens that a response of n tokens sees; P if it sees none of them.
 __device__ __forceinline__ int first_position(const DecodeArgs& A, int P, int n) {
-  return A.window > 0 ? (int)max((int64_t)0, (int64_t)P + n - A.window) : 0;
+  return A.window > 0 ? (int)min((int64_t)P, max((int64_t)0, (int64_t)P + n - A.window)) : 0;
 }
 // Tiles of tokens [lo, end).
 template <int TILE>

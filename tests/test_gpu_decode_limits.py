@@ -100,3 +100,29 @@ def test_a_window_at_the_end_of_the_longest_table(D, bits, ps, n):
 
 def test_every_token_of_the_longest_table():
     _own(MOST, 0, 64, 4, 1, 1, 256)
+
+
+@pytest.mark.parametrize("bits,D,times", [(16, 64, 1), (4, 128, 1), (16, 512, 1), (16, 128, 2), (4, 64, 2)])
+@pytest.mark.parametrize("P,lens,window", [
+    (2 ** 31 - 65536, [200_000, 150_000, 70_000, 66_000], 1000),  # every response past 2^31: the prompt is out of sight
+    (2 ** 31 - 65536, [65_000, 65_536 + 600, 300, 70_000], 1000),  # some see its end
+    (2 ** 31 - 65536, [0, 64, 1, 2 ** 31 - 65536], 128),
+    (2 ** 31 - 65536, [100, 50_000, 7, 0], 150_000),  # 32 queries for 150,000 of its tokens: the prompts' kernel
+])
+def test_positions_past_2_31(bits, D, times, P, lens, window):
+    # prompt and responses repeat a page each; positions run up to 2^32
+    ps, Hkv = 65536, 1
+    lens = lens * times
+    B, Hq = len(lens), 4
+    cache = _cache(ps, Hkv, D, bits, pages=2)
+    prompt_pages = torch.zeros(1, P // ps, dtype=torch.int32, device="cuda")
+    pages = torch.ones(B, max(lens) // ps + 1 if max(lens) < P else P // ps, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(10)
+    q = torch.randn(B, Hq, D, generator=g, device="cuda").to(BF)
+    out, lse = dk.decode(q, cache, prompt_pages, _i32(P), pages, _i32(*lens), [0, B], window)
+    dk.dualkv_check_status()
+    held = [_values(cache, page) for page in (0, 1)]
+    for b, n in enumerate(lens):
+        lo = max(0, P + n - window)
+        parts = [(*held[0], _counts(min(lo, P), P, ps)), (*held[1], _counts(max(lo - P, 0), n, ps))]
+        _check(_np(out)[b], _np(lse)[:, b], _np(q)[b], parts, D ** -0.5, 150_000 // (16 * 152) + 8)
