@@ -437,7 +437,8 @@ int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int ma
  *                   A response that sees no token has out 0 and lse -inf
  *   workspace       device, 256-byte aligned, >= dualkv_decode_workspace_bytes() (0 for invalid input);
  *                   calls that may overlap need one each
- * Keys and values that no query of the call sees may hold anything.  What one of a group's
+ * Keys and values that no query of the call sees may hold anything, and under a window the entries of pages
+ * that lie wholly in front of what they see are not used.  What one of a group's
  * responses sees has to be finite for all of them to be.
  * No output may share memory with an input or another output (DUALKV_ERR_INVALID).
  * The lengths stay on the device: these three calls may be captured into a CUDA graph whose replays

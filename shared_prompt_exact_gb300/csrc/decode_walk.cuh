@@ -247,9 +247,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
     };
     auto issue_keys = [&]() {
       if (tile_k < last) {
-        has_page = (uint32_t)page < (uint32_t)A.kv.pages;
+        // sub-tiles in front of every row's window are not looked at: their pages may have been given away
+        const bool seen = token < end && (!WINDOW || token + 16 > lo_min);
+        has_page = seen && (uint32_t)page < (uint32_t)A.kv.pages;
         const uint32_t bit = 1u << (tile_k & 31);
-        missing = __any_sync(0xffffffffu, !has_page && token < end) ? missing | bit : missing & ~bit;
+        missing = __any_sync(0xffffffffu, seen && !has_page) ? missing | bit : missing & ~bit;
         row = cache_row(A.kv, page, kvh, in_page);
         if (has_page) copy_rows(A.kv.k, A.kv.ks, C::KP);
         token += TILE;
@@ -319,7 +321,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
       uint32_t gone = 0;  // sub-tiles without a page: their keys do not count
       if (missing >> (tile & 31) & 1) {
         const int at_key = key0 + 16 * lane;
-        const bool bad = lane < KT && at_key < end && page_at(A.kv, table, max_pages, A.by_ps(at_key), A.status) < 0;
+        const bool bad = lane < KT && at_key < end && (!WINDOW || at_key + 16 > lo_min) &&
+                         page_at(A.kv, table, max_pages, A.by_ps(at_key), A.status) < 0;
         gone = __ballot_sync(0xffffffffu, bad);
         edge = true;
       }
