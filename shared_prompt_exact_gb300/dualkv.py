@@ -662,9 +662,10 @@ _I32, _U8 = (torch.int32,), (torch.uint8,)
 class KVCache:
     """A paged cache of keys and values: bf16 pools [pages, Hkv, page_size, D], or 4-bit codes, two to a byte
     (uint8 [pages, Hkv, page_size, D / 2]), with bf16 scales [pages, Hkv, page_size, D / 32].  It wraps tensors
-    that the caller owns; ``KVCache.empty`` allocates them."""
+    that the caller owns; ``KVCache.empty`` allocates them.  A cache keeps the tensors that it was made of, where
+    they were: calls refuse it once one of them has other memory (``set_``, ``resize_`` beyond it)."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "Hkv", "page_size", "D", "device", "_c")
+    __slots__ = ("_pools", "_at", "_c", "_shape", "_device")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if not isinstance(k, _Tensor) or not k.is_cuda or k.dim() != 4:
@@ -672,22 +673,24 @@ class KVCache:
         shape, dev = k.shape, k.get_device()
         pages, Hkv, ps, width = shape
         if k_scale is None and v_scale is None:
-            struct = _CacheStruct(_arg("KVCache", "k", k, shape, _BF16, dev), _arg("KVCache", "v", v, shape, _BF16, dev),
-                                  None, None, pages, ps, 16)
+            at = _arg("KVCache", "k", k, shape, _BF16, dev), _arg("KVCache", "v", v, shape, _BF16, dev)
+            struct = _CacheStruct(*at, None, None, pages, ps, 16)
         elif k_scale is None or v_scale is None:
             raise ValueError("KVCache: k_scale and v_scale go together")
         else:
             width *= 2
             groups = (pages, Hkv, ps, width // CACHE_GROUP)
-            struct = _CacheStruct(_arg("KVCache", "k", k, shape, _U8, dev), _arg("KVCache", "v", v, shape, _U8, dev),
-                                  _arg("KVCache", "k_scale", k_scale, groups, _BF16, dev),
-                                  _arg("KVCache", "v_scale", v_scale, groups, _BF16, dev), pages, ps, 4)
-        self.k, self.v, self.k_scale, self.v_scale, self.device, self._c = k, v, k_scale, v_scale, dev, struct
-        self.pages, self.Hkv, self.page_size, self.D = pages, Hkv, ps, width
+            at = (_arg("KVCache", "k", k, shape, _U8, dev), _arg("KVCache", "v", v, shape, _U8, dev),
+                  _arg("KVCache", "k_scale", k_scale, groups, _BF16, dev),
+                  _arg("KVCache", "v_scale", v_scale, groups, _BF16, dev))
+            struct = _CacheStruct(*at, pages, ps, 4)
+        self._pools, self._at, self._c = (k, v, k_scale, v_scale), at, struct
+        self._shape, self._device = (pages, Hkv, ps, width), dev
 
-    @property
-    def bits(self):
-        return self._c.bits
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._pools[i]) for i in range(4))
+    pages, Hkv, page_size, D = (property(lambda self, i=i: self._shape[i]) for i in range(4))
+    device = property(lambda self: self._device)
+    bits = property(lambda self: self._c.bits)
 
     @classmethod
     def empty(cls, pages, Hkv, page_size, D, bits=16, device="cuda"):
@@ -706,10 +709,15 @@ class KVCache:
 def _cache_arg(where, cache, Hkv, D, device):
     if not isinstance(cache, KVCache):
         raise ValueError(f"{where}: cache must be a KVCache")
-    if cache.Hkv != Hkv or cache.D != D:
-        raise ValueError(f"{where}: cache holds {cache.Hkv} heads of {cache.D}, not {Hkv} of {D}")
-    if cache.device != device:
-        raise ValueError(f"{where}: cache is on cuda:{cache.device}, the current device is cuda:{device}")
+    _, heads, _, width = cache._shape
+    if heads != Hkv or width != D:
+        raise ValueError(f"{where}: cache holds {heads} heads of {width}, not {Hkv} of {D}")
+    if cache._device != device:
+        raise ValueError(f"{where}: cache is on cuda:{cache._device}, the current device is cuda:{device}")
+    k, v, ks, vs = cache._pools
+    at = (k.data_ptr(), v.data_ptr()) if ks is None else (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
+    if at != cache._at:
+        raise ValueError(f"{where}: cache: its tensors have other memory by now, wrap them in a new KVCache")
     return cache._c
 
 
