@@ -434,7 +434,8 @@ int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int ma
  *   scale           > 0; scale * log2(e) has to be finite
  *   window          <= 0: all tokens; else the last `window` ones
  *   out             device bf16 [B, Hq, D], written; lse device fp32 [Hq, B], written, may be NULL.
- *                   A response that sees no token has out 0 and lse -inf
+ *                   A response that sees no token has out 0 and lse -inf; one that sees a key
+ *                   with a NaN has NaN in both
  *   workspace       device, 256-byte aligned, >= dualkv_decode_workspace_bytes() (0 for invalid input);
  *                   calls that may overlap need one each
  * Keys and values that no query of the call sees may hold anything, and under a window the entries of pages

@@ -117,12 +117,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
   }
   if (!live) return;
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;  // 0: nothing seen; NaN stays NaN, here and in lse
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D);
 #pragma unroll
   for (int e = 0; e < E; ++e) out[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
   if (lane == 0 && A.lse)
-    A.lse[(int64_t)h * A.B + b] = total > 0.f ? (top + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    A.lse[(int64_t)h * A.B + b] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.69314718055994530942f;
 }
 
 template <int D, int CAP>
