@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const bool live = row < (int64_t)A.B * A.Hq;
   const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
   const int GQ = (int)A.by_heads.d, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
-  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  const Workspace ws = carve(A.workspace, D, A.B, A.Hq, GQ);
   // which sources the row sees, as the kernels that left the partial results decided
   const int len = response_len(A, b, nullptr), P = prompt_len(A, g, nullptr);
   const bool sees_own = live && len > 0, sees_prompt = live && len >= 0 && first_position(A, P, len) < P;
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   auto hold = [&](Partial& p) {
     const bool block = p.worker & kBlockWorker;
     const size_t end = (size_t)(p.worker & ~kBlockWorker) + (size_t)max(p.parts, 0);
-    if (p.parts >= 1 && end * (size_t)(block ? 128 : cols) <= (block ? kBlockSlots : kWarpSlots)) return;
+    if (p.parts >= 1 && end * (size_t)(block ? 128 : cols) <= (block ? block_slots(D, A.B, GQ) : warp_slots(D, GQ))) return;
     if (A.status) atomicOr(A.status, kDevErrBounds);
     p = none;
   };
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const bool big = p0.worker & kBlockWorker;
   const int n = p0.parts + p1.parts;
   // slots of the workers behind a source's first one
-  const size_t behind0 = big ? own + kWarpSlots + (size_t)(p0.worker & ~kBlockWorker) * 128 + (in_group & 127)
+  const size_t behind0 = big ? own + warp_slots(D, GQ) + (size_t)(p0.worker & ~kBlockWorker) * 128 + (in_group & 127)
                              : own + (size_t)p0.worker * cols + (in_group & (cols - 1));
   const size_t behind1 = own + (size_t)p1.worker * cols + (j & (cols - 1));
   auto place = [&](int i) {
@@ -149,9 +149,9 @@ cudaError_t launch_decode(int D, const DecodeArgs& a, const CUtensorMap& tk, con
   return D == 64 ? join<64>(a, groups, st) : D == 128 ? join<128>(a, groups, st) : join<512>(a, groups, st);
 }
 
-size_t decode_workspace_bytes(int B, int Hq, int, int D) {
-  const Workspace w = carve(nullptr, B, Hq);
-  return reinterpret_cast<size_t>(w.o) + sizeof(float) * slots_of(B, Hq) * (size_t)D;
+size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
+  const Workspace w = carve(nullptr, D, B, Hq, Hq / Hkv);
+  return reinterpret_cast<size_t>(w.o) + sizeof(float) * slots_of(D, B, Hq, Hq / Hkv) * (size_t)D;
 }
 
 }  // namespace dkv

@@ -84,15 +84,22 @@ struct Workspace {
 };
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Slots: the rows' own ones of the responses and of the prompts, for a source's first tiles; then those for what a
-// worker goes on with that another one began: 16 for a warp, 128 for a block of prompt.cu.
-constexpr size_t kWarpSlots = (size_t)kBlocks * 16 * 16, kBlockSlots = (size_t)kBlocks * 128;
+// worker goes on with that another one began: its rows for each warp of the walk (COLS, by Cfg's warps to a block), and where some
+// group may have kBigRows rows, 128 for each block of prompt.cu.
+__host__ __device__ constexpr int warp_rows(int D, int GQ) { return D == 512 ? 8 * 8 : GQ > 8 ? 12 * 16 : 16 * 8; }  // of a block
 __host__ __device__ inline size_t own_slots(int B, int Hq) { return 2 * (size_t)B * Hq; }
-__host__ __device__ inline size_t slots_of(int B, int Hq) { return own_slots(B, Hq) + kWarpSlots + kBlockSlots; }
-__host__ __device__ inline Workspace carve(void* p, int B, int Hq) {
+__host__ __device__ inline size_t warp_slots(int D, int GQ) { return (size_t)kBlocks * warp_rows(D, GQ); }
+__host__ __device__ inline size_t block_slots(int D, int B, int GQ) {
+  return D != 512 && (int64_t)B * GQ >= kBigRows ? (size_t)kBlocks * 128 : 0;
+}
+__host__ __device__ inline size_t slots_of(int D, int B, int Hq, int GQ) {
+  return own_slots(B, Hq) + warp_slots(D, GQ) + block_slots(D, B, GQ);
+}
+__host__ __device__ inline Workspace carve(void* p, int D, int B, int Hq, int GQ) {
   uint8_t* at = static_cast<uint8_t*>(p);
   Workspace w;
   w.partial = reinterpret_cast<Partial*>(at);
-  w.o = reinterpret_cast<float*>(at + align256(sizeof(Partial) * slots_of(B, Hq)));
+  w.o = reinterpret_cast<float*>(at + align256(sizeof(Partial) * slots_of(D, B, Hq, GQ)));
   return w;
 }
 

@@ -58,6 +58,7 @@ struct Cfg {
   static constexpr int SLOTS = D == 64 && BITS == 4 ? 4 : 2;
   static constexpr int COLS = 8 * NT;
   static constexpr int RING = SLOTS * SLOT;  // bytes of a warp's ring
+  static_assert(WARPS * COLS <= warp_rows(D, NT == 2 ? 9 : 8), "the workspace has a place for each row of each warp");
 };
 
 // Rows that a warp takes at once: 16 where a kv-head has more than 8 and the accumulators leave the registers.
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::WARPS * 32, 1)
   __shared__ uint32_t scratch[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int GQ = (int)A.by_heads.d, sources = A.G + A.B;
-  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  const Workspace ws = carve(A.workspace, D, A.B, A.Hq, GQ);
   if (!A.big) cudaGridDependencySynchronize();  // else prompt.cu's kernel has seen to it before this one could start
   deal_sources<C::COLS, C::TILE, false, WINDOW>(A, seg, src, scratch);
   const Deal deal = make_deal(cum[sources], A.kv.Hkv, kBlocks * warps);

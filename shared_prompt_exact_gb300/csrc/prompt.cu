@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
   tc_fence_after();
   cudaTriggerProgrammaticLaunchCompletion();  // the responses' kernel may start where SMs are free
   const uint32_t tmem = ctl.tmem_base;
-  const Workspace ws = carve(A.workspace, A.B, A.Hq);
+  const Workspace ws = carve(A.workspace, D, A.B, A.Hq, GQ);
   const uint32_t* cum = src.cum;
   if (ctl.chunk) {
     cum = padded;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(PromptCfg<D, BITS>::THREADS, 1)
       const float mtot = fmaxf(m0, m1), mref = mtot == -INFINITY ? kLowest : mtot;
       const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mref), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mref);
       const size_t own = own_slots(A.B, A.Hq);
-      const size_t to = s.parts ? own / 2 + (size_t)b_of * A.Hq + head : own + kWarpSlots + (size_t)blockIdx.x * 128 + row;
+      const size_t to = s.parts ? own / 2 + (size_t)b_of * A.Hq + head : own + warp_slots(D, GQ) + (size_t)blockIdx.x * 128 + row;
       constexpr int OC = D / 2;  // output columns of this thread
       // 16 columns at a time through 2 KB of the queries' place (their products are done), so that 4 lanes write
       // 64 bytes of one row; the rows' slots are consecutive but where a response's other heads lie between
