@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int b = live ? (int)(row / A.Hq) : 0, h = live ? (int)(row - (int64_t)b * A.Hq) : 0;
   const int GQ = (int)A.by_heads.d, j = h - A.by_heads(h) * GQ, g = seg_of(seg, b);
   const Workspace ws = carve(A.workspace, D, A.B, A.Hq, GQ);
-  // which sources the row sees, as the kernels that left the partial results decided
+  // which sources the row sees, as the kernels that left the partial results decided (who wrote the lengths was complete
+  // before those began, so they may be read before the wait)
   const int len = response_len(A, b, nullptr), P = prompt_len(A, g, nullptr);
   const bool sees_own = live && len > 0, sees_prompt = live && len >= 0 && first_position(A, P, len) < P;
   const size_t own = own_slots(A.B, A.Hq);
