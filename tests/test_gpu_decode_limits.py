@@ -126,3 +126,48 @@ def test_positions_past_2_31(bits, D, times, P, lens, window):
         lo = max(0, P + n - window)
         parts = [(*held[0], _counts(min(lo, P), P, ps)), (*held[1], _counts(max(lo - P, 0), n, ps))]
         _check(_np(out)[b], _np(lse)[:, b], _np(q)[b], parts, D ** -0.5, 150_000 // (16 * 152) + 8)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("tiles", [2 ** 20, 2 ** 21 - 1, 2 ** 21, 2 ** 21 + 1, 2 ** 21 + 2431, 2 ** 24 - 1, 2 ** 24 + 3])
+def test_deals_around_2_21_tiles(tiles, bits):
+    # the deal's quotients come from fp32 below 2^21 and from integers above; tiles of 64 keys (D = 64)
+    ps, D = 256, 64
+    _own(64 * tiles - 5, 0, D, bits, 1, 1, ps, table_tokens=64 * 2 ** 24 + 1024)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens", [[64 * 911, 1, 64 * 7001 + 3, 0], [3, 64 * 2 ** 19, 64 * 2 ** 19 + 1, 64 * 2 ** 19 - 1]])
+def test_deals_of_several_sources(lens, bits):
+    # some 2^21 tiles of four responses and two kv-heads (the second one's tiles behind the first one's), a page each
+    ps, D, Hkv, Hq = 64, 64, 2, 4
+    cache = _cache(ps, Hkv, D, bits, pages=4)
+    pages = torch.arange(4, dtype=torch.int32, device="cuda")[:, None].repeat(1, max(lens) // ps + 1)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q = torch.randn(4, Hq, D, generator=g, device="cuda").to(BF)
+    out, lse = dk.decode(q, cache, None, None, pages, _i32(*lens), [0, 1, 2, 3, 4])
+    dk.dualkv_check_status()
+    for b, n in enumerate(lens):
+        if n:
+            _check(_np(out)[b], _np(lse)[:, b], _np(q)[b], [(*_values(cache, b), _counts(0, n, ps))], D ** -0.5,
+                   sum(lens) // (16 * 912) + 8)
+        else:
+            assert not bool(out[b].any()) and bool(torch.isneginf(lse[:, b]).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("tiles", [2 ** 20 // 151, 2 ** 20 + 1, 2 ** 21 + 5])
+def test_long_prompts_of_a_large_group(tiles, bits):
+    # the prompts' kernel: 32 queries, tiles of 128 keys
+    ps, D = 128, 64
+    P = 128 * tiles - 77
+    cache = _cache(ps, 1, D, bits, pages=2)
+    prompt_pages = torch.zeros(1, tiles, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q = torch.randn(8, 4, D, generator=g, device="cuda").to(BF)
+    lens = [3, 0, 100, 1, 7, 64, 65, 20]
+    out, lse = dk.decode(q, cache, prompt_pages, _i32(P), torch.ones(8, 1, dtype=torch.int32, device="cuda"), _i32(*lens), [0, 8])
+    dk.dualkv_check_status()
+    for b, n in enumerate(lens):
+        parts = [(*_values(cache, 0), _counts(0, P, ps)), (*_values(cache, 1), _counts(0, n, ps))]
+        _check(_np(out)[b], _np(lse)[:, b], _np(q)[b], parts, D ** -0.5, P // (16 * 152) + 8)
