@@ -420,7 +420,8 @@ int dualkv_cache_read(const dualkv_kv_cache* cache, const int32_t* pages, int ma
  * response b stands at position P + n - 1 and sees, by the rule above, the prompt's tokens (positions
  * 0 .. P - 1) and its own n (positions P ..): out = softmax(scale q k^T) v, lse its log-sum-exp.
  * The query's own key is expected in the cache (dualkv_cache_append, with lens counting it).
- * A prompt is read for a whole group at once.
+ * A prompt is read for a whole group at once.  Scores, sums and partial results are fp32; the weights exp(x - max)
+ * are rounded to bf16 for their product with the values (their sum is taken before), as in dualkv_fwd.
  *
  *   q               device bf16: head h of response b at [b * q_stride + h * D], q_stride as above
  *   prompt_pages    device int32 [G, max_prompt_pages], prompt_lens device int32 [G] (0: no prompt);
