@@ -358,8 +358,10 @@ int dualkv_policy_loss_bwd(const float* logp, const float* old_logp, const float
  *             scale * (code - 8), codes 1 .. 15, with its group's scale (32 values of a head): a seventh of
  *             the group's largest magnitude rounded up to 5 significant bits, so the value
  *             is exact in bf16; a magnitude goes to the nearest code, from half way to the larger one.
- *             Keys are quantised as their exact values behind norm and rotation, off by 2^-42 of
- *             their pair's size and 2^-52 of their angle: only a border that near may be missed.
+ *             Keys are quantised as fp32 gives them behind norm and rotation, each operation rounded once:
+ *             mean of squares (of its exact value), + eps, inverse root (rsqrtf), x r, w + w0, their
+ *             product, cosine and sine (of the angle in 64 bits), two products and their sum; so are top / 7,
+ *             key / step and + 1/2.  Next to a border a program in another order may find another code.
  *             A group with a value that is not finite has the scale NaN.  |x| up to 9e37 (with a norm 1e18,
  *             as in dualkv_qk_norm_rope: its mean of squares is in fp32)
  * page_size is a multiple of 16 up to 65,536; all pointers are 16-byte aligned.  A stream's tokens lie in

@@ -10,17 +10,22 @@
 //     a group with a value that is not finite gets the scale NaN
 // read: the same rows back in bf16.
 //
-// Codes and steps jump at borders, so those of the keys are decided by more than fp32: where its rounding errors could put a key
-// of a group on the other side (kKeyError), the group's keys are formed again in two floats each (exact_group).
+// Codes and steps jump at borders, so which arithmetic a key comes from shows.  4-bit keys are what fp32 gives, each operation
+// rounded once:
+//   m = mean x^2 (of its exact value), r = rsqrt(m + eps), a = (x r) (w + w0), c and s = cosine and sine of the angle in 64 bits,
+//   key = (a c) - (b s) or (b c) + (a s);  step = ceil5(max |key| / 7), n = floor(|key| / step + 1/2)
+// so that any fp32 program in that order finds the same codes, but for the last bit of its mean.  The kernel forms them in the
+// order that is fastest (rope.cu's) and knows the error of that (kKeyError): a group with a border that near is formed
+// again, in this order (settle_group).
 //
 // Both touch each value once and are bound by HBM bandwidth (few rows: by latency).  The walk over
 // rows and heads, the loads ahead through shared memory and the arithmetic are rope.cu's: one warp per
 // row, q's heads first, then k's, then v's.  Keys are quantised before any rounding to bf16.
 // Measured: append of 71,680 rows of 32 + 2 x 8 heads of 128 in bf16 267 us (6.6 TB/s); of 23,200 rows of 8 + 2 x 2 heads of
-// 512 in 4 bits, with their read back, 118 us (bound by issue; 109 without the look at borders, which costs 4 % of the
-// instructions and, in 2 % of the steps, a group formed again: 2.7 us for a warp's first one; in fp64 it was 7 and the call 140 us;
-// 4 us less would remain of them if the bound were 8 times as small); read of 131,072 rows of 8 heads of 128 156 us (6.9 TB/s;
-// 177 with the values asked for behind the keys).
+// 512 in 4 bits 98 us (5.1 TB/s: bound by issue, 2,860 instructions a row; 90 us without the look at borders, of which
+// 4 are its instructions and 4 the groups formed again, in 2 % of the steps: 2.7 us for a warp's first one; in fp64 it was 7 us and the
+// launch 120; with a bound 8 times as small 95 us); read of 131,072 rows of 8 heads of 128 156 us (6.9 TB/s; 177 with the
+// values asked for behind the keys).
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
@@ -110,10 +115,12 @@ __device__ __forceinline__ float magnitude8(const Vec8& x) {
                     magnitude3(x.v[2].y, x.v[3].x, x.v[3].y), 0.f);
 }
 
-// Error of a key in fp32, by the largest magnitude of the two vectors that its lane turned.  With u = 2^-24: sum of
-// squares 14 u, + eps u, root half of that and 4 u, product with the weight 3 u: 14.5 u of each value of a pair; cosine and
-// sine 1.6 u for the angle's float and 4 u; their products' roundings 2 u.  In all 16.5 u sqrt(2) + 5.6 u * 2 = 35 u.
-constexpr float kKeyError = 40.f * 0x1p-24f;
+// Difference between a key as the walk forms it and as it is defined, by the largest magnitude of the two vectors that its lane
+// turned, with u = 2^-24.  The walk: sum of squares 14 u, + eps u, root half of that and 4 u, product with the weight 3 u: 14.5 u of each
+// value of a pair; cosine and sine 1.6 u for the angle's float and 4 u; their products' roundings 2 u: in all 16.5 u sqrt(2) +
+// 5.6 u * 2 = 35 u.  The definition: mean and eps u, root 4 u, products and weight 3 u, cosine and sine, their products
+// and sum 3 u: 11 u sqrt(2) = 16 u.
+constexpr float kKeyError = 52.f * 0x1p-24f;
 
 // x rounded up to 5 significant bits.
 __device__ __forceinline__ uint32_t five_bits(float x) { return (__float_as_uint(x) + 0x7ffffu) & ~0x7ffffu; }
@@ -169,7 +176,7 @@ __device__ __forceinline__ uint2 quantise16(Vec8 (&x)[2], float size, __nv_bfloa
     for (int e = 7; e >= 0; --e) sum = (sum << 4) + __float_as_uint(codes[e]);
     out[w] = sum - 0x4b400000u * 0x11111111u;
   }
-  // (2^-20: the reciprocal's error of 7 2^-24, and the differences')
+  // (2^-20: the reciprocal's error of 7 2^-24 here, the quotient's and the sum's of 4 2^-24 each in the definition)
   if (KEYS) near |= !exact && !(far <= 0.5f - fmaf(size, kKeyError * inv, 0x1p-20f));
   return make_uint2(out[0], out[1]);
 }
@@ -206,26 +213,22 @@ __device__ __forceinline__ void store_codes(const uint2& c, __nv_bfloat16 scale,
   if ((i & 1) == 0) scales[row * (D / kGroup) + i / 2] = scale;
 }
 
-__device__ __forceinline__ Two shuffled(Two x, int o) {
-  return Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
-}
-
-// One group of 32 keys from its row of k, a value to a lane: codes and scale into the pool.  Each key is off by 2^-42 of its
-// pair's size and 2^-52 of its angle; borders (7 step, an odd number of half steps) are exact in fp32.
+// One group of 32 keys from its row of k, a value to a lane, as the keys' definition has them (above): codes and scale into the
+// pool.  The sum of squares and the cosines and sines come from two floats, rounded once.
 template <int D>
-__device__ __noinline__ void exact_group(const AppendArgs& A, const uint64_t* freq, const Undecided& u) {
+__device__ __noinline__ void settle_group(const AppendArgs& A, const uint64_t* freq, const Undecided& u) {
   const int lane = threadIdx.x & 31, d = kGroup * u.group + lane, half = A.half;
   const __nv_bfloat16* x = A.k + u.t * A.k_stride + (int64_t)u.head * D;
   // the value's partner in the rotation, if it is turned
   const bool is_turned = d < 2 * half, second = A.inter ? (d & 1) != 0 : d >= half;
   const int j = A.inter ? d >> 1 : second ? d - half : d, other = !is_turned ? d : A.inter ? d ^ 1 : second ? j : d + half;
-  Two y{__bfloat162float(x[d]), 0.f}, z{__bfloat162float(x[other]), 0.f};
+  float y = __bfloat162float(x[d]), z = __bfloat162float(x[other]);
   if (A.k_weight) {
     auto weight = [&](int e) {
-      return two_sum(A.weight_f32 ? static_cast<const float*>(A.k_weight)[e]
-                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(A.k_weight)[e]), A.w0);
+      return __fadd_rn(A.weight_f32 ? static_cast<const float*>(A.k_weight)[e]
+                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(A.k_weight)[e]), A.w0);
     };
-    const Two wy = weight(d), wz = weight(other);
+    const float wy = weight(d), wz = weight(other);
     float v[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = __bfloat162float(x[lane + 32 * e]);
@@ -236,33 +239,24 @@ __device__ __noinline__ void exact_group(const AppendArgs& A, const uint64_t* fr
       ss = Two{s.hi, ss.lo + s.lo};
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss = ss + shuffled(ss, o);
-    const Two mean = Two{ss.hi * (1.f / D), ss.lo * (1.f / D)} + Two{A.eps, 0.f}, r = refine_rsqrt(mean, rsqrtf(mean.hi));
-    y = y * r * wy;
-    z = z * r * wz;
+    for (int o = 16; o > 0; o >>= 1)
+      ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)};
+    const float r = rsqrtf(__fadd_rn(ss.hi * (1.f / D), A.eps));
+    y = product(product(y, r), wy);
+    z = product(product(z, r), wz);
   }
   if (is_turned) {
     Two c, s;
     cos_sin_turns((uint64_t)u.pos * freq[j], c, s);
-    y = y * c + (second ? z * s : -(z * s));
+    const float yc = product(y, c.hi), zs = product(z, s.hi);
+    y = second ? __fadd_rn(yc, zs) : __fsub_rn(yc, zs);
   }
-  const bool negative = y.hi < 0.f;
-  if (negative) y = -y;
-  Two top = y;
+  float top = fabsf(y);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Two v = shuffled(top, o);
-    if (v > top) top = v;
-  }
-  // the smallest step of five bits with top <= 7 step: one that may be too small by one, then the comparison
-  uint32_t bits = five_bits(product(__fdiv_rn(top.hi, 7.f), 1.f - 0x1p-21f));
-  if (top > Two{product(7.f, __uint_as_float(bits)), 0.f}) bits += 0x80000u;
-  const float step = __uint_as_float(bits);
-  // the same for n with (n - 1/2) step <= y < (n + 1/2) step
-  int n = bits ? (int)rintf(__fdiv_rn(y.hi, step)) : 0;
-  auto reaches = [&](int k) { return !(Two{product((float)k - 0.5f, step), 0.f} > y); };
-  if (bits) n = n < 7 && reaches(n + 1) ? n + 1 : n > 0 && !reaches(n) ? n - 1 : n;
-  const int code = 8 + (negative ? -n : n), pair = code | __shfl_down_sync(0xffffffffu, code, 1) << 4;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const uint32_t bits = five_bits(__fdiv_rn(top, 7.f));
+  const int n = bits ? (int)floorf(__fadd_rn(__fdiv_rn(fabsf(y), __uint_as_float(bits)), 0.5f)) : 0;
+  const int code = 8 + (y < 0.f ? -n : n), pair = code | __shfl_down_sync(0xffffffffu, code, 1) << 4;
   if ((lane & 1) == 0) static_cast<uint8_t*>(A.kv.k)[u.row * (D / 2) + d / 2] = (uint8_t)pair;
   if (lane == 0) A.kv.ks[u.row * (D / kGroup) + u.group] = __ushort_as_bfloat16((unsigned short)(bits >> 16));
 }
@@ -413,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
         if (live && !(again >> (lane & ~1) & 1)) store_codes<D>(c, scale, A.kv.k, A.kv.ks, row, i);
         for (; again; again &= again - 1) {
           const int from = __ffs(again) - 1, head = from / G + (step - nq) * S;
-          exact_group<D>(A, sh.freq, Undecided{page_row + (int64_t)head * A.kv.ps, (int)t, head, from % G / 2, at_row.pos});
+          settle_group<D>(A, sh.freq, Undecided{page_row + (int64_t)head * A.kv.ps, (int)t, head, from % G / 2, at_row.pos});
         }
       }
     }

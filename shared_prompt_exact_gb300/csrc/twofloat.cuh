@@ -42,16 +42,9 @@ __host__ __device__ __forceinline__ Two operator*(Two a, Two b) {
 }
 __host__ __device__ __forceinline__ Two operator-(Two a) { return Two{-a.hi, -a.lo}; }
 __host__ __device__ constexpr Two two(double x) { return Two{(float)x, (float)(x - (double)(float)x)}; }
-__host__ __device__ __forceinline__ bool operator>(Two a, Two b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
-// 1 / sqrt(x) from an approximation r good to 1e-6: r + r (e / 2 + 3 e^2 / 8), e = 1 - x r^2.
-__host__ __device__ __forceinline__ Two refine_rsqrt(Two x, float r) {
-  const Two p = x * Two{r, 0.f} * Two{r, 0.f};
-  const float e = (1.f - p.hi) - p.lo;
-  return fast_sum(r, product(r, fmaf(0.375f * e, e, 0.5f * e)));
-}
-
-// Cosine and sine of `turns` 2^-64 turns: the nearest quarter off, Taylor's series of what is left (up to pi / 4).
+// Cosine and sine of `turns` 2^-64 turns, off by 2^-44: the nearest quarter off, Taylor's series of what is left (up to
+// pi / 4).
 __host__ __device__ __forceinline__ void cos_sin_turns(uint64_t turns, Two& c, Two& s) {
   const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);  // 4 of them is 0 again
   const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));
