@@ -85,7 +85,8 @@ __device__ __forceinline__ bool has_page(const PagedKV& kv, const Place& p, uint
   return false;
 }
 
-// A group of keys that fp32 does not decide: group `group` of head `head` in row t at position pos, bound for row `row` of the pool.
+// A group of keys whose codes the walk's arithmetic does not decide: group `group` of head `head` in row t at position pos,
+// bound for row `row` of the pool.
 struct Undecided {
   int64_t row;
   int t, head, group;
@@ -124,6 +125,7 @@ constexpr float kKeyError = 52.f * 0x1p-24f;
 
 // x rounded up to 5 significant bits.
 __device__ __forceinline__ uint32_t five_bits(float x) { return (__float_as_uint(x) + 0x7ffffu) & ~0x7ffffu; }
+
 // Codes of 16 consecutive values; the neighbouring lane holds the other 16 of the group.  `size`: 0 where the values are bf16
 // as they came, else the magnitude that their errors go by (kKeyError); then `near` is set where an error could change a
 // code or the scale.
@@ -394,9 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
         __syncwarp();
         Vec8 v[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[e] = load8(keys + spread(16 * lane + 8 * e), keys + spread(16 * lane + 8 * e + 4));
-        }
+        for (int e = 0; e < 2; ++e) v[e] = load8(keys + spread(16 * lane + 8 * e), keys + spread(16 * lane + 8 * e + 4));
         const float2 sizes = *reinterpret_cast<const float2*>(&sh.size[warp][2 * lane]);
         __syncwarp();
         __nv_bfloat16 scale;
